@@ -75,8 +75,9 @@ def draw(rng):
         D = _log(rng, 32, 4096)
         if rng.random() < 0.7:
             D = max(64, D // 64 * 64)
-        T = _log(rng, 1, 16384)
-        return {"kind": kind, "T": T, "E": E, "e0": e0, "e1": e1, "k": k, "D": D, "dtype": rng.choice(["bf16", "fp32"]),
+        dtype = rng.choice(["bf16", "fp32"])
+        T = _log(rng, 1, 16384 if dtype == "bf16" else 8192)
+        return {"kind": kind, "T": T, "E": E, "e0": e0, "e1": e1, "k": k, "D": D, "dtype": dtype,
                 "skew": skew, "pad": rng.choice([0.0, 0.1])}
     N, K = 128 * _log(rng, 1, 40), 128 * _log(rng, 1, 32)
     e1 = min(e1, e0 + 96)
