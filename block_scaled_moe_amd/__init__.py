@@ -18,6 +18,8 @@ import os
 
 import torch
 
+from . import ops
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
 
@@ -96,7 +98,7 @@ def lib():
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is not built; run __graft_entry__.build() first")
         handle = ctypes.CDLL(LIB_PATH)
-        for name, (args, res) in SIGNATURES.items():
+        for name, (args, res) in {**SIGNATURES, **ops.SIGNATURES}.items():
             fn = getattr(handle, name)
             fn.argtypes = args
             fn.restype = res
@@ -333,3 +335,10 @@ class Layer:
         _check(lib().moe_forward_plan(ctypes.byref(self.args), ctypes.byref(info)), "moe_forward_plan")
         return {"gate_up_kernel": info.gate_up_kernel.decode(), "down_kernel": info.down_kernel.decode(),
                 "m_tile_rows": int(info.m_tile_rows), "workspace_bytes": int(info.workspace_bytes)}
+
+
+# the operators around the layer (include/moe_ops.h)
+from .ops import (  # noqa: E402,F401
+    BlockColumns, BlockRows, BlockWeights, Groups, block_product, block_product_grad, block_weight_grad, combine,
+    combine_backward, gather, gather_backward, pack_block_weights, quantize_block, quantize_block_both,
+    quantize_block_columns, quantize_block_weights, sort_tokens)

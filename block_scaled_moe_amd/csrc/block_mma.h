@@ -1,0 +1,60 @@
+// block_mma.h - pieces shared by the products of E4M3 codes with a scale per block of 128
+// (block_gemm.hip, block_wgrad.hip).
+//
+// One v_mfma_f32_16x16x128 takes a whole block of 128 of the reduction: D[i][j] = sum over k of
+// A[i][k] B[j][k], lane l holding 32 codes of row l % 16 of A and of B and accumulator v =
+// D[4 (l / 16) + v][l % 16]. A lane's codes are two pieces of 16: 16 g .. 16 g + 15 and
+// 64 + 16 g .. 64 + 16 g + 15 of the block for g = l / 16 (any order serves, the same for A and
+// B), the two quarters g of the block's 64-value halves in the tiled layout. The MFMA starts
+// from zero and its result is added to the fp32 accumulator times the block's two scales.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace moe {
+namespace block {
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ v8i operand(u32x4 lo, u32x4 hi) {
+    return (v8i){(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+}
+
+// sum over one block of 128 (E8M0 scale operands 127: 2^0)
+__device__ __forceinline__ f4 block_dot(v8i a, v8i b) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, (f4){0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 127, 0, 127);
+}
+
+// 16 bytes per lane from global memory straight into LDS at dst + 16 * lane (dst the same for
+// the wave)
+__device__ __forceinline__ void copy_to_lds(const uint8_t *src, uint8_t *dst) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
+                                     (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
+}
+
+// Workgroup barrier that leaves the wave's copies into LDS in flight (__syncthreads waits for
+// them all); LDS reads and writes complete first.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// at most N of the wave's vector loads, copies and stores outstanding
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {  // nearest, ties to even
+    return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)b) << 16;
+}
+
+// Row of a 32-row weight tile kept at position `pos` of its quarter in LDS (an involution).
+// Lane i of an operand read takes row 16 (i / 4) + 4 s + i % 4 of 64 rows (two tiles), so that
+// its accumulators of four reads s hold 16 consecutive outputs; the swap puts the four runs of
+// 64 bytes that 16 lanes read at four different 64-byte offsets of 256.
+__device__ __forceinline__ int swizzled_row(int pos, int tile) {
+    return pos ^ (((pos >> 4) & 1) << 2) ^ ((tile & 1) << 3);
+}
+
+}  // namespace block
+}  // namespace moe

@@ -91,6 +91,7 @@ struct PermuteArgs {
     int32_t *sorted_slot;   // [T*k]
     int32_t *slot_pos;      // [T*k]  sorted position of each slot or -1
     Ctrl *ctrl;
+    int32_t fill_tail;      // sorted_slot positions behind the last local slot become -1
     ActQuant quant;         // hidden-state quantisation carried by extra workgroups of the
                             // first launch (fmt kActNone: none)
 };

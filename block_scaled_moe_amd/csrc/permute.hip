@@ -247,6 +247,8 @@ __global__ void __launch_bounds__(64) scatter_kernel(PermuteArgs a, int32_t n_sl
     const int64_t s0 = (int64_t)blockIdx.x * chunk_slots;
     const int64_t s1 = min<int64_t>(s0 + chunk_slots, n_slots);
     for (int64_t g = s0; g < s1; g += 64) place_group(a, cursor, g + lane, g + lane < s1);
+    if (a.fill_tail)  // this chunk's share of the positions behind the last local slot
+        for (int64_t p = max<int64_t>(s0, a.offsets[n]) + lane; p < s1; p += 64) a.sorted_slot[p] = -1;
 }
 
 // Whole permutation in one workgroup for small batches (T*k <= 8192 slots, <= 1024
@@ -316,6 +318,8 @@ __global__ void __launch_bounds__(kSmallThreads) permute_small_kernel(PermuteArg
     __syncthreads();
     int32_t *cursor = cnt[wave];
     for (int32_t g = s0; g < s1; g += 64) place_group(a, cursor, g + lane, g + lane < s1);
+    if (a.fill_tail)
+        for (int32_t p = S + tid; p < n_slots; p += kSmallThreads) a.sorted_slot[p] = -1;
 }
 
 }  // namespace

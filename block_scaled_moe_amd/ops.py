@@ -1,0 +1,400 @@
+"""Operators around the routed-expert layer (include/moe_ops.h): tokens grouped by expert and
+back, and the expert product in FP8 with a scale for each block of 128, each with its gradient.
+
+The functions marshal arguments like the package's other calls: torch provides device memory
+and the current stream of the tensors' device, every step runs in the library's kernels, and an
+argument the library refuses raises MoeError. Wrong dtypes, shapes, devices or strides raise
+ValueError before the call; tensors are contiguous.
+
+    g = sort_tokens(topk_idx, E)                       # after route()
+    y = block_product(quantize_block(x), w, g, by_token=True)      # rows [T * k, N], sorted
+    out = combine(g, y, topk_w)
+
+Arrays of sorted rows have T * top_k rows; rows behind the last local one keep what they hold.
+"""
+from __future__ import annotations
+
+import ctypes
+import dataclasses
+
+import torch
+
+DTYPES = {torch.bfloat16: 1, torch.float32: 2}
+
+
+class MoeGroups(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("top_k", ctypes.c_int32), ("E", ctypes.c_int32), ("e_begin", ctypes.c_int32),
+                ("e_end", ctypes.c_int32), ("offsets", ctypes.c_void_p), ("sorted_slot", ctypes.c_void_p),
+                ("slot_pos", ctypes.c_void_p), ("plan", ctypes.c_void_p), ("plan_bytes", ctypes.c_size_t)]
+
+
+class MoeBlockWeights(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p)]
+
+
+class MoeBlockQuantizeArgs(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("C", ctypes.c_int32), ("by_token", ctypes.c_int32),
+                ("g", ctypes.POINTER(MoeGroups)), ("x", ctypes.c_void_p), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("col_codes", ctypes.c_void_p), ("col_scales", ctypes.c_void_p)]
+
+
+class MoeBlockGemmArgs(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("by_token", ctypes.c_int32), ("transposed", ctypes.c_int32),
+                ("g", ctypes.POINTER(MoeGroups)), ("x_codes", ctypes.c_void_p), ("x_scales", ctypes.c_void_p),
+                ("w", MoeBlockWeights), ("out", ctypes.c_void_p)]
+
+
+class MoeBlockWgradArgs(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("g", ctypes.POINTER(MoeGroups)), ("g_codes", ctypes.c_void_p), ("g_scales", ctypes.c_void_p),
+                ("x_codes", ctypes.c_void_p), ("x_scales", ctypes.c_void_p), ("dw", ctypes.c_void_p)]
+
+
+_G, _P, _I = ctypes.POINTER(MoeGroups), ctypes.c_void_p, ctypes.c_int32
+
+# every symbol include/moe_ops.h declares, with its ctypes signature
+SIGNATURES = {
+    "moe_ops_abi_version": ([], _I),
+    "moe_groups_plan_bytes": ([_G], ctypes.c_size_t),
+    "moe_sort": ([_G, _P, _P], _I),
+    "moe_gather": ([_G, _I, _I, _P, _P, _P], _I),
+    "moe_gather_backward": ([_G, _I, _I, _P, _P, _P], _I),
+    "moe_combine": ([_G, _I, _I, _I, _P, _P, _P, _P], _I),
+    "moe_combine_backward": ([_G, _I, _I, _I, _P, _P, _P, _P, _P, _P], _I),
+    "moe_block_column_blocks": ([_I, _I], ctypes.c_int64),
+    "moe_block_quantize": ([ctypes.POINTER(MoeBlockQuantizeArgs), _P], _I),
+    "moe_block_quantize_weights": ([_P, _I, _I, _I, _P, _P, _P], _I),
+    "moe_block_pack_weights": ([_P, _I, _I, _I, _P, _P], _I),
+    "moe_block_gemm": ([ctypes.POINTER(MoeBlockGemmArgs), _P], _I),
+    "moe_block_wgrad": ([ctypes.POINTER(MoeBlockWgradArgs), _P], _I),
+}
+
+
+def _call(name: str, device: torch.device, *args):
+    """The library's entry point `name` on the current stream of `device`, made current for the call."""
+    from . import _check, lib
+    fn = getattr(lib(), name)
+    if device.type != "cuda" or device.index == torch.cuda.current_device():
+        stream = torch.cuda.current_stream(device).cuda_stream if device.type == "cuda" else None
+        _check(fn(*args, stream), name)
+        return
+    with torch.cuda.device(device):
+        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream), name)
+
+
+def _ask(what: str, t: torch.Tensor, shape: tuple, dtype, device: torch.device):
+    """t has this shape, dtype (one or a tuple of them) and device, and is contiguous."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype not in (dtype if isinstance(dtype, (tuple, dict)) else (dtype,)):
+        raise ValueError(f"{what}: dtype {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: not contiguous")
+    return t
+
+
+def _out(what: str, out: torch.Tensor | None, shape: tuple, dtype, device: torch.device):
+    return torch.empty(shape, dtype=dtype, device=device) if out is None else _ask(what, out, shape, dtype, device)
+
+
+# ------------------------------------------------------------------ tokens by expert
+
+@dataclasses.dataclass
+class Groups:
+    """The token-slots of a batch sorted by expert (moe_groups; filled by sort_tokens)."""
+    T: int
+    top_k: int
+    E: int
+    e_begin: int
+    e_end: int
+    offsets: torch.Tensor      # int32 [n + 1] first sorted row of each local expert; [n] = local slots
+    sorted_slot: torch.Tensor  # int32 [T * top_k] slot of each sorted row, -1 behind the local ones
+    slot_pos: torch.Tensor     # int32 [T, top_k] sorted row of each slot, -1 if not local
+    plan: torch.Tensor         # work lists of the grouped products
+    struct: MoeGroups
+
+    @property
+    def rows(self) -> int:
+        return self.T * self.top_k
+
+    @property
+    def n(self) -> int:
+        return self.e_end - self.e_begin
+
+    @property
+    def device(self) -> torch.device:
+        return self.offsets.device
+
+    @staticmethod
+    def empty(T: int, top_k: int, E: int, e_begin: int = 0, e_end: int | None = None, device="cuda") -> "Groups":
+        from . import MoeError, lib
+        e_end = E if e_end is None else e_end
+        st = MoeGroups(T, top_k, E, e_begin, e_end)
+        n_plan = int(lib().moe_groups_plan_bytes(ctypes.byref(st)))
+        if n_plan == 0:
+            raise MoeError("moe_groups_plan_bytes", -1)
+        # one allocation, each array at a multiple of 256 bytes
+        up = lambda b: (b + 255) // 256 * 256
+        n = e_end - e_begin
+        sizes = [up(4 * (n + 1)), up(4 * T * top_k), up(4 * T * top_k), n_plan]
+        buf = torch.empty(sum(sizes), dtype=torch.uint8, device=device)
+        at = [0, sizes[0], sizes[0] + sizes[1], sizes[0] + 2 * sizes[1]]
+        i32 = buf.view(torch.int32)
+        part = lambda i, count: i32.narrow(0, at[i] // 4, count)
+        base = buf.data_ptr()
+        st.offsets, st.sorted_slot, st.slot_pos, st.plan = (base + a for a in at)
+        st.plan_bytes = n_plan
+        return Groups(T, top_k, E, e_begin, e_end, part(0, n + 1), part(1, T * top_k),
+                      part(2, T * top_k).view(T, top_k), buf.narrow(0, at[3], n_plan), st)
+
+
+def sort_tokens(topk_idx: torch.Tensor, E: int, e_begin: int = 0, e_end: int | None = None,
+                out: Groups | None = None) -> Groups:
+    """topk_idx int32 [T, k] -> Groups (moe_sort). Experts outside [e_begin, e_end), such as -1
+    for padding, have no row. `out`: groups of the same sizes to fill again."""
+    if topk_idx.dim() != 2:
+        raise ValueError(f"topk_idx: shape {tuple(topk_idx.shape)}, expected [T, k]")
+    T, k = topk_idx.shape
+    _ask("topk_idx", topk_idx, (T, k), torch.int32, topk_idx.device)
+    e_end = E if e_end is None else e_end
+    if out is None:
+        out = Groups.empty(T, k, E, e_begin, e_end, device=topk_idx.device)
+    elif (out.T, out.top_k, out.E, out.e_begin, out.e_end, out.device) != (T, k, E, e_begin, e_end, topk_idx.device):
+        raise ValueError("out: groups of other sizes or on another device")
+    _call("moe_sort", out.device, ctypes.byref(out.struct), topk_idx.data_ptr())
+    return out
+
+
+def _row_width(what: str, t: torch.Tensor) -> int:
+    if t.dim() != 2:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected [rows, D]")
+    return t.shape[1]
+
+
+def gather(g: Groups, x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Token rows x [T, D] (bf16 or fp32) -> sorted rows [T * k, D] (moe_gather)."""
+    D = _row_width("x", x)
+    _ask("x", x, (g.T, D), DTYPES, g.device)
+    out = _out("out", out, (g.rows, D), x.dtype, g.device)
+    _call("moe_gather", g.device, ctypes.byref(g.struct), DTYPES[x.dtype], D, x.data_ptr(), out.data_ptr())
+    return out
+
+
+def gather_backward(g: Groups, d_rows: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of gather: d_rows [T * k, D] -> dx [T, D], the sum over each token's local rows."""
+    D = _row_width("d_rows", d_rows)
+    _ask("d_rows", d_rows, (g.rows, D), DTYPES, g.device)
+    out = _out("out", out, (g.T, D), d_rows.dtype, g.device)
+    _call("moe_gather_backward", g.device, ctypes.byref(g.struct), DTYPES[d_rows.dtype], D, d_rows.data_ptr(),
+          out.data_ptr())
+    return out
+
+
+def combine(g: Groups, y: torch.Tensor, w: torch.Tensor, out: torch.Tensor | None = None,
+            out_dtype: torch.dtype = torch.float32) -> torch.Tensor:
+    """Sorted rows y [T * k, D] and weights w fp32 [T, k] -> out [T, D], each token's weighted sum over its
+    local slots (moe_combine). `out`'s dtype, or out_dtype, is bf16 or fp32."""
+    D = _row_width("y", y)
+    _ask("y", y, (g.rows, D), DTYPES, g.device)
+    _ask("w", w, (g.T, g.top_k), torch.float32, g.device)
+    if out is None and out_dtype not in DTYPES:
+        raise ValueError(f"out_dtype: {out_dtype}")
+    out = _out("out", out, (g.T, D), out_dtype if out is None else DTYPES, g.device)
+    _call("moe_combine", g.device, ctypes.byref(g.struct), DTYPES[y.dtype], DTYPES[out.dtype], D, y.data_ptr(),
+          w.data_ptr(), out.data_ptr())
+    return out
+
+
+def combine_backward(g: Groups, d_out: torch.Tensor, y: torch.Tensor, w: torch.Tensor, dy: torch.Tensor | None = None,
+                     dw: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Gradient of combine: d_out [T, D] -> (dy [T * k, D] in y's dtype, dw fp32 [T, k])."""
+    D = _row_width("y", y)
+    _ask("y", y, (g.rows, D), DTYPES, g.device)
+    _ask("w", w, (g.T, g.top_k), torch.float32, g.device)
+    _ask("d_out", d_out, (g.T, D), DTYPES, g.device)
+    dy = _out("dy", dy, (g.rows, D), y.dtype, g.device)
+    dw = _out("dw", dw, (g.T, g.top_k), torch.float32, g.device)
+    _call("moe_combine_backward", g.device, ctypes.byref(g.struct), DTYPES[y.dtype], DTYPES[d_out.dtype], D,
+          d_out.data_ptr(), y.data_ptr(), w.data_ptr(), dy.data_ptr(), dw.data_ptr())
+    return dy, dw
+
+
+# ------------------------------------------------------------------ FP8 with a scale per block of 128
+
+@dataclasses.dataclass
+class BlockRows:
+    """Rows in E4M3 with an fp32 scale per 1 x 128 block: codes uint8 [rows, C], scales [rows, C / 128]."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+@dataclasses.dataclass
+class BlockColumns:
+    """Sorted rows in E4M3 with an fp32 scale per column of each run of 128 rows of an expert (the column
+    form of include/moe_ops.h): codes uint8 [blocks, C / 32, 2, 4, 32, 16], scales [blocks, C]."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+@dataclasses.dataclass
+class BlockWeights:
+    """Expert weights [E, N, K] in E4M3 with an fp32 scale per 128 x 128 block: codes uint8
+    [E, N/32, K/64, 4, 32, 16] (the tiled layout of moe.h's FP8 weights), scales [E, N/128, K/128]."""
+    E: int
+    N: int
+    K: int
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    @staticmethod
+    def empty(E: int, N: int, K: int, device="cuda") -> "BlockWeights":
+        if N % 128 or K % 128:
+            raise ValueError(f"block weights need N and K in multiples of 128 (got N={N}, K={K})")
+        return BlockWeights(E, N, K, torch.empty((E, N // 32, K // 64, 4, 32, 16), dtype=torch.uint8, device=device),
+                            torch.empty((E, N // 128, K // 128), dtype=torch.float32, device=device))
+
+    def experts(self, e0: int, e1: int) -> "BlockWeights":
+        """View of experts e0..e1-1."""
+        return BlockWeights(e1 - e0, self.N, self.K, self.codes[e0:e1], self.scales[e0:e1])
+
+    def struct(self, device: torch.device) -> MoeBlockWeights:
+        E, N, K = self.E, self.N, self.K
+        _ask("weight codes", self.codes, (E, N // 32, K // 64, 4, 32, 16), torch.uint8, device)
+        _ask("weight scales", self.scales, (E, N // 128, K // 128), torch.float32, device)
+        return MoeBlockWeights(E, N, K, self.codes.data_ptr(), self.scales.data_ptr())
+
+
+def quantize_block_weights(w: torch.Tensor, out: BlockWeights | None = None) -> BlockWeights:
+    """bf16 weights [E, N, K] -> BlockWeights (moe_block_quantize_weights)."""
+    if w.dim() != 3:
+        raise ValueError(f"w: shape {tuple(w.shape)}, expected [E, N, K]")
+    E, N, K = w.shape
+    _ask("w", w, (E, N, K), torch.bfloat16, w.device)
+    out = BlockWeights.empty(E, N, K, device=w.device) if out is None else out
+    if (out.E, out.N, out.K) != (E, N, K):
+        raise ValueError("out: weights of another shape")
+    st = out.struct(w.device)
+    _call("moe_block_quantize_weights", w.device, w.data_ptr(), E, N, K, st.codes, st.scales)
+    return out
+
+
+def pack_block_weights(codes: torch.Tensor, scales: torch.Tensor, out: BlockWeights | None = None) -> BlockWeights:
+    """A checkpoint's E4M3 codes (uint8 or float8_e4m3fn [E, N, K], row-major) and fp32 scales
+    [E, N/128, K/128] -> BlockWeights (moe_block_pack_weights; the scales are kept, not copied)."""
+    if codes.dim() != 3:
+        raise ValueError(f"codes: shape {tuple(codes.shape)}, expected [E, N, K]")
+    E, N, K = codes.shape
+    _ask("codes", codes, (E, N, K), (torch.uint8, torch.float8_e4m3fn), codes.device)
+    _ask("scales", scales, (E, N // 128, K // 128), torch.float32, codes.device)
+    out = BlockWeights.empty(E, N, K, device=codes.device) if out is None else out
+    if (out.E, out.N, out.K) != (E, N, K):
+        raise ValueError("out: weights of another shape")
+    out.scales = scales
+    st = out.struct(codes.device)
+    _call("moe_block_pack_weights", codes.device, codes.data_ptr(), E, N, K, st.codes)
+    return out
+
+
+def _blocks_of_128(what: str, C: int):
+    if C % 128 or C < 128:
+        raise ValueError(f"{what}: {C} columns are not a multiple of 128")
+
+
+def _quantize(x: torch.Tensor, g: Groups | None, by_token: bool, rows: bool, columns: bool):
+    C = _row_width("x", x)
+    _blocks_of_128("x", C)
+    dev = x.device if g is None else g.device
+    R = x.shape[0] if g is None else g.T if by_token else g.rows
+    _ask("x", x, (R, C), torch.bfloat16, dev)
+    a = MoeBlockQuantizeArgs(rows=R, C=C, by_token=int(by_token), x=x.data_ptr())
+    if g is not None:
+        a.g = ctypes.pointer(g.struct)
+    r = c = None
+    if rows:
+        r = BlockRows(torch.empty((R, C), dtype=torch.uint8, device=dev),
+                      torch.empty((R, C // 128), dtype=torch.float32, device=dev))
+        a.codes, a.scales = r.codes.data_ptr(), r.scales.data_ptr()
+    if columns:
+        n = (R if g is None else g.rows) // 128 + (1 if g is None else g.n)  # moe_block_column_blocks
+        c = BlockColumns(torch.empty((n, C // 32, 2, 4, 32, 16), dtype=torch.uint8, device=dev),
+                         torch.empty((n, C), dtype=torch.float32, device=dev))
+        a.col_codes, a.col_scales = c.codes.data_ptr(), c.scales.data_ptr()
+    if R > 0:
+        _call("moe_block_quantize", dev, ctypes.byref(a))
+    return r, c
+
+
+def quantize_block(x: torch.Tensor, g: Groups | None = None) -> BlockRows:
+    """bf16 x [rows, C] by rows; with g, x holds sorted rows, of which the local ones are quantised."""
+    return _quantize(x, g, False, True, False)[0]
+
+
+def quantize_block_columns(x: torch.Tensor, g: Groups | None = None, by_token: bool = False) -> BlockColumns:
+    """bf16 sorted rows x [T * k, C] by columns; by_token: x is [T, C] and a sorted row is its token's row.
+    Without g, all rows of x are one group."""
+    return _quantize(x, g, by_token, False, True)[1]
+
+
+def quantize_block_both(x: torch.Tensor, g: Groups | None = None) -> tuple[BlockRows, BlockColumns]:
+    """bf16 sorted rows x by rows and by columns, from one read."""
+    return _quantize(x, g, False, True, True)
+
+
+def _product(x: BlockRows, w: BlockWeights, g: Groups | None, by_token: bool, transposed: bool, out):
+    dev = x.codes.device if g is None else g.device
+    R, C = (w.N, w.K) if transposed else (w.K, w.N)
+    n_x = x.codes.shape[0] if g is None else g.T if by_token else g.rows
+    _ask("x codes", x.codes, (n_x, R), torch.uint8, dev)
+    _ask("x scales", x.scales, (n_x, R // 128), torch.float32, dev)
+    if w.E != (1 if g is None else g.n):
+        raise ValueError(f"w: {w.E} experts, expected {1 if g is None else g.n}")
+    if g is None and by_token:
+        raise ValueError("by_token needs groups")
+    out = _out("out", out, (n_x if g is None else g.rows, C), torch.bfloat16, dev)
+    a = MoeBlockGemmArgs(rows=n_x, by_token=int(by_token), transposed=int(transposed), x_codes=x.codes.data_ptr(),
+                         x_scales=x.scales.data_ptr(), w=w.struct(dev), out=out.data_ptr())
+    if g is not None:
+        a.g = ctypes.pointer(g.struct)
+    if n_x > 0:
+        _call("moe_block_gemm", dev, ctypes.byref(a))
+    return out
+
+
+def block_product(x: BlockRows, w: BlockWeights, g: Groups | None = None, by_token: bool = False,
+                  out: torch.Tensor | None = None) -> torch.Tensor:
+    """Each sorted row times its expert's weight, x [rows, K] -> bf16 [T * k, N] (moe_block_gemm). by_token: x
+    has one row per token. Without groups, every row of x times the one expert of w."""
+    return _product(x, w, g, by_token, False, out)
+
+
+def block_product_grad(dy: BlockRows, w: BlockWeights, g: Groups | None = None,
+                       out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of block_product's (sorted) input rows: dy [T * k, N] -> bf16 [T * k, K]."""
+    return _product(dy, w, g, False, True, out)
+
+
+def block_weight_grad(dy: BlockColumns, x: BlockColumns, g: Groups | None = None, rows: int | None = None,
+                      out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of every expert's weight, bf16 [n, N, K], from the column forms of the output gradient and of
+    the input (moe_block_wgrad). Without groups, `rows` says how many rows they hold."""
+    if g is None and rows is None:
+        raise ValueError("rows: needed without groups")
+    dev = dy.codes.device if g is None else g.device
+    R = rows if g is None else g.rows
+    N, K, n = dy.scales.shape[-1], x.scales.shape[-1], 1 if g is None else g.n
+    _blocks_of_128("dy", N)
+    _blocks_of_128("x", K)
+    blocks = R // 128 + n
+    for what, q, C in (("dy", dy, N), ("x", x, K)):
+        _ask(what + " codes", q.codes, (blocks, C // 32, 2, 4, 32, 16), torch.uint8, dev)
+        _ask(what + " scales", q.scales, (blocks, C), torch.float32, dev)
+    out = _out("out", out, (n, N, K), torch.bfloat16, dev)
+    a = MoeBlockWgradArgs(rows=R, N=N, K=K, g_codes=dy.codes.data_ptr(), g_scales=dy.scales.data_ptr(),
+                          x_codes=x.codes.data_ptr(), x_scales=x.scales.data_ptr(), dw=out.data_ptr())
+    if g is not None:
+        a.g = ctypes.pointer(g.struct)
+    _call("moe_block_wgrad", dev, ctypes.byref(a))
+    return out

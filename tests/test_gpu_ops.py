@@ -1,0 +1,475 @@
+"""The operators of include/moe_ops.h on the GPU against plain forms in 64 bits (ops_ref.py):
+tokens grouped by expert and back, the FP8 quantisers with a scale per block of 128, the grouped
+product and its gradients, at the sizes and routings where they can go wrong; a run of them
+together; streams and graph replays."""
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_moe_amd as moe
+import ops_ref as ref
+from gpu_util import host
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+INT_MIN = -2 ** 31
+
+
+def dev(a, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    return t if dtype is None else t.to(dtype)
+
+
+def values(rng, shape, dtype="fp32"):
+    x = rng.standard_normal(shape).astype(np.float32)
+    return ref.bf16(x) if dtype == "bf16" else x
+
+
+def num(t):
+    return host(t.float() if t.dtype == torch.bfloat16 else t)
+
+
+# ---------------------------------------------------------------- sort
+
+def routing(kind, T, k, E, rng):
+    if kind == "distinct":
+        return np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32) if T else np.zeros((0, k), np.int32)
+    if kind == "one":      # every slot on one expert, the same one k times in a token
+        return np.full((T, k), E // 2, np.int32)
+    if kind == "none":
+        return np.full((T, k), -1, np.int32)
+    if kind == "wild":     # padding and values that are no expert, up to the ends of the type
+        idx = rng.integers(0, E, (T, k)).astype(np.int32)
+        bad = rng.choice(np.array([-1, -7, E, E + 5, INT_MIN, 2 ** 31 - 1], np.int64), (T, k)).astype(np.int32)
+        return np.where(rng.random((T, k)) < 0.4, bad, idx).astype(np.int32)
+    return rng.integers(0, E, (T, k)).astype(np.int32)  # "dup": repeats allowed
+
+
+SORTS = [
+    ("distinct", 1, 8, 384, 0, 384), ("distinct", 64, 8, 384, 96, 192), ("wild", 64, 8, 384, 96, 192),
+    ("one", 50, 8, 16, 0, 16), ("none", 9, 4, 32, 0, 32), ("dup", 0, 8, 16, 0, 16), ("dup", 33, 3, 5, 4, 5),
+    ("wild", 2000, 8, 60, 7, 50), ("dup", 1500, 7, 4096, 0, 4096), ("wild", 700, 1, 2000, 100, 2000),
+    ("dup", 5000, 2, 1, 0, 1), ("dup", 0, 1, 2000, 0, 2000), ("one", 3000, 4, 3, 0, 3), ("dup", 1, 1, 1, 0, 1),
+]
+
+
+@pytest.mark.parametrize("kind,T,k,E,e0,e1", SORTS)
+def test_sort(kind, T, k, E, e0, e1):
+    rng = np.random.default_rng(T * 7 + E)
+    idx = routing(kind, T, k, E, rng)
+    g = moe.sort_tokens(dev(idx), E, e0, e1)
+    off, ss, sp = ref.sort(idx, e0, e1)
+    assert np.array_equal(host(g.offsets), off)
+    assert np.array_equal(host(g.slot_pos), sp)
+    assert np.array_equal(host(g.sorted_slot), ss)
+    again = moe.sort_tokens(dev(np.roll(idx, 1, 0)), E, e0, e1, out=g)  # the same buffers for another batch
+    off, ss, sp = ref.sort(np.roll(idx, 1, 0), e0, e1)
+    assert again is g and np.array_equal(host(g.sorted_slot), ss) and np.array_equal(host(g.slot_pos), sp)
+
+
+# ---------------------------------------------------------------- rows by expert and back
+
+ROWS = [
+    ("distinct", 1, 8, 64, 0, 64, 4096), ("wild", 37, 8, 16, 3, 11, 257), ("dup", 130, 3, 7, 0, 7, 1001),
+    ("wild", 65, 5, 9, 0, 9, 8), ("none", 4, 2, 4, 0, 4, 72), ("one", 20, 8, 4, 0, 4, 640), ("dup", 9, 1, 3, 1, 3, 1),
+    ("wild", 1300, 4, 12, 0, 6, 136), ("dup", 3, 6, 8, 0, 8, 2052), ("dup", 7, 2, 4, 0, 4, 516), ("dup", 300, 8, 8, 0, 4, 20),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("kind,T,k,E,e0,e1,D", ROWS)
+def test_gather_and_its_gradient(kind, T, k, E, e0, e1, D, dtype):
+    rng = np.random.default_rng(D + T)
+    idx = routing(kind, T, k, E, rng)
+    g = moe.sort_tokens(dev(idx), E, e0, e1)
+    off, ss, sp = ref.sort(idx, e0, e1)
+    S = off[-1]
+    x = values(rng, (T, D), dtype)
+    buf = torch.full((T * k + 3, D), 7.0, dtype=DT[dtype], device="cuda")
+    rows = moe.gather(g, dev(x, DT[dtype]), out=buf[:T * k])
+    assert np.array_equal(num(rows)[:S], x[ss[:S] // k])
+    assert (num(buf)[S:] == 7.0).all()          # rows behind the last local one keep what they hold
+    d = values(rng, (T * k, D), dtype)
+    d[S:] = np.nan                              # and are not read
+    dx = num(moe.gather_backward(g, dev(d, DT[dtype]))).astype(np.float64)
+    terms = np.where(sp[:, :, None] >= 0, d[np.maximum(sp, 0)], 0).astype(np.float64)
+    want, size = terms.sum(1), np.abs(terms).sum(1)
+    bound = k * ref.U24 * size                  # k fp32 additions
+    if dtype == "bf16":
+        bound = bound + ref.U_BF16 * (np.abs(want) + bound)
+    assert (np.abs(dx - want) <= bound).all()
+
+
+@pytest.mark.parametrize("out_dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("kind,T,k,E,e0,e1,D", ROWS)
+def test_combine_and_its_gradient(kind, T, k, E, e0, e1, D, dtype, out_dtype):
+    rng = np.random.default_rng(D + T + 1)
+    idx = routing(kind, T, k, E, rng)
+    g = moe.sort_tokens(dev(idx), E, e0, e1)
+    off, ss, sp = ref.sort(idx, e0, e1)
+    S = off[-1]
+    y, w, d = values(rng, (T * k, D), dtype), values(rng, (T, k)), values(rng, (T, D), out_dtype)
+    y[S:] = np.nan
+    local = (sp >= 0)[:, :, None]
+    ys = np.where(local, y[np.maximum(sp, 0)], 0).astype(np.float64)
+    terms = ys * w[:, :, None].astype(np.float64)
+    want, size = terms.sum(1), np.abs(terms).sum(1)
+    out = num(moe.combine(g, dev(y, DT[dtype]), dev(w), out_dtype=DT[out_dtype]))
+    bound = k * ref.U24 * size                  # k fused multiply-adds
+    if out_dtype == "bf16":
+        bound = bound + ref.U_BF16 * (np.abs(want) + bound)
+    assert (np.abs(out - want) <= bound).all()
+
+    buf = torch.full((T * k + 2, D), 5.0, dtype=DT[dtype], device="cuda")
+    dy, dw = moe.combine_backward(g, dev(d, DT[out_dtype]), dev(y, DT[dtype]), dev(w), dy=buf[:T * k])
+    want_dy = (w.reshape(-1)[ss[:S]][:, None].astype(np.float64) * d[ss[:S] // k])
+    step = ref.U24 * np.abs(want_dy)            # one product
+    if dtype == "bf16":
+        step = step + ref.U_BF16 * (np.abs(want_dy) + step)
+    assert (np.abs(num(dy)[:S] - want_dy) <= step).all()
+    assert (num(buf)[S:] == 5.0).all()
+    prod = ys * d[:, None, :].astype(np.float64)
+    # each thread's chain of multiply-adds (at most 8 per 256 of the row's pieces of one element), then a tree of at most 10
+    depth = 8 * ((D + 255) // 256) + 10
+    assert (np.abs(num(dw) - prod.sum(2)) <= depth * ref.U24 * np.abs(prod).sum(2)).all()
+    assert (num(dw)[sp < 0] == 0).all()
+
+
+def test_non_finite_rows_stay_in_their_sums():
+    """A NaN or infinite row reaches its own token and no other; non-local slots contribute nothing."""
+    idx = np.array([[0, 1], [1, 5], [-1, -1], [0, 0]], np.int32)  # expert 5 is remote
+    g = moe.sort_tokens(dev(idx), 8, 0, 2)
+    y = np.ones((8, 64), np.float32)
+    y[4] = np.nan                                    # token 1's row at expert 1: slots sorted 0,6,7 | 1,2
+    y[5:] = np.inf
+    w = np.full((4, 2), 0.5, np.float32)
+    w[1, 1] = np.inf                                 # weight of the remote slot
+    out = num(moe.combine(g, dev(y), dev(w)))
+    assert np.isnan(out[1]).all() and (out[0] == 1).all() and (out[2] == 0).all() and (out[3] == 1).all()
+
+
+# ---------------------------------------------------------------- quantisers
+
+def hard_values(rng, shape):
+    """bf16 values whose blocks of 128 differ in size, with zeros, zero blocks, ends of the range, subnormals and ties."""
+    x = rng.standard_normal(shape).astype(np.float32)
+    x = x * np.exp2(rng.integers(-30, 30, size=shape[:-1] + (shape[-1] // 128,))).repeat(128, -1).astype(np.float32)
+    flat = x.reshape(-1, 128)
+    for i, f in enumerate((0.0, 2.0 ** -126, 2.0 ** -133, 2.0 ** 120, 2.0 ** -75, 2.0 ** 75)):
+        if i < len(flat):
+            flat[i] = 0.0 if f == 0 else rng.integers(-255, 256, 128) * np.float32(f)
+    if len(flat) > 8:
+        flat[7] = np.where(rng.random(128) < 0.5, 448.0, rng.integers(0, 64, 128) * 0.25)  # scale 1: exact ties
+        flat[8, :] = 0.0
+        flat[8, 5] = -3e38
+    return ref.bf16(x)
+
+
+@pytest.mark.parametrize("R,C", [(1, 128), (3, 384), (129, 256), (300, 4096), (17, 1152)])
+def test_quantise_rows(R, C):
+    x = hard_values(np.random.default_rng(R), (R, C))
+    q = moe.quantize_block(dev(x, torch.bfloat16))
+    c, s = ref.rows(x)
+    assert np.array_equal(host(q.scales).view(np.uint32), s.view(np.uint32))
+    assert np.array_equal(host(q.codes), c)
+
+
+@pytest.mark.parametrize("E,N,K", [(1, 128, 128), (3, 256, 384), (2, 640, 128)])
+def test_quantise_and_pack_weights(E, N, K):
+    w = hard_values(np.random.default_rng(N), (E, N, K))
+    q = moe.quantize_block_weights(dev(w, torch.bfloat16))
+    c, s = ref.weights(w)
+    assert np.array_equal(host(q.scales).view(np.uint32), s.view(np.uint32))
+    assert np.array_equal(host(q.codes), ref.tile(c))
+    p = moe.pack_block_weights(dev(c), dev(s))
+    assert torch.equal(p.codes, q.codes) and torch.equal(p.scales, q.scales)
+    v = p.experts(E - 1, E)
+    assert v.E == 1 and np.array_equal(host(v.codes)[0], ref.tile(c)[E - 1])
+
+
+def exact_counts(counts, k=1):
+    """Routing of k = 1 whose local expert e has counts[e] rows, tokens in a random order."""
+    idx = np.repeat(np.arange(len(counts)), counts).astype(np.int32)
+    return np.random.default_rng(3).permutation(idx)[:, None]
+
+
+COUNTS = [[1], [0, 3, 0], [128, 129, 0, 127], [300, 0, 1, 260], [5] * 70, [0, 0], [16, 17, 15, 240, 272]]
+
+
+@pytest.mark.parametrize("C", [128, 640])
+@pytest.mark.parametrize("counts", COUNTS, ids=str)
+def test_quantise_columns(counts, C):
+    rng = np.random.default_rng(sum(counts))
+    idx = exact_counts(counts)
+    T = len(idx)
+    g = moe.sort_tokens(dev(idx.reshape(T, 1)), len(counts))
+    off, ss, _ = ref.sort(idx, 0, len(counts))
+    x = hard_values(rng, (T, C)) if T else np.zeros((0, C), np.float32)
+    sorted_x = x[ss]
+    want = ref.columns(sorted_x, off)
+    rows, cols = moe.quantize_block_both(dev(sorted_x, torch.bfloat16), g)
+    only = moe.quantize_block_columns(dev(sorted_x, torch.bfloat16), g)
+    tok = moe.quantize_block_columns(dev(x, torch.bfloat16), g, by_token=True)
+    for q in (cols, only, tok):
+        qc, qs = host(q.codes), host(q.scales)
+        for b, (c, s) in want.items():
+            assert np.array_equal(qs[b].view(np.uint32), s.view(np.uint32)), b
+            assert np.array_equal(qc[b], c), b
+    if T:
+        c, s = ref.rows(sorted_x)
+        assert np.array_equal(host(rows.codes), c) and np.array_equal(host(rows.scales), s)
+
+
+def test_quantise_leaves_rows_behind_the_last_one():
+    """Rows of remote experts are not quantised: their codes and scales keep what they hold."""
+    idx = np.array([[0, 9], [9, 1], [9, 9]], np.int32)
+    g = moe.sort_tokens(dev(idx), 16, 0, 2)
+    x = torch.full((6, 256), float("nan"), dtype=torch.bfloat16, device="cuda")
+    x[:2] = 1.5
+    codes = torch.full((6, 256), 9, dtype=torch.uint8, device="cuda")
+    scales = torch.full((6, 2), 9.0, device="cuda")
+    import ctypes
+    from block_scaled_moe_amd import ops
+    a = ops.MoeBlockQuantizeArgs(rows=6, C=256, g=ctypes.pointer(g.struct), x=x.data_ptr(), codes=codes.data_ptr(),
+                                 scales=scales.data_ptr())
+    ops._call("moe_block_quantize", x.device, ctypes.byref(a))
+    assert (host(codes)[:2] == 0x7E).all() and (host(codes)[2:] == 9).all() and (host(scales)[2:] == 9).all()
+
+
+# ---------------------------------------------------------------- products
+
+def check(got, want, bound, what):
+    bad = np.abs(got.astype(np.float64) - want) > bound
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} off, worst {np.abs(got - want)[bad].max()}"
+
+
+GEMMS = [(c, n, k) for c in COUNTS for n, k in ((128, 128), (384, 640))] + [
+    ([257, 40, 600], 512, 256), ([1, 2, 0, 9], 256, 4352), ([70, 33], 128, 8448), ([513], 768, 384), ([20], 5120, 512)]
+
+
+def setup_product(counts, N, K, seed, spread=True):
+    rng = np.random.default_rng(seed)
+    idx = exact_counts(counts)
+    T = len(idx)
+    g = moe.sort_tokens(dev(idx.reshape(T, 1)), len(counts))
+    off, ss, _ = ref.sort(idx, 0, len(counts))
+    w = ref.bf16(rng.standard_normal((len(counts), N, K)).astype(np.float32) *
+                 np.exp2(rng.integers(-6, 6, (len(counts), N // 128, K // 128))).repeat(128, 1).repeat(128, 2))
+    wq = moe.quantize_block_weights(dev(w, torch.bfloat16))
+    expert = np.repeat(np.arange(len(counts)), counts)
+    return rng, g, off, ss, wq, ref.weights(w), expert
+
+
+@pytest.mark.parametrize("counts,N,K", GEMMS, ids=str)
+def test_product(counts, N, K):
+    rng, g, off, ss, wq, (wc, ws), expert = setup_product(counts, N, K, sum(counts) + N)
+    T = g.T
+    x = ref.bf16(rng.standard_normal((T, K)).astype(np.float32) * np.exp2(rng.integers(-4, 5, (T, 1))))
+    xc, xs = ref.rows(x) if T else (np.zeros((0, K), np.uint8), np.zeros((0, K // 128), np.float32))
+    y, bound = ref.product(xc[ss], xs[ss], wc, ws, expert)
+    q = moe.quantize_block(dev(x, torch.bfloat16))
+    check(num(moe.block_product(q, wq, g, by_token=True)), y, bound, "by token")
+    qs = moe.quantize_block(dev(x[ss], torch.bfloat16), g)
+    buf = torch.full((T + 1, N), 3.0, dtype=torch.bfloat16, device="cuda")
+    check(num(moe.block_product(qs, wq, g, out=buf[:T])), y, bound, "sorted")
+    assert (num(buf)[T:] == 3.0).all()
+
+
+@pytest.mark.parametrize("counts,N,K", GEMMS, ids=str)
+def test_product_gradients(counts, N, K):
+    rng, g, off, ss, wq, (wc, ws), expert = setup_product(counts, N, K, sum(counts) + K)
+    T = g.T
+    dy = ref.bf16(rng.standard_normal((T, N)).astype(np.float32) * np.exp2(rng.integers(-4, 5, (T, 1))))
+    x = ref.bf16(rng.standard_normal((T, K)).astype(np.float32))
+    gq, gc = moe.quantize_block_both(dev(dy, torch.bfloat16), g)
+    xq = moe.quantize_block_columns(dev(x, torch.bfloat16), g)
+    if T:
+        c, s = ref.rows(dy)
+        want, bound = ref.product(c, s, wc, ws, expert, transposed=True)
+        buf = torch.full((T + 1, K), 3.0, dtype=torch.bfloat16, device="cuda")
+        check(num(moe.block_product_grad(gq, wq, g, out=buf[:T])), want, bound, "dx")
+        assert (num(buf)[T:] == 3.0).all()
+    dw = num(moe.block_weight_grad(gc, xq, g))
+    cg, cx = ref.columns(dy, off), ref.columns(x, off)
+    for e in range(len(counts) if T else 0):
+        check(dw[e], *ref.weight_grad(cg, cx, off, e), f"dw[{e}]")
+    assert (dw[np.array(counts) == 0] == 0).all()
+
+
+@pytest.mark.parametrize("M", [1, 16, 17, 300, 513])
+def test_one_group(M):
+    """Without groups: a dense projection and its gradients."""
+    rng = np.random.default_rng(M)
+    N, K = 384, 512
+    x, dy = values(rng, (M, K), "bf16"), values(rng, (M, N), "bf16")
+    w = values(rng, (1, N, K), "bf16")
+    wq = moe.quantize_block_weights(dev(w, torch.bfloat16))
+    wc, ws = ref.weights(w)
+    expert, off = np.zeros(M, int), np.array([0, M])
+    check(num(moe.block_product(moe.quantize_block(dev(x, torch.bfloat16)), wq)), *ref.product(*ref.rows(x), wc, ws, expert), "y")
+    gq, gc = moe.quantize_block_both(dev(dy, torch.bfloat16))
+    check(num(moe.block_product_grad(gq, wq)), *ref.product(*ref.rows(dy), wc, ws, expert, transposed=True), "dx")
+    xq = moe.quantize_block_columns(dev(x, torch.bfloat16))
+    check(num(moe.block_weight_grad(gc, xq, rows=M))[0], *ref.weight_grad(ref.columns(dy, off), ref.columns(x, off), off, 0), "dw")
+
+
+@pytest.mark.parametrize("k1,k2,k3", [(0, 1, 2), (0, 64, 1), (0, 127, 64), (5, 6, 100), (17, 90, 18)])
+def test_small_products_beside_large_ones(k1, k2, k3):
+    """A product counts in full beside one 2^13 times its size in the same block: 2^16 - 2^16 + 2^j keeps 2^j for
+    j >= 3 at any places of the block (the tolerances of the products rest on it). Two unused values fix the scales at 1."""
+    js = list(range(3, 17))
+    x, w = np.zeros((len(js), 128), np.float32), np.zeros((1, 128, 128), np.float32)
+    free = [k for k in range(128) if k not in (k1, k2, k3)][:2]
+    x[:, free[0]], w[0, :, free[1]] = 448.0, 448.0
+    x[:, k1], x[:, k2], w[0, :, k1], w[0, :, k2], w[0, :, k3] = 256.0, -256.0, 256.0, 256.0, 2.0 ** 8
+    x[:, k3] = np.exp2(np.array(js) - 8)
+    y = num(moe.block_product(moe.quantize_block(dev(x, torch.bfloat16)), moe.quantize_block_weights(dev(w, torch.bfloat16))))
+    assert (y == np.exp2(np.array(js))[:, None]).all()
+
+
+def test_gradients_against_differences():
+    """The product's gradients against differences of the product itself. Where the values are E4M3 values
+    with a scale that a change of one element does not move (each block holds a 448), quantising is exact, the
+    product is bilinear, and a difference gives the derivative up to the roundings of y."""
+    rng = np.random.default_rng(5)
+    N, K, M = 128, 128, 6
+    vals = ref.e4m3_value(np.arange(0x30, 0x60, dtype=np.uint8)).astype(np.float32)  # 1/4 .. 15
+    x, w = rng.choice(vals, (M, K)), rng.choice(vals, (1, N, K))
+    x[:, 0], w[0, 0, 0] = 448.0, 448.0
+    dy = np.zeros((M, N), np.float32)
+    dy[:, 3] = 448.0                       # the loss is 448 * sum of column 3 of y, scale 1
+    wq = moe.quantize_block_weights(dev(w, torch.bfloat16))
+    f = lambda xx, ww: num(moe.block_product(moe.quantize_block(dev(xx, torch.bfloat16)),
+                                             moe.quantize_block_weights(dev(ww, torch.bfloat16)))).astype(np.float64)
+    gq, gc = moe.quantize_block_both(dev(dy, torch.bfloat16))
+    dx = num(moe.block_product_grad(gq, wq))
+    dw = num(moe.block_weight_grad(gc, moe.quantize_block_columns(dev(x, torch.bfloat16)), rows=M))[0]
+    base = f(x, w)
+    for m, k in ((0, 5), (3, 77), (5, 127)):
+        x2 = x.copy()
+        x2[m, k] = 240.0 if x[m, k] < 16 else 1.0   # a value E4M3 holds
+        diff = 448.0 * (f(x2, w)[m, 3] - base[m, 3]) / (x2[m, k] - x[m, k])
+        slack = 448.0 * ref.U_BF16 * (abs(f(x2, w)[m, 3]) + abs(base[m, 3])) / abs(x2[m, k] - x[m, k])
+        assert abs(diff - dx[m, k]) <= slack + ref.U_BF16 * abs(dx[m, k]) + 1e-3
+    for k in (4, 90):
+        w2 = w.copy()
+        w2[0, 3, k] = 240.0
+        diff = 448.0 * (f(x, w2)[:, 3] - base[:, 3]).sum() / (w2[0, 3, k] - w[0, 3, k])
+        slack = 448.0 * ref.U_BF16 * (np.abs(f(x, w2)[:, 3]) + np.abs(base[:, 3])).sum() / abs(w2[0, 3, k] - w[0, 3, k])
+        # x's columns are quantised anew for dw: half an E4M3 step of each element
+        assert abs(diff - dw[3, k]) <= slack + (2.0 ** -4 + ref.U_BF16) * 448.0 * np.abs(x[:, k]).sum()
+
+
+# ---------------------------------------------------------------- together
+
+def chain(h, wr, w1, w2, d_out, k, E, e0, e1):
+    """A small expert layer and its gradients, as a training step runs them; every stage's tensors."""
+    idx, w, _, _ = moe.route(h, wr, top_k=k)
+    g = moe.sort_tokens(idx, E, e0, e1)
+    y1 = moe.block_product(moe.quantize_block(h), w1, g, by_token=True)
+    a = torch.relu(y1)                                  # the program's own activation between the products
+    y2 = moe.block_product(moe.quantize_block(a, g), w2, g)
+    out = moe.combine(g, y2, w)
+    dy2, dw = moe.combine_backward(g, d_out, y2, w)
+    q2, c2 = moe.quantize_block_both(dy2, g)
+    da = moe.block_product_grad(q2, w2, g)
+    dw2 = moe.block_weight_grad(c2, moe.quantize_block_columns(a, g), g)
+    dy1 = torch.where(y1 > 0, da, torch.zeros_like(da))
+    q1, c1 = moe.quantize_block_both(dy1, g)
+    dh = moe.gather_backward(g, moe.block_product_grad(q1, w1, g))
+    dw1 = moe.block_weight_grad(c1, moe.quantize_block_columns(h, g, by_token=True), g)
+    return dict(idx=idx, w=w, y1=y1, a=a, y2=y2, out=out, dy2=dy2, dw=dw, da=da, dw2=dw2, dy1=dy1, dh=dh, dw1=dw1, g=g)
+
+
+def chain_inputs(T, D, F, E, n, seed):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    r = lambda *s: torch.randn(s, device="cuda", generator=gen).to(torch.bfloat16)
+    return (r(T, D), r(E, D), moe.quantize_block_weights(r(n, F, D)), moe.quantize_block_weights(r(n, D, F)),
+            torch.randn((T, D), device="cuda", generator=gen))
+
+
+def dequant(w):
+    c = host(w.codes).transpose(0, 1, 4, 2, 3, 5).reshape(w.E, w.N, w.K)
+    return c, host(w.scales)
+
+
+@pytest.mark.parametrize("T,E,e0,e1", [(1, 16, 0, 16), (90, 16, 0, 16), (200, 16, 4, 9)])
+def test_layer_and_gradients_stage_by_stage(T, E, e0, e1):
+    """route, sort, product, product, combine and all gradients: each stage against its definition in 64 bits on
+    the tensors that the stage before it gave."""
+    D, F, k = 256, 128, 4
+    h, wr, w1, w2, d_out = chain_inputs(T, D, F, E, e1 - e0, T)
+    r = chain(h, wr, w1, w2, d_out, k, E, e0, e1)
+    off, ss, sp = ref.sort(host(r["idx"]), e0, e1)
+    S = off[-1]
+    expert = np.repeat(np.arange(e1 - e0), np.diff(off))
+    tok = ss[:S] // k
+
+    def prod(x, w, got, what, transposed=False):
+        if S == 0:
+            return
+        check(num(got)[:S], *ref.product(*ref.rows(x), *dequant(w), expert, transposed), what)
+
+    prod(num(h)[tok], w1, r["y1"], "y1")
+    prod(num(r["a"])[:S], w2, r["y2"], "y2")
+    prod(num(r["dy2"])[:S], w2, r["da"], "da", True)
+    w = host(r["w"]).astype(np.float64)
+    ys = np.where((sp >= 0)[:, :, None], num(r["y2"])[np.maximum(sp, 0)].astype(np.float64), 0)
+    terms = ys * w[:, :, None]
+    assert (np.abs(num(r["out"]) - terms.sum(1)) <= k * ref.U24 * np.abs(terms).sum(1)).all()
+    p = ys * num(d_out)[:, None, :].astype(np.float64)
+    assert (np.abs(num(r["dw"]) - p.sum(2)) <= 26 * ref.U24 * np.abs(p).sum(2)).all()
+    for name, gy, x, wq in (("dw2", r["dy2"], num(r["a"])[:S], w2), ("dw1", r["dy1"], num(h)[tok], w1)):
+        cg, cx = ref.columns(num(gy)[:S], off), ref.columns(x, off)
+        for e in range(e1 - e0 if S else 0):
+            check(num(r[name])[e], *ref.weight_grad(cg, cx, off, e), f"{name}[{e}]")
+
+
+FINAL = ("out", "dw", "dw2", "dh", "dw1")
+
+
+def test_graph_replays_and_streams():
+    """The layer and its gradients captured into a graph, replayed with new inputs between eager runs, and run on two
+    streams at once with separate groups: the same bits as alone."""
+    T, D, F, E, k = 150, 256, 128, 16, 4
+    sets = [chain_inputs(T, D, F, E, E, s) for s in (1, 2, 3)]
+    want = []
+    for s in sets:
+        r = chain(*s, k, E, 0, E)
+        want.append({n: r[n].clone() for n in FINAL})
+    torch.cuda.synchronize()
+    own_copy = lambda t: t.clone() if torch.is_tensor(t) else moe.BlockWeights(t.E, t.N, t.K, t.codes.clone(), t.scales.clone())
+    static = tuple(own_copy(t) for t in sets[0])
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        chain(*static, k, E, 0, E)
+    torch.cuda.current_stream().wait_stream(side)
+    with torch.cuda.graph(graph):
+        r = chain(*static, k, E, 0, E)
+    for i in (0, 1, 2, 0, 1):
+        for a, b in ((static[0], sets[i][0]), (static[1], sets[i][1]), (static[4], sets[i][4])):
+            a.copy_(b)
+        for a, b in ((static[2], sets[i][2]), (static[3], sets[i][3])):
+            a.codes.copy_(b.codes)
+            a.scales.copy_(b.scales)
+        graph.replay()
+        torch.cuda.synchronize()
+        for n in FINAL:
+            assert torch.equal(r[n], want[i][n]), (i, n)
+        chain(*sets[2], k, E, 0, E)  # eager work between the replays
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [None, None]
+    for _ in range(3):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                got[i] = chain(*sets[i + 1], k, E, 0, E)
+        torch.cuda.synchronize()
+        for i in (0, 1):
+            for n in FINAL:
+                assert torch.equal(got[i][n], want[i + 1][n]), n

@@ -1,0 +1,160 @@
+"""The C ABI of include/moe_ops.h on the host (no GPU needed): exported symbols, the documented
+refusals before anything is enqueued, and the binding's own checks."""
+import ctypes
+import os
+import re
+
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_moe_amd as moe
+import ops_ref as ref
+from block_scaled_moe_amd import ops
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "moe_ops.h")
+OK, EINVAL, EUNSUP, EALIGN, EWS = 0, -1, -2, -3, -4
+A = 0x10000  # a fake, aligned "device" address: never dereferenced on these paths
+
+
+def test_header_functions_are_exported_and_bound():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = sorted(set(re.findall(r"\b(moe_[a-z_]+)\s*\(", text)))
+    assert sorted(ops.SIGNATURES) == names
+    lib = moe.lib()
+    for n in names:
+        assert hasattr(lib, n)
+    assert lib.moe_ops_abi_version() == 1
+
+
+def groups(**over):
+    g = ops.MoeGroups(64, 8, 384, 0, 96, A, A, A, A, 1 << 30)
+    for k, v in over.items():
+        setattr(g, k, v)
+    return g
+
+
+def test_plan_bytes():
+    f = lambda **o: moe.lib().moe_groups_plan_bytes(ctypes.byref(groups(**o)))
+    assert f() > 0 and f(T=0) > 0 and f(T=8192) > f() and f(T=-1) == 0 and f(top_k=9) == 0 and f(E=5000, e_end=5000) == 0
+    assert f(e_begin=96) == 0 and f(e_end=385) == 0 and f(T=2 ** 30) == 0
+    c = moe.lib().moe_block_column_blocks
+    assert c(0, 1) == 1 and c(127, 1) == 1 and c(128, 3) == 4 and c(-1, 1) == 0 and c(5, 0) == 0
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(T=-1), EINVAL), (dict(top_k=0), EINVAL), (dict(top_k=9), EINVAL), (dict(E=0), EINVAL), (dict(E=4097), EINVAL),
+    (dict(e_begin=-1), EINVAL), (dict(e_begin=96), EINVAL), (dict(e_end=385), EINVAL), (dict(offsets=0), EINVAL),
+    (dict(sorted_slot=0), EINVAL), (dict(slot_pos=0), EINVAL), (dict(plan=0), EWS), (dict(plan_bytes=256), EWS),
+    (dict(offsets=A + 4), EALIGN), (dict(plan=A + 16), EALIGN), (dict(T=2 ** 30), EINVAL)])
+def test_every_call_checks_its_groups(over, status):
+    lib, g = moe.lib(), groups(**over)
+    r = ctypes.byref(g)
+    assert lib.moe_sort(r, A, None) == status
+    assert lib.moe_gather(r, 1, 64, A, A, None) == status
+    assert lib.moe_gather_backward(r, 1, 64, A, A, None) == status
+    assert lib.moe_combine(r, 1, 2, 64, A, A, A, None) == status
+    assert lib.moe_combine_backward(r, 1, 2, 64, A, A, A, 2 * A, A, None) == status
+    rows = 64 * 8
+    q = ops.MoeBlockQuantizeArgs(rows, 128, 0, ctypes.pointer(g), A, A, A, 0, 0)
+    assert lib.moe_block_quantize(ctypes.byref(q), None) == status
+    m = ops.MoeBlockGemmArgs(rows, 0, 0, ctypes.pointer(g), A, A, ops.MoeBlockWeights(96, 128, 128, A, A), A)
+    assert lib.moe_block_gemm(ctypes.byref(m), None) == status
+    w = ops.MoeBlockWgradArgs(rows, 128, 128, ctypes.pointer(g), A, A, A, A, A)
+    assert lib.moe_block_wgrad(ctypes.byref(w), None) == status
+
+
+def test_row_calls_refuse():
+    lib, g = moe.lib(), groups()
+    r = ctypes.byref(g)
+    assert lib.moe_sort(r, 0, None) == EINVAL and lib.moe_sort(r, A + 4, None) == EALIGN
+    assert lib.moe_sort(None, A, None) == EINVAL
+    assert lib.moe_gather(r, 3, 64, A, A, None) == EINVAL and lib.moe_gather(r, 1, 0, A, A, None) == EINVAL
+    assert lib.moe_gather(r, 1, 64, 0, A, None) == EINVAL and lib.moe_gather(r, 1, 64, A + 2, A, None) == EALIGN
+    assert lib.moe_combine(r, 1, 0, 64, A, A, A, None) == EINVAL and lib.moe_combine(r, 1, 1, 64, A, 0, A, None) == EINVAL
+    assert lib.moe_combine_backward(r, 1, 1, 64, A, 2 * A, A, 2 * A, A, None) == EINVAL  # dy on top of y
+    assert lib.moe_combine_backward(r, 1, 1, 64, A, A, A, 2 * A, A + 8, None) == EALIGN
+    empty = ctypes.byref(groups(T=0))
+    assert lib.moe_gather(empty, 1, 64, 0, 0, None) == OK  # no tokens: nothing to do
+
+
+def test_block_calls_refuse():
+    lib = moe.lib()
+    quant = lambda *a: lib.moe_block_quantize(ctypes.byref(ops.MoeBlockQuantizeArgs(*a)), None)
+    g = ctypes.pointer(groups())
+    assert quant(4, 130, 0, None, A, A, A, 0, 0) == EUNSUP
+    assert quant(4, 128, 0, None, A, 0, 0, 0, 0) == EINVAL          # no output
+    assert quant(4, 128, 0, None, A, A, 0, 0, 0) == EINVAL          # codes without scales
+    assert quant(4, 128, 0, None, A, 0, 0, A, 0) == EINVAL
+    assert quant(4, 128, 1, None, A, 0, 0, A, A) == EINVAL          # by token without groups
+    assert quant(64, 128, 1, g, A, A, A, A, A) == EINVAL            # rows of the sorted order from tokens
+    assert quant(64, 128, 0, g, A, A, A, 0, 0) == EINVAL            # not T * top_k rows
+    assert quant(4, 128, 0, None, A + 2, A, A, 0, 0) == EALIGN
+    assert quant(0, 128, 0, None, 0, A, A, 0, 0) == OK
+    W = ops.MoeBlockWeights
+    gemm = lambda *a: lib.moe_block_gemm(ctypes.byref(ops.MoeBlockGemmArgs(*a)), None)
+    assert gemm(4, 0, 0, None, A, A, W(1, 192, 128, A, A), A) == EUNSUP
+    assert gemm(4, 0, 0, None, A, A, W(2, 128, 128, A, A), A) == EINVAL   # two experts, no groups
+    assert gemm(4, 1, 0, None, A, A, W(1, 128, 128, A, A), A) == EINVAL
+    assert gemm(512, 0, 0, g, A, A, W(95, 128, 128, A, A), A) == EINVAL
+    assert gemm(64, 0, 0, g, A, A, W(96, 128, 128, A, A), A) == EINVAL
+    assert gemm(4, 0, 0, None, A, 0, W(1, 128, 128, A, A), A) == EINVAL
+    assert gemm(4, 0, 0, None, A, A, W(1, 128, 128, A, 0), A) == EINVAL
+    assert gemm(4, 0, 0, None, A, A, W(1, 128, 128, A + 8, A), A) == EALIGN
+    assert gemm(0, 0, 0, None, 0, 0, W(1, 128, 128, A, A), 0) == OK
+    wgrad = lambda *a: lib.moe_block_wgrad(ctypes.byref(ops.MoeBlockWgradArgs(*a)), None)
+    assert wgrad(4, 128, 100, None, A, A, A, A, A) == EUNSUP
+    assert wgrad(4, 128, 128, None, A, A, A, A, 0) == EINVAL
+    assert wgrad(4, 128, 128, None, 0, A, A, A, A) == EINVAL
+    assert wgrad(64, 128, 128, g, A, A, A, A, A) == EINVAL
+    assert wgrad(4, 128, 128, None, A, A + 4, A, A, A) == EALIGN
+    assert lib.moe_block_quantize_weights(A, 1, 64, 128, A, A, None) == EUNSUP
+    assert lib.moe_block_quantize_weights(0, 1, 128, 128, A, A, None) == EINVAL
+    assert lib.moe_block_pack_weights(A, 1, 128, 128, A, None) == EINVAL      # onto itself
+    assert lib.moe_block_pack_weights(A + 4, 1, 128, 128, A, None) == EALIGN
+
+
+def test_binding_checks_its_tensors():
+    g = moe.Groups.empty(4, 2, 8, 2, 6, device="cpu")
+    x = torch.zeros((4, 128))
+    for bad in (x[:3], x.half(), x.t(), x[0]):
+        with pytest.raises(ValueError):
+            moe.gather(g, bad)
+    with pytest.raises(ValueError):
+        moe.combine(g, torch.zeros((8, 16)), torch.zeros((4, 2), dtype=torch.float64))
+    with pytest.raises(ValueError):
+        moe.combine(g, torch.zeros((8, 16)), torch.zeros((4, 2)), out_dtype=torch.float16)
+    with pytest.raises(ValueError):
+        moe.sort_tokens(torch.zeros((4, 2), dtype=torch.int64), 8)
+    with pytest.raises(ValueError):
+        moe.sort_tokens(torch.zeros((4, 2), dtype=torch.int32), 8, 2, 7, out=g)
+    with pytest.raises(moe.MoeError):
+        moe.Groups.empty(4, 9, 8, device="cpu")
+    with pytest.raises(ValueError):
+        moe.quantize_block(torch.zeros((4, 192), dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        moe.quantize_block(torch.zeros((4, 256), dtype=torch.bfloat16)[:, :128])  # strided
+    with pytest.raises(ValueError):
+        moe.BlockWeights.empty(1, 130, 128, device="cpu")
+    w = moe.BlockWeights.empty(2, 128, 256, device="cpu")
+    q = moe.BlockRows(torch.zeros((8, 256), dtype=torch.uint8), torch.zeros((8, 2)))
+    with pytest.raises(ValueError):
+        moe.block_product(q, w)                      # two experts without groups
+    with pytest.raises(ValueError):
+        moe.block_product(q, w.experts(0, 1), by_token=True)
+    with pytest.raises(ValueError):
+        moe.block_product(q, w, g)                   # the groups have four experts
+    with pytest.raises(ValueError):
+        moe.block_weight_grad(moe.BlockColumns(q.codes, q.scales), moe.BlockColumns(q.codes, q.scales))
+
+
+def test_plain_forms_of_the_format():
+    """The tests' own E4M3 rounding: every code is its value's code, midpoints go to the even code."""
+    codes = np.array([c for c in range(256) if c & 0x7F != 0x7F], np.uint8)
+    assert np.array_equal(ref.e4m3_code(ref.e4m3_value(codes).astype(np.float32)), codes)
+    pos = ref.e4m3_value(np.arange(0x7F, dtype=np.uint8))
+    mid = ((pos[:-1] + pos[1:]) / 2).astype(np.float32)
+    want = np.where(np.arange(0x7E) % 2 == 0, np.arange(0x7E), np.arange(1, 0x7F))
+    assert np.array_equal(ref.e4m3_code(mid), want)
+    assert (ref.e4m3_code(np.array([460.0, 1e30], np.float32)) == 0x7E).all()
