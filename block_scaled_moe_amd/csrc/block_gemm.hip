@@ -28,6 +28,8 @@
 #include "block_mma.h"
 #include "ops_internal.h"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
@@ -59,13 +61,12 @@ __device__ __forceinline__ bool work_item(const GroupView &v, int n_tiles, int w
 
 template <bool TRANS>
 __global__ void __launch_bounds__(kThreads) tile_kernel(const BlockGemmArgs p) {
-    __shared__ __attribute__((aligned(16))) uint8_t xb0[kOperand];
-    __shared__ __attribute__((aligned(16))) uint8_t xb1[kOperand];
-    __shared__ __attribute__((aligned(16))) uint8_t wb0[kOperand];
-    __shared__ __attribute__((aligned(16))) uint8_t wb1[kOperand];
+    // row codes (two buffers), weight codes (two buffers), row scales [block][row]
+    __shared__ __attribute__((aligned(16))) uint8_t xb[2 * kOperand];
+    __shared__ __attribute__((aligned(16))) uint8_t wb[2 * kOperand];
     __shared__ __attribute__((aligned(16))) float sc[kSeg * kBM];
 
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
     const int wm = wave >> 2, wn = wave & 3;
     const int i16 = lane & 15, g = lane >> 4;
     const int R = p.R, C = p.C, n = R / 128;
@@ -73,170 +74,195 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const BlockGemmArgs p) {
     const int n_tiles = p.v.offsets ? p.v.ctrl->n_tiles : p.v.max_tiles;
     const int per_xcd = (n_tiles * nb + 7) / 8;
     const int step = (gridDim.x + 7) / 8;
+    const uint32_t x_lds = lds_address(xb) + wave * 4096, w_lds = lds_address(wb) + wave * 4096;
 
     for (int it = blockIdx.x >> 3; it < per_xcd; it += step) {
         int tile, cb;
         if (!work_item(p.v, n_tiles, (blockIdx.x & 7) * per_xcd + it, nb, tile, cb)) break;
         int e = 0, p0 = tile * kBM, rows = p.v.rows - p0;
         if (p.v.offsets) {
-            e = p.v.tile_expert[tile];
-            p0 = p.v.tile_row0[tile];
+            e = uniform(p.v.tile_expert[tile]);
+            p0 = uniform(p.v.tile_row0[tile]);
             rows = p.v.offsets[e + 1] - p0;
         }
-        rows = min(rows, kBM);
-        const int n_sub = (rows + 15) / 16, msa = (n_sub - wm + 1) / 2;
+        rows = uniform(min(rows, kBM));
+        const int n_sub = (rows + 15) / 16;
         const int c0 = cb * kBN;
         auto src_row = [&](int r) -> int64_t {
             const int pos = p0 + min(r, rows - 1);
             return p.by_token ? p.v.sorted_slot[pos] / p.v.top_k : pos;
         };
 
-        // ---- sources of this lane's copies
+        // ---- sources of this lane's copies: four pieces of rows; the wave's weights and the
+        // lane's offset in them
         const uint8_t *xs[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             xs[j] = p.x_codes + src_row(32 * wave + 8 * j + (lane >> 3)) * R + (((lane & 7) ^ (lane >> 3)) * 16);
+        const int x_copies = min(4, max(0, 2 * n_sub - 4 * wave));  // of 8 rows each that hold rows
         const uint8_t *ws = p.w_codes + e * p.w_expert_bytes;
+        uint32_t w_lane;
         if (TRANS) {
             int kc = c0 / 64 + 2 * (wave & 1);
             if (kc * 64 >= C) kc = c0 / 64;  // half a column block: its first half again, unused
-            ws += ((int64_t)(wave >> 1) * (C / 64) + kc) * 2048 + lane * 16;
+            ws += ((int64_t)(wave >> 1) * (C / 64) + kc) * 2048;
+            w_lane = lane * 16;
         } else {
             int rb = c0 / 32 + wave;
             if (rb * 32 >= C) rb -= 4;
-            ws += (int64_t)rb * (R / 64) * 2048 + (lane >> 5) * 512 + swizzled_row(lane & 31, wave) * 16;
+            ws += (int64_t)rb * (R / 64) * 2048;
+            w_lane = (lane >> 5) * 512 + swizzled_row(lane & 31, wave) * 16;
         }
+        ws = uniform(ws);
         const int64_t w_step = TRANS ? (int64_t)C * 128 : 4096;
-        auto copy_x = [&](uint8_t *dst, int s) __attribute__((always_inline)) {
+        auto copy_x = [&](int s) __attribute__((always_inline)) {
+            const uint32_t dst = x_lds + (s & 1) * kOperand;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (32 * wave + 8 * j < 16 * n_sub) copy_to_lds(xs[j] + s * 128, dst + wave * 4096 + j * 1024);
+                if (j < x_copies) copy_to_lds(xs[j] + s * 128, dst + j * 1024);
         };
-        auto copy_w = [&](uint8_t *dst, int s) __attribute__((always_inline)) {
+        auto copy_w = [&](int s) __attribute__((always_inline)) {
+            const uint32_t dst = w_lds + (s & 1) * kOperand;
+            const uint8_t *src = ws + s * w_step;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) copy_to_lds(ws + s * w_step + j * 1024, dst + wave * 4096 + j * 1024);
+            for (int j = 0; j < 4; ++j) copy_to_lds(src + j * 1024, w_lane, dst + j * 1024);
         };
 
-        // ---- scales of blocks seg .. seg + 31: the rows' to LDS, the weights' one per lane
         const int col_block = min(c0 / 128 + (wn >> 1), C / 128 - 1);
         const float *sw = p.w_scales + (int64_t)e * p.w_expert_scales + (TRANS ? col_block : col_block * p.w_kb);
-        const float *sx = p.x_scales + src_row(t >> 1) * n;
-        float swv = 0.0f;
-        auto load_scales = [&](int seg) {
-            const int b = min(seg + (lane & 31), n - 1);
-            swv = sw[TRANS ? (int64_t)b * p.w_kb : b];
-            float v[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = sx[min(seg + 16 * (t & 1) + j, n - 1)];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) sc[(16 * (t & 1) + j) * kBM + (t >> 1)] = v[j];
-        };
 
-        f4 acc[8][4];
+        auto run = [&](auto msa_c) __attribute__((always_inline)) {
+            constexpr int MSA = decltype(msa_c)::value;  // this wave's pieces of 16 rows
+            f4 acc[MSA > 0 ? MSA : 1][4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < MSA; ++i)
 #pragma unroll
-            for (int s = 0; s < 4; ++s) acc[i][s] = (f4){0.0f, 0.0f, 0.0f, 0.0f};
+                for (int s = 0; s < 4; ++s) acc[i][s] = (f4){0.0f, 0.0f, 0.0f, 0.0f};
 
-        // the wave's operand for its columns, read s of 4
-        auto w_operand = [&](const uint8_t *w, int s) __attribute__((always_inline)) -> v8i {
-            if constexpr (TRANS) {
-                // columns 16 s + i16 of tile column wn; block rows 16 g .. and 64 + 16 g ..
-                const uint8_t *q = w + (g >> 1) * 8192 + wn * 2048 + s * 512 + (g & 1) * 256 + i16 * 8;
-                auto tr = [&](int at) {
-                    return __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) v2i *)(q + at));
-                };
-                const v2i a = tr(0), b = tr(128), c = tr(2 * 8192), d = tr(2 * 8192 + 128);
-                return (v8i){a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
-            } else {
-                const int rt = 2 * wn + (i16 >> 3);  // 32-row tile
-                const int r = 16 * ((i16 >> 2) & 1) + 4 * s + (i16 & 3);
-                const uint8_t *q = w + rt * 4096 + g * 512 + swizzled_row(r, rt) * 16;
-                return operand(*reinterpret_cast<const u32x4 *>(q), *reinterpret_cast<const u32x4 *>(q + 2048));
-            }
-        };
-        auto x_operand = [&](const uint8_t *x, int i) __attribute__((always_inline)) -> v8i {
-            const int r = 16 * (2 * i + wm) + i16;
-            const uint8_t *q = x + r * 128;
-            return operand(*reinterpret_cast<const u32x4 *>(q + ((g ^ (r & 7)) * 16)),
-                           *reinterpret_cast<const u32x4 *>(q + (((4 + g) ^ (r & 7)) * 16)));
-        };
-
-        // block s from buffers x, w
-        auto block_step = [&](const uint8_t *x, uint8_t *x_next, uint8_t *w, int s) __attribute__((always_inline)) {
-            // this block's copies are all but the weights of block s + 1
-            if (s + 1 < n) wait_copies<4>();
-            else wait_copies<0>();
-            lds_barrier();
-            if ((s & (kSeg - 1)) == 0 && s > 0) {
-                load_scales(s);
-                lds_barrier();
-            }
-            if (s + 1 < n) copy_x(x_next, s + 1);
-            v8i wf[4];
+            copy_x(0);
+            copy_w(0);
+            if (n > 1) copy_w(1);
+            for (int seg = 0; seg < n; seg += kSeg) {
+                // ---- scales of blocks seg ..: the rows' to LDS, the weights' one per lane
+                if (seg > 0) lds_barrier();  // the last segment's reads
+                const int bw = min(seg + (lane & 31), n - 1);
+                const float swv = sw[TRANS ? (int64_t)bw * p.w_kb : bw];
+                {
+                    const float *sx = p.x_scales + src_row(t >> 1) * n;
+                    const int b0 = 16 * (t & 1);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) wf[q] = w_operand(w, q);
-            const float fw = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(swv), s & (kSeg - 1)));
-            const float *fs = sc + (s & (kSeg - 1)) * kBM;
-            v8i xf = x_operand(x, 0);
-            float f = fs[16 * wm + i16] * fw;
+                    for (int h = 0; h < 16; h += 4) {
+                        float v[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (i < msa) {
-                    const v8i xi = xf;
-                    const float fi = f;
-                    if (i + 1 < 8) {
-                        xf = x_operand(x, i + 1);
-                        f = fs[16 * (2 * (i + 1) + wm) + i16] * fw;
+                        for (int j = 0; j < 4; ++j) v[j] = sx[min(seg + b0 + h + j, n - 1)];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) sc[(b0 + h + j) * kBM + (t >> 1)] = v[j];
                     }
-                    f4 d[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) d[q] = block_dot(wf[q], xi);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) acc[i][q][v] = fmaf(d[q][v], fi, acc[i][q][v]);
                 }
-                if (i == 0) {  // every wave holds its columns' codes: refill their buffer
+                const int end = min(seg + kSeg, n);
+#pragma clang loop unroll(disable)
+                for (int s = seg; s < end; ++s) {
+                    // this block's copies are all but the weights of block s + 1
+                    if (s + 1 < n) wait_copies<4>();
+                    else wait_copies<0>();
                     lds_barrier();
-                    if (s + 2 < n) copy_w(w, s + 2);
-                }
-            }
-        };
-
-        lds_barrier();  // the previous item's reads
-        load_scales(0);
-        copy_x(xb0, 0);
-        copy_w(wb0, 0);
-        if (n > 1) copy_w(wb1, 1);
-        for (int s = 0; s < n; s += 2) {
-            block_step(xb0, xb1, wb0, s);
-            if (s + 1 < n) block_step(xb1, xb0, wb1, s + 1);
-        }
-
-        // ---- outputs
-        if (c0 + 64 * wn < C) {
+                    if (s + 1 < n) copy_x(s + 1);
+                    if constexpr (MSA > 0) {
+                        const uint8_t *x = xb + (s & 1) * kOperand, *w = wb + (s & 1) * kOperand;
+                        const float *fs = sc + (s - seg) * kBM + 16 * wm + i16;
+                        const float fw = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(swv), s - seg));
+                        auto x_operand = [&](int i) __attribute__((always_inline)) -> v8i {
+                            const uint8_t *q = x + (16 * wm + i16) * 128 + i * 4096;
+                            return operand(*reinterpret_cast<const u32x4 *>(q + ((g ^ (i16 & 7)) * 16)),
+                                           *reinterpret_cast<const u32x4 *>(q + (((4 + g) ^ (i16 & 7)) * 16)));
+                        };
+                        v8i wf[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int m = 16 * (2 * i + wm) + i16;
-                if (i < msa && m < rows) {
-                    uint16_t *o = p.out + (int64_t)(p0 + m) * C + c0 + 64 * wn;
-                    if (TRANS) {  // read s holds columns 16 s + 4 g ..
+                        for (int q = 0; q < 4; ++q) {
+                            if constexpr (TRANS) {
+                                // columns 16 q + i16 of tile column wn; block rows 16 g .. and 64 + 16 g ..
+                                const uint8_t *a = w + (g >> 1) * 8192 + wn * 2048 + q * 512 + (g & 1) * 256 + i16 * 8;
+                                auto tr = [&](int at) {
+                                    return __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                                        (__attribute__((address_space(3))) v2i *)(a + at));
+                                };
+                                const v2i a0 = tr(0), a1 = tr(128), a2 = tr(2 * 8192), a3 = tr(2 * 8192 + 128);
+                                wf[q] = (v8i){a0.x, a0.y, a1.x, a1.y, a2.x, a2.y, a3.x, a3.y};
+                            } else {
+                                const int rt = 2 * wn + (i16 >> 3);  // 32-row tile
+                                const int r = 16 * ((i16 >> 2) & 1) + 4 * q + (i16 & 3);
+                                const uint8_t *a = w + rt * 4096 + g * 512 + swizzled_row(r, rt) * 16;
+                                wf[q] = operand(*reinterpret_cast<const u32x4 *>(a),
+                                                *reinterpret_cast<const u32x4 *>(a + 2048));
+                            }
+                        }
+                        v8i xf = x_operand(0);
+                        float f = fs[0] * fw;
 #pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            *reinterpret_cast<uint2 *>(o + 16 * s + 4 * g) =
-                                make_uint2(bf16_pair(acc[i][s][0], acc[i][s][1]), bf16_pair(acc[i][s][2], acc[i][s][3]));
-                    } else {  // read s holds columns 16 g + 4 s ..
+                        for (int i = 0; i < MSA; ++i) {
+                            const v8i xi = xf;
+                            const float fi = f;
+                            if (i + 1 < MSA) {
+                                xf = x_operand(i + 1);
+                                f = fs[32 * (i + 1)] * fw;
+                            }
+                            f4 d[4];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            *reinterpret_cast<uint4 *>(o + 16 * g + 8 * h) =
-                                make_uint4(bf16_pair(acc[i][2 * h][0], acc[i][2 * h][1]),
-                                           bf16_pair(acc[i][2 * h][2], acc[i][2 * h][3]),
-                                           bf16_pair(acc[i][2 * h + 1][0], acc[i][2 * h + 1][1]),
-                                           bf16_pair(acc[i][2 * h + 1][2], acc[i][2 * h + 1][3]));
+                            for (int q = 0; q < 4; ++q) d[q] = block_dot(wf[q], xi);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                                for (int v = 0; v < 4; ++v) acc[i][q][v] = fmaf(d[q][v], fi, acc[i][q][v]);
+                            if (i == 0) {  // every wave holds its columns' codes: refill their buffer
+                                lds_barrier();
+                                if (s + 2 < n) copy_w(s + 2);
+                            }
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    } else {
+                        lds_barrier();
+                        if (s + 2 < n) copy_w(s + 2);
                     }
                 }
             }
+
+            // ---- outputs
+            if (c0 + 64 * wn < C) {
+#pragma unroll
+                for (int i = 0; i < MSA; ++i) {
+                    const int m = 16 * (2 * i + wm) + i16;
+                    if (m < rows) {
+                        uint16_t *o = p.out + (int64_t)(p0 + m) * C + c0 + 64 * wn;
+                        if (TRANS) {  // read s holds columns 16 s + 4 g ..
+#pragma unroll
+                            for (int s = 0; s < 4; ++s)
+                                *reinterpret_cast<uint2 *>(o + 16 * s + 4 * g) = make_uint2(
+                                    bf16_pair(acc[i][s][0], acc[i][s][1]), bf16_pair(acc[i][s][2], acc[i][s][3]));
+                        } else {  // read s holds columns 16 g + 4 s ..
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                *reinterpret_cast<uint4 *>(o + 16 * g + 8 * h) =
+                                    make_uint4(bf16_pair(acc[i][2 * h][0], acc[i][2 * h][1]),
+                                               bf16_pair(acc[i][2 * h][2], acc[i][2 * h][3]),
+                                               bf16_pair(acc[i][2 * h + 1][0], acc[i][2 * h + 1][1]),
+                                               bf16_pair(acc[i][2 * h + 1][2], acc[i][2 * h + 1][3]));
+                        }
+                    }
+                }
+            }
+        };
+        lds_barrier();  // the previous item's reads
+        // pieces 2 i + wm < n_sub; every wave runs the same copies and barriers
+        switch ((n_sub - wm + 1) / 2) {
+            case 0: run(std::integral_constant<int, 0>{}); break;
+            case 1: run(std::integral_constant<int, 1>{}); break;
+            case 2: run(std::integral_constant<int, 2>{}); break;
+            case 3: run(std::integral_constant<int, 3>{}); break;
+            case 4: run(std::integral_constant<int, 4>{}); break;
+            case 5: run(std::integral_constant<int, 5>{}); break;
+            case 6: run(std::integral_constant<int, 6>{}); break;
+            case 7: run(std::integral_constant<int, 7>{}); break;
+            default: run(std::integral_constant<int, 8>{}); break;
         }
     }
 }

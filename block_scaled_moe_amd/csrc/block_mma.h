@@ -29,11 +29,30 @@ __device__ __forceinline__ f4 block_dot(v8i a, v8i b) {
 }
 
 // 16 bytes per lane from global memory straight into LDS at dst + 16 * lane (dst the same for
-// the wave)
-__device__ __forceinline__ void copy_to_lds(const uint8_t *src, uint8_t *dst) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
-                                     (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
+// the wave): from src, or from base + offset with the base the same for the wave. Written in
+// assembly, as it has no register to wait for: behind the builtin the compiler puts a wait for
+// every copy in flight before the next LDS read, which a ring of buffers cannot have. The
+// caller waits (wait_copies) and meets its workgroup (lds_barrier) before the bytes are read.
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p);
 }
+__device__ __forceinline__ void copy_to_lds(const uint8_t *src, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(dst), "v"(src) : "memory", "m0");
+}
+__device__ __forceinline__ void copy_to_lds(const uint8_t *base, uint32_t offset, uint32_t dst) {
+    // five wait states between a vector instruction that wrote base and the copy that reads it
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst), "v"(offset), "s"(base)
+                 : "memory", "m0");
+}
+// p, the same for every lane of the wave, as a scalar
+template <typename T>
+__device__ __forceinline__ T *uniform(T *p) {
+    const uint64_t v = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);  // unsigned: it comes back as an int
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return (T *)((uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // Workgroup barrier that leaves the wave's copies into LDS in flight (__syncthreads waits for
 // them all); LDS reads and writes complete first.

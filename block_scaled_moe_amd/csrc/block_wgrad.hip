@@ -3,11 +3,12 @@
 //
 //   dw[e][n][k] = sum over e's runs b of 128 rows of sg[b][n] sx[b][k] * sum over the run of cg * cx
 //
-// 256 (n) x 256 (k) outputs per work item, 8 waves as 2 (n) x 4 (k), 16-column pieces of n
-// alternating between the two. The input's columns are the MFMA's A operand, so a lane's
-// accumulators are consecutive k of one n. Both operands of a run are contiguous 32 KiB in the
-// column form and go straight into one of two LDS buffers. An expert has few runs (its rows /
-// 128), so the item is mostly its 128 KiB of output: bound by the writes of dw.
+// 128 (n) x 256 (k) outputs per workgroup of four waves, a wave 128 x 64. The input's columns
+// are the MFMA's A operand, so a lane's accumulators are consecutive k of one n. Both operands
+// of a run are contiguous in the column form and go straight into LDS, with their scales. An
+// expert has few runs (its rows / 128), so a workgroup is mostly its 64 KiB of output: bound by
+// the writes of dw. Two workgroups share a CU (one buffer of 50 KiB, 256 registers a lane), one
+// loading or storing while the other multiplies.
 #include "block_mma.h"
 #include "ops_internal.h"
 
@@ -16,23 +17,20 @@ namespace {
 
 using namespace block;
 
-constexpr int kThreads = 512, kBN = 256;
-constexpr int kOperand = 256 * 128;
+constexpr int kThreads = 256, kBN = 128, kBK = 256;
 
-__global__ void __launch_bounds__(kThreads) wgrad_kernel(const BlockWgradArgs p) {
-    __shared__ __attribute__((aligned(16))) uint8_t gb0[kOperand];
-    __shared__ __attribute__((aligned(16))) uint8_t gb1[kOperand];
-    __shared__ __attribute__((aligned(16))) uint8_t xb0[kOperand];
-    __shared__ __attribute__((aligned(16))) uint8_t xb1[kOperand];
+__global__ void __launch_bounds__(kThreads, 2) wgrad_kernel(const BlockWgradArgs p) {
+    __shared__ __attribute__((aligned(16))) uint8_t gl[kBN * 128];
+    __shared__ __attribute__((aligned(16))) uint8_t xl[kBK * 128];
+    __shared__ __attribute__((aligned(16))) float sg[kBN], sx[kBK];
 
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    const int wm = wave >> 2, wn = wave & 3;
+    const int t = threadIdx.x, lane = t & 63, wn = uniform(t >> 6);
     const int i16 = lane & 15, g = lane >> 4;
     const int N = p.N, K = p.K;
-    const int nbn = (N + kBN - 1) / kBN, nbk = (K + kBN - 1) / kBN;
-    const int64_t w = blockIdx.x;
-    const int e = (int)(w / (nbn * nbk)), r = (int)(w % (nbn * nbk));
-    const int n0 = r / nbk * kBN, k0 = r % nbk * kBN;
+    const int nbn = N / kBN, nbk = (K + kBK - 1) / kBK;
+    const int w = blockIdx.x;
+    const int e = w / (nbn * nbk), r = w % (nbn * nbk);
+    const int n0 = r / nbk * kBN, k0 = r % nbk * kBK;
 
     int first = 0, cnt = p.rows;
     if (p.offsets) {
@@ -41,24 +39,30 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(const BlockWgradArgs p)
     }
     const int runs = (cnt + 127) / 128;
     const int64_t run0 = p.offsets ? first / 128 + e : 0;
+    const bool half = k0 + 128 >= K;  // half a block of k: its first half again, unused
 
-    // this wave's 32 columns of both operands (half a block of columns: its first half again)
-    int gt = n0 / 32 + wave, xt = k0 / 32 + wave;
-    if (gt * 32 >= N) gt -= 4;
-    if (xt * 32 >= K) xt -= 4;
-    const uint8_t *gs = p.g_codes + run0 * N * 128 + (int64_t)gt * 4096 + lane * 16;
-    const uint8_t *xs = p.x_codes + run0 * K * 128 + (int64_t)xt * 4096 + (lane >> 5) * 512 + swizzled_row(lane & 31, wave) * 16;
-    auto copy = [&](uint8_t *gd, uint8_t *xd, int s) __attribute__((always_inline)) {
+    // the wave copies 32 columns of n and 64 of k, wave 0 the scales
+    const uint8_t *gs = uniform(p.g_codes + run0 * N * 128 + (int64_t)(n0 / 32 + wn) * 4096);
+    const uint8_t *xs = uniform(p.x_codes + run0 * K * 128 + (int64_t)(k0 / 32 + 2 * (half ? wn & 1 : wn)) * 4096);
+    const uint32_t x_even = (lane >> 5) * 512 + swizzled_row(lane & 31, 0) * 16;
+    const uint32_t x_odd = 4096 + (lane >> 5) * 512 + swizzled_row(lane & 31, 1) * 16;
+    const uint8_t *gf = uniform(reinterpret_cast<const uint8_t *>(p.g_scales + run0 * N + n0));
+    const uint8_t *xf32 = uniform(reinterpret_cast<const uint8_t *>(p.x_scales + run0 * K + k0));
+    const uint32_t g_lds = lds_address(gl) + wn * 4096, x_lds = lds_address(xl) + wn * 8192;
+    const uint32_t sg_lds = lds_address(sg), sx_lds = lds_address(sx);
+    auto copy = [&](int s) __attribute__((always_inline)) {
+        const uint8_t *gsrc = gs + (int64_t)s * N * 128, *xsrc = xs + (int64_t)s * K * 128;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            copy_to_lds(gs + (int64_t)s * N * 128 + j * 1024, gd + wave * 4096 + j * 1024);
-            copy_to_lds(xs + (int64_t)s * K * 128 + j * 1024, xd + wave * 4096 + j * 1024);
+            copy_to_lds(gsrc + j * 1024, lane * 16, g_lds + j * 1024);
+            copy_to_lds(xsrc + j * 1024, x_even, x_lds + j * 1024);
+            copy_to_lds(xsrc + j * 1024, x_odd, x_lds + 4096 + j * 1024);
+        }
+        if (wn == 0) {
+            copy_to_lds(xf32 + (int64_t)s * K * 4, (half ? lane & 31 : lane) * 16, sx_lds);
+            if (lane < 32) copy_to_lds(gf + (int64_t)s * N * 4, lane * 16, sg_lds);
         }
     };
-    // scales of this lane's outputs: n = n0 + 16 (2 i + wm) + i16, k = k0 + 64 wn + 16 g + 4 s + v
-    const bool k_in = k0 + 64 * wn < K;
-    const float *sg = p.g_scales + run0 * N, *sx = p.x_scales + run0 * K + (k_in ? k0 + 64 * wn + 16 * g : 0);
-    auto n_of = [&](int i) { return n0 + 16 * (2 * i + wm) + i16; };
 
     f4 acc[8][4];
 #pragma unroll
@@ -66,60 +70,48 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(const BlockWgradArgs p)
 #pragma unroll
         for (int s = 0; s < 4; ++s) acc[i][s] = (f4){0.0f, 0.0f, 0.0f, 0.0f};
 
-    auto run_step = [&](const uint8_t *gl, const uint8_t *xl, uint8_t *g_next, uint8_t *x_next, int s)
-                        __attribute__((always_inline)) {
+#pragma clang loop unroll(disable)
+    for (int s = 0; s < runs; ++s) {
+        if (s > 0) lds_barrier();  // the last run's reads
+        copy(s);
         wait_copies<0>();
         lds_barrier();
-        f4 fx[4];
-        float fg[8];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) fx[q] = *reinterpret_cast<const f4 *>(sx + (int64_t)s * K + 4 * q);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) fg[i] = sg[(int64_t)s * N + min(n_of(i), N - 1)];
-        if (s + 1 < runs) copy(g_next, x_next, s + 1);
+        // n = n0 + 16 i + i16, k = k0 + 64 wn + 16 g + 4 q + v
         v8i xf[4];
+        f4 fx[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const int rt = 2 * wn + (i16 >> 3), row = 16 * ((i16 >> 2) & 1) + 4 * q + (i16 & 3);
             const uint8_t *a = xl + rt * 4096 + g * 512 + swizzled_row(row, rt) * 16;
             xf[q] = operand(*reinterpret_cast<const u32x4 *>(a), *reinterpret_cast<const u32x4 *>(a + 2048));
+            fx[q] = *reinterpret_cast<const f4 *>(sx + 64 * wn + 16 * g + 4 * q);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int c = 16 * (2 * i + wm);  // column of the item
-            const uint8_t *b = gl + (c >> 5) * 4096 + g * 512 + ((c & 31) + i16) * 16;
-            const v8i gf = operand(*reinterpret_cast<const u32x4 *>(b), *reinterpret_cast<const u32x4 *>(b + 2048));
+            const uint8_t *b = gl + (i >> 1) * 4096 + g * 512 + (16 * (i & 1) + i16) * 16;
+            const v8i gv = operand(*reinterpret_cast<const u32x4 *>(b), *reinterpret_cast<const u32x4 *>(b + 2048));
+            const float fg = sg[16 * i + i16];
             f4 d[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) d[q] = block_dot(xf[q], gf);
+            for (int q = 0; q < 4; ++q) d[q] = block_dot(xf[q], gv);
 #pragma unroll
             for (int q = 0; q < 4; ++q)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) acc[i][q][v] = fmaf(d[q][v], fx[q][v] * fg[i], acc[i][q][v]);
-        }
-        lds_barrier();  // every wave is done with the buffer before it is refilled
-    };
-
-    if (runs > 0) {
-        copy(gb0, xb0, 0);
-        for (int s = 0; s < runs; s += 2) {
-            run_step(gb0, xb0, gb1, xb1, s);
-            if (s + 1 < runs) run_step(gb1, xb1, gb0, xb0, s + 1);
+                for (int v = 0; v < 4; ++v) acc[i][q][v] = fmaf(d[q][v], fx[q][v] * fg, acc[i][q][v]);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 
-    if (k_in) {
+    if (k0 + 64 * wn < K) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int nn = n_of(i);
-            if (nn < N) {
-                uint16_t *o = p.dw + ((int64_t)e * N + nn) * K + k0 + 64 * wn + 16 * g;
+            uint16_t *o = p.dw + ((int64_t)e * N + n0 + 16 * i + i16) * K + k0 + 64 * wn + 16 * g;
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    *reinterpret_cast<uint4 *>(o + 8 * h) =
-                        make_uint4(bf16_pair(acc[i][2 * h][0], acc[i][2 * h][1]), bf16_pair(acc[i][2 * h][2], acc[i][2 * h][3]),
-                                   bf16_pair(acc[i][2 * h + 1][0], acc[i][2 * h + 1][1]),
-                                   bf16_pair(acc[i][2 * h + 1][2], acc[i][2 * h + 1][3]));
+            for (int h = 0; h < 2; ++h) {
+                const u32x4 v = {bf16_pair(acc[i][2 * h][0], acc[i][2 * h][1]), bf16_pair(acc[i][2 * h][2], acc[i][2 * h][3]),
+                                 bf16_pair(acc[i][2 * h + 1][0], acc[i][2 * h + 1][1]),
+                                 bf16_pair(acc[i][2 * h + 1][2], acc[i][2 * h + 1][3])};
+                *reinterpret_cast<u32x4 *>(o + 8 * h) = v;
             }
         }
     }
@@ -128,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(const BlockWgradArgs p)
 }  // namespace
 
 hipError_t launch_block_wgrad(const BlockWgradArgs &a, hipStream_t s) {
-    const int64_t items = (int64_t)a.n * ((a.N + kBN - 1) / kBN) * ((a.K + kBN - 1) / kBN);
+    const int64_t items = (int64_t)a.n * (a.N / kBN) * ((a.K + kBK - 1) / kBK);
     if (items > INT32_MAX) return hipErrorInvalidValue;
     hipLaunchKernelGGL(wgrad_kernel, dim3((unsigned)items), dim3(kThreads), 0, s, a);
     return hipGetLastError();
