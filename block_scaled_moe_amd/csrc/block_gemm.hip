@@ -95,10 +95,11 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const BlockGemmArgs p) {
 
         // ---- sources of this lane's copies: four pieces of rows; the wave's weights and the
         // lane's offset in them
-        const uint8_t *xs[4];
+        uint32_t x_lane[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            xs[j] = p.x_codes + src_row(32 * wave + 8 * j + (lane >> 3)) * R + (((lane & 7) ^ (lane >> 3)) * 16);
+            x_lane[j] = (uint32_t)src_row(32 * wave + 8 * j + (lane >> 3)) * 128 + (((lane & 7) ^ (lane >> 3)) * 16);
+        const int64_t x_step = (int64_t)p.x_rows * 128;
         const int x_copies = min(4, max(0, 2 * n_sub - 4 * wave));  // of 8 rows each that hold rows
         const uint8_t *ws = p.w_codes + e * p.w_expert_bytes;
         uint32_t w_lane;
@@ -111,15 +112,16 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const BlockGemmArgs p) {
             int rb = c0 / 32 + wave;
             if (rb * 32 >= C) rb -= 4;
             ws += (int64_t)rb * (R / 64) * 2048;
-            w_lane = (lane >> 5) * 512 + swizzled_row(lane & 31, wave) * 16;
+            w_lane = (lane >> 5) * 512 + swizzled_row(lane & 31) * 16;
         }
         ws = uniform(ws);
         const int64_t w_step = TRANS ? (int64_t)C * 128 : 4096;
         auto copy_x = [&](int s) __attribute__((always_inline)) {
             const uint32_t dst = x_lds + (s & 1) * kOperand;
+            const uint8_t *src = p.x_codes + s * x_step;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (j < x_copies) copy_to_lds(xs[j] + s * 128, dst + j * 1024);
+                if (j < x_copies) copy_to_lds(src, x_lane[j], dst + j * 1024);
         };
         auto copy_w = [&](int s) __attribute__((always_inline)) {
             const uint32_t dst = w_lds + (s & 1) * kOperand;
@@ -138,6 +140,18 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const BlockGemmArgs p) {
             for (int i = 0; i < MSA; ++i)
 #pragma unroll
                 for (int s = 0; s < 4; ++s) acc[i][s] = (f4){0.0f, 0.0f, 0.0f, 0.0f};
+            // Block sums of two pieces of rows: a piece's are added to its accumulators behind
+            // the MFMAs of the next one, the last piece's behind those of the next block's first
+            // (where the two do not fall on the same registers)
+            constexpr bool kCarry = MSA % 2 == 0;
+            f4 d[2][4];
+            float fd = 0.0f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) d[0][q] = (f4){0.0f, 0.0f, 0.0f, 0.0f};
+            auto add = [&](int i, int b, int q, float f) __attribute__((always_inline)) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[i][q][v] = fmaf(d[b][q][v], f, acc[i][q][v]);
+            };
 
             copy_x(0);
             copy_w(0);
@@ -150,14 +164,16 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const BlockGemmArgs p) {
                 {
                     const float *sx = p.x_scales + src_row(t >> 1) * n;
                     const int b0 = 16 * (t & 1);
+                    f4 v[4];
+                    if (n % 4 == 0) {
 #pragma unroll
-                    for (int h = 0; h < 16; h += 4) {
-                        float v[4];
+                        for (int h = 0; h < 4; ++h) v[h] = *reinterpret_cast<const f4 *>(sx + min(seg + b0 + 4 * h, n - 4));
+                    } else {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) v[j] = sx[min(seg + b0 + h + j, n - 1)];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) sc[(b0 + h + j) * kBM + (t >> 1)] = v[j];
+                        for (int h = 0; h < 16; ++h) v[h >> 2][h & 3] = sx[min(seg + b0 + h, n - 1)];
                     }
+#pragma unroll
+                    for (int h = 0; h < 16; ++h) sc[(b0 + h) * kBM + (t >> 1)] = v[h >> 2][h & 3];
                 }
                 const int end = min(seg + kSeg, n);
 #pragma clang loop unroll(disable)
@@ -189,9 +205,7 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const BlockGemmArgs p) {
                                 const v2i a0 = tr(0), a1 = tr(128), a2 = tr(2 * 8192), a3 = tr(2 * 8192 + 128);
                                 wf[q] = (v8i){a0.x, a0.y, a1.x, a1.y, a2.x, a2.y, a3.x, a3.y};
                             } else {
-                                const int rt = 2 * wn + (i16 >> 3);  // 32-row tile
-                                const int r = 16 * ((i16 >> 2) & 1) + 4 * q + (i16 & 3);
-                                const uint8_t *a = w + rt * 4096 + g * 512 + swizzled_row(r, rt) * 16;
+                                const uint8_t *a = w + (2 * wn + (q >> 1)) * 4096 + g * 512 + swizzled_row(a_row(i16, q)) * 16;
                                 wf[q] = operand(*reinterpret_cast<const u32x4 *>(a),
                                                 *reinterpret_cast<const u32x4 *>(a + 2048));
                             }
@@ -206,24 +220,32 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const BlockGemmArgs p) {
                                 xf = x_operand(i + 1);
                                 f = fs[32 * (i + 1)] * fw;
                             }
-                            f4 d[4];
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) d[q] = block_dot(wf[q], xi);
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                                for (int v = 0; v < 4; ++v) acc[i][q][v] = fmaf(d[q][v], fi, acc[i][q][v]);
+                            for (int q = 0; q < 4; ++q) {
+                                d[(MSA - 1 - i) & 1][q] = block_dot(wf[q], xi);
+                                if (i > 0 || kCarry) add(i > 0 ? i - 1 : MSA - 1, (MSA - i) & 1, q, fd);
+                                __builtin_amdgcn_sched_barrier(0);
+                            }
+                            fd = fi;
                             if (i == 0) {  // every wave holds its columns' codes: refill their buffer
                                 lds_barrier();
                                 if (s + 2 < n) copy_w(s + 2);
                             }
-                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                        if (!kCarry) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) add(MSA - 1, 0, q, fd);
                         }
                     } else {
                         lds_barrier();
                         if (s + 2 < n) copy_w(s + 2);
                     }
                 }
+            }
+
+            if constexpr (MSA > 0 && kCarry) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) add(MSA - 1, 0, q, fd);
             }
 
             // ---- outputs
@@ -238,10 +260,10 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const BlockGemmArgs p) {
                             for (int s = 0; s < 4; ++s)
                                 *reinterpret_cast<uint2 *>(o + 16 * s + 4 * g) = make_uint2(
                                     bf16_pair(acc[i][s][0], acc[i][s][1]), bf16_pair(acc[i][s][2], acc[i][s][3]));
-                        } else {  // read s holds columns 16 g + 4 s ..
+                        } else {  // reads 2 h, 2 h + 1 hold columns 32 h + 8 g ..
 #pragma unroll
                             for (int h = 0; h < 2; ++h)
-                                *reinterpret_cast<uint4 *>(o + 16 * g + 8 * h) =
+                                *reinterpret_cast<uint4 *>(o + 32 * h + 8 * g) =
                                     make_uint4(bf16_pair(acc[i][2 * h][0], acc[i][2 * h][1]),
                                                bf16_pair(acc[i][2 * h][2], acc[i][2 * h][3]),
                                                bf16_pair(acc[i][2 * h + 1][0], acc[i][2 * h + 1][1]),

@@ -67,13 +67,15 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {  // nearest, t
     return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)b) << 16;
 }
 
-// Row of a 32-row weight tile kept at position `pos` of its quarter in LDS (an involution).
-// Lane i of an operand read takes row 16 (i / 4) + 4 s + i % 4 of 64 rows (two tiles), so that
-// its accumulators of four reads s hold 16 consecutive outputs; the swap puts the four runs of
-// 64 bytes that 16 lanes read at four different 64-byte offsets of 256.
-__device__ __forceinline__ int swizzled_row(int pos, int tile) {
-    return pos ^ (((pos >> 4) & 1) << 2) ^ ((tile & 1) << 3);
-}
+// The MFMA's A operand is read so that a lane's accumulators of four reads q, over 64 columns in
+// two tiles of 32, are outputs 32 h + 8 g .. 32 h + 8 g + 7 (h = q / 2): 16 bytes of bf16, and
+// the four g of a row 64 bytes in a row. Lane i then takes row 8 (i / 4) + 4 (q % 2) + i % 4 of
+// tile q / 2.
+__device__ __forceinline__ int a_row(int i, int q) { return 8 * (i >> 2) + 4 * (q & 1) + (i & 3); }
+// Row of a 32-row tile kept at position `pos` of its quarter in LDS (an involution): 16 lanes of
+// such a read take four runs of 64 bytes, which the swap puts at four different 64-byte
+// offsets of 256.
+__device__ __forceinline__ int swizzled_row(int pos) { return pos ^ (((pos >> 4) & 1) << 2); }
 
 }  // namespace block
 }  // namespace moe

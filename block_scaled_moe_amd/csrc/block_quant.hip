@@ -35,13 +35,18 @@ __device__ __forceinline__ void widen(uint32_t w, float &lo, float &hi) {
     hi = __uint_as_float(w & 0xffff0000u);
 }
 
-// ---- rows: 16 lanes per block, 8 values each
+// ---- rows: 16 lanes per block, 8 values each. A workgroup takes four blocks of four rows at a
+// time: a wave reads 1 KiB of one row, and each block's plane of codes gets 512 bytes in a row.
 __global__ void __launch_bounds__(kThreads) rows_kernel(const BlockQuantArgs a) {
     const int32_t rows = a.offsets ? a.offsets[a.n] : a.rows;
     const int32_t kb = a.C / 128;
-    const int64_t n = (int64_t)rows * kb;  // blocks
-    const int sub = threadIdx.x & 15;
-    for (int64_t b = (int64_t)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4); b < n; b += (int64_t)gridDim.x * (kThreads / 16)) {
+    const int sub = threadIdx.x & 15, quads = (kb + 3) / 4;
+    const int64_t n = (int64_t)((rows + 3) / 4) * quads;
+    for (int64_t w = blockIdx.x; w < n; w += gridDim.x) {
+        const int64_t row = w / quads * 4 + (threadIdx.x >> 6);
+        const int blk = (int)(w % quads) * 4 + ((threadIdx.x >> 4) & 3);
+        if (row >= rows || blk >= kb) continue;
+        const int64_t b = row * kb + blk;
         const uint4 u = reinterpret_cast<const uint4 *>(a.x)[b * 16 + sub];
         float x[8];
         widen(u.x, x[0], x[1]);
@@ -57,7 +62,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const BlockQuantArgs a) 
         uint2 c;
         c.x = codes4(d.quotient(x[0]), d.quotient(x[1]), d.quotient(x[2]), d.quotient(x[3]));
         c.y = codes4(d.quotient(x[4]), d.quotient(x[5]), d.quotient(x[6]), d.quotient(x[7]));
-        reinterpret_cast<uint2 *>(a.codes)[b * 16 + sub] = c;
+        reinterpret_cast<uint2 *>(a.codes)[((int64_t)blk * a.rows + row) * 16 + sub] = c;
         if (sub == 0) a.scales[b] = d.s;
     }
 }
@@ -131,7 +136,7 @@ __global__ void __launch_bounds__(kThreads) columns_kernel(const BlockQuantArgs 
                 const int row = 16 * h + r;
                 if (row < left) {
                     const int64_t p = r0 + row;
-                    *reinterpret_cast<uint32_t *>(a.codes + p * a.C + ct * 128 + 4 * q) =
+                    *reinterpret_cast<uint32_t *>(a.codes + ((int64_t)ct * a.rows + p) * 128 + 4 * q) =
                         codes4(d.quotient(x[0]), d.quotient(x[1]), d.quotient(x[2]), d.quotient(x[3]));
                     if (q == 0) a.scales[p * kb + ct] = d.s;
                 }
@@ -222,8 +227,7 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const uint16_t *__res
 }  // namespace
 
 hipError_t launch_block_quant_rows(const BlockQuantArgs &a, hipStream_t s) {
-    const int64_t blocks = (int64_t)a.rows * (a.C / 128);
-    const int64_t want = (blocks + kThreads / 16 - 1) / (kThreads / 16);
+    const int64_t want = (int64_t)((a.rows + 3) / 4) * ((a.C / 128 + 3) / 4);
     hipLaunchKernelGGL(rows_kernel, dim3((unsigned)(want < 16384 ? want : 16384)), dim3(kThreads), 0, s, a);
     return hipGetLastError();
 }

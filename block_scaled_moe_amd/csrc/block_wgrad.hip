@@ -17,18 +17,21 @@ namespace {
 
 using namespace block;
 
-constexpr int kThreads = 256, kBN = 128, kBK = 256;
+constexpr int kThreads = 256, kBN = 128, kBK = 128;
 
-__global__ void __launch_bounds__(kThreads, 2) wgrad_kernel(const BlockWgradArgs p) {
+__global__ void __launch_bounds__(kThreads, 4) wgrad_kernel(const BlockWgradArgs p) {
     __shared__ __attribute__((aligned(16))) uint8_t gl[kBN * 128];
     __shared__ __attribute__((aligned(16))) uint8_t xl[kBK * 128];
     __shared__ __attribute__((aligned(16))) float sg[kBN], sx[kBK];
 
-    const int t = threadIdx.x, lane = t & 63, wn = uniform(t >> 6);
+    const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6), wm = wave >> 1, wn = wave & 1;
     const int i16 = lane & 15, g = lane >> 4;
     const int N = p.N, K = p.K;
-    const int nbn = N / kBN, nbk = (K + kBK - 1) / kBK;
-    const int w = blockIdx.x;
+    const int nbn = N / kBN, nbk = K / kBK;
+    // each XCD takes a contiguous range of items, expert by expert
+    const int items = p.n * nbn * nbk, per_xcd = (items + 7) / 8;
+    const int w = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+    if (w >= items) return;
     const int e = w / (nbn * nbk), r = w % (nbn * nbk);
     const int n0 = r / nbk * kBN, k0 = r % nbk * kBK;
 
@@ -39,34 +42,31 @@ __global__ void __launch_bounds__(kThreads, 2) wgrad_kernel(const BlockWgradArgs
     }
     const int runs = (cnt + 127) / 128;
     const int64_t run0 = p.offsets ? first / 128 + e : 0;
-    const bool half = k0 + 128 >= K;  // half a block of k: its first half again, unused
 
-    // the wave copies 32 columns of n and 64 of k, wave 0 the scales
-    const uint8_t *gs = uniform(p.g_codes + run0 * N * 128 + (int64_t)(n0 / 32 + wn) * 4096);
-    const uint8_t *xs = uniform(p.x_codes + run0 * K * 128 + (int64_t)(k0 / 32 + 2 * (half ? wn & 1 : wn)) * 4096);
-    const uint32_t x_even = (lane >> 5) * 512 + swizzled_row(lane & 31, 0) * 16;
-    const uint32_t x_odd = 4096 + (lane >> 5) * 512 + swizzled_row(lane & 31, 1) * 16;
+    // a wave copies 32 columns of n and of k, wave 0 the scales
+    const uint8_t *gs = uniform(p.g_codes + run0 * N * 128 + (int64_t)(n0 / 32 + wave) * 4096);
+    const uint8_t *xs = uniform(p.x_codes + run0 * K * 128 + (int64_t)(k0 / 32 + wave) * 4096);
+    const uint32_t x_lane = (lane >> 5) * 512 + swizzled_row(lane & 31) * 16;
     const uint8_t *gf = uniform(reinterpret_cast<const uint8_t *>(p.g_scales + run0 * N + n0));
     const uint8_t *xf32 = uniform(reinterpret_cast<const uint8_t *>(p.x_scales + run0 * K + k0));
-    const uint32_t g_lds = lds_address(gl) + wn * 4096, x_lds = lds_address(xl) + wn * 8192;
+    const uint32_t g_lds = lds_address(gl) + wave * 4096, x_lds = lds_address(xl) + wave * 4096;
     const uint32_t sg_lds = lds_address(sg), sx_lds = lds_address(sx);
     auto copy = [&](int s) __attribute__((always_inline)) {
         const uint8_t *gsrc = gs + (int64_t)s * N * 128, *xsrc = xs + (int64_t)s * K * 128;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             copy_to_lds(gsrc + j * 1024, lane * 16, g_lds + j * 1024);
-            copy_to_lds(xsrc + j * 1024, x_even, x_lds + j * 1024);
-            copy_to_lds(xsrc + j * 1024, x_odd, x_lds + 4096 + j * 1024);
+            copy_to_lds(xsrc + j * 1024, x_lane, x_lds + j * 1024);
         }
-        if (wn == 0) {
-            copy_to_lds(xf32 + (int64_t)s * K * 4, (half ? lane & 31 : lane) * 16, sx_lds);
-            if (lane < 32) copy_to_lds(gf + (int64_t)s * N * 4, lane * 16, sg_lds);
+        if (wave == 0 && lane < 32) {
+            copy_to_lds(xf32 + (int64_t)s * K * 4, lane * 16, sx_lds);
+            copy_to_lds(gf + (int64_t)s * N * 4, lane * 16, sg_lds);
         }
     };
 
-    f4 acc[8][4];
+    f4 acc[4][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int s = 0; s < 4; ++s) acc[i][s] = (f4){0.0f, 0.0f, 0.0f, 0.0f};
 
@@ -76,21 +76,20 @@ __global__ void __launch_bounds__(kThreads, 2) wgrad_kernel(const BlockWgradArgs
         copy(s);
         wait_copies<0>();
         lds_barrier();
-        // n = n0 + 16 i + i16, k = k0 + 64 wn + 16 g + 4 q + v
+        // n = n0 + 64 wm + 16 i + i16, k = k0 + 64 wn + 32 (q / 2) + 8 g + 4 (q % 2) + v
         v8i xf[4];
         f4 fx[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const int rt = 2 * wn + (i16 >> 3), row = 16 * ((i16 >> 2) & 1) + 4 * q + (i16 & 3);
-            const uint8_t *a = xl + rt * 4096 + g * 512 + swizzled_row(row, rt) * 16;
+            const uint8_t *a = xl + (2 * wn + (q >> 1)) * 4096 + g * 512 + swizzled_row(a_row(i16, q)) * 16;
             xf[q] = operand(*reinterpret_cast<const u32x4 *>(a), *reinterpret_cast<const u32x4 *>(a + 2048));
-            fx[q] = *reinterpret_cast<const f4 *>(sx + 64 * wn + 16 * g + 4 * q);
+            fx[q] = *reinterpret_cast<const f4 *>(sx + 64 * wn + 32 * (q >> 1) + 8 * g + 4 * (q & 1));
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint8_t *b = gl + (i >> 1) * 4096 + g * 512 + (16 * (i & 1) + i16) * 16;
+        for (int i = 0; i < 4; ++i) {
+            const uint8_t *b = gl + (2 * wm + (i >> 1)) * 4096 + g * 512 + (16 * (i & 1) + i16) * 16;
             const v8i gv = operand(*reinterpret_cast<const u32x4 *>(b), *reinterpret_cast<const u32x4 *>(b + 2048));
-            const float fg = sg[16 * i + i16];
+            const float fg = sg[64 * wm + 16 * i + i16];
             f4 d[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) d[q] = block_dot(xf[q], gv);
@@ -102,16 +101,16 @@ __global__ void __launch_bounds__(kThreads, 2) wgrad_kernel(const BlockWgradArgs
         }
     }
 
-    if (k0 + 64 * wn < K) {
+    {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint16_t *o = p.dw + ((int64_t)e * N + n0 + 16 * i + i16) * K + k0 + 64 * wn + 16 * g;
+        for (int i = 0; i < 4; ++i) {
+            uint16_t *o = p.dw + ((int64_t)e * N + n0 + 64 * wm + 16 * i + i16) * K + k0 + 64 * wn + 8 * g;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const u32x4 v = {bf16_pair(acc[i][2 * h][0], acc[i][2 * h][1]), bf16_pair(acc[i][2 * h][2], acc[i][2 * h][3]),
                                  bf16_pair(acc[i][2 * h + 1][0], acc[i][2 * h + 1][1]),
                                  bf16_pair(acc[i][2 * h + 1][2], acc[i][2 * h + 1][3])};
-                *reinterpret_cast<u32x4 *>(o + 8 * h) = v;
+                *reinterpret_cast<u32x4 *>(o + 32 * h) = v;
             }
         }
     }
@@ -120,9 +119,9 @@ __global__ void __launch_bounds__(kThreads, 2) wgrad_kernel(const BlockWgradArgs
 }  // namespace
 
 hipError_t launch_block_wgrad(const BlockWgradArgs &a, hipStream_t s) {
-    const int64_t items = (int64_t)a.n * (a.N / kBN) * ((a.K + kBK - 1) / kBK);
-    if (items > INT32_MAX) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(wgrad_kernel, dim3((unsigned)items), dim3(kThreads), 0, s, a);
+    const int64_t items = (int64_t)a.n * (a.N / kBN) * (a.K / kBK);
+    if (items > INT32_MAX - 8) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(wgrad_kernel, dim3((unsigned)((items + 7) / 8 * 8)), dim3(kThreads), 0, s, a);
     return hipGetLastError();
 }
 

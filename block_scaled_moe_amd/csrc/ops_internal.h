@@ -17,6 +17,9 @@ struct GroupsPlan {
 };
 GroupsPlan groups_plan(int32_t T, int32_t top_k, int32_t n);
 
+// Rows of a rows form: a row's place in its block's plane is a 32-bit byte offset.
+constexpr int32_t kMaxBlockRows = 1 << 25;
+
 // What a grouped product's workgroups read to find their rows. offsets == NULL: one group of
 // `rows` rows, tiles computed from it.
 struct GroupView {
@@ -55,6 +58,7 @@ hipError_t launch_block_quant_weights(const uint16_t *w, int32_t E, int32_t N, i
 struct BlockGemmArgs {
     GroupView v;
     int32_t by_token;
+    int32_t x_rows;  // rows of the rows form x
     int32_t R, C;  // reduction length and output columns: K, N (transposed: N, K)
     const uint8_t *x_codes;
     const float *x_scales;

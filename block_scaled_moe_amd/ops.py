@@ -226,7 +226,7 @@ def combine_backward(g: Groups, d_out: torch.Tensor, y: torch.Tensor, w: torch.T
 
 @dataclasses.dataclass
 class BlockRows:
-    """Rows in E4M3 with an fp32 scale per 1 x 128 block: codes uint8 [rows, C], scales [rows, C / 128]."""
+    """Rows in E4M3 with an fp32 scale per 1 x 128 block: codes uint8 [C / 128, rows, 128], scales [rows, C / 128]."""
     codes: torch.Tensor
     scales: torch.Tensor
 
@@ -314,7 +314,7 @@ def _quantize(x: torch.Tensor, g: Groups | None, by_token: bool, rows: bool, col
         a.g = ctypes.pointer(g.struct)
     r = c = None
     if rows:
-        r = BlockRows(torch.empty((R, C), dtype=torch.uint8, device=dev),
+        r = BlockRows(torch.empty((C // 128, R, 128), dtype=torch.uint8, device=dev),
                       torch.empty((R, C // 128), dtype=torch.float32, device=dev))
         a.codes, a.scales = r.codes.data_ptr(), r.scales.data_ptr()
     if columns:
@@ -345,9 +345,11 @@ def quantize_block_both(x: torch.Tensor, g: Groups | None = None) -> tuple[Block
 
 def _product(x: BlockRows, w: BlockWeights, g: Groups | None, by_token: bool, transposed: bool, out):
     dev = x.codes.device if g is None else g.device
+    if x.codes.dim() != 3:
+        raise ValueError(f"x codes: shape {tuple(x.codes.shape)}, expected [blocks, rows, 128]")
     R, C = (w.N, w.K) if transposed else (w.K, w.N)
-    n_x = x.codes.shape[0] if g is None else g.T if by_token else g.rows
-    _ask("x codes", x.codes, (n_x, R), torch.uint8, dev)
+    n_x = x.codes.shape[1] if g is None else g.T if by_token else g.rows
+    _ask("x codes", x.codes, (R // 128, n_x, 128), torch.uint8, dev)
     _ask("x scales", x.scales, (n_x, R // 128), torch.float32, dev)
     if w.E != (1 if g is None else g.n):
         raise ValueError(f"w: {w.E} experts, expected {1 if g is None else g.n}")

@@ -167,13 +167,19 @@ def hard_values(rng, shape):
     return ref.bf16(x)
 
 
+def rows_codes(q):
+    """Codes [C/128, R, 128] -> [R, C]."""
+    c = host(q.codes)
+    return c.transpose(1, 0, 2).reshape(c.shape[1], -1)
+
+
 @pytest.mark.parametrize("R,C", [(1, 128), (3, 384), (129, 256), (300, 4096), (17, 1152)])
 def test_quantise_rows(R, C):
     x = hard_values(np.random.default_rng(R), (R, C))
     q = moe.quantize_block(dev(x, torch.bfloat16))
     c, s = ref.rows(x)
     assert np.array_equal(host(q.scales).view(np.uint32), s.view(np.uint32))
-    assert np.array_equal(host(q.codes), c)
+    assert np.array_equal(rows_codes(q), c)
 
 
 @pytest.mark.parametrize("E,N,K", [(1, 128, 128), (3, 256, 384), (2, 640, 128)])
@@ -219,7 +225,7 @@ def test_quantise_columns(counts, C):
             assert np.array_equal(qc[b], c), b
     if T:
         c, s = ref.rows(sorted_x)
-        assert np.array_equal(host(rows.codes), c) and np.array_equal(host(rows.scales), s)
+        assert np.array_equal(rows_codes(rows), c) and np.array_equal(host(rows.scales), s)
 
 
 def test_quantise_leaves_rows_behind_the_last_one():
@@ -228,14 +234,14 @@ def test_quantise_leaves_rows_behind_the_last_one():
     g = moe.sort_tokens(dev(idx), 16, 0, 2)
     x = torch.full((6, 256), float("nan"), dtype=torch.bfloat16, device="cuda")
     x[:2] = 1.5
-    codes = torch.full((6, 256), 9, dtype=torch.uint8, device="cuda")
+    codes = torch.full((2, 6, 128), 9, dtype=torch.uint8, device="cuda")
     scales = torch.full((6, 2), 9.0, device="cuda")
     import ctypes
     from block_scaled_moe_amd import ops
     a = ops.MoeBlockQuantizeArgs(rows=6, C=256, g=ctypes.pointer(g.struct), x=x.data_ptr(), codes=codes.data_ptr(),
                                  scales=scales.data_ptr())
     ops._call("moe_block_quantize", x.device, ctypes.byref(a))
-    assert (host(codes)[:2] == 0x7E).all() and (host(codes)[2:] == 9).all() and (host(scales)[2:] == 9).all()
+    assert (host(codes)[:, :2] == 0x7E).all() and (host(codes)[:, 2:] == 9).all() and (host(scales)[2:] == 9).all()
 
 
 # ---------------------------------------------------------------- products

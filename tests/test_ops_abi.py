@@ -92,6 +92,7 @@ def test_block_calls_refuse():
     assert quant(64, 128, 0, g, A, A, A, 0, 0) == EINVAL            # not T * top_k rows
     assert quant(4, 128, 0, None, A + 2, A, A, 0, 0) == EALIGN
     assert quant(0, 128, 0, None, 0, A, A, 0, 0) == OK
+    assert quant(1 << 25, 128, 0, None, A, A, A, 0, 0) == EUNSUP     # 32-bit places in a block's plane
     W = ops.MoeBlockWeights
     gemm = lambda *a: lib.moe_block_gemm(ctypes.byref(ops.MoeBlockGemmArgs(*a)), None)
     assert gemm(4, 0, 0, None, A, A, W(1, 192, 128, A, A), A) == EUNSUP
@@ -102,6 +103,7 @@ def test_block_calls_refuse():
     assert gemm(4, 0, 0, None, A, 0, W(1, 128, 128, A, A), A) == EINVAL
     assert gemm(4, 0, 0, None, A, A, W(1, 128, 128, A, 0), A) == EINVAL
     assert gemm(4, 0, 0, None, A, A, W(1, 128, 128, A + 8, A), A) == EALIGN
+    assert gemm(1 << 25, 0, 0, None, A, A, W(1, 128, 128, A, A), A) == EUNSUP
     assert gemm(0, 0, 0, None, 0, 0, W(1, 128, 128, A, A), 0) == OK
     wgrad = lambda *a: lib.moe_block_wgrad(ctypes.byref(ops.MoeBlockWgradArgs(*a)), None)
     assert wgrad(4, 128, 100, None, A, A, A, A, A) == EUNSUP
@@ -138,7 +140,7 @@ def test_binding_checks_its_tensors():
     with pytest.raises(ValueError):
         moe.BlockWeights.empty(1, 130, 128, device="cpu")
     w = moe.BlockWeights.empty(2, 128, 256, device="cpu")
-    q = moe.BlockRows(torch.zeros((8, 256), dtype=torch.uint8), torch.zeros((8, 2)))
+    q = moe.BlockRows(torch.zeros((2, 8, 128), dtype=torch.uint8), torch.zeros((8, 2)))
     with pytest.raises(ValueError):
         moe.block_product(q, w)                      # two experts without groups
     with pytest.raises(ValueError):
