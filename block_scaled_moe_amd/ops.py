@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 
 import torch
 
@@ -71,23 +72,38 @@ SIGNATURES = {
 }
 
 
+_FN: dict = {}  # the library's functions by name, once loaded
+
+
+def _function(name: str):
+    fn = _FN.get(name)
+    if fn is None:
+        from . import lib
+        fn = _FN[name] = getattr(lib(), name)
+    return fn
+
+
 def _call(name: str, device: torch.device, *args):
     """The library's entry point `name` on the current stream of `device`, made current for the call."""
-    from . import _check, lib
-    fn = getattr(lib(), name)
-    if device.type != "cuda" or device.index == torch.cuda.current_device():
-        stream = torch.cuda.current_stream(device).cuda_stream if device.type == "cuda" else None
-        _check(fn(*args, stream), name)
-        return
-    with torch.cuda.device(device):
-        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream), name)
+    fn = _FN.get(name) or _function(name)
+    i = device.index
+    if i is None:
+        raise ValueError(f"{name}: tensors on {device}, expected a GPU")
+    if i == torch._C._cuda_getDevice():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        with torch.cuda.device(i):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    if rc:
+        from . import MoeError
+        raise MoeError(name, rc)
 
 
 def _ask(what: str, t: torch.Tensor, shape: tuple, dtype, device: torch.device):
-    """t has this shape, dtype (one or a tuple of them) and device, and is contiguous."""
-    if tuple(t.shape) != tuple(shape):
+    """t has this shape, dtype (one or a collection of them) and device, and is contiguous."""
+    if t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype not in (dtype if isinstance(dtype, (tuple, dict)) else (dtype,)):
+    if t.dtype is not dtype and (isinstance(dtype, torch.dtype) or t.dtype not in dtype):
         raise ValueError(f"{what}: dtype {t.dtype}")
     if t.device != device:
         raise ValueError(f"{what}: on {t.device}, expected {device}")
@@ -102,53 +118,58 @@ def _out(what: str, out: torch.Tensor | None, shape: tuple, dtype, device: torch
 
 # ------------------------------------------------------------------ tokens by expert
 
-@dataclasses.dataclass
 class Groups:
-    """The token-slots of a batch sorted by expert (moe_groups; filled by sort_tokens)."""
-    T: int
-    top_k: int
-    E: int
-    e_begin: int
-    e_end: int
-    offsets: torch.Tensor      # int32 [n + 1] first sorted row of each local expert; [n] = local slots
-    sorted_slot: torch.Tensor  # int32 [T * top_k] slot of each sorted row, -1 behind the local ones
-    slot_pos: torch.Tensor     # int32 [T, top_k] sorted row of each slot, -1 if not local
-    plan: torch.Tensor         # work lists of the grouped products
-    struct: MoeGroups
+    """The token-slots of a batch sorted by expert (moe_groups; filled by sort_tokens). Its arrays share one
+    allocation; offsets, sorted_slot and slot_pos are views of it."""
 
-    @property
-    def rows(self) -> int:
-        return self.T * self.top_k
-
-    @property
-    def n(self) -> int:
-        return self.e_end - self.e_begin
-
-    @property
-    def device(self) -> torch.device:
-        return self.offsets.device
+    def __init__(self, T: int, top_k: int, E: int, e_begin: int = 0, e_end: int | None = None, device="cuda"):
+        e_end = E if e_end is None else e_end
+        self.T, self.top_k, self.E, self.e_begin, self.e_end = T, top_k, E, e_begin, e_end
+        self.n, self.rows = e_end - e_begin, T * top_k
+        self._at = _groups_layout(T, top_k, E, e_begin, e_end)
+        slots, pos, plan, end = self._at
+        self.buffer = torch.empty(end, dtype=torch.uint8, device=device)
+        self.device = self.buffer.device
+        base = self.buffer.data_ptr()
+        self.struct = MoeGroups(T, top_k, E, e_begin, e_end, base, base + slots, base + pos, base + plan, end - plan)
+        self.ref, self.pointer = ctypes.byref(self.struct), ctypes.pointer(self.struct)
 
     @staticmethod
     def empty(T: int, top_k: int, E: int, e_begin: int = 0, e_end: int | None = None, device="cuda") -> "Groups":
-        from . import MoeError, lib
-        e_end = E if e_end is None else e_end
-        st = MoeGroups(T, top_k, E, e_begin, e_end)
-        n_plan = int(lib().moe_groups_plan_bytes(ctypes.byref(st)))
-        if n_plan == 0:
-            raise MoeError("moe_groups_plan_bytes", -1)
-        # one allocation, each array at a multiple of 256 bytes
-        up = lambda b: (b + 255) // 256 * 256
-        n = e_end - e_begin
-        sizes = [up(4 * (n + 1)), up(4 * T * top_k), up(4 * T * top_k), n_plan]
-        buf = torch.empty(sum(sizes), dtype=torch.uint8, device=device)
-        at = [0, sizes[0], sizes[0] + sizes[1], sizes[0] + 2 * sizes[1]]
-        i32 = buf.view(torch.int32)
-        part = lambda i, count: i32.narrow(0, at[i] // 4, count)
-        base = buf.data_ptr()
-        st.offsets, st.sorted_slot, st.slot_pos, st.plan = (base + a for a in at)
-        st.plan_bytes = n_plan
-        return Groups(T, top_k, E, e_begin, e_end, part(0, n + 1), part(1, T * top_k),
-                      part(2, T * top_k).view(T, top_k), buf.narrow(0, at[3], n_plan), st)
+        return Groups(T, top_k, E, e_begin, e_end, device)
+
+    def _view(self, at: int, count: int) -> torch.Tensor:
+        return self.buffer.view(torch.int32).narrow(0, at // 4, count)
+
+    @functools.cached_property
+    def offsets(self) -> torch.Tensor:
+        """int32 [n + 1]: first sorted row of each local expert; [n] = local slots."""
+        return self._view(0, self.n + 1)
+
+    @functools.cached_property
+    def sorted_slot(self) -> torch.Tensor:
+        """int32 [T * top_k]: slot of each sorted row, -1 behind the local ones."""
+        return self._view(self._at[0], self.rows)
+
+    @functools.cached_property
+    def slot_pos(self) -> torch.Tensor:
+        """int32 [T, top_k]: sorted row of each slot, -1 if not local."""
+        return self._view(self._at[1], self.rows).view(self.T, self.top_k)
+
+
+@functools.lru_cache(maxsize=256)
+def _groups_layout(T: int, top_k: int, E: int, e_begin: int, e_end: int) -> tuple[int, int, int, int]:
+    """Byte offsets of sorted_slot, slot_pos and the plan behind offsets, and the total, each a multiple of 256."""
+    from . import MoeError
+    st = MoeGroups(T, top_k, E, e_begin, e_end)
+    n_plan = int(_function("moe_groups_plan_bytes")(ctypes.byref(st)))
+    if n_plan == 0:
+        raise MoeError("moe_groups_plan_bytes", -1)
+    up = lambda b: (b + 255) // 256 * 256
+    slots = up(4 * (e_end - e_begin + 1))
+    pos = slots + up(4 * T * top_k)
+    plan = pos + up(4 * T * top_k)
+    return slots, pos, plan, plan + n_plan
 
 
 def sort_tokens(topk_idx: torch.Tensor, E: int, e_begin: int = 0, e_end: int | None = None,
@@ -164,7 +185,7 @@ def sort_tokens(topk_idx: torch.Tensor, E: int, e_begin: int = 0, e_end: int | N
         out = Groups.empty(T, k, E, e_begin, e_end, device=topk_idx.device)
     elif (out.T, out.top_k, out.E, out.e_begin, out.e_end, out.device) != (T, k, E, e_begin, e_end, topk_idx.device):
         raise ValueError("out: groups of other sizes or on another device")
-    _call("moe_sort", out.device, ctypes.byref(out.struct), topk_idx.data_ptr())
+    _call("moe_sort", out.device, out.ref, topk_idx.data_ptr())
     return out
 
 
@@ -179,7 +200,7 @@ def gather(g: Groups, x: torch.Tensor, out: torch.Tensor | None = None) -> torch
     D = _row_width("x", x)
     _ask("x", x, (g.T, D), DTYPES, g.device)
     out = _out("out", out, (g.rows, D), x.dtype, g.device)
-    _call("moe_gather", g.device, ctypes.byref(g.struct), DTYPES[x.dtype], D, x.data_ptr(), out.data_ptr())
+    _call("moe_gather", g.device, g.ref, DTYPES[x.dtype], D, x.data_ptr(), out.data_ptr())
     return out
 
 
@@ -188,7 +209,7 @@ def gather_backward(g: Groups, d_rows: torch.Tensor, out: torch.Tensor | None = 
     D = _row_width("d_rows", d_rows)
     _ask("d_rows", d_rows, (g.rows, D), DTYPES, g.device)
     out = _out("out", out, (g.T, D), d_rows.dtype, g.device)
-    _call("moe_gather_backward", g.device, ctypes.byref(g.struct), DTYPES[d_rows.dtype], D, d_rows.data_ptr(),
+    _call("moe_gather_backward", g.device, g.ref, DTYPES[d_rows.dtype], D, d_rows.data_ptr(),
           out.data_ptr())
     return out
 
@@ -203,7 +224,7 @@ def combine(g: Groups, y: torch.Tensor, w: torch.Tensor, out: torch.Tensor | Non
     if out is None and out_dtype not in DTYPES:
         raise ValueError(f"out_dtype: {out_dtype}")
     out = _out("out", out, (g.T, D), out_dtype if out is None else DTYPES, g.device)
-    _call("moe_combine", g.device, ctypes.byref(g.struct), DTYPES[y.dtype], DTYPES[out.dtype], D, y.data_ptr(),
+    _call("moe_combine", g.device, g.ref, DTYPES[y.dtype], DTYPES[out.dtype], D, y.data_ptr(),
           w.data_ptr(), out.data_ptr())
     return out
 
@@ -217,7 +238,7 @@ def combine_backward(g: Groups, d_out: torch.Tensor, y: torch.Tensor, w: torch.T
     _ask("d_out", d_out, (g.T, D), DTYPES, g.device)
     dy = _out("dy", dy, (g.rows, D), y.dtype, g.device)
     dw = _out("dw", dw, (g.T, g.top_k), torch.float32, g.device)
-    _call("moe_combine_backward", g.device, ctypes.byref(g.struct), DTYPES[y.dtype], DTYPES[d_out.dtype], D,
+    _call("moe_combine_backward", g.device, g.ref, DTYPES[y.dtype], DTYPES[d_out.dtype], D,
           d_out.data_ptr(), y.data_ptr(), w.data_ptr(), dy.data_ptr(), dw.data_ptr())
     return dy, dw
 
@@ -309,20 +330,19 @@ def _quantize(x: torch.Tensor, g: Groups | None, by_token: bool, rows: bool, col
     dev = x.device if g is None else g.device
     R = x.shape[0] if g is None else g.T if by_token else g.rows
     _ask("x", x, (R, C), torch.bfloat16, dev)
-    a = MoeBlockQuantizeArgs(rows=R, C=C, by_token=int(by_token), x=x.data_ptr())
-    if g is not None:
-        a.g = ctypes.pointer(g.struct)
     r = c = None
+    rc = rs = cc = cs = None
     if rows:
         r = BlockRows(torch.empty((C // 128, R, 128), dtype=torch.uint8, device=dev),
                       torch.empty((R, C // 128), dtype=torch.float32, device=dev))
-        a.codes, a.scales = r.codes.data_ptr(), r.scales.data_ptr()
+        rc, rs = r.codes.data_ptr(), r.scales.data_ptr()
     if columns:
         n = (R if g is None else g.rows) // 128 + (1 if g is None else g.n)  # moe_block_column_blocks
         c = BlockColumns(torch.empty((n, C // 32, 2, 4, 32, 16), dtype=torch.uint8, device=dev),
                          torch.empty((n, C), dtype=torch.float32, device=dev))
-        a.col_codes, a.col_scales = c.codes.data_ptr(), c.scales.data_ptr()
+        cc, cs = c.codes.data_ptr(), c.scales.data_ptr()
     if R > 0:
+        a = MoeBlockQuantizeArgs(R, C, by_token, None if g is None else g.pointer, x.data_ptr(), rc, rs, cc, cs)
         _call("moe_block_quantize", dev, ctypes.byref(a))
     return r, c
 
@@ -356,10 +376,8 @@ def _product(x: BlockRows, w: BlockWeights, g: Groups | None, by_token: bool, tr
     if g is None and by_token:
         raise ValueError("by_token needs groups")
     out = _out("out", out, (n_x if g is None else g.rows, C), torch.bfloat16, dev)
-    a = MoeBlockGemmArgs(rows=n_x, by_token=int(by_token), transposed=int(transposed), x_codes=x.codes.data_ptr(),
-                         x_scales=x.scales.data_ptr(), w=w.struct(dev), out=out.data_ptr())
-    if g is not None:
-        a.g = ctypes.pointer(g.struct)
+    a = MoeBlockGemmArgs(n_x, by_token, transposed, None if g is None else g.pointer, x.codes.data_ptr(),
+                         x.scales.data_ptr(), w.struct(dev), out.data_ptr())
     if n_x > 0:
         _call("moe_block_gemm", dev, ctypes.byref(a))
     return out
@@ -394,9 +412,7 @@ def block_weight_grad(dy: BlockColumns, x: BlockColumns, g: Groups | None = None
         _ask(what + " codes", q.codes, (blocks, C // 32, 2, 4, 32, 16), torch.uint8, dev)
         _ask(what + " scales", q.scales, (blocks, C), torch.float32, dev)
     out = _out("out", out, (n, N, K), torch.bfloat16, dev)
-    a = MoeBlockWgradArgs(rows=R, N=N, K=K, g_codes=dy.codes.data_ptr(), g_scales=dy.scales.data_ptr(),
-                          x_codes=x.codes.data_ptr(), x_scales=x.scales.data_ptr(), dw=out.data_ptr())
-    if g is not None:
-        a.g = ctypes.pointer(g.struct)
+    a = MoeBlockWgradArgs(R, N, K, None if g is None else g.pointer, dy.codes.data_ptr(), dy.scales.data_ptr(),
+                          x.codes.data_ptr(), x.scales.data_ptr(), out.data_ptr())
     _call("moe_block_wgrad", dev, ctypes.byref(a))
     return out

@@ -120,7 +120,7 @@ def test_block_calls_refuse():
 def test_binding_checks_its_tensors():
     g = moe.Groups.empty(4, 2, 8, 2, 6, device="cpu")
     x = torch.zeros((4, 128))
-    for bad in (x[:3], x.half(), x.t(), x[0]):
+    for bad in (x[:3], x.half(), x.t(), x[0], x):  # the last: not on a GPU
         with pytest.raises(ValueError):
             moe.gather(g, bad)
     with pytest.raises(ValueError):
