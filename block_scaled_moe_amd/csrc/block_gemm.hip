@@ -48,9 +48,9 @@ __device__ __forceinline__ bool work_item(const GroupView &v, int n_tiles, int w
     const int tq = w / nb;
     int t0 = 0, te = n_tiles;
     if (v.offsets) {
-        const int e = v.tile_expert[tq], o = v.offsets[e];
-        t0 = tq - (v.tile_row0[tq] - o) / kBM;
-        te = (v.offsets[e + 1] - o + kBM - 1) / kBM;
+        const int e = scalar_load(v.tile_expert + tq), o = scalar_load(v.offsets + e);
+        t0 = tq - (scalar_load(v.tile_row0 + tq) - o) / kBM;
+        te = (scalar_load(v.offsets + e + 1) - o + kBM - 1) / kBM;
     }
     const int local = w - nb * t0, g = local / (4 * nb), r = local % (4 * nb);
     const int gs = min(4, te - 4 * g);
@@ -81,9 +81,9 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const BlockGemmArgs p) {
         if (!work_item(p.v, n_tiles, (blockIdx.x & 7) * per_xcd + it, nb, tile, cb)) break;
         int e = 0, p0 = tile * kBM, rows = p.v.rows - p0;
         if (p.v.offsets) {
-            e = uniform(p.v.tile_expert[tile]);
-            p0 = uniform(p.v.tile_row0[tile]);
-            rows = p.v.offsets[e + 1] - p0;
+            e = scalar_load(p.v.tile_expert + tile);
+            p0 = scalar_load(p.v.tile_row0 + tile);
+            rows = scalar_load(p.v.offsets + e + 1) - p0;
         }
         rows = uniform(min(rows, kBM));
         const int n_sub = (rows + 15) / 16;
@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const BlockGemmArgs p) {
             auto add = [&](int i, int b, int q, float f) __attribute__((always_inline)) {
 #pragma unroll
                 for (int v = 0; v < 4; ++v) acc[i][q][v] = fmaf(d[b][q][v], f, acc[i][q][v]);
+                pin(acc[i][q]);
             };
 
             copy_x(0);
@@ -223,6 +224,7 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const BlockGemmArgs p) {
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
                                 d[(MSA - 1 - i) & 1][q] = block_dot(wf[q], xi);
+                                pin(d[(MSA - 1 - i) & 1][q]);
                                 if (i > 0 || kCarry) add(i > 0 ? i - 1 : MSA - 1, (MSA - i) & 1, q, fd);
                                 __builtin_amdgcn_sched_barrier(0);
                             }

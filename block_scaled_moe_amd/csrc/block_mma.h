@@ -29,21 +29,11 @@ __device__ __forceinline__ f4 block_dot(v8i a, v8i b) {
 }
 
 // 16 bytes per lane from global memory straight into LDS at dst + 16 * lane (dst the same for
-// the wave): from src, or from base + offset with the base the same for the wave. Written in
+// the wave) from base + offset, the base the same for the wave. Written in
 // assembly, as it has no register to wait for: behind the builtin the compiler puts a wait for
 // every copy in flight before the next LDS read, which a ring of buffers cannot have. The
 // caller waits (wait_copies) and meets its workgroup (lds_barrier) before the bytes are read.
-__device__ __forceinline__ uint32_t lds_address(const void *p) {
-    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p);
-}
-__device__ __forceinline__ void copy_to_lds(const uint8_t *src, uint32_t dst) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(dst), "v"(src) : "memory", "m0");
-}
-__device__ __forceinline__ void copy_to_lds(const uint8_t *base, uint32_t offset, uint32_t dst) {
-    // five wait states between a vector instruction that wrote base and the copy that reads it
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst), "v"(offset), "s"(base)
-                 : "memory", "m0");
-}
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 // p, the same for every lane of the wave, as a scalar
 template <typename T>
 __device__ __forceinline__ T *uniform(T *p) {
@@ -52,7 +42,21 @@ __device__ __forceinline__ T *uniform(T *p) {
     const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
     return (T *)((uint64_t)hi << 32 | lo);
 }
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+// *p through the scalar cache, the address the same for the wave: a vector load would have to
+// wait for every copy and store in flight before it. For data no kernel writes while this one runs.
+__device__ __forceinline__ int scalar_load(const int *p) {
+    return *(const __attribute__((address_space(4))) int *)(uint64_t)uniform(p);
+}
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+    return (uint32_t)uniform((int)(uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p);
+}
+__device__ __forceinline__ void copy_to_lds(const uint8_t *base, uint32_t offset, uint32_t dst) {
+    // m0 (nothing else here uses it) holds the LDS address; five wait states between a vector
+    // instruction that wrote base and the copy that reads it
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uniform((int)dst)), "v"(offset),
+                 "s"(uniform(base))
+                 : "memory");
+}
 
 // Workgroup barrier that leaves the wave's copies into LDS in flight (__syncthreads waits for
 // them all); LDS reads and writes complete first.
@@ -62,6 +66,10 @@ template <int N>
 __device__ __forceinline__ void wait_copies() {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
+
+// Keeps v's computation above this point: the compiler otherwise sinks a loop's MFMAs behind the
+// barriers and copies that follow them, with all of their operands held in registers.
+__device__ __forceinline__ void pin(const f4 &v) { asm volatile("" ::"v"(v)); }
 
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {  // nearest, ties to even
     return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)b) << 16;
