@@ -75,6 +75,24 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {  // nearest, t
     return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a) | (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)b) << 16;
 }
 
+// Lane l and lane l ^ 1 hold 16 bytes each, a and b, of two rows (l even: the first); after the
+// swap the even lane holds a of both rows and the odd lane b of both: x[0] of the first row, x[1]
+// of the second. Eight lanes then store 128 bytes of one row in one instruction.
+struct RowPair {
+    u32x4 x[2];
+};
+__device__ __forceinline__ RowPair swap_rows(u32x4 a, u32x4 b, bool odd) {
+    RowPair r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t give = odd ? a[j] : b[j];
+        const uint32_t got = __builtin_amdgcn_update_dpp(0, give, 0xB1, 0xF, 0xF, true);  // quad_perm 1, 0, 3, 2
+        r.x[0][j] = odd ? got : a[j];
+        r.x[1][j] = odd ? b[j] : got;
+    }
+    return r;
+}
+
 // The MFMA's A operand is read so that a lane's accumulators of four reads q, over 64 columns in
 // two tiles of 32, are outputs 32 h + 8 g .. 32 h + 8 g + 7 (h = q / 2): 16 bytes of bf16, and
 // the four g of a row 64 bytes in a row. Lane i then takes row 8 (i / 4) + 4 (q % 2) + i % 4 of

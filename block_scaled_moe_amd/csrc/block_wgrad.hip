@@ -9,9 +9,15 @@
 // form and go straight into LDS with their scales (two buffers).
 //
 // An expert has few runs (its rows / 128), so an item is mostly its 128 KiB of output: bound by
-// the writes of dw. One workgroup per CU walks its items, and the first two runs of the next item
-// are copied before the outputs of the last are stored: a wave's vector memory operations
-// complete in order, so the copies can be waited for while the stores drain behind them.
+// the writes of dw, with the copies of a run (64 KiB) and its products behind them. One workgroup
+// per CU walks its items; the runs of all of them make one sequence of steps, and a step's buffer
+// is refilled for the step after next, of this item or of a later one, as soon as every wave is
+// done with it. A wave's vector memory operations complete in order, so a step waits for its own
+// copies by the number of copies and stores issued behind them, and the stores of an item drain
+// under the next steps. (Copying the next item only at the end of the last one left nothing in
+// flight there: 617 us against MEASURED on two runs for each of 96 experts of 4096 x 2560.)
+// A lane swaps half its outputs with its neighbour, so that every store instruction writes whole
+// 128-byte lines, which go past L2 (non-temporal) and leave the operands there.
 #include "block_mma.h"
 #include "ops_internal.h"
 
@@ -20,91 +26,116 @@ namespace {
 
 using namespace block;
 
-constexpr int kThreads = 512, kB = 256, kMaxGrid = 256;
-constexpr int kOperand = kB * 128;
+constexpr int kThreads = 512, kB = 256, kOperand = kB * 128, kMaxGrid = 256;
+constexpr int kCopies = 8;  // of a step by a wave (the two that copy scales: nine)
 #ifndef NT
-#define NT 0
+#define NT 1
 #endif
 #define MOE_WGRAD_STORE(v, p) do { if (NT) __builtin_nontemporal_store(v, p); else *(p) = v; } while (0)
 
 __global__ void __launch_bounds__(kThreads) wgrad_kernel(const BlockWgradArgs p) {
     __shared__ __attribute__((aligned(16))) uint8_t gb[2 * kOperand];
     __shared__ __attribute__((aligned(16))) uint8_t xb[2 * kOperand];
-    __shared__ __attribute__((aligned(16))) float sg[2 * kB], sx[2 * kB];
+    __shared__ __attribute__((aligned(16))) float sgb[2 * kB], sxb[2 * kB];
 
     const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
     const int wm = wave >> 2, wn = wave & 3;
     const int i16 = lane & 15, g = lane >> 4;
     const int N = p.N, K = p.K;
-    const int nbn = (N + kB - 1) / kB, nbk = (K + kB - 1) / kB;
-    const int items = p.n * nbn * nbk, per_xcd = (items + 7) / 8;  // each XCD: a contiguous range
-    const int step = (gridDim.x + 7) / 8;
+    const int nbk = (K + kB - 1) / kB, tiles = (N + kB - 1) / kB * nbk;
+
+    // An expert's tiles are split over `split` XCDs and the experts dealt to the 8 / split sets of
+    // XCDs, so that experts of very different size load them evenly; a part has four tiles or
+    // more, which share operands in the XCD's L2.
+    const int split = tiles >= 32 ? 8 : tiles >= 16 ? 4 : tiles >= 8 ? 2 : 1;
+    const int xcd = blockIdx.x & 7, sets = 8 / split, part = (tiles + split - 1) / split;
+    const int r0 = xcd % split * part, mine = min(part, tiles - r0), e0 = xcd / split;
+    const int end = mine > 0 && e0 < p.n ? (p.n - e0 + sets - 1) / sets * mine : 0;
+    const int step = gridDim.x >> 3;
+
     const uint32_t g_lds = lds_address(gb) + wave * 4096, x_lds = lds_address(xb) + wave * 4096;
-    const uint32_t s_lds = wave == 0 ? lds_address(sx) : lds_address(sg);
+    const uint32_t sx_lds = lds_address(sxb), sg_lds = lds_address(sgb);
     const uint32_t x_lane = (lane >> 5) * 512 + swizzled_row(lane & 31) * 16;
 
     struct Item {
-        int e, n0, k0, runs;
-        bool n_half, k_half;  // only 128 of the 256 columns exist: the first half is copied twice
-        const uint8_t *g, *x, *s;  // this wave's 32 columns of both operands; scales (waves 0, 1)
+        int it, e, n0, k0, runs;
+        int64_t run0;
     };
-    auto item = [&](int w) __attribute__((always_inline)) {
+    auto item = [&](int it) __attribute__((always_inline)) {
         Item a;
-        a.e = w / (nbn * nbk);
-        const int r = w % (nbn * nbk);
+        const int r = r0 + it % mine;
+        a.it = it;
+        a.e = e0 + it / mine * sets;
         a.n0 = r / nbk * kB;
         a.k0 = r % nbk * kB;
-        int first = 0, cnt = p.rows;
+        int o = 0, cnt = p.rows;
         if (p.offsets) {
-            first = scalar_load(p.offsets + a.e);
-            cnt = scalar_load(p.offsets + a.e + 1) - first;
+            o = scalar_load(p.offsets + a.e);
+            cnt = scalar_load(p.offsets + a.e + 1) - o;
         }
         a.runs = (cnt + 127) / 128;
-        const int64_t run0 = p.offsets ? first / 128 + a.e : 0;
-        a.n_half = a.n0 + 128 >= N;
-        a.k_half = a.k0 + 128 >= K;
-        a.g = p.g_codes + run0 * N * 128 + (int64_t)(a.n0 / 32 + (a.n_half ? wave & 3 : wave)) * 4096;
-        a.x = p.x_codes + run0 * K * 128 + (int64_t)(a.k0 / 32 + (a.k_half ? wave & 3 : wave)) * 4096;
-        a.s = reinterpret_cast<const uint8_t *>(wave == 0 ? p.x_scales + run0 * K + a.k0 : p.g_scales + run0 * N + a.n0);
-        a.g = uniform(a.g);
-        a.x = uniform(a.x);
-        a.s = uniform(a.s);
+        a.run0 = p.offsets ? o / 128 + a.e : 0;
         return a;
     };
-    constexpr int kCopies = 8;  // of a run by a wave (nine by the two that copy scales)
-    auto copy = [&](const Item &a, int s) __attribute__((always_inline)) {
-        const uint8_t *gsrc = a.g + (int64_t)s * N * 128, *xsrc = a.x + (int64_t)s * K * 128;
-        const uint32_t b = (s & 1) * kOperand;
+    // Only 128 of a block's 256 columns may exist: they are copied twice then.
+    auto n_half = [&](const Item &a) { return a.n0 + 128 >= N; };
+    auto k_half = [&](const Item &a) { return a.k0 + 128 >= K; };
+    auto copy = [&](const Item &a, int s, int buffer) __attribute__((always_inline)) {
+        const int64_t run = a.run0 + s;
+        const uint32_t b = buffer * kOperand, f = buffer * kB * 4;
+        const uint8_t *x = p.x_codes + run * K * 128 + (int64_t)(a.k0 / 32 + (k_half(a) ? wave & 3 : wave)) * 4096;
+        const uint8_t *n = p.g_codes + run * N * 128 + (int64_t)(a.n0 / 32 + (n_half(a) ? wave & 3 : wave)) * 4096;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            copy_to_lds(gsrc + j * 1024, lane * 16, g_lds + b + j * 1024);
-            copy_to_lds(xsrc + j * 1024, x_lane, x_lds + b + j * 1024);
+            copy_to_lds(x + j * 1024, x_lane, x_lds + b + j * 1024);
+            copy_to_lds(n + j * 1024, lane * 16, g_lds + b + j * 1024);
         }
-        if (wave < 2) {
-            const bool half = wave == 0 ? a.k_half : a.n_half;
-            copy_to_lds(a.s + (int64_t)s * (wave == 0 ? K : N) * 4, (half ? lane & 31 : lane) * 16, s_lds + (s & 1) * kB * 4);
-        }
+        if (wave == 0)
+            copy_to_lds(reinterpret_cast<const uint8_t *>(p.x_scales + run * K + a.k0), (k_half(a) ? lane & 31 : lane) * 16,
+                        sx_lds + f);
+        if (wave == 1)
+            copy_to_lds(reinterpret_cast<const uint8_t *>(p.g_scales + run * N + a.n0), (n_half(a) ? lane & 31 : lane) * 16,
+                        sg_lds + f);
     };
-    // at most `newer` (rounded down to 0, 8, 16, 24) of the wave's operations outstanding
+    // at most `newer` (a multiple of 8; 40 stands for more) of the wave's operations outstanding
     auto wait = [&](int newer) __attribute__((always_inline)) {
-        if (newer >= 24) wait_copies<24>();
+        if (newer >= 40) wait_copies<40>();
+        else if (newer >= 32) wait_copies<32>();
+        else if (newer >= 24) wait_copies<24>();
         else if (newer >= 16) wait_copies<16>();
         else if (newer >= 8) wait_copies<8>();
         else wait_copies<0>();
     };
 
     int it = blockIdx.x >> 3;
-    const int base = (blockIdx.x & 7) * per_xcd, end = min(per_xcd, items - base);
     if (it >= end) return;
-    Item cur = item(base + it);
-    if (cur.runs > 0) copy(cur, 0);
-    if (cur.runs > 1) copy(cur, 1);
-    int stores = 0;  // of the last item by this wave, issued behind the copies of cur's first two runs
+    Item cur = item(it);
+    // the next step to copy: run cs of item c; experts without rows have no steps
+    Item c = cur;
+    int cs = -1;
+    bool left = true;
+    auto advance = [&]() __attribute__((always_inline)) {
+        ++cs;
+        while (left && cs >= c.runs) {
+            left = c.it + step < end;
+            if (left) c = item(c.it + step);
+            cs = 0;
+        }
+    };
+    // operations behind the copies of the next step to compute, and of the one after it
+    int behind0 = 0, behind1 = 0;
+    advance();
+    if (left) {
+        copy(c, cs, 0);
+        advance();
+        if (left) {
+            copy(c, cs, 1);
+            behind0 = kCopies;
+            advance();
+        }
+    }
+    int buffer = 0;
     for (;;) {
-        it += step;
-        const bool more = it < end;
-        const Item next = item(base + (more ? it : end - 1));
-
         f4 acc[8][4];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -113,11 +144,10 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(const BlockWgradArgs p)
 
 #pragma clang loop unroll(disable)
         for (int s = 0; s < cur.runs; ++s) {
-            const int ahead = s + 1 < cur.runs ? kCopies : 0;  // the next run's copies
-            wait(s < 2 ? ahead + stores : ahead);
+            wait(behind0);
             lds_barrier();
-            const uint8_t *xl = xb + (s & 1) * kOperand, *gl = gb + (s & 1) * kOperand;
-            const float *fsx = sx + (s & 1) * kB, *fsg = sg + (s & 1) * kB;
+            const uint8_t *xl = xb + buffer * kOperand, *gl = gb + buffer * kOperand;
+            const float *sx = sxb + buffer * kB, *sg = sgb + buffer * kB + 16 * wm + i16;
             // n = n0 + 16 (2 i + wm) + i16, k = k0 + 64 wn + 32 (q / 2) + 8 g + 4 (q % 2) + v
             v8i xf[4];
             f4 fx[4];
@@ -125,68 +155,80 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(const BlockWgradArgs p)
             for (int q = 0; q < 4; ++q) {
                 const uint8_t *a = xl + (2 * wn + (q >> 1)) * 4096 + g * 512 + swizzled_row(a_row(i16, q)) * 16;
                 xf[q] = operand(*reinterpret_cast<const u32x4 *>(a), *reinterpret_cast<const u32x4 *>(a + 2048));
-                fx[q] = *reinterpret_cast<const f4 *>(fsx + 64 * wn + 32 * (q >> 1) + 8 * g + 4 * (q & 1));
+                fx[q] = *reinterpret_cast<const f4 *>(sx + 64 * wn + 32 * (q >> 1) + 8 * g + 4 * (q & 1));
             }
-            auto g_operand = [&](int i) __attribute__((always_inline)) -> v8i {  // columns 16 (2 i + wm) ..
+            auto g_operand = [&](int i) __attribute__((always_inline)) -> v8i {
                 const uint8_t *b = gl + i * 4096 + g * 512 + (16 * wm + i16) * 16;
                 return operand(*reinterpret_cast<const u32x4 *>(b), *reinterpret_cast<const u32x4 *>(b + 2048));
             };
             // block sums are added to their accumulators two MFMAs later
             f4 d[3];
             float f[8];
-            auto add = [&](int u) __attribute__((always_inline)) {
+            auto add = [&](int m) __attribute__((always_inline)) {
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
-                    acc[u / 4][u % 4][v] = fmaf(d[u % 3][v], fx[u % 4][v] * f[u / 4], acc[u / 4][u % 4][v]);
-                pin(acc[u / 4][u % 4]);
+                    acc[m / 4][m % 4][v] = fmaf(d[m % 3][v], fx[m % 4][v] * f[m / 4], acc[m / 4][m % 4][v]);
+                pin(acc[m / 4][m % 4]);
             };
             v8i gv = g_operand(0);
-            f[0] = fsg[16 * wm + i16];
+            f[0] = sg[0];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const v8i gi = gv;
                 if (i + 1 < 8) {
                     gv = g_operand(i + 1);
-                    f[i + 1] = fsg[32 * (i + 1) + 16 * wm + i16];
+                    f[i + 1] = sg[32 * (i + 1)];
                 }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int u = 4 * i + q;
-                    d[u % 3] = block_dot(xf[q], gi);
-                    pin(d[u % 3]);
-                    if (u >= 2) add(u - 2);
+                    const int m = 4 * i + q;
+                    d[m % 3] = block_dot(xf[q], gi);
+                    pin(d[m % 3]);
+                    if (m >= 2) add(m - 2);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
             add(30);
             add(31);
             lds_barrier();  // every wave is done with the buffer
-            if (s + 2 < cur.runs) copy(cur, s + 2);
+            behind0 = behind1;
+            behind1 = 0;
+            if (left) {
+                copy(c, cs, buffer);
+                behind0 += kCopies;
+                advance();
+            }
+            buffer ^= 1;
         }
 
-        if (more && next.runs > 0) copy(next, 0);
-        if (more && next.runs > 1) copy(next, 1);
-        stores = 0;
-        if (!cur.k_half || wn < 2) {
-            stores = cur.n_half ? 8 : 16;
+        if (!k_half(cur) || wn < 2) {
+            const int stores = n_half(cur) ? 8 : 16;
+            behind0 += stores;
+            behind1 += stores;
             uint8_t *o = reinterpret_cast<uint8_t *>(p.dw + ((int64_t)cur.e * N + cur.n0) * K + cur.k0);
-            const uint32_t at = ((uint32_t)(16 * wm + i16) * K + 64 * wn + 8 * g) * 2;
+            // row pair i16 & ~1 of a piece, this lane's eight of its 64 k
+            const bool odd = i16 & 1;
+            const uint32_t at = ((uint32_t)(16 * wm + (i16 & ~1)) * K + 64 * wn + (odd ? 32 : 0) + 8 * g) * 2;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                if (i < 4 || !cur.n_half) {
+                if (i < 4 || !n_half(cur)) {
+                    u32x4 v[2];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const u32x4 v = {bf16_pair(acc[i][2 * h][0], acc[i][2 * h][1]),
-                                         bf16_pair(acc[i][2 * h][2], acc[i][2 * h][3]),
-                                         bf16_pair(acc[i][2 * h + 1][0], acc[i][2 * h + 1][1]),
-                                         bf16_pair(acc[i][2 * h + 1][2], acc[i][2 * h + 1][3])};
-                        MOE_WGRAD_STORE(v, reinterpret_cast<u32x4 *>(o + (int64_t)64 * i * K + 64 * h + at));
-                    }
+                    for (int h = 0; h < 2; ++h)
+                        v[h] = (u32x4){bf16_pair(acc[i][2 * h][0], acc[i][2 * h][1]),
+                                       bf16_pair(acc[i][2 * h][2], acc[i][2 * h][3]),
+                                       bf16_pair(acc[i][2 * h + 1][0], acc[i][2 * h + 1][1]),
+                                       bf16_pair(acc[i][2 * h + 1][2], acc[i][2 * h + 1][3])};
+                    const RowPair r = swap_rows(v[0], v[1], odd);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        MOE_WGRAD_STORE(r.x[h], reinterpret_cast<u32x4 *>(o + (int64_t)(64 * i + 2 * h) * K + at));
                 }
             }
         }
-        if (!more) break;
-        cur = next;
+        it += step;
+        if (it >= end) break;
+        cur = item(it);
     }
 }
 
@@ -194,9 +236,9 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(const BlockWgradArgs p)
 
 hipError_t launch_block_wgrad(const BlockWgradArgs &a, hipStream_t s) {
     const int64_t items = (int64_t)a.n * ((a.N + kB - 1) / kB) * ((a.K + kB - 1) / kB);
-    if (items > INT32_MAX - 8) return hipErrorInvalidValue;
-    const unsigned grid = (unsigned)(items >= kMaxGrid ? kMaxGrid : (items + 7) / 8 * 8);
-    hipLaunchKernelGGL(wgrad_kernel, dim3(grid), dim3(kThreads), 0, s, a);
+    if (items > INT32_MAX / 2) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(wgrad_kernel, dim3((unsigned)(items >= kMaxGrid ? kMaxGrid : (items + 7) / 8 * 8)), dim3(kThreads), 0,
+                       s, a);
     return hipGetLastError();
 }
 
