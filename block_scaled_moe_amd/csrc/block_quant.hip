@@ -7,6 +7,8 @@
 #include "formats.h"
 #include "ops_internal.h"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
@@ -69,12 +71,41 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const BlockQuantArgs a) 
 
 // ---- columns (and rows): one workgroup takes a run of 128 sorted rows of one expert and
 // kColumnTiles tiles of 128 columns. Thread (q, h) holds columns 4q..4q+3 of rows 16h..16h+15:
-// its loads are 8 bytes, 256 consecutive bytes a row over 32 threads, and it stores the 16
-// codes of one column as 16 bytes.
-constexpr int kColumnTiles = 4;
+// its loads are 8 bytes, 256 consecutive bytes a row over 32 threads, the next tile's issued
+// before this one is quantised, and it stores the 16 codes of one column as 16 bytes. A block's
+// two divisions are done once, by one lane, and reach the others through LDS.
+constexpr int kColumnTiles = 8;
 
+// v[r] holds this lane's part of the maximum of row r over the 16 lanes of a DPP row; returns the
+// whole maximum of row (lane & 15). Each step gives half of its rows to a partner lane and takes
+// the partner's part of the other half: partners l ^ 8, l ^ 7, l ^ 2, l ^ 1 reach all 16 lanes.
+__device__ __forceinline__ float row_maxima(float (&v)[16], int lane) {
+#define MOE_HALVE(COUNT, BIT, CTRL)                                                                               \
+    _Pragma("unroll") for (int r = 0; r < COUNT; ++r) {                                                           \
+        const float keep = (lane & BIT) ? v[r + COUNT] : v[r], give = (lane & BIT) ? v[r] : v[r + COUNT];         \
+        v[r] = fmaxf(keep, __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(give), CTRL, 0xF, 0xF, true))); \
+    }
+    MOE_HALVE(8, 8, 0x128)  // row_ror:8
+    MOE_HALVE(4, 4, 0x141)  // row_half_mirror
+    MOE_HALVE(2, 2, 0x4E)   // quad_perm 2, 3, 0, 1
+    MOE_HALVE(1, 1, 0xB1)   // quad_perm 1, 0, 3, 2
+#undef MOE_HALVE
+    return v[0];
+}
+
+// Four codes with the scale s, r = fl32(1 / s); FAST where the short quotient serves (r != 0)
+template <bool FAST>
+__device__ __forceinline__ uint32_t quotient_codes(const float (&x)[4], float s, float r) {
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = FAST ? quotient_by(x[i], s, r) : x[i] / s;
+    return codes4(v[0], v[1], v[2], v[3]);
+}
+
+template <bool TOKEN, bool ROWS>
 __global__ void __launch_bounds__(kThreads) columns_kernel(const BlockQuantArgs a) {
-    __shared__ float col_max[8][128];
+    __shared__ __attribute__((aligned(16))) float col_max[8][128], col_s[128], col_r[128];
+    __shared__ __attribute__((aligned(16))) float row_s[8][16], row_r[8][16];
     const int tid = threadIdx.x, q = tid & 31, h = tid >> 5;
     const int32_t run = blockIdx.x;
     // the run's expert: run b belongs to the last e with offsets[e] / 128 + e <= b
@@ -97,21 +128,29 @@ __global__ void __launch_bounds__(kThreads) columns_kernel(const BlockQuantArgs 
     if (left <= 0) return;
     const int32_t r0 = first + 128 * i;
     const int kb = a.C / 128;
-    int64_t src_row[16];
+    int32_t token[TOKEN ? 16 : 1];
+    if (TOKEN) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        const int row = 16 * h + r;
-        const int32_t p = r0 + (row < left ? row : 0);
-        src_row[r] = a.sorted_slot ? a.sorted_slot[p] / a.top_k : p;
+        for (int r = 0; r < 16; ++r) token[r] = a.sorted_slot[r0 + (16 * h + r < left ? 16 * h + r : 0)] / a.top_k;
     }
-    for (int ct = blockIdx.y * kColumnTiles; ct < min(kb, (int)(blockIdx.y + 1) * kColumnTiles); ++ct) {
-        uint2 u[16];
+    const uint16_t *src = a.x + (TOKEN ? 0 : (int64_t)(r0 + 16 * h) * a.C) + 4 * q;
+    auto load = [&](uint2 (&u)[16], int ct) __attribute__((always_inline)) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             u[r] = make_uint2(0u, 0u);
-            if (16 * h + r < left) u[r] = *reinterpret_cast<const uint2 *>(a.x + src_row[r] * a.C + ct * 128 + 4 * q);
+            if (16 * h + r < left)
+                u[r] = *reinterpret_cast<const uint2 *>(src + (TOKEN ? (int64_t)token[r] * a.C : (int64_t)r * a.C) + ct * 128);
         }
-        float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    };
+    const int ct1 = min(kb, (int)(blockIdx.y + 1) * kColumnTiles);
+    uint2 u[16], next[16];
+    load(next, blockIdx.y * kColumnTiles);
+#pragma clang loop unroll(disable)
+    for (int ct = blockIdx.y * kColumnTiles; ct < ct1; ++ct) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) u[r] = next[r];
+        if (ct + 1 < ct1) load(next, ct + 1);
+        float m[4] = {0.0f, 0.0f, 0.0f, 0.0f}, rm[16];
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             float x[4];
@@ -119,53 +158,72 @@ __global__ void __launch_bounds__(kThreads) columns_kernel(const BlockQuantArgs 
             widen(u[r].y, x[2], x[3]);
 #pragma unroll
             for (int c = 0; c < 4; ++c) m[c] = fmaxf(m[c], fabsf(x[c]));
+            rm[r] = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
         }
-        __syncthreads();  // the previous tile's reads of col_max
-#pragma unroll
-        for (int c = 0; c < 4; ++c) col_max[h][4 * q + c] = m[c];
-        if (a.codes) {  // by rows: the 32 threads of a row are half a wave
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                float x[4];
-                widen(u[r].x, x[0], x[1]);
-                widen(u[r].y, x[2], x[3]);
-                float rm = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) rm = fmaxf(rm, __shfl_xor(rm, off));
-                const Divisor d(rm);
-                const int row = 16 * h + r;
-                if (row < left) {
-                    const int64_t p = r0 + row;
-                    *reinterpret_cast<uint32_t *>(a.codes + ((int64_t)ct * a.rows + p) * 128 + 4 * q) =
-                        codes4(d.quotient(x[0]), d.quotient(x[1]), d.quotient(x[2]), d.quotient(x[3]));
-                    if (q == 0) a.scales[p * kb + ct] = d.s;
-                }
+        *reinterpret_cast<float4 *>(&col_max[h][4 * q]) = make_float4(m[0], m[1], m[2], m[3]);
+        bool fast = true;
+        if (ROWS) {  // the 32 threads of a row are half a wave
+            float top = row_maxima(rm, tid & 15);
+            top = fmaxf(top, __shfl_xor(top, 16));
+            const Divisor d(top);
+            fast = __all(d.fast);
+            if (q < 16) {
+                row_s[h][q] = d.s;
+                row_r[h][q] = d.r;
+                if (16 * h + q < left) a.scales[(int64_t)(r0 + 16 * h + q) * kb + ct] = d.s;
             }
         }
         __syncthreads();
+        if (tid < 128) {
+            float cm = col_max[0][tid];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            float cm = col_max[0][4 * q + c];
-#pragma unroll
-            for (int g = 1; g < 8; ++g) cm = fmaxf(cm, col_max[g][4 * q + c]);
+            for (int g = 1; g < 8; ++g) cm = fmaxf(cm, col_max[g][tid]);
             const Divisor d(cm);
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float v[4];
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const uint32_t word = c < 2 ? u[4 * j + b].x : u[4 * j + b].y;
-                    v[b] = d.quotient(__uint_as_float(c & 1 ? word & 0xffff0000u : word << 16));
-                }
-                w[j] = codes4(v[0], v[1], v[2], v[3]);
-            }
-            const int64_t col = ct * 128 + 4 * q + c;
-            uint8_t *dst = a.col_codes + (int64_t)run * a.C * 128 + (col >> 5) * 4096 + (h >> 2) * 2048 + (h & 3) * 512 +
-                           (col & 31) * 16;
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-            if (h == 0) a.col_scales[(int64_t)run * a.C + col] = d.s;
+            col_s[tid] = d.s;
+            col_r[tid] = d.r;
+            a.col_scales[(int64_t)run * a.C + ct * 128 + tid] = d.s;
         }
+        if (ROWS) {
+            auto store_rows = [&](auto fast_c) __attribute__((always_inline)) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    float x[4];
+                    widen(u[r].x, x[0], x[1]);
+                    widen(u[r].y, x[2], x[3]);
+                    const uint32_t c = quotient_codes<decltype(fast_c)::value>(x, row_s[h][r], row_r[h][r]);
+                    if (16 * h + r < left)
+                        *reinterpret_cast<uint32_t *>(a.codes + ((int64_t)ct * a.rows + r0 + 16 * h + r) * 128 + 4 * q) = c;
+                }
+            };
+            if (fast) store_rows(std::true_type{});
+            else store_rows(std::false_type{});
+        }
+        __syncthreads();
+        uint8_t *dst = a.col_codes + (int64_t)run * a.C * 128 + ct * 16384 + (q >> 3) * 4096 + (h >> 2) * 2048 + (h & 3) * 512 +
+                       (q & 7) * 64;
+        const float4 cs = *reinterpret_cast<const float4 *>(&col_s[4 * q]), cr = *reinterpret_cast<const float4 *>(&col_r[4 * q]);
+        auto store_columns = [&](auto fast_c) __attribute__((always_inline)) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float s = c == 0 ? cs.x : c == 1 ? cs.y : c == 2 ? cs.z : cs.w;
+                const float r = c == 0 ? cr.x : c == 1 ? cr.y : c == 2 ? cr.z : cr.w;
+                uint32_t code[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float x[4];
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const uint32_t word = c < 2 ? u[4 * j + b].x : u[4 * j + b].y;
+                        x[b] = __uint_as_float(c & 1 ? word & 0xffff0000u : word << 16);
+                    }
+                    code[j] = quotient_codes<decltype(fast_c)::value>(x, s, r);
+                }
+                *reinterpret_cast<uint4 *>(dst + 16 * c) = make_uint4(code[0], code[1], code[2], code[3]);
+            }
+        };
+        if (__all(cr.x != 0.0f && cr.y != 0.0f && cr.z != 0.0f && cr.w != 0.0f)) store_columns(std::true_type{});
+        else store_columns(std::false_type{});
+        __syncthreads();  // before the next tile writes the maxima and scales
     }
 }
 
@@ -235,7 +293,10 @@ hipError_t launch_block_quant_rows(const BlockQuantArgs &a, hipStream_t s) {
 hipError_t launch_block_quant_columns(const BlockQuantArgs &a, hipStream_t s) {
     const int64_t runs = a.offsets ? (int64_t)a.rows / 128 + a.n : ((int64_t)a.rows + 127) / 128;
     const int tiles = (a.C / 128 + kColumnTiles - 1) / kColumnTiles;
-    hipLaunchKernelGGL(columns_kernel, dim3((unsigned)runs, (unsigned)tiles), dim3(kThreads), 0, s, a);
+    const dim3 grid((unsigned)runs, (unsigned)tiles);
+    if (a.sorted_slot) hipLaunchKernelGGL((columns_kernel<true, false>), grid, dim3(kThreads), 0, s, a);
+    else if (a.codes) hipLaunchKernelGGL((columns_kernel<false, true>), grid, dim3(kThreads), 0, s, a);
+    else hipLaunchKernelGGL((columns_kernel<false, false>), grid, dim3(kThreads), 0, s, a);
     return hipGetLastError();
 }
 

@@ -14,10 +14,15 @@
 // is refilled for the step after next, of this item or of a later one, as soon as every wave is
 // done with it. A wave's vector memory operations complete in order, so a step waits for its own
 // copies by the number of copies and stores issued behind them, and the stores of an item drain
-// under the next steps. (Copying the next item only at the end of the last one left nothing in
-// flight there: 617 us against MEASURED on two runs for each of 96 experts of 4096 x 2560.)
-// A lane swaps half its outputs with its neighbour, so that every store instruction writes whole
-// 128-byte lines, which go past L2 (non-temporal) and leave the operands there.
+// under the next steps. A lane swaps half its outputs with its neighbour, so that every store
+// instruction writes whole 128-byte lines, which go past L2 (non-temporal) and leave the operands
+// there.
+//
+// 96 experts of 4096 x 2560, 16384 rows unevenly routed: 590 us, of which the stores alone are 340 us
+// (2.0 GB, 5.9 TB/s) and the steps alone 325 us (the products 150 us of them). The two hardly overlap:
+// copies that a CU issues behind its stores wait until those have drained. Tiles of 128 x 256 with
+// two workgroups a CU took 600 us, 128 x 128 690 us, sweeps along k that keep the block of n in LDS
+// 700 us (uneven experts), ordinary stores 620 us.
 #include "block_mma.h"
 #include "ops_internal.h"
 
@@ -28,10 +33,6 @@ using namespace block;
 
 constexpr int kThreads = 512, kB = 256, kOperand = kB * 128, kMaxGrid = 256;
 constexpr int kCopies = 8;  // of a step by a wave (the two that copy scales: nine)
-#ifndef NT
-#define NT 1
-#endif
-#define MOE_WGRAD_STORE(v, p) do { if (NT) __builtin_nontemporal_store(v, p); else *(p) = v; } while (0)
 
 __global__ void __launch_bounds__(kThreads) wgrad_kernel(const BlockWgradArgs p) {
     __shared__ __attribute__((aligned(16))) uint8_t gb[2 * kOperand];
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(const BlockWgradArgs p)
                     const RowPair r = swap_rows(v[0], v[1], odd);
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        MOE_WGRAD_STORE(r.x[h], reinterpret_cast<u32x4 *>(o + (int64_t)(64 * i + 2 * h) * K + at));
+                        __builtin_nontemporal_store(r.x[h], reinterpret_cast<u32x4 *>(o + (int64_t)(64 * i + 2 * h) * K + at));
                 }
             }
         }
