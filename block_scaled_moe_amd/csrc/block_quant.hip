@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const BlockQuantArgs a) 
 // its loads are 8 bytes, 256 consecutive bytes a row over 32 threads, the next tile's issued
 // before this one is quantised, and it stores the 16 codes of one column as 16 bytes. A block's
 // two divisions are done once, by one lane, and reach the others through LDS.
-constexpr int kColumnTiles = 8;
+constexpr int kColumnTiles = 4;
 
 // v[r] holds this lane's part of the maximum of row r over the 16 lanes of a DPP row; returns the
 // whole maximum of row (lane & 15). Each step gives half of its rows to a partner lane and takes
@@ -103,7 +103,7 @@ __device__ __forceinline__ uint32_t quotient_codes(const float (&x)[4], float s,
 }
 
 template <bool TOKEN, bool ROWS>
-__global__ void __launch_bounds__(kThreads) columns_kernel(const BlockQuantArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) columns_kernel(const BlockQuantArgs a) {
     __shared__ __attribute__((aligned(16))) float col_max[8][128], col_s[128], col_r[128];
     __shared__ __attribute__((aligned(16))) float row_s[8][16], row_r[8][16];
     const int tid = threadIdx.x, q = tid & 31, h = tid >> 5;

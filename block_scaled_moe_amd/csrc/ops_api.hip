@@ -12,9 +12,13 @@ GroupsPlan groups_plan(int32_t T, int32_t top_k, int32_t n) {
     const int64_t TK = (int64_t)T * top_k;
     p.n = n;
     p.max_tiles = (int32_t)((TK < n ? TK : n) + TK / kGroupTile);  // a last partial tile per non-empty group
-    const int32_t ct = T / 256;
-    p.chunk_tokens = ct < 8 ? 8 : (ct > 64 ? 64 : ct);
-    p.n_chunks = (T + p.chunk_tokens - 1) / p.chunk_tokens;
+    if (n <= kSortMaxLocal) {
+        p.n_chunks = (int32_t)((TK + sort_chunk_slots(TK) - 1) / sort_chunk_slots(TK));
+    } else {
+        const int32_t ct = T / 256;
+        p.chunk_tokens = ct < 8 ? 8 : (ct > 64 ? 64 : ct);
+        p.n_chunks = (T + p.chunk_tokens - 1) / p.chunk_tokens;
+    }
     if (p.n_chunks < 1) p.n_chunks = 1;
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -124,7 +128,7 @@ int32_t moe_sort(const moe_groups *g, const int32_t *topk_idx, void *stream) {
     a.ctrl = reinterpret_cast<Ctrl *>(at + p.ctrl);
     a.fill_tail = 1;
     hipStream_t s = (hipStream_t)stream;
-    return to_status(permute_small_ok(g->T, g->top_k, n) ? launch_permute_small(a, s) : launch_permute(a, s));
+    return to_status(n <= kSortMaxLocal ? launch_sort(a, g->T * g->top_k, s) : launch_permute(a, s));
 }
 
 int32_t moe_gather(const moe_groups *g, int32_t dtype, int32_t D, const void *x, void *rows, void *stream) {

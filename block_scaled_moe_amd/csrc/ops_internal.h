@@ -29,6 +29,11 @@ struct GroupView {
     int32_t mean_rows;  // average rows of a group for an even routing (host's rule for the kernel)
 };
 
+// ---- sort (sort.hip), for up to kSortMaxLocal local experts: fills what launch_permute does
+constexpr int32_t kSortMaxLocal = 1024;
+int32_t sort_chunk_slots(int64_t n_slots);  // slots of one row of chunk_counts
+hipError_t launch_sort(const PermuteArgs &a, int32_t n_slots, hipStream_t s);
+
 // ---- rows by expert and back (tokens.hip)
 hipError_t launch_gather(const moe_groups &g, int32_t dtype, int32_t D, const void *x, void *rows, hipStream_t s);
 // w NULL: weights of 1

@@ -318,8 +318,6 @@ __global__ void __launch_bounds__(kSmallThreads) permute_small_kernel(PermuteArg
     __syncthreads();
     int32_t *cursor = cnt[wave];
     for (int32_t g = s0; g < s1; g += 64) place_group(a, cursor, g + lane, g + lane < s1);
-    if (a.fill_tail)
-        for (int32_t p = S + tid; p < n_slots; p += kSmallThreads) a.sorted_slot[p] = -1;
 }
 
 }  // namespace

@@ -128,7 +128,7 @@ class Groups:
         self.n, self.rows = e_end - e_begin, T * top_k
         self._at = _groups_layout(T, top_k, E, e_begin, e_end)
         slots, pos, plan, end = self._at
-        self.buffer = torch.empty(end, dtype=torch.uint8, device=device)
+        self.buffer = torch.empty(end // 4, dtype=torch.int32, device=device)
         self.device = self.buffer.device
         base = self.buffer.data_ptr()
         self.struct = MoeGroups(T, top_k, E, e_begin, e_end, base, base + slots, base + pos, base + plan, end - plan)
@@ -138,23 +138,20 @@ class Groups:
     def empty(T: int, top_k: int, E: int, e_begin: int = 0, e_end: int | None = None, device="cuda") -> "Groups":
         return Groups(T, top_k, E, e_begin, e_end, device)
 
-    def _view(self, at: int, count: int) -> torch.Tensor:
-        return self.buffer.view(torch.int32).narrow(0, at // 4, count)
-
     @functools.cached_property
     def offsets(self) -> torch.Tensor:
         """int32 [n + 1]: first sorted row of each local expert; [n] = local slots."""
-        return self._view(0, self.n + 1)
+        return self.buffer.as_strided((self.n + 1,), (1,), 0)
 
     @functools.cached_property
     def sorted_slot(self) -> torch.Tensor:
         """int32 [T * top_k]: slot of each sorted row, -1 behind the local ones."""
-        return self._view(self._at[0], self.rows)
+        return self.buffer.as_strided((self.rows,), (1,), self._at[0] // 4)
 
     @functools.cached_property
     def slot_pos(self) -> torch.Tensor:
         """int32 [T, top_k]: sorted row of each slot, -1 if not local."""
-        return self._view(self._at[1], self.rows).view(self.T, self.top_k)
+        return self.buffer.as_strided((self.T, self.top_k), (self.top_k, 1), self._at[1] // 4)
 
 
 @functools.lru_cache(maxsize=256)
