@@ -40,6 +40,33 @@ struct alignas(sizeof(T) * V > 16 ? 16 : sizeof(T) * V) Piece {
     T v[V];
 };
 
+// Rows are read once and written once here, and the sorted ones of a long batch fill the caches many
+// times over: pieces of 16 bytes go past them (16384 tokens of 4096 bf16 values in eight slots:
+// gather 276 -> 240 us, join 290 -> 208 us, the gradient of combine 554 -> 476 us, 4.8 to 5.8 TB/s).
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <typename P>
+__device__ __forceinline__ P load_row(const P *p) {
+    if constexpr (sizeof(P) % 16 == 0) {
+        P r;
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(P) / 16; ++i)
+            reinterpret_cast<u32x4 *>(&r)[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p) + i);
+        return r;
+    } else {
+        return *p;
+    }
+}
+template <typename P>
+__device__ __forceinline__ void store_row(P *p, const P &v) {
+    if constexpr (sizeof(P) % 16 == 0) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(P) / 16; ++i)
+            __builtin_nontemporal_store(reinterpret_cast<const u32x4 *>(&v)[i], reinterpret_cast<u32x4 *>(p) + i);
+    } else {
+        *p = v;
+    }
+}
+
 // Where a workgroup's threads stand: `lanes` (a power of two) threads share a token's row.
 struct Span {
     int32_t log_lanes;  // of threads per token
@@ -70,7 +97,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(int32_t n_tokens, int3
         const P v = src[c];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (pos[j] >= 0) dst[(int64_t)pos[j] * sp.pieces + c] = v;
+            if (pos[j] >= 0) store_row(dst + (int64_t)pos[j] * sp.pieces + c, v);
     }
 }
 
@@ -98,7 +125,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(int32_t n_tokens, int32_
         PY v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (pos[j] >= 0) v[j] = src[(int64_t)pos[j] * sp.pieces + c];
+            if (pos[j] >= 0) v[j] = load_row(src + (int64_t)pos[j] * sp.pieces + c);
         float acc[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = 0.0f;
@@ -112,7 +139,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(int32_t n_tokens, int32_
         PO o;
 #pragma unroll
         for (int i = 0; i < V; ++i) o.v[i] = from_f32<TO>(acc[i]);
-        dst[c] = o;
+        store_row(dst + c, o);
     }
 }
 
@@ -148,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(int32_t n_to
             PY v[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (pos[j] >= 0) v[j] = ys[(int64_t)pos[j] * sp.pieces + c];
+                if (pos[j] >= 0) v[j] = load_row(ys + (int64_t)pos[j] * sp.pieces + c);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (pos[j] >= 0) {
@@ -159,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(int32_t n_to
                         dot[j] = fmaf(gi, to_f32(v[j].v[i]), dot[j]);
                         o.v[i] = from_f32<TY>(wj[j] * gi);
                     }
-                    dst[(int64_t)pos[j] * sp.pieces + c] = o;
+                    store_row(dst + (int64_t)pos[j] * sp.pieces + c, o);
                 }
         }
     }
