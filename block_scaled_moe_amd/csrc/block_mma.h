@@ -44,8 +44,9 @@ __device__ __forceinline__ T *uniform(T *p) {
 }
 // *p through the scalar cache, the address the same for the wave: a vector load would have to
 // wait for every copy and store in flight before it. For data no kernel writes while this one runs.
-__device__ __forceinline__ int scalar_load(const int *p) {
-    return *(const __attribute__((address_space(4))) int *)(uint64_t)uniform(p);
+template <typename T>
+__device__ __forceinline__ T scalar_load(const T *p) {
+    return *(const __attribute__((address_space(4))) T *)(uint64_t)uniform(p);
 }
 __device__ __forceinline__ uint32_t lds_address(const void *p) {
     return (uint32_t)uniform((int)(uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p);
@@ -54,6 +55,13 @@ __device__ __forceinline__ void copy_to_lds(const uint8_t *base, uint32_t offset
     // m0 (nothing else here uses it) holds the LDS address; five wait states between a vector
     // instruction that wrote base and the copy that reads it
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uniform((int)dst)), "v"(offset),
+                 "s"(uniform(base))
+                 : "memory");
+}
+
+// the same with 4 bytes per lane, at dst + 4 * lane
+__device__ __forceinline__ void copy4_to_lds(const uint8_t *base, uint32_t offset, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2" ::"s"(uniform((int)dst)), "v"(offset),
                  "s"(uniform(base))
                  : "memory");
 }
@@ -91,6 +99,15 @@ __device__ __forceinline__ RowPair swap_rows(u32x4 a, u32x4 b, bool odd) {
         r.x[1][j] = odd ? b[j] : got;
     }
     return r;
+}
+
+// 8 bytes per lane, a of one and b of another run of 16 outputs, lane group g (of 16 lanes) holding
+// outputs 4 g .. 4 g + 3 of each: after the swap with the neighbouring group a lane holds 16 bytes,
+// outputs 8 (g / 2) .. 8 (g / 2) + 7 of run a (g even) or b (g odd).
+__device__ __forceinline__ u32x4 swap_groups(uint2 a, uint2 b) {
+    const auto x = __builtin_amdgcn_permlane16_swap(a.x, b.x, false, false);
+    const auto y = __builtin_amdgcn_permlane16_swap(a.y, b.y, false, false);
+    return (u32x4){x[0], y[0], x[1], y[1]};
 }
 
 // The MFMA's A operand is read so that a lane's accumulators of four reads q, over 64 columns in

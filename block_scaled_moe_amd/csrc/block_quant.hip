@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const BlockQuantArgs a) 
         c.x = codes4(d.quotient(x[0]), d.quotient(x[1]), d.quotient(x[2]), d.quotient(x[3]));
         c.y = codes4(d.quotient(x[4]), d.quotient(x[5]), d.quotient(x[6]), d.quotient(x[7]));
         reinterpret_cast<uint2 *>(a.codes)[((int64_t)blk * a.rows + row) * 16 + sub] = c;
-        if (sub == 0) a.scales[b] = d.s;
+        if (sub == 0) a.scales[row * scale_stride(a.C) + blk] = d.s;
     }
 }
 
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 3) columns_kernel(const BlockQuantAr
             if (q < 16) {
                 row_s[h][q] = d.s;
                 row_r[h][q] = d.r;
-                if (16 * h + q < left) a.scales[(int64_t)(r0 + 16 * h + q) * kb + ct] = d.s;
+                if (16 * h + q < left) a.scales[(int64_t)(r0 + 16 * h + q) * scale_stride(a.C) + ct] = d.s;
             }
         }
         __syncthreads();

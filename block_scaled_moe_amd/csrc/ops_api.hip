@@ -192,7 +192,7 @@ int32_t moe_block_quantize(const moe_block_quantize_args *q, void *stream) {
         if (rc != MOE_OK) return rc;
         if (q->rows != (q->by_token ? q->g->T : q->g->T * q->g->top_k)) return MOE_ERR_INVALID_ARG;
     }
-    if (by_rows && q->rows >= kMaxBlockRows) return MOE_ERR_UNSUPPORTED;
+    if (by_rows && !rows_form_fits(q->rows, q->C)) return MOE_ERR_UNSUPPORTED;
     if (q->rows == 0) return MOE_OK;
     if (!q->x) return MOE_ERR_INVALID_ARG;
     if (!aligned16(q->x) || !aligned16(q->codes) || !aligned16(q->scales) || !aligned16(q->col_codes) ||
@@ -252,7 +252,7 @@ int32_t moe_block_gemm(const moe_block_gemm_args *a, void *stream) {
     } else if (a->by_token || a->w.E != 1) {
         return MOE_ERR_INVALID_ARG;
     }
-    if (a->rows >= kMaxBlockRows) return MOE_ERR_UNSUPPORTED;
+    if (!rows_form_fits(a->rows, a->transposed ? a->w.N : a->w.K)) return MOE_ERR_UNSUPPORTED;
     if (a->rows == 0) return MOE_OK;
     if (!a->x_codes || !a->x_scales || !a->out) return MOE_ERR_INVALID_ARG;
     if (!aligned16(a->x_codes) || !aligned16(a->x_scales) || !aligned16(a->out)) return MOE_ERR_ALIGNMENT;

@@ -8,7 +8,7 @@
 namespace moe {
 
 // Rows per work-list tile of the grouped products; the lists are written by moe_sort.
-constexpr int32_t kGroupTile = 256;
+constexpr int32_t kGroupTile = 224;
 
 // Byte offsets inside moe_groups::plan.
 struct GroupsPlan {
@@ -17,8 +17,12 @@ struct GroupsPlan {
 };
 GroupsPlan groups_plan(int32_t T, int32_t top_k, int32_t n);
 
-// Rows of a rows form: a row's place in its block's plane is a 32-bit byte offset.
-constexpr int32_t kMaxBlockRows = 1 << 25;
+// Scales of a row of a rows form, padded so that four blocks' are one aligned 16-byte load.
+__host__ __device__ inline int32_t scale_stride(int32_t C) { return (C / 128 + 3) / 4 * 4; }
+// A row's place in its block's plane of codes, and in the scales, is a 32-bit byte offset.
+inline bool rows_form_fits(int32_t rows, int32_t C) {
+    return rows < (1 << 25) && (int64_t)rows * scale_stride(C) < (1 << 30);
+}
 
 // What a grouped product's workgroups read to find their rows. offsets == NULL: one group of
 // `rows` rows, tiles computed from it.

@@ -244,7 +244,8 @@ def combine_backward(g: Groups, d_out: torch.Tensor, y: torch.Tensor, w: torch.T
 
 @dataclasses.dataclass
 class BlockRows:
-    """Rows in E4M3 with an fp32 scale per 1 x 128 block: codes uint8 [C / 128, rows, 128], scales [rows, C / 128]."""
+    """Rows in E4M3 with an fp32 scale per 1 x 128 block: codes uint8 [C / 128, rows, 128], scales
+    [rows, S], S being C / 128 rounded up to a multiple of 4 (the rest is unused)."""
     codes: torch.Tensor
     scales: torch.Tensor
 
@@ -331,7 +332,7 @@ def _quantize(x: torch.Tensor, g: Groups | None, by_token: bool, rows: bool, col
     rc = rs = cc = cs = None
     if rows:
         r = BlockRows(torch.empty((C // 128, R, 128), dtype=torch.uint8, device=dev),
-                      torch.empty((R, C // 128), dtype=torch.float32, device=dev))
+                      torch.empty((R, (C // 128 + 3) // 4 * 4), dtype=torch.float32, device=dev))
         rc, rs = r.codes.data_ptr(), r.scales.data_ptr()
     if columns:
         n = (R if g is None else g.rows) // 128 + (1 if g is None else g.n)  # moe_block_column_blocks
@@ -367,7 +368,7 @@ def _product(x: BlockRows, w: BlockWeights, g: Groups | None, by_token: bool, tr
     R, C = (w.N, w.K) if transposed else (w.K, w.N)
     n_x = x.codes.shape[1] if g is None else g.T if by_token else g.rows
     _ask("x codes", x.codes, (R // 128, n_x, 128), torch.uint8, dev)
-    _ask("x scales", x.scales, (n_x, R // 128), torch.float32, dev)
+    _ask("x scales", x.scales, (n_x, (R // 128 + 3) // 4 * 4), torch.float32, dev)
     if w.E != (1 if g is None else g.n):
         raise ValueError(f"w: {w.E} experts, expected {1 if g is None else g.n}")
     if g is None and by_token:

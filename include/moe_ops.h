@@ -80,7 +80,8 @@ int32_t moe_combine_backward(const moe_groups *g, int32_t y_dtype, int32_t out_d
  * 1 for an all-zero block; code = E4M3(fl32(x / s)), nearest, ties to even. The value is
  * code * s. All dimensions that blocks run along are multiples of 128.
  *   rows     codes [C/128][R][128] (the rows' first blocks, then their second ones, ..),
- *            scales [R][C/128]: blocks of 1 x 128; R < 2^25
+ *            scales [R][S], S = C/128 rounded up to a multiple of 4 (the rest of a row is
+ *            neither written nor used): blocks of 1 x 128; R < 2^25 and R * S < 2^30
  *   columns  of sorted rows, blocks of 128 x 1: expert e's rows in runs of 128 from its first
  *            row (the last one padded with zeros), run i at block b = offsets[e] / 128 + e + i
  *            (integer division; blocks that belong to no run are never read):

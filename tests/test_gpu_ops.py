@@ -178,7 +178,7 @@ def test_quantise_rows(R, C):
     x = hard_values(np.random.default_rng(R), (R, C))
     q = moe.quantize_block(dev(x, torch.bfloat16))
     c, s = ref.rows(x)
-    assert np.array_equal(host(q.scales).view(np.uint32), s.view(np.uint32))
+    assert np.array_equal(host(q.scales)[:, :C // 128].copy().view(np.uint32), s.view(np.uint32))
     assert np.array_equal(rows_codes(q), c)
 
 
@@ -201,7 +201,7 @@ def exact_counts(counts, k=1):
     return np.random.default_rng(3).permutation(idx)[:, None]
 
 
-COUNTS = [[1], [0, 3, 0], [128, 129, 0, 127], [300, 0, 1, 260], [5] * 70, [0, 0], [16, 17, 15, 240, 272]]
+COUNTS = [[1], [0, 3, 0], [128, 129, 0, 127], [300, 0, 1, 260], [5] * 70, [0, 0], [16, 17, 15, 223, 224, 225, 449]]
 
 
 @pytest.mark.parametrize("C", [128, 640])
@@ -225,7 +225,7 @@ def test_quantise_columns(counts, C):
             assert np.array_equal(qc[b], c), b
     if T:
         c, s = ref.rows(sorted_x)
-        assert np.array_equal(rows_codes(rows), c) and np.array_equal(host(rows.scales), s)
+        assert np.array_equal(rows_codes(rows), c) and np.array_equal(host(rows.scales)[:, :C // 128], s)
 
 
 def test_quantise_leaves_rows_behind_the_last_one():
@@ -235,13 +235,14 @@ def test_quantise_leaves_rows_behind_the_last_one():
     x = torch.full((6, 256), float("nan"), dtype=torch.bfloat16, device="cuda")
     x[:2] = 1.5
     codes = torch.full((2, 6, 128), 9, dtype=torch.uint8, device="cuda")
-    scales = torch.full((6, 2), 9.0, device="cuda")
+    scales = torch.full((6, 4), 9.0, device="cuda")
     import ctypes
     from block_scaled_moe_amd import ops
     a = ops.MoeBlockQuantizeArgs(rows=6, C=256, g=ctypes.pointer(g.struct), x=x.data_ptr(), codes=codes.data_ptr(),
                                  scales=scales.data_ptr())
     ops._call("moe_block_quantize", x.device, ctypes.byref(a))
     assert (host(codes)[:, :2] == 0x7E).all() and (host(codes)[:, 2:] == 9).all() and (host(scales)[2:] == 9).all()
+    assert (host(scales)[:, 2:] == 9).all()     # nor the padding of a row's scales
 
 
 # ---------------------------------------------------------------- products

@@ -93,6 +93,7 @@ def test_block_calls_refuse():
     assert quant(4, 128, 0, None, A + 2, A, A, 0, 0) == EALIGN
     assert quant(0, 128, 0, None, 0, A, A, 0, 0) == OK
     assert quant(1 << 25, 128, 0, None, A, A, A, 0, 0) == EUNSUP     # 32-bit places in a block's plane
+    assert quant(1 << 24, 128 * 65, 0, None, A, A, A, 0, 0) == EUNSUP  # and in the scales
     W = ops.MoeBlockWeights
     gemm = lambda *a: lib.moe_block_gemm(ctypes.byref(ops.MoeBlockGemmArgs(*a)), None)
     assert gemm(4, 0, 0, None, A, A, W(1, 192, 128, A, A), A) == EUNSUP
@@ -140,7 +141,7 @@ def test_binding_checks_its_tensors():
     with pytest.raises(ValueError):
         moe.BlockWeights.empty(1, 130, 128, device="cpu")
     w = moe.BlockWeights.empty(2, 128, 256, device="cpu")
-    q = moe.BlockRows(torch.zeros((2, 8, 128), dtype=torch.uint8), torch.zeros((8, 2)))
+    q = moe.BlockRows(torch.zeros((2, 8, 128), dtype=torch.uint8), torch.zeros((8, 4)))
     with pytest.raises(ValueError):
         moe.block_product(q, w)                      # two experts without groups
     with pytest.raises(ValueError):
