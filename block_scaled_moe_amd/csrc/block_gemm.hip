@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const BlockGemmArgs p) {
                 lds_barrier();
                 if ((s & 3) == 0 && s + 4 < n) copy_s(cur, s + 4);
                 if (s > 0 && s + 1 < n) copy_x(cur, s + 1);
-                if (s + 3 < n) copy_w(s + 3, wc);
+                if (MSA < 2 && s + 3 < n) copy_w(s + 3, wc);
                 if (s == 0 && more) announce(next);
                 if constexpr (MSA > 0) {
                     const uint8_t *x = xb + (s & 1) * kX + (16 * wm + i16) * 128;
@@ -262,6 +262,7 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const BlockGemmArgs p) {
                             __builtin_amdgcn_sched_barrier(0);
                         }
                         f_prev = fi;
+                        if (i == 1 && s + 3 < n) copy_w(s + 3, wc);  // not in one burst with the rows
                     }
                     f_last = f_prev;
                 }
@@ -331,9 +332,94 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const BlockGemmArgs p) {
     }
 }
 
+// Few rows per group (decode): bound by the weights' bytes, with the tile kernel's 256-column items
+// too few to go round the CUs. A workgroup takes 32 columns of one tile of rows, its four waves a
+// quarter of the blocks each; weights go straight into registers, 16 bytes a lane and 512 bytes in a
+// row over 32 lanes, kUnroll blocks' loads ahead of the products, and the four partial sums meet in
+// LDS in the waves' order. More than 16 rows take further turns.
+constexpr int kUnroll = 4;
+
+__global__ void __launch_bounds__(256) stream_kernel(const BlockGemmArgs p) {
+    __shared__ __attribute__((aligned(16))) float part[4][16][36];
+    const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
+    const int i16 = lane & 15, g = lane >> 4;
+    const int n = p.R / 128, nb = p.C / 32;
+    const int n_tiles = p.v.offsets ? scalar_load(&p.v.ctrl->n_tiles) : p.v.max_tiles;
+    const int tile = blockIdx.x / nb, cb = blockIdx.x % nb;
+    if (tile >= n_tiles) return;
+    int e = 0, p0 = tile * kBM, rows = p.v.rows - p0;
+    if (p.v.offsets) {
+        e = scalar_load(p.v.tile_expert + tile);
+        p0 = scalar_load(p.v.tile_row0 + tile);
+        rows = scalar_load(p.v.offsets + e + 1) - p0;
+    }
+    rows = min(rows, kBM);
+    // columns 16 q + i16 of the 32, pieces g of both halves of a block
+    const uint8_t *w = uniform(p.w_codes + e * p.w_expert_bytes + (int64_t)cb * (p.R / 64) * 2048);
+    const uint32_t w_lane = g * 512 + i16 * 16;
+    const float *sw = uniform(p.w_scales + (int64_t)e * p.w_expert_scales + cb / 4 * p.w_kb);
+    const int64_t x_step = (int64_t)p.x_rows * 128;
+    for (int m0 = 0; m0 < rows; m0 += 16) {
+        const int pos = p0 + min(m0 + i16, rows - 1);
+        const uint32_t row = p.by_token ? p.v.sorted_slot[pos] / p.v.top_k : pos;
+        const uint8_t *x = p.x_codes + row * 128 + g * 16;
+        const float *sx = p.x_scales + (int64_t)row * scale_stride(p.R);
+        f4 acc[2] = {};
+        for (int b0 = wave; b0 < n; b0 += 4 * kUnroll) {
+            u32x4 wv[kUnroll][4], xv[kUnroll][2];
+            float f[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int b = min(b0 + 4 * u, n - 1);  // past the end: the last block again, with factor 0
+                const uint8_t *wb = w + (int64_t)b * 4096;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)  // column half j / 2, block half j % 2
+                    wv[u][j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wb + w_lane + (j >> 1) * 256 + (j & 1) * 2048));
+                xv[u][0] = *reinterpret_cast<const u32x4 *>(x + b * x_step);
+                xv[u][1] = *reinterpret_cast<const u32x4 *>(x + b * x_step + 64);
+                f[u] = b0 + 4 * u < n ? sx[b] * sw[b] : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const v8i xo = operand(xv[u][0], xv[u][1]);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const f4 d = block_dot(operand(wv[u][2 * q], wv[u][2 * q + 1]), xo);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) acc[q][v] = fmaf(d[v], f[u], acc[q][v]);
+                }
+            }
+        }
+        // accumulator v of read q: column 16 q + 4 g + v of row i16
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) *reinterpret_cast<f4 *>(&part[wave][i16][16 * q + 4 * g]) = acc[q];
+        __syncthreads();
+        const int r = t >> 4, c = 2 * (t & 15);
+        if (m0 + r < rows) {
+            float a = part[0][r][c], b = part[0][r][c + 1];
+#pragma unroll
+            for (int k = 1; k < 4; ++k) {
+                a += part[k][r][c];
+                b += part[k][r][c + 1];
+            }
+            *reinterpret_cast<uint32_t *>(p.out + (int64_t)(p0 + m0 + r) * p.C + 32 * cb + c) = bf16_pair(a, b);
+        }
+    }
+}
+
 }  // namespace
 
+#ifndef STREAM_ROWS
+#define STREAM_ROWS 4
+#endif
 hipError_t launch_block_gemm(const BlockGemmArgs &a, bool transposed, hipStream_t s) {
+    if (!transposed && a.v.mean_rows < STREAM_ROWS) {
+        const int64_t groups = (int64_t)a.v.max_tiles * (a.C / 32);
+        if (groups > INT32_MAX) return hipErrorInvalidValue;
+        hipLaunchKernelGGL(stream_kernel, dim3((unsigned)groups), dim3(256), 0, s, a);
+        return hipGetLastError();
+    }
     const int64_t items = (int64_t)a.v.max_tiles * ((a.C + kBN - 1) / kBN);
     if (items > INT32_MAX - 8) return hipErrorInvalidValue;
     const unsigned grid = (unsigned)(items >= kMaxGrid ? kMaxGrid : (items + 7) / 8 * 8);
