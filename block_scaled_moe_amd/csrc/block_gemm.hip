@@ -332,15 +332,16 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const BlockGemmArgs p) {
     }
 }
 
-// Few rows per group (decode): bound by the weights' bytes, with the tile kernel's 256-column items
-// too few to go round the CUs. A workgroup takes 32 columns of one tile of rows, its four waves a
-// quarter of the blocks each; weights go straight into registers, 16 bytes a lane and 512 bytes in a
-// row over 32 lanes, kUnroll blocks' loads ahead of the products, and the four partial sums meet in
-// LDS in the waves' order. More than 16 rows take further turns.
-constexpr int kUnroll = 4;
-
-__global__ void __launch_bounds__(256) stream_kernel(const BlockGemmArgs p) {
-    __shared__ __attribute__((aligned(16))) float part[4][16][36];
+// Few rows per group (decode): bound by the weights' bytes, and the tile kernel's items of 256
+// columns are too few to go round the CUs. A workgroup takes 32 columns of one tile of rows, its
+// four waves a quarter of the blocks each; weights go straight into registers, 16 bytes a lane from
+// 512 consecutive bytes an instruction's half, and the four partial sums meet in LDS in the waves'
+// order. Up to 16 rows have four blocks' loads ahead of the products, more rows share a turn's
+// weights in up to four pieces with fewer blocks ahead: 134 registers, three workgroups a CU (four
+// blocks ahead of two pieces or two ahead of four cost that and 5 %). One token through 8 of 64
+// experts, 5120 x 4096: 28 us for 168 MB (6.0 TB/s); 64 tokens, 96 of 384 experts: 202 us.
+__global__ void __launch_bounds__(256, 3) stream_kernel(const BlockGemmArgs p) {
+    __shared__ __attribute__((aligned(16))) float part[4][64][36];
     const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
     const int i16 = lane & 15, g = lane >> 4;
     const int n = p.R / 128, nb = p.C / 32;
@@ -359,62 +360,90 @@ __global__ void __launch_bounds__(256) stream_kernel(const BlockGemmArgs p) {
     const uint32_t w_lane = g * 512 + i16 * 16;
     const float *sw = uniform(p.w_scales + (int64_t)e * p.w_expert_scales + cb / 4 * p.w_kb);
     const int64_t x_step = (int64_t)p.x_rows * 128;
-    for (int m0 = 0; m0 < rows; m0 += 16) {
-        const int pos = p0 + min(m0 + i16, rows - 1);
-        const uint32_t row = p.by_token ? p.v.sorted_slot[pos] / p.v.top_k : pos;
-        const uint8_t *x = p.x_codes + row * 128 + g * 16;
-        const float *sx = p.x_scales + (int64_t)row * scale_stride(p.R);
-        f4 acc[2] = {};
-        for (int b0 = wave; b0 < n; b0 += 4 * kUnroll) {
-            u32x4 wv[kUnroll][4], xv[kUnroll][2];
-            float f[kUnroll];
+    // MT pieces of 16 rows from m0 on, UNROLL blocks' loads ahead of the products
+    auto turn = [&](int m0, auto mt_c, auto unroll_c) __attribute__((always_inline)) {
+        constexpr int MT = decltype(mt_c)::value, UNROLL = decltype(unroll_c)::value;
+        const uint8_t *x[MT];
+        const float *sx[MT];
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
+        for (int m = 0; m < MT; ++m) {
+            const int pos = p0 + min(m0 + 16 * m + i16, rows - 1);
+            const uint32_t row = p.by_token ? p.v.sorted_slot[pos] / p.v.top_k : pos;
+            x[m] = p.x_codes + row * 128 + g * 16;
+            sx[m] = p.x_scales + (int64_t)row * scale_stride(p.R);
+        }
+        f4 acc[MT][2] = {};
+        for (int b0 = wave; b0 < n; b0 += 4 * UNROLL) {
+            u32x4 wv[UNROLL][4], xv[UNROLL][MT][2];
+            float f[UNROLL][MT];
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {
                 const int b = min(b0 + 4 * u, n - 1);  // past the end: the last block again, with factor 0
                 const uint8_t *wb = w + (int64_t)b * 4096;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)  // column half j / 2, block half j % 2
-                    wv[u][j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wb + w_lane + (j >> 1) * 256 + (j & 1) * 2048));
-                xv[u][0] = *reinterpret_cast<const u32x4 *>(x + b * x_step);
-                xv[u][1] = *reinterpret_cast<const u32x4 *>(x + b * x_step + 64);
-                f[u] = b0 + 4 * u < n ? sx[b] * sw[b] : 0.0f;
-            }
+                    wv[u][j] = __builtin_nontemporal_load(
+                        reinterpret_cast<const u32x4 *>(wb + w_lane + (j >> 1) * 256 + (j & 1) * 2048));
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const v8i xo = operand(xv[u][0], xv[u][1]);
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const f4 d = block_dot(operand(wv[u][2 * q], wv[u][2 * q + 1]), xo);
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) acc[q][v] = fmaf(d[v], f[u], acc[q][v]);
+                for (int m = 0; m < MT; ++m) {
+                    xv[u][m][0] = *reinterpret_cast<const u32x4 *>(x[m] + b * x_step);
+                    xv[u][m][1] = *reinterpret_cast<const u32x4 *>(x[m] + b * x_step + 64);
+                    f[u][m] = b0 + 4 * u < n ? sx[m][b] * sw[b] : 0.0f;
                 }
             }
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const v8i xo = operand(xv[u][m][0], xv[u][m][1]);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const f4 d = block_dot(operand(wv[u][2 * q], wv[u][2 * q + 1]), xo);
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) acc[m][q][v] = fmaf(d[v], f[u][m], acc[m][q][v]);
+                    }
+                }
         }
-        // accumulator v of read q: column 16 q + 4 g + v of row i16
+        // accumulator v of read q: column 16 q + 4 g + v of row 16 m + i16
         __syncthreads();
 #pragma unroll
-        for (int q = 0; q < 2; ++q) *reinterpret_cast<f4 *>(&part[wave][i16][16 * q + 4 * g]) = acc[q];
-        __syncthreads();
-        const int r = t >> 4, c = 2 * (t & 15);
-        if (m0 + r < rows) {
-            float a = part[0][r][c], b = part[0][r][c + 1];
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int k = 1; k < 4; ++k) {
-                a += part[k][r][c];
-                b += part[k][r][c + 1];
+            for (int q = 0; q < 2; ++q) *reinterpret_cast<f4 *>(&part[wave][16 * m + i16][16 * q + 4 * g]) = acc[m][q];
+        __syncthreads();
+        const int c = 2 * (t & 15);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int r = 16 * m + (t >> 4);
+            if (m0 + r < rows) {
+                float a = part[0][r][c], b = part[0][r][c + 1];
+#pragma unroll
+                for (int k = 1; k < 4; ++k) {
+                    a += part[k][r][c];
+                    b += part[k][r][c + 1];
+                }
+                *reinterpret_cast<uint32_t *>(p.out + (int64_t)(p0 + m0 + r) * p.C + 32 * cb + c) = bf16_pair(a, b);
             }
-            *reinterpret_cast<uint32_t *>(p.out + (int64_t)(p0 + m0 + r) * p.C + 32 * cb + c) = bf16_pair(a, b);
         }
-    }
+    };
+    using std::integral_constant;
+    int m0 = 0;
+    for (; rows - m0 > 32; m0 += 64) turn(m0, integral_constant<int, 4>{}, integral_constant<int, 1>{});
+    if (rows - m0 > 16) turn(m0, integral_constant<int, 2>{}, integral_constant<int, 2>{});
+    else if (rows > m0) turn(m0, integral_constant<int, 1>{}, integral_constant<int, 4>{});
 }
 
 }  // namespace
 
-#ifndef STREAM_ROWS
-#define STREAM_ROWS 4
-#endif
+// The stream kernel from here down; 5120 x 4096, stream against tile kernel. 96 experts of 384, top 8,
+// even routing: 64 tokens 202 : 243 us, 256 292 : 350, 384 303 : 347; but with a few hot experts (rows
+// of one group take turns over its weights) 256 tokens 295 : 292, 448 403 : 338, so the grouped limit
+// stays below the even crossing. One group: 16 rows 9.1 : 18.7, 64 17.3 : 25.9, 96 26.4 : 30.0, 128
+// 32.1 : 33.3.
+constexpr int kStreamMean = 5, kStreamRows = 96;
+
 hipError_t launch_block_gemm(const BlockGemmArgs &a, bool transposed, hipStream_t s) {
-    if (!transposed && a.v.mean_rows < STREAM_ROWS) {
+    if (!transposed && a.v.mean_rows <= (a.v.offsets ? kStreamMean : kStreamRows)) {
         const int64_t groups = (int64_t)a.v.max_tiles * (a.C / 32);
         if (groups > INT32_MAX) return hipErrorInvalidValue;
         hipLaunchKernelGGL(stream_kernel, dim3((unsigned)groups), dim3(256), 0, s, a);

@@ -284,6 +284,17 @@ def test_product(counts, N, K):
     assert (num(buf)[T:] == 3.0).all()
 
 
+FEW = [([0, 5, 16, 17] + [0] * 20, 256, 640), ([33, 64, 65] + [0] * 40, 128, 1152), ([300] + [0] * 59, 128, 256),
+       ([1] * 7 + [100] + [2] * 40, 384, 128), ([224, 225] + [0] * 90, 128, 1664)]
+
+
+@pytest.mark.parametrize("counts,N,K", FEW, ids=lambda v: str(v)[:20])
+def test_product_few_rows_on_average(counts, N, K):
+    """Groups of few rows on average (a decode batch), some with many rows, and blocks that the four waves share unevenly."""
+    assert sum(counts) // len(counts) <= 5
+    test_product(counts, N, K)
+
+
 @pytest.mark.parametrize("counts,N,K", GEMMS, ids=str)
 def test_product_gradients(counts, N, K):
     rng, g, off, ss, wq, (wc, ws), expert = setup_product(counts, N, K, sum(counts) + K)
@@ -305,7 +316,7 @@ def test_product_gradients(counts, N, K):
     assert (dw[np.array(counts) == 0] == 0).all()
 
 
-@pytest.mark.parametrize("M", [1, 16, 17, 300, 513])
+@pytest.mark.parametrize("M", [1, 16, 17, 48, 65, 96, 97, 300, 513])
 def test_one_group(M):
     """Without groups: a dense projection and its gradients."""
     rng = np.random.default_rng(M)
