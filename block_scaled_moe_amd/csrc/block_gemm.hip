@@ -443,9 +443,8 @@ __global__ void __launch_bounds__(256, 3) stream_kernel(const BlockGemmArgs p) {
 constexpr int kStreamMean = 5, kStreamRows = 96;
 
 hipError_t launch_block_gemm(const BlockGemmArgs &a, bool transposed, hipStream_t s) {
-    if (!transposed && a.v.mean_rows <= (a.v.offsets ? kStreamMean : kStreamRows)) {
-        const int64_t groups = (int64_t)a.v.max_tiles * (a.C / 32);
-        if (groups > INT32_MAX) return hipErrorInvalidValue;
+    const int64_t groups = (int64_t)a.v.max_tiles * (a.C / 32);  // 2^24 workgroups are a grid's limit
+    if (!transposed && a.v.mean_rows <= (a.v.offsets ? kStreamMean : kStreamRows) && groups < 1 << 24) {
         hipLaunchKernelGGL(stream_kernel, dim3((unsigned)groups), dim3(256), 0, s, a);
         return hipGetLastError();
     }

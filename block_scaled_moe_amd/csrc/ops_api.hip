@@ -61,6 +61,24 @@ int32_t check_groups(const moe_groups *g) {
     return MOE_OK;
 }
 
+// The row operators' arguments beside their groups: tokens below 2^24 (workgroups of a grid), rows of
+// up to 2^30 elements.
+int32_t check_rows(const moe_groups *g, int32_t D) {
+    if (D < 1) return MOE_ERR_INVALID_ARG;
+    return g->T < (1 << 24) && D <= (1 << 30) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+
+// Buffers a and b of rows of D elements overlap.
+struct Rows {
+    const void *p;
+    int64_t rows;
+    int32_t dtype;
+};
+bool overlap(int32_t D, const Rows &a, const Rows &b) {
+    const auto end = [&](const Rows &r) { return (uintptr_t)r.p + (uintptr_t)r.rows * D * (r.dtype == MOE_DT_BF16 ? 2 : 4); };
+    return (uintptr_t)a.p < end(b) && (uintptr_t)b.p < end(a);
+}
+
 bool dtype_ok(int32_t d) { return d == MOE_DT_BF16 || d == MOE_DT_FP32; }
 
 GroupView group_view(const moe_groups *g, int32_t rows) {
@@ -134,20 +152,26 @@ int32_t moe_sort(const moe_groups *g, const int32_t *topk_idx, void *stream) {
 int32_t moe_gather(const moe_groups *g, int32_t dtype, int32_t D, const void *x, void *rows, void *stream) {
     const int32_t rc = check_groups(g);
     if (rc != MOE_OK) return rc;
-    if (!dtype_ok(dtype) || D < 1) return MOE_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
+    const int32_t rr = check_rows(g, D);
+    if (rr != MOE_OK) return rr;
     if (g->T == 0) return MOE_OK;
     if (!x || !rows) return MOE_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(rows)) return MOE_ERR_ALIGNMENT;
+    if (overlap(D, {x, g->T, dtype}, {rows, (int64_t)g->T * g->top_k, dtype})) return MOE_ERR_INVALID_ARG;
     return to_status(launch_gather(*g, dtype, D, x, rows, (hipStream_t)stream));
 }
 
 int32_t moe_gather_backward(const moe_groups *g, int32_t dtype, int32_t D, const void *d_rows, void *dx, void *stream) {
     const int32_t rc = check_groups(g);
     if (rc != MOE_OK) return rc;
-    if (!dtype_ok(dtype) || D < 1) return MOE_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
+    const int32_t rr = check_rows(g, D);
+    if (rr != MOE_OK) return rr;
     if (g->T == 0) return MOE_OK;
     if (!d_rows || !dx) return MOE_ERR_INVALID_ARG;
     if (!aligned16(d_rows) || !aligned16(dx)) return MOE_ERR_ALIGNMENT;
+    if (overlap(D, {dx, g->T, dtype}, {d_rows, (int64_t)g->T * g->top_k, dtype})) return MOE_ERR_INVALID_ARG;
     return to_status(launch_combine_rows(*g, dtype, dtype, D, d_rows, nullptr, dx, (hipStream_t)stream));
 }
 
@@ -155,10 +179,13 @@ int32_t moe_combine(const moe_groups *g, int32_t y_dtype, int32_t out_dtype, int
                     void *out, void *stream) {
     const int32_t rc = check_groups(g);
     if (rc != MOE_OK) return rc;
-    if (!dtype_ok(y_dtype) || !dtype_ok(out_dtype) || D < 1) return MOE_ERR_INVALID_ARG;
+    if (!dtype_ok(y_dtype) || !dtype_ok(out_dtype)) return MOE_ERR_INVALID_ARG;
+    const int32_t rr = check_rows(g, D);
+    if (rr != MOE_OK) return rr;
     if (g->T == 0) return MOE_OK;
     if (!y || !w || !out) return MOE_ERR_INVALID_ARG;
     if (!aligned16(y) || !aligned16(w) || !aligned16(out)) return MOE_ERR_ALIGNMENT;
+    if (overlap(D, {out, g->T, out_dtype}, {y, (int64_t)g->T * g->top_k, y_dtype})) return MOE_ERR_INVALID_ARG;
     return to_status(launch_combine_rows(*g, y_dtype, out_dtype, D, y, w, out, (hipStream_t)stream));
 }
 
@@ -166,11 +193,16 @@ int32_t moe_combine_backward(const moe_groups *g, int32_t y_dtype, int32_t out_d
                              const void *y, const float *w, void *d_y, float *d_w, void *stream) {
     const int32_t rc = check_groups(g);
     if (rc != MOE_OK) return rc;
-    if (!dtype_ok(y_dtype) || !dtype_ok(out_dtype) || D < 1) return MOE_ERR_INVALID_ARG;
+    if (!dtype_ok(y_dtype) || !dtype_ok(out_dtype)) return MOE_ERR_INVALID_ARG;
+    const int32_t rr = check_rows(g, D);
+    if (rr != MOE_OK) return rr;
     if (g->T == 0) return MOE_OK;
-    if (!d_out || !y || !w || !d_y || !d_w || d_y == y) return MOE_ERR_INVALID_ARG;
+    if (!d_out || !y || !w || !d_y || !d_w) return MOE_ERR_INVALID_ARG;
     if (!aligned16(d_out) || !aligned16(y) || !aligned16(w) || !aligned16(d_y) || !aligned16(d_w))
         return MOE_ERR_ALIGNMENT;
+    const int64_t slots = (int64_t)g->T * g->top_k;
+    if (overlap(D, {d_y, slots, y_dtype}, {y, slots, y_dtype}) || overlap(D, {d_y, slots, y_dtype}, {d_out, g->T, out_dtype}))
+        return MOE_ERR_INVALID_ARG;
     return to_status(launch_combine_backward(*g, y_dtype, out_dtype, D, d_out, y, w, d_y, d_w, (hipStream_t)stream));
 }
 
@@ -181,7 +213,7 @@ int64_t moe_block_column_blocks(int32_t rows, int32_t n) {
 
 int32_t moe_block_quantize(const moe_block_quantize_args *q, void *stream) {
     if (!q || q->rows < 0 || q->C < 1) return MOE_ERR_INVALID_ARG;
-    if (q->C % 128) return MOE_ERR_UNSUPPORTED;
+    if (q->C % 128 || q->C > kMaxBlockDim) return MOE_ERR_UNSUPPORTED;
     const bool by_rows = q->codes || q->scales, by_columns = q->col_codes || q->col_scales;
     if (!by_rows && !by_columns) return MOE_ERR_INVALID_ARG;
     if (by_rows && (!q->codes || !q->scales)) return MOE_ERR_INVALID_ARG;
@@ -217,9 +249,10 @@ int32_t moe_block_quantize(const moe_block_quantize_args *q, void *stream) {
 // Sizes and buffers of weights [E][N][K].
 static int32_t check_weights(int32_t E, int32_t N, int32_t K, const void *codes, const void *scales) {
     if (E < 1 || N < 1 || K < 1) return MOE_ERR_INVALID_ARG;
-    if (N % 128 || K % 128) return MOE_ERR_UNSUPPORTED;
+    if (N % 128 || K % 128 || N > kMaxBlockDim || K > kMaxBlockDim) return MOE_ERR_UNSUPPORTED;
     if (!codes || !scales) return MOE_ERR_INVALID_ARG;
-    if (!aligned16(codes) || !aligned16(scales)) return MOE_ERR_ALIGNMENT;
+    // the scales are read one at a time: those of an expert in the middle are as good as the first's
+    if (!aligned16(codes) || ((uintptr_t)scales & 3u)) return MOE_ERR_ALIGNMENT;
     return MOE_OK;
 }
 
@@ -252,6 +285,7 @@ int32_t moe_block_gemm(const moe_block_gemm_args *a, void *stream) {
     } else if (a->by_token || a->w.E != 1) {
         return MOE_ERR_INVALID_ARG;
     }
+    if (a->by_token && a->transposed) return MOE_ERR_INVALID_ARG;  // gradients come in sorted rows
     if (!rows_form_fits(a->rows, a->transposed ? a->w.N : a->w.K)) return MOE_ERR_UNSUPPORTED;
     if (a->rows == 0) return MOE_OK;
     if (!a->x_codes || !a->x_scales || !a->out) return MOE_ERR_INVALID_ARG;
@@ -275,7 +309,7 @@ int32_t moe_block_gemm(const moe_block_gemm_args *a, void *stream) {
 
 int32_t moe_block_wgrad(const moe_block_wgrad_args *a, void *stream) {
     if (!a || a->rows < 0 || a->N < 1 || a->K < 1) return MOE_ERR_INVALID_ARG;
-    if (a->N % 128 || a->K % 128) return MOE_ERR_UNSUPPORTED;
+    if (a->N % 128 || a->K % 128 || a->N > kMaxBlockDim || a->K > kMaxBlockDim) return MOE_ERR_UNSUPPORTED;
     if (a->g) {
         const int32_t rc = check_groups(a->g);
         if (rc != MOE_OK) return rc;

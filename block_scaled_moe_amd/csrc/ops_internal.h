@@ -9,6 +9,8 @@ namespace moe {
 
 // Rows per work-list tile of the grouped products; the lists are written by moe_sort.
 constexpr int32_t kGroupTile = 224;
+// Largest dimension that blocks of 128 run along (32-bit byte offsets of 128 of its columns).
+constexpr int32_t kMaxBlockDim = 1 << 24;
 
 // Byte offsets inside moe_groups::plan.
 struct GroupsPlan {

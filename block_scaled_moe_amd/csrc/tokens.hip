@@ -224,7 +224,10 @@ Span make_span(int32_t T, int32_t pieces, bool whole_rows, dim3 &grid) {
     sp.per_block = pieces;
     const int tokens = kThreads >> sp.log_lanes;  // per workgroup
     grid.x = (unsigned)((T + tokens - 1) / tokens);
-    if (!whole_rows && grid.x < 1024) sp.per_block = 1 << sp.log_lanes;
+    if (!whole_rows && grid.x < 1024) {  // a grid has at most 65535 in y
+        const int lanes = 1 << sp.log_lanes;
+        sp.per_block = ((pieces - 1) / (65535 * lanes) + 1) * lanes;
+    }
     grid.y = (unsigned)((pieces + sp.per_block - 1) / sp.per_block);
     return sp;
 }

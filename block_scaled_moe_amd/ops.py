@@ -11,6 +11,8 @@ ValueError before the call; tensors are contiguous.
     out = combine(g, y, topk_w)
 
 Arrays of sorted rows have T * top_k rows; rows behind the last local one keep what they hold.
+As with torch's own operators, a tensor (or Groups.buffer) that is used on another stream than its
+own needs record_stream before it is freed.
 """
 from __future__ import annotations
 
@@ -130,6 +132,7 @@ class Groups:
         slots, pos, plan, end = self._at
         self.buffer = torch.empty(end // 4, dtype=torch.int32, device=device)
         self.device = self.buffer.device
+        self.filled = False  # by sort_tokens
         base = self.buffer.data_ptr()
         self.struct = MoeGroups(T, top_k, E, e_begin, e_end, base, base + slots, base + pos, base + plan, end - plan)
         self.ref, self.pointer = ctypes.byref(self.struct), ctypes.pointer(self.struct)
@@ -183,7 +186,13 @@ def sort_tokens(topk_idx: torch.Tensor, E: int, e_begin: int = 0, e_end: int | N
     elif (out.T, out.top_k, out.E, out.e_begin, out.e_end, out.device) != (T, k, E, e_begin, e_end, topk_idx.device):
         raise ValueError("out: groups of other sizes or on another device")
     _call("moe_sort", out.device, out.ref, topk_idx.data_ptr())
+    out.filled = True
     return out
+
+
+def _filled(g: Groups | None):
+    if g is not None and not g.filled:
+        raise ValueError("groups that sort_tokens has not filled")
 
 
 def _row_width(what: str, t: torch.Tensor) -> int:
@@ -197,6 +206,7 @@ def gather(g: Groups, x: torch.Tensor, out: torch.Tensor | None = None) -> torch
     D = _row_width("x", x)
     _ask("x", x, (g.T, D), DTYPES, g.device)
     out = _out("out", out, (g.rows, D), x.dtype, g.device)
+    _filled(g)
     _call("moe_gather", g.device, g.ref, DTYPES[x.dtype], D, x.data_ptr(), out.data_ptr())
     return out
 
@@ -206,6 +216,7 @@ def gather_backward(g: Groups, d_rows: torch.Tensor, out: torch.Tensor | None = 
     D = _row_width("d_rows", d_rows)
     _ask("d_rows", d_rows, (g.rows, D), DTYPES, g.device)
     out = _out("out", out, (g.T, D), d_rows.dtype, g.device)
+    _filled(g)
     _call("moe_gather_backward", g.device, g.ref, DTYPES[d_rows.dtype], D, d_rows.data_ptr(),
           out.data_ptr())
     return out
@@ -221,6 +232,7 @@ def combine(g: Groups, y: torch.Tensor, w: torch.Tensor, out: torch.Tensor | Non
     if out is None and out_dtype not in DTYPES:
         raise ValueError(f"out_dtype: {out_dtype}")
     out = _out("out", out, (g.T, D), out_dtype if out is None else DTYPES, g.device)
+    _filled(g)
     _call("moe_combine", g.device, g.ref, DTYPES[y.dtype], DTYPES[out.dtype], D, y.data_ptr(),
           w.data_ptr(), out.data_ptr())
     return out
@@ -235,6 +247,7 @@ def combine_backward(g: Groups, d_out: torch.Tensor, y: torch.Tensor, w: torch.T
     _ask("d_out", d_out, (g.T, D), DTYPES, g.device)
     dy = _out("dy", dy, (g.rows, D), y.dtype, g.device)
     dw = _out("dw", dw, (g.T, g.top_k), torch.float32, g.device)
+    _filled(g)
     _call("moe_combine_backward", g.device, g.ref, DTYPES[y.dtype], DTYPES[d_out.dtype], D,
           d_out.data_ptr(), y.data_ptr(), w.data_ptr(), dy.data_ptr(), dw.data_ptr())
     return dy, dw
@@ -339,6 +352,7 @@ def _quantize(x: torch.Tensor, g: Groups | None, by_token: bool, rows: bool, col
         c = BlockColumns(torch.empty((n, C // 32, 2, 4, 32, 16), dtype=torch.uint8, device=dev),
                          torch.empty((n, C), dtype=torch.float32, device=dev))
         cc, cs = c.codes.data_ptr(), c.scales.data_ptr()
+    _filled(g)
     if R > 0:
         a = MoeBlockQuantizeArgs(R, C, by_token, None if g is None else g.pointer, x.data_ptr(), rc, rs, cc, cs)
         _call("moe_block_quantize", dev, ctypes.byref(a))
@@ -374,6 +388,7 @@ def _product(x: BlockRows, w: BlockWeights, g: Groups | None, by_token: bool, tr
     if g is None and by_token:
         raise ValueError("by_token needs groups")
     out = _out("out", out, (n_x if g is None else g.rows, C), torch.bfloat16, dev)
+    _filled(g)
     a = MoeBlockGemmArgs(n_x, by_token, transposed, None if g is None else g.pointer, x.codes.data_ptr(),
                          x.scales.data_ptr(), w.struct(dev), out.data_ptr())
     if n_x > 0:
@@ -410,6 +425,7 @@ def block_weight_grad(dy: BlockColumns, x: BlockColumns, g: Groups | None = None
         _ask(what + " codes", q.codes, (blocks, C // 32, 2, 4, 32, 16), torch.uint8, dev)
         _ask(what + " scales", q.scales, (blocks, C), torch.float32, dev)
     out = _out("out", out, (n, N, K), torch.bfloat16, dev)
+    _filled(g)
     a = MoeBlockWgradArgs(R, N, K, None if g is None else g.pointer, dy.codes.data_ptr(), dy.scales.data_ptr(),
                           x.codes.data_ptr(), x.scales.data_ptr(), out.data_ptr())
     _call("moe_block_wgrad", dev, ctypes.byref(a))

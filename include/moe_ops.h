@@ -55,7 +55,8 @@ size_t moe_groups_plan_bytes(const moe_groups *g);
 int32_t moe_sort(const moe_groups *g, const int32_t *topk_idx, void *stream);
 
 /* rows[p] = x[sorted_slot[p] / top_k] for p < S. x [T][D], rows [T * top_k][D], both of
- * type dtype (MOE_DT_*), D >= 1. */
+ * type dtype (MOE_DT_*). This call and the next three: T < 2^24, 1 <= D <= 2^30, and an
+ * output that overlaps the rows it is made from is refused. */
 int32_t moe_gather(const moe_groups *g, int32_t dtype, int32_t D, const void *x, void *rows, void *stream);
 
 /* Gradient of moe_gather: dx[t] = sum over the token's local slots, j ascending, of
@@ -71,14 +72,15 @@ int32_t moe_combine(const moe_groups *g, int32_t y_dtype, int32_t out_dtype, int
 /* Gradient of moe_combine for d_out [T][D] of out_dtype:
  *   d_y[slot_pos] = w[t][j] * d_out[t]  (rounded once to y_dtype; rows behind S untouched)
  *   d_w[t][j]     = sum over D of d_out[t] * y[slot_pos], fp32; 0 for a slot not local.
- * d_y must not overlap y. */
+ * d_y must not overlap y or d_out. */
 int32_t moe_combine_backward(const moe_groups *g, int32_t y_dtype, int32_t out_dtype, int32_t D, const void *d_out,
                              const void *y, const float *w, void *d_y, float *d_w, void *stream);
 
 /* ------------------------------------------------------------------ FP8, blocks of 128
  * E4M3 (OCP "FN") codes with one fp32 scale per block of 128: s = fl32(max |block| / 448),
  * 1 for an all-zero block; code = E4M3(fl32(x / s)), nearest, ties to even. The value is
- * code * s. All dimensions that blocks run along are multiples of 128.
+ * code * s. All dimensions that blocks run along are multiples of 128 up to 2^24. Outputs
+ * must not overlap inputs or each other.
  *   rows     codes [C/128][R][128] (the rows' first blocks, then their second ones, ..),
  *            scales [R][S], S = C/128 rounded up to a multiple of 4 (the rest of a row is
  *            neither written nor used): blocks of 1 x 128; R < 2^25 and R * S < 2^30
@@ -95,7 +97,7 @@ int32_t moe_combine_backward(const moe_groups *g, int32_t y_dtype, int32_t out_d
 typedef struct moe_block_weights {
     int32_t E, N, K;   /* N % 128 == 0, K % 128 == 0 */
     const uint8_t *codes;
-    const float *scales;
+    const float *scales;   /* 4-byte aligned: experts of a longer array may be given */
 } moe_block_weights;
 
 /* Runs of 128 rows (blocks) that the column form of `rows` sorted rows in `n` groups has
@@ -134,8 +136,8 @@ int32_t moe_block_pack_weights(const uint8_t *rowmajor, int32_t E, int32_t N, in
  * the largest of the products it adds (about 2^-16 of the sum's size on normally distributed
  * values, far below the E4M3 rounding of the operands and the bf16 rounding of the result);
  * the sum over blocks is in fp32 in a fixed order, with one rounding to bf16.
- * by_token: x has T rows and sorted row p reads row sorted_slot[p] / top_k; otherwise
- * rows = T * top_k, already sorted. W has n experts (the local ones). */
+ * by_token (not with transposed): x has T rows and sorted row p reads row sorted_slot[p] / top_k;
+ * otherwise rows = T * top_k, already sorted. W has n experts (the local ones). */
 typedef struct moe_block_gemm_args {
     int32_t rows;             /* rows of x */
     int32_t by_token, transposed;

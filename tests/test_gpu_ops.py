@@ -380,6 +380,41 @@ def test_gradients_against_differences():
         assert abs(diff - dw[3, k]) <= slack + (2.0 ** -4 + ref.U_BF16) * 448.0 * np.abs(x[:, k]).sum()
 
 
+def test_experts_out_of_a_longer_array():
+    """Weights whose scales do not start on 16 bytes: experts 1 .. 2 of four with one block each."""
+    rng = np.random.default_rng(3)
+    w, x = values(rng, (4, 128, 128), "bf16"), values(rng, (40, 128), "bf16")
+    wq = moe.quantize_block_weights(dev(w, torch.bfloat16))
+    out = moe.BlockWeights.empty(4, 128, 128)
+    for t in (out.codes, out.scales):
+        t.zero_()
+    moe.quantize_block_weights(dev(w[1:3], torch.bfloat16), out=out.experts(1, 3))
+    assert torch.equal(out.scales[1:3], wq.scales[1:3]) and torch.equal(out.codes[1:3], wq.codes[1:3])
+    assert not out.scales[0].any() and not out.codes[3].any()
+    wc, ws = ref.weights(w)
+    idx = rng.integers(0, 4, 40).astype(np.int32)
+    g = moe.sort_tokens(dev(idx.reshape(40, 1)), 4, 1, 3)
+    off, ss, _ = ref.sort(idx, 1, 3)
+    S = off[-1]
+    expert = np.repeat(np.arange(1, 3), np.diff(off))
+    y = num(moe.block_product(moe.quantize_block(dev(x, torch.bfloat16)), wq.experts(1, 3), g, by_token=True))
+    check(y[:S], *ref.product(*ref.rows(x[ss[:S]]), wc, ws, expert), "y")
+    d = moe.quantize_block(dev(np.concatenate([x[ss[:S]], x[S:]]), torch.bfloat16), g)
+    check(num(moe.block_product_grad(d, wq.experts(1, 3), g))[:S],
+          *ref.product(*ref.rows(x[ss[:S]]), wc, ws, expert, transposed=True), "dx")
+
+
+@pytest.mark.parametrize("D", [8 * 256 * 65535 + 8, 256 * 65535 + 3])
+def test_one_long_row(D):
+    """One token's row in more pieces than a grid has workgroups in y."""
+    g = moe.sort_tokens(dev(np.array([[1, 0]], np.int32)), 2)
+    x = torch.arange(D, device="cuda", dtype=torch.int32).bitwise_and_(127).to(torch.bfloat16).reshape(1, D)
+    rows = moe.gather(g, x)
+    assert torch.equal(rows[0], x[0]) and torch.equal(rows[1], x[0])
+    out = moe.combine(g, rows, torch.tensor([[1.0, 0.5]], device="cuda"), out_dtype=torch.bfloat16)
+    assert torch.equal(out[0], x[0] * 1.5)   # both the rounded exact product
+
+
 # ---------------------------------------------------------------- together
 
 def chain(h, wr, w1, w2, d_out, k, E, e0, e1):

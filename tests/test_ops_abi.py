@@ -75,6 +75,16 @@ def test_row_calls_refuse():
     assert lib.moe_combine(r, 1, 0, 64, A, A, A, None) == EINVAL and lib.moe_combine(r, 1, 1, 64, A, 0, A, None) == EINVAL
     assert lib.moe_combine_backward(r, 1, 1, 64, A, 2 * A, A, 2 * A, A, None) == EINVAL  # dy on top of y
     assert lib.moe_combine_backward(r, 1, 1, 64, A, A, A, 2 * A, A + 8, None) == EALIGN
+    B = A + 64 * 8 * 64 * 4  # behind the sorted rows
+    for x, rows in ((A, A), (A + 64 * 64 * 2 - 16, A), (A, A + 64 * 64 * 2 - 16)):  # on top of the other, wholly or in part
+        assert lib.moe_gather(r, 1, 64, x, rows, None) == EINVAL
+        assert lib.moe_gather_backward(r, 1, 64, rows, x, None) == EINVAL
+        assert lib.moe_combine(r, 1, 1, 64, rows, A, x, None) == EINVAL
+        assert lib.moe_combine_backward(r, 1, 1, 64, x, B, A, rows, B, None) == EINVAL
+        assert lib.moe_combine_backward(r, 1, 1, 64, B, x, A, rows, B, None) == EINVAL
+    assert lib.moe_gather(r, 1, (1 << 30) + 8, A, B, None) == EUNSUP
+    many = ctypes.byref(groups(T=1 << 24, plan_bytes=1 << 40))
+    assert lib.moe_gather(many, 1, 8, A, 1 << 60, None) == EUNSUP and lib.moe_combine(many, 1, 1, 8, A, A, 1 << 60, None) == EUNSUP
     empty = ctypes.byref(groups(T=0))
     assert lib.moe_gather(empty, 1, 64, 0, 0, None) == OK  # no tokens: nothing to do
 
@@ -99,6 +109,10 @@ def test_block_calls_refuse():
     assert gemm(4, 0, 0, None, A, A, W(1, 192, 128, A, A), A) == EUNSUP
     assert gemm(4, 0, 0, None, A, A, W(2, 128, 128, A, A), A) == EINVAL   # two experts, no groups
     assert gemm(4, 1, 0, None, A, A, W(1, 128, 128, A, A), A) == EINVAL
+    assert gemm(64, 1, 1, g, A, A, W(96, 128, 128, A, A), A) == EINVAL    # transposed by token
+    assert gemm(4, 0, 0, None, A, A, W(1, (1 << 24) + 128, 128, A, A), A) == EUNSUP
+    assert gemm(4, 0, 0, None, A, A, W(1, 128, 128, A, A + 2), A) == EALIGN
+    assert quant(4, (1 << 24) + 128, 0, None, A, 0, 0, A, A) == EUNSUP
     assert gemm(512, 0, 0, g, A, A, W(95, 128, 128, A, A), A) == EINVAL
     assert gemm(64, 0, 0, g, A, A, W(96, 128, 128, A, A), A) == EINVAL
     assert gemm(4, 0, 0, None, A, 0, W(1, 128, 128, A, A), A) == EINVAL
@@ -108,6 +122,7 @@ def test_block_calls_refuse():
     assert gemm(0, 0, 0, None, 0, 0, W(1, 128, 128, A, A), 0) == OK
     wgrad = lambda *a: lib.moe_block_wgrad(ctypes.byref(ops.MoeBlockWgradArgs(*a)), None)
     assert wgrad(4, 128, 100, None, A, A, A, A, A) == EUNSUP
+    assert wgrad(4, 128, (1 << 24) + 128, None, A, A, A, A, A) == EUNSUP
     assert wgrad(4, 128, 128, None, A, A, A, A, 0) == EINVAL
     assert wgrad(4, 128, 128, None, 0, A, A, A, A) == EINVAL
     assert wgrad(64, 128, 128, g, A, A, A, A, A) == EINVAL
@@ -150,6 +165,20 @@ def test_binding_checks_its_tensors():
         moe.block_product(q, w, g)                   # the groups have four experts
     with pytest.raises(ValueError):
         moe.block_weight_grad(moe.BlockColumns(q.codes, q.scales), moe.BlockColumns(q.codes, q.scales))
+
+
+def test_groups_that_were_not_sorted_are_refused():
+    g = moe.Groups.empty(4, 2, 8, 2, 6, device="cpu")
+    x, rows, w = torch.zeros((4, 128)), torch.zeros((8, 128)), torch.zeros((4, 2))
+    xb, bw = rows.bfloat16(), moe.BlockWeights.empty(4, 128, 128, device="cpu")
+    q = moe.BlockRows(torch.zeros((1, 8, 128), dtype=torch.uint8), torch.zeros((8, 4)))
+    c = moe.BlockColumns(torch.zeros((4, 4, 2, 4, 32, 16), dtype=torch.uint8), torch.zeros((4, 128)))
+    for call in (lambda: moe.gather(g, x), lambda: moe.gather_backward(g, rows), lambda: moe.combine(g, rows, w),
+                 lambda: moe.combine_backward(g, x, rows, w), lambda: moe.quantize_block(xb, g),
+                 lambda: moe.quantize_block_columns(xb[:4], g, by_token=True), lambda: moe.block_product(q, bw, g),
+                 lambda: moe.block_product_grad(q, bw, g), lambda: moe.block_weight_grad(c, c, g)):
+        with pytest.raises(ValueError, match="sort_tokens"):
+            call()
 
 
 def test_plain_forms_of_the_format():
