@@ -415,6 +415,39 @@ def test_one_long_row(D):
     assert torch.equal(out[0], x[0] * 1.5)   # both the rounded exact product
 
 
+def test_places_past_32_bits():
+    """Sorted rows of more than 2^31 values: the second expert's 300 rows, the last ones, give the bits that they
+    give alone."""
+    T, D, last = 530000, 4096, 300
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    idx = torch.zeros((T, 1), dtype=torch.int32, device="cuda")
+    pick = torch.randperm(T, device="cuda", generator=gen)[:last].sort().values
+    idx[pick] = 1
+    x = torch.randn((T, D), dtype=torch.bfloat16, device="cuda", generator=gen)
+    w = moe.quantize_block_weights(torch.randn((2, D, D), dtype=torch.bfloat16, device="cuda", generator=gen))
+    g = moe.sort_tokens(idx, 2)
+    one = moe.sort_tokens(torch.zeros((last, 1), dtype=torch.int32, device="cuda"), 1)
+    rows = moe.gather(g, x)
+    xs = x[pick]
+    assert rows.numel() > 2 ** 31 and torch.equal(rows[-last:], xs)
+    ones = torch.ones((T, 1), device="cuda")
+    out = moe.combine(g, rows, ones, out_dtype=torch.bfloat16)
+    assert torch.equal(out[pick], xs) and torch.equal(out[-1], x[-1])
+    dy, dw = moe.combine_backward(g, out, rows, ones)
+    assert torch.equal(dy[-last:], xs) and torch.equal(dw[pick], moe.combine_backward(one, xs, xs, ones[:last])[1])
+    del out, dy
+    q, c = moe.quantize_block_both(rows, g)
+    q1, c1 = moe.quantize_block_both(xs, one)
+    assert torch.equal(q.codes[:, -last:], q1.codes) and torch.equal(q.scales[-last:], q1.scales)
+    w1 = w.experts(1, 2)
+    y1 = moe.block_product(q1, w1, one)
+    assert torch.equal(moe.block_product(q, w, g)[-last:], y1)
+    assert torch.equal(moe.block_product(moe.quantize_block(x), w, g, by_token=True)[-last:], y1)
+    assert torch.equal(moe.block_product_grad(q, w, g)[-last:], moe.block_product_grad(q1, w1, one))
+    assert torch.equal(moe.block_weight_grad(c, c, g)[1], moe.block_weight_grad(c1, c1, one)[0])
+
+
 # ---------------------------------------------------------------- together
 
 def chain(h, wr, w1, w2, d_out, k, E, e0, e1):
