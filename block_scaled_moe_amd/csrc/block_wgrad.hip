@@ -10,21 +10,25 @@
 //
 // An expert has few runs (its rows / 128), so an item is mostly its 128 KiB of output: bound by
 // the writes of dw, with the copies of a run (64 KiB) and its products behind them. One workgroup
-// per CU walks its items; the runs of all of them make one sequence of steps, and a step's buffer
-// is refilled for the step after next, of this item or of a later one, as soon as every wave is
-// done with it. A wave's vector memory operations complete in order, so a step waits for its own
-// copies by the number of copies and stores issued behind them, and the stores of an item drain
-// under the next steps. A lane swaps half its outputs with its neighbour, so that every store
-// instruction writes whole 128-byte lines, which go past L2 (non-temporal) and leave the operands
-// there.
+// per CU walks its items; the runs of all of them make one sequence of steps. A step's copies go to
+// the buffer of the step before it, a quarter behind each of the first pieces' products of the step
+// in between: one barrier a step, and no burst of copies that the waves wait to issue. A wave's vector memory
+// operations complete in order, so a step waits for its own copies by the number of stores issued
+// behind them, and the stores of an item drain under the next steps. A lane swaps half its outputs
+// with its neighbour, so that every store instruction writes whole 128-byte lines, which go past
+// L2 (non-temporal) and leave the operands there.
 //
-// 96 experts of 4096 x 2560, 16384 rows unevenly routed: 590 us, of which the stores alone are 340 us
-// (2.0 GB, 5.9 TB/s) and the steps alone 325 us (the products 150 us of them). The two hardly overlap:
-// copies that a CU issues behind its stores wait until those have drained. Tiles of 128 x 256 with
-// two workgroups a CU took 600 us, 128 x 128 690 us, sweeps along k that keep the block of n in LDS
-// 700 us (uneven experts), ordinary stores 620 us.
+// 96 experts of 4096 x 2560, 16384 rows unevenly routed: 508 us, of which the stores alone are 340 to
+// 380 us (2.0 GB, up to 5.9 TB/s), the copies alone 130 us and the products about 200 us (as many
+// cycles of the vector unit: each MFMA's four results take four products of scales and four multiply-adds).
+// Stores overlap with products, but hardly with copies of the same CU: stores spread over the next
+// item's first step, among its copies, took 615 us, a step's copies in one burst behind the step before
+// 590 us; tiles of 128 x 256 with two workgroups a CU 600 us, sweeps along k that keep the block of n
+// in LDS 700 us (uneven experts), ordinary stores 546 us, an expert on one XCD instead of eight 603 us.
 #include "block_mma.h"
 #include "ops_internal.h"
+
+#include <type_traits>
 
 namespace moe {
 namespace {
@@ -32,7 +36,6 @@ namespace {
 using namespace block;
 
 constexpr int kThreads = 512, kB = 256, kOperand = kB * 128, kMaxGrid = 256;
-constexpr int kCopies = 8;  // of a step by a wave (the two that copy scales: nine)
 
 __global__ void __launch_bounds__(kThreads) wgrad_kernel(const BlockWgradArgs p) {
     __shared__ __attribute__((aligned(16))) uint8_t gb[2 * kOperand];
@@ -81,20 +84,18 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(const BlockWgradArgs p)
     // Only 128 of a block's 256 columns may exist: they are copied twice then.
     auto n_half = [&](const Item &a) { return a.n0 + 128 >= N; };
     auto k_half = [&](const Item &a) { return a.k0 + 128 >= K; };
-    auto copy = [&](const Item &a, int s, int buffer) __attribute__((always_inline)) {
+    // a quarter of a step's copies
+    auto copy = [&](const Item &a, int s, int buffer, int j) __attribute__((always_inline)) {
         const int64_t run = a.run0 + s;
         const uint32_t b = buffer * kOperand, f = buffer * kB * 4;
         const uint8_t *x = p.x_codes + run * K * 128 + (int64_t)(a.k0 / 32 + (k_half(a) ? wave & 3 : wave)) * 4096;
         const uint8_t *n = p.g_codes + run * N * 128 + (int64_t)(a.n0 / 32 + (n_half(a) ? wave & 3 : wave)) * 4096;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            copy_to_lds(x + j * 1024, x_lane, x_lds + b + j * 1024);
-            copy_to_lds(n + j * 1024, lane * 16, g_lds + b + j * 1024);
-        }
-        if (wave == 0)
+        copy_to_lds(x + j * 1024, x_lane, x_lds + b + j * 1024);
+        copy_to_lds(n + j * 1024, lane * 16, g_lds + b + j * 1024);
+        if (j == 0 && wave == 0)
             copy_to_lds(reinterpret_cast<const uint8_t *>(p.x_scales + run * K + a.k0), (k_half(a) ? lane & 31 : lane) * 16,
                         sx_lds + f);
-        if (wave == 1)
+        if (j == 0 && wave == 1)
             copy_to_lds(reinterpret_cast<const uint8_t *>(p.g_scales + run * N + a.n0), (n_half(a) ? lane & 31 : lane) * 16,
                         sg_lds + f);
     };
@@ -123,30 +124,21 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(const BlockWgradArgs p)
             cs = 0;
         }
     };
-    // operations behind the copies of the next step to compute, and of the one after it
-    int behind0 = 0, behind1 = 0;
     advance();
     if (left) {
-        copy(c, cs, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) copy(c, cs, 0, j);
         advance();
-        if (left) {
-            copy(c, cs, 1);
-            behind0 = kCopies;
-            advance();
-        }
     }
-    int buffer = 0;
+    int buffer = 0, behind = 0;  // operations behind the copies of the next step to compute
     for (;;) {
         f4 acc[8][4];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) acc[i][q] = (f4){0.0f, 0.0f, 0.0f, 0.0f};
-
-#pragma clang loop unroll(disable)
-        for (int s = 0; s < cur.runs; ++s) {
-            wait(behind0);
-            lds_barrier();
+        // the first step sets the accumulators, the others add to them
+        auto run_step = [&](auto first_c) __attribute__((always_inline)) {
+            constexpr bool FIRST = decltype(first_c)::value;
+            wait(behind);
+            lds_barrier();  // and every wave is done with the other buffer
+            behind = 0;
             const uint8_t *xl = xb + buffer * kOperand, *gl = gb + buffer * kOperand;
             const float *sx = sxb + buffer * kB, *sg = sgb + buffer * kB + 16 * wm + i16;
             // n = n0 + 16 (2 i + wm) + i16, k = k0 + 64 wn + 32 (q / 2) + 8 g + 4 (q % 2) + v
@@ -168,7 +160,8 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(const BlockWgradArgs p)
             auto add = [&](int m) __attribute__((always_inline)) {
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
-                    acc[m / 4][m % 4][v] = fmaf(d[m % 3][v], fx[m % 4][v] * f[m / 4], acc[m / 4][m % 4][v]);
+                    acc[m / 4][m % 4][v] = FIRST ? d[m % 3][v] * (fx[m % 4][v] * f[m / 4])
+                                                 : fmaf(d[m % 3][v], fx[m % 4][v] * f[m / 4], acc[m / 4][m % 4][v]);
                 pin(acc[m / 4][m % 4]);
             };
             v8i gv = g_operand(0);
@@ -188,24 +181,27 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(const BlockWgradArgs p)
                     if (m >= 2) add(m - 2);
                     __builtin_amdgcn_sched_barrier(0);
                 }
+                if (i < 4 && left) copy(c, cs, buffer ^ 1, i);
             }
             add(30);
             add(31);
-            lds_barrier();  // every wave is done with the buffer
-            behind0 = behind1;
-            behind1 = 0;
-            if (left) {
-                copy(c, cs, buffer);
-                behind0 += kCopies;
-                advance();
-            }
+            if (left) advance();
             buffer ^= 1;
+        };
+        if (cur.runs > 0) {
+            run_step(std::true_type{});
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[i][q] = (f4){0.0f, 0.0f, 0.0f, 0.0f};
         }
+#pragma clang loop unroll(disable)
+        for (int s = 1; s < cur.runs; ++s) run_step(std::false_type{});
 
         if (!k_half(cur) || wn < 2) {
             const int stores = n_half(cur) ? 8 : 16;
-            behind0 += stores;
-            behind1 += stores;
+            behind += stores;
             uint8_t *o = reinterpret_cast<uint8_t *>(p.dw + ((int64_t)cur.e * N + cur.n0) * K + cur.k0);
             // row pair i16 & ~1 of a piece, this lane's eight of its 64 k
             const bool odd = i16 & 1;
