@@ -239,14 +239,14 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const BlockGemmArgs p) {
                                        *reinterpret_cast<const u32x4 *>(q + (((4 + g) ^ (i16 & 7)) * 16)));
                     };
                     v8i xf = x_operand(0);
-                    float f = fs[0] * fw, f_prev = f_last;
+                    float f = fs[0], f_prev = f_last;
 #pragma unroll
                     for (int i = 0; i < MSA; ++i) {
                         const v8i xi = xf;
-                        const float fi = f;
+                        const float fi = f * fw;
                         if (i + 1 < MSA) {
                             xf = x_operand(i + 1);
-                            f = fs[128 * (i + 1)] * fw;
+                            f = fs[128 * (i + 1)];  // times fw a piece later, when it is there
                         }
                         // the next block's weights: one read a piece, the rest with the last
 #pragma unroll
@@ -257,6 +257,7 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const BlockGemmArgs p) {
                             const int u = 4 * i + q;
                             d[q] = block_dot(wf[H][q], xi);
                             pin(d[q]);
+                            __builtin_amdgcn_sched_barrier(0);  // the sums behind the MFMA, not before it
                             if (q < 2) add((u + U - 2) % U, f_prev);
                             else add(u - 2, fi);
                             __builtin_amdgcn_sched_barrier(0);

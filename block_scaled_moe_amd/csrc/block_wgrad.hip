@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(const BlockWgradArgs p)
                     const int m = 4 * i + q;
                     d[m % 3] = block_dot(xf[q], gi);
                     pin(d[m % 3]);
+                    __builtin_amdgcn_sched_barrier(0);  // the sums behind the MFMA, not before it
                     if (m >= 2) add(m - 2);
                     __builtin_amdgcn_sched_barrier(0);
                 }
