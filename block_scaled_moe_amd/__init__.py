@@ -9,6 +9,10 @@ The layer (vLLM recipe "thinkingmachines/Inkling-2-Small", section "Overview"; A
 Primer "Thinking Machines releases Inkling 2 Small weights under Apache 2.0",
 sections "TL;DR" and "NVFP4 and MXFP8 experts"): top-8 of 384 routed experts, no
 shared expert, NVFP4 or MXFP8 experts with activations quantised to the same format.
+
+Operators for programs that run or train their own experts next to it (include/moe_ops.h, ops.py):
+tokens grouped by expert and back (sort_tokens, gather, combine), the expert product in FP8 with a scale for
+each block of 128 (quantize_block, block_product), and the gradients of all of them.
 """
 from __future__ import annotations
 

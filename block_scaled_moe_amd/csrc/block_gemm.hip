@@ -21,6 +21,12 @@
 //    one L2.
 // Transposed, the reduction runs along the weights' rows: the same bytes are copied, and the
 // operand is read with the transposing LDS read (8 rows x 16 columns per 16 lanes).
+//
+// One group of 8191 rows, 5120 x 4096: 177 us (1.94 PFLOP/s), of which the products alone take 130 us, the
+// barriers 8, the stores 15, the copies 24. 96 groups of about 170 rows, 5120 x 4096: 466 us (1.47 PFLOP/s,
+// 4.8 TB/s of weights, rows and results; a group's last tile is as long in copies as a full one). Transposed
+// on 16384 unevenly grouped rows, 4096 x 2560: 273 us.
+// stream_kernel below takes over where groups have few rows.
 #include "block_mma.h"
 #include "ops_internal.h"
 

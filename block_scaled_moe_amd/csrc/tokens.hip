@@ -10,7 +10,8 @@
 // with no arithmetic to speak of. So work is laid out by token: a thread owns one piece of
 // 16 bytes (one element where rows do not end on 16 bytes) of a token's row, finds the
 // token's positions, and touches all of its sorted rows; every output is written once by one
-// thread, without atomics, so results do not depend on the order of workgroups.
+// thread, without atomics, so results do not depend on the order of workgroups. 16384 tokens in
+// eight slots, 4096 bf16 values: 4.5 to 5.8 TB/s (below, at load_row); one token 3 us, a launch.
 #include "ops_internal.h"
 
 namespace moe {
