@@ -288,6 +288,7 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const BlockGemmArgs p) {
                 block(s, std::integral_constant<int, 0>{});
                 if (s + 1 < n) block(s + 1, std::integral_constant<int, 1>{});
             }
+            if (n < 3) wait_copies<0>();  // the announced slots: from block 2 on they are waited for with its copies
             lds_barrier();  // every wave is done with the buffers
             if (more) {
                 sources(next, true);

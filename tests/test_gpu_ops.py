@@ -284,6 +284,13 @@ def test_product(counts, N, K):
     assert (num(buf)[T:] == 3.0).all()
 
 
+@pytest.mark.parametrize("K", [128, 256, 384])
+def test_short_sums_over_many_items(K):
+    """More work items than CUs with one to three blocks each, by token: an item's rows are looked up while the last
+    one is computed."""
+    test_product([40, 7, 33, 90] * 6, 5120, K)
+
+
 FEW = [([0, 5, 16, 17] + [0] * 20, 256, 640), ([33, 64, 65] + [0] * 40, 128, 1152), ([300] + [0] * 59, 128, 256),
        ([1] * 7 + [100] + [2] * 40, 384, 128), ([224, 225] + [0] * 90, 128, 1664)]
 
