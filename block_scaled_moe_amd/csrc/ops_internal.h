@@ -54,6 +54,7 @@ struct BlockQuantArgs {
     const int32_t *offsets;      // NULL: one group of `rows` rows
     const int32_t *sorted_slot;  // by token: row p is x[sorted_slot[p] / top_k]
     int32_t rows, n, top_k, C;
+    int32_t tiles;  // of 128 columns per workgroup (set by the launcher)
     const uint16_t *x;
     uint8_t *codes;
     float *scales;
@@ -61,7 +62,7 @@ struct BlockQuantArgs {
     float *col_scales;
 };
 hipError_t launch_block_quant_rows(const BlockQuantArgs &a, hipStream_t s);
-hipError_t launch_block_quant_columns(const BlockQuantArgs &a, hipStream_t s);  // with rows if codes is set
+hipError_t launch_block_quant_columns(BlockQuantArgs a, hipStream_t s);  // with rows if codes is set
 hipError_t launch_block_quant_weights(const uint16_t *w, int32_t E, int32_t N, int32_t K, uint8_t *codes, float *scales,
                                       hipStream_t s);
 

@@ -11,7 +11,7 @@
 // 16 bytes (one element where rows do not end on 16 bytes) of a token's row, finds the
 // token's positions, and touches all of its sorted rows; every output is written once by one
 // thread, without atomics, so results do not depend on the order of workgroups. 16384 tokens in
-// eight slots, 4096 bf16 values: 4.5 to 5.8 TB/s (below, at load_row); one token 3 us, a launch.
+// eight slots, 4096 bf16 values: 5.0 to 5.8 TB/s (below, at load_row); one token 3 us, a launch.
 #include "ops_internal.h"
 
 namespace moe {
@@ -43,7 +43,8 @@ struct alignas(sizeof(T) * V > 16 ? 16 : sizeof(T) * V) Piece {
 
 // Rows are read once and written once here, and the sorted ones of a long batch fill the caches many
 // times over: pieces of 16 bytes go past them (16384 tokens of 4096 bf16 values in eight slots:
-// gather 276 -> 240 us, join 290 -> 208 us, the gradient of combine 554 -> 476 us, 4.8 to 5.8 TB/s).
+// gather 276 -> 240 us, join 290 -> 208 us, the gradient of combine 554 -> 476 us; with the sums' exchange
+// below 443 us: 5.0 to 5.8 TB/s).
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 template <typename P>
 __device__ __forceinline__ P load_row(const P *p) {
@@ -191,16 +192,23 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(int32_t n_to
                 }
         }
     }
-    const int in_wave = min(lanes, 64);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        for (int off = in_wave >> 1; off > 0; off >>= 1) dot[j] += __shfl_xor(dot[j], off);
     if (lanes > 64) {
         const int wave = threadIdx.x >> 6, per = lanes >> 6;  // waves of one token
-        if ((threadIdx.x & 63) == 0) {
+        // each of the first three steps gives half of the sums to the partner lane: ten exchanges, not 48
+        // (517 tokens of 1001 fp32 values 9.7 -> 8.0 us)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) part[wave][j] = dot[j];
+        for (int half = 4, off = 32; half > 0; half >>= 1, off >>= 1) {
+            const bool upper = threadIdx.x & off;
+#pragma unroll
+            for (int j = 0; j < half; ++j) {
+                const float give = upper ? dot[j] : dot[j + half];
+                dot[j] = (upper ? dot[j + half] : dot[j]) + __shfl_xor(give, off);
+            }
         }
+#pragma unroll
+        for (int off = 4; off > 0; off >>= 1) dot[0] += __shfl_xor(dot[0], off);
+        // lane bits 5, 4, 3 are the sum's number, highest first
+        if ((threadIdx.x & 7) == 0) part[wave][(threadIdx.x & 63) >> 3] = dot[0];
         __syncthreads();
         if (lane < 8 && lane < k && valid) {
             const int first = wave;  // the token's first wave: lane < 8 lies in it
@@ -208,10 +216,15 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(int32_t n_to
             for (int i = 0; i < per; ++i) sum += part[first + i][lane];
             d_w[t * k + lane] = sum;
         }
-    } else if (lane == 0 && valid) {
+    } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (j < k) d_w[t * k + j] = dot[j];
+            for (int off = lanes >> 1; off > 0; off >>= 1) dot[j] += __shfl_xor(dot[j], off);
+        if (lane == 0 && valid) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < k) d_w[t * k + j] = dot[j];
+        }
     }
 }
 

@@ -135,7 +135,11 @@ class Groups:
         self.filled = False  # by sort_tokens
         base = self.buffer.data_ptr()
         self.struct = MoeGroups(T, top_k, E, e_begin, e_end, base, base + slots, base + pos, base + plan, end - plan)
-        self.ref, self.pointer = ctypes.byref(self.struct), ctypes.pointer(self.struct)
+        self.ref = ctypes.byref(self.struct)
+
+    @functools.cached_property
+    def pointer(self):
+        return ctypes.pointer(self.struct)
 
     @staticmethod
     def empty(T: int, top_k: int, E: int, e_begin: int = 0, e_end: int | None = None, device="cuda") -> "Groups":
