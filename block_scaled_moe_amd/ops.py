@@ -120,6 +120,22 @@ def _out(what: str, out: torch.Tensor | None, shape: tuple, dtype, device: torch
 
 # ------------------------------------------------------------------ tokens by expert
 
+class _once:
+    """A property computed at its first use and kept as the object's attribute (functools' takes a lock)."""
+
+    def __init__(self, f):
+        self.f, self.__doc__ = f, f.__doc__
+
+    def __set_name__(self, owner, name):
+        self.name = name
+
+    def __get__(self, obj, owner=None):
+        if obj is None:
+            return self
+        v = obj.__dict__[self.name] = self.f(obj)
+        return v
+
+
 class Groups:
     """The token-slots of a batch sorted by expert (moe_groups; filled by sort_tokens). Its arrays share one
     allocation; offsets, sorted_slot and slot_pos are views of it."""
@@ -137,7 +153,7 @@ class Groups:
         self.struct = MoeGroups(T, top_k, E, e_begin, e_end, base, base + slots, base + pos, base + plan, end - plan)
         self.ref = ctypes.byref(self.struct)
 
-    @functools.cached_property
+    @_once
     def pointer(self):
         return ctypes.pointer(self.struct)
 
@@ -145,17 +161,17 @@ class Groups:
     def empty(T: int, top_k: int, E: int, e_begin: int = 0, e_end: int | None = None, device="cuda") -> "Groups":
         return Groups(T, top_k, E, e_begin, e_end, device)
 
-    @functools.cached_property
+    @_once
     def offsets(self) -> torch.Tensor:
         """int32 [n + 1]: first sorted row of each local expert; [n] = local slots."""
         return self.buffer.as_strided((self.n + 1,), (1,), 0)
 
-    @functools.cached_property
+    @_once
     def sorted_slot(self) -> torch.Tensor:
         """int32 [T * top_k]: slot of each sorted row, -1 behind the local ones."""
         return self.buffer.as_strided((self.rows,), (1,), self._at[0] // 4)
 
-    @functools.cached_property
+    @_once
     def slot_pos(self) -> torch.Tensor:
         """int32 [T, top_k]: sorted row of each slot, -1 if not local."""
         return self.buffer.as_strided((self.T, self.top_k), (self.top_k, 1), self._at[1] // 4)
@@ -259,20 +275,84 @@ def combine_backward(g: Groups, d_out: torch.Tensor, y: torch.Tensor, w: torch.T
 
 # ------------------------------------------------------------------ FP8 with a scale per block of 128
 
-@dataclasses.dataclass
-class BlockRows:
+class _Quantised:
+    """Codes and scales: either two tensors given, or one allocation of which they are views, made when asked for."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        self.codes, self.scales, self.buffer = codes, scales, None
+
+    @classmethod
+    def empty(cls, rows: int, C: int, device: torch.device):
+        """Room for `rows` rows (of the column form: blocks) of C columns on `device`."""
+        q = cls.__new__(cls)
+        q.rows, q.C, q.device = rows, C, device
+        n, m = cls.sizes(rows, C)
+        q.split = (n + 255) // 256 * 256
+        q.buffer = torch.empty(q.split + 4 * m, dtype=torch.uint8, device=device)
+        return q
+
+    @_once
+    def codes(self) -> torch.Tensor:
+        n, _ = self.sizes(self.rows, self.C)
+        return self.buffer[:n].view(self.shapes(self.rows, self.C)[0])
+
+    @_once
+    def scales(self) -> torch.Tensor:
+        return self.buffer[self.split:].view(torch.float32).view(self.shapes(self.rows, self.C)[1])
+
+    def place(self) -> torch.device:
+        """Device of the codes."""
+        return self.codes.device if "codes" in self.__dict__ else self.device
+
+    def pointers(self, what: str, rows: int, C: int, device: torch.device) -> tuple[int, int]:
+        """Addresses of codes and scales, which hold `rows` rows of C columns on `device`."""
+        own = self.__dict__
+        if "codes" not in own and "scales" not in own:  # nobody has set them: as allocated
+            if (self.rows, self.C, self.device) != (rows, C, device):
+                raise ValueError(f"{what}: {self.rows} x {self.C} on {self.device}, expected {rows} x {C} on {device}")
+            base = self.buffer.data_ptr()
+            return base, base + self.split
+        codes, scales = self.shapes(rows, C)
+        return (_ask(what + " codes", self.codes, codes, torch.uint8, device).data_ptr(),
+                _ask(what + " scales", self.scales, scales, torch.float32, device).data_ptr())
+
+
+class BlockRows(_Quantised):
     """Rows in E4M3 with an fp32 scale per 1 x 128 block: codes uint8 [C / 128, rows, 128], scales
     [rows, S], S being C / 128 rounded up to a multiple of 4 (the rest is unused)."""
-    codes: torch.Tensor
-    scales: torch.Tensor
+
+    @property
+    def height(self) -> int:
+        if "codes" not in self.__dict__:
+            return self.rows
+        if self.codes.dim() != 3:
+            raise ValueError(f"x codes: shape {tuple(self.codes.shape)}, expected [blocks, rows, 128]")
+        return self.codes.shape[1]
+
+    @staticmethod
+    def sizes(rows: int, C: int):
+        return rows * C, rows * ((C // 128 + 3) // 4 * 4)
+
+    @staticmethod
+    def shapes(rows: int, C: int):
+        return (C // 128, rows, 128), (rows, (C // 128 + 3) // 4 * 4)
 
 
-@dataclasses.dataclass
-class BlockColumns:
+class BlockColumns(_Quantised):
     """Sorted rows in E4M3 with an fp32 scale per column of each run of 128 rows of an expert (the column
     form of include/moe_ops.h): codes uint8 [blocks, C / 32, 2, 4, 32, 16], scales [blocks, C]."""
-    codes: torch.Tensor
-    scales: torch.Tensor
+
+    @property
+    def width(self) -> int:
+        return self.scales.shape[-1] if "scales" in self.__dict__ else self.C
+
+    @staticmethod
+    def sizes(blocks: int, C: int):
+        return blocks * C * 128, blocks * C
+
+    @staticmethod
+    def shapes(blocks: int, C: int):
+        return (blocks, C // 32, 2, 4, 32, 16), (blocks, C)
 
 
 @dataclasses.dataclass
@@ -348,14 +428,14 @@ def _quantize(x: torch.Tensor, g: Groups | None, by_token: bool, rows: bool, col
     r = c = None
     rc = rs = cc = cs = None
     if rows:
-        r = BlockRows(torch.empty((C // 128, R, 128), dtype=torch.uint8, device=dev),
-                      torch.empty((R, (C // 128 + 3) // 4 * 4), dtype=torch.float32, device=dev))
-        rc, rs = r.codes.data_ptr(), r.scales.data_ptr()
+        r = BlockRows.empty(R, C, dev)
+        rc = r.buffer.data_ptr()
+        rs = rc + r.split
     if columns:
         n = (R if g is None else g.rows) // 128 + (1 if g is None else g.n)  # moe_block_column_blocks
-        c = BlockColumns(torch.empty((n, C // 32, 2, 4, 32, 16), dtype=torch.uint8, device=dev),
-                         torch.empty((n, C), dtype=torch.float32, device=dev))
-        cc, cs = c.codes.data_ptr(), c.scales.data_ptr()
+        c = BlockColumns.empty(n, C, dev)
+        cc = c.buffer.data_ptr()
+        cs = cc + c.split
     _filled(g)
     if R > 0:
         a = MoeBlockQuantizeArgs(R, C, by_token, None if g is None else g.pointer, x.data_ptr(), rc, rs, cc, cs)
@@ -380,21 +460,20 @@ def quantize_block_both(x: torch.Tensor, g: Groups | None = None) -> tuple[Block
 
 
 def _product(x: BlockRows, w: BlockWeights, g: Groups | None, by_token: bool, transposed: bool, out):
-    dev = x.codes.device if g is None else g.device
-    if x.codes.dim() != 3:
-        raise ValueError(f"x codes: shape {tuple(x.codes.shape)}, expected [blocks, rows, 128]")
     R, C = (w.N, w.K) if transposed else (w.K, w.N)
-    n_x = x.codes.shape[1] if g is None else g.T if by_token else g.rows
-    _ask("x codes", x.codes, (R // 128, n_x, 128), torch.uint8, dev)
-    _ask("x scales", x.scales, (n_x, (R // 128 + 3) // 4 * 4), torch.float32, dev)
+    if g is not None:
+        dev, n_x = g.device, g.T if by_token else g.rows
+    else:
+        dev, n_x = x.place(), x.height
+    codes, scales = x.pointers("x", n_x, R, dev)
     if w.E != (1 if g is None else g.n):
         raise ValueError(f"w: {w.E} experts, expected {1 if g is None else g.n}")
     if g is None and by_token:
         raise ValueError("by_token needs groups")
     out = _out("out", out, (n_x if g is None else g.rows, C), torch.bfloat16, dev)
     _filled(g)
-    a = MoeBlockGemmArgs(n_x, by_token, transposed, None if g is None else g.pointer, x.codes.data_ptr(),
-                         x.scales.data_ptr(), w.struct(dev), out.data_ptr())
+    a = MoeBlockGemmArgs(n_x, by_token, transposed, None if g is None else g.pointer, codes, scales,
+                         w.struct(dev), out.data_ptr())
     if n_x > 0:
         _call("moe_block_gemm", dev, ctypes.byref(a))
     return out
@@ -419,18 +498,17 @@ def block_weight_grad(dy: BlockColumns, x: BlockColumns, g: Groups | None = None
     the input (moe_block_wgrad). Without groups, `rows` says how many rows they hold."""
     if g is None and rows is None:
         raise ValueError("rows: needed without groups")
-    dev = dy.codes.device if g is None else g.device
+    dev = dy.place() if g is None else g.device
     R = rows if g is None else g.rows
-    N, K, n = dy.scales.shape[-1], x.scales.shape[-1], 1 if g is None else g.n
+    N, K, n = dy.width, x.width, 1 if g is None else g.n
     _blocks_of_128("dy", N)
     _blocks_of_128("x", K)
     blocks = R // 128 + n
-    for what, q, C in (("dy", dy, N), ("x", x, K)):
-        _ask(what + " codes", q.codes, (blocks, C // 32, 2, 4, 32, 16), torch.uint8, dev)
-        _ask(what + " scales", q.scales, (blocks, C), torch.float32, dev)
+    g_codes, g_scales = dy.pointers("dy", blocks, N, dev)
+    x_codes, x_scales = x.pointers("x", blocks, K, dev)
     out = _out("out", out, (n, N, K), torch.bfloat16, dev)
     _filled(g)
-    a = MoeBlockWgradArgs(R, N, K, None if g is None else g.pointer, dy.codes.data_ptr(), dy.scales.data_ptr(),
-                          x.codes.data_ptr(), x.scales.data_ptr(), out.data_ptr())
+    a = MoeBlockWgradArgs(R, N, K, None if g is None else g.pointer, g_codes, g_scales, x_codes, x_scales,
+                          out.data_ptr())
     _call("moe_block_wgrad", dev, ctypes.byref(a))
     return out

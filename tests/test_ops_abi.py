@@ -181,6 +181,35 @@ def test_groups_that_were_not_sorted_are_refused():
             call()
 
 
+def test_quantised_forms_in_one_allocation():
+    """Codes and scales are views of one buffer; tensors put in their place are the ones that are used and checked."""
+    cpu = torch.device("cpu")
+    q, c = ops.BlockRows.empty(8, 640, cpu), ops.BlockColumns.empty(3, 640, cpu)
+    at = q.pointers("x", 8, 640, cpu)
+    assert q.codes.shape == (5, 8, 128) and q.scales.shape == (8, 8) and q.scales.dtype == torch.float32
+    assert (q.codes.data_ptr(), q.scales.data_ptr()) == at == q.pointers("x", 8, 640, cpu)
+    assert q.scales.data_ptr() % 16 == 0 and q.scales.data_ptr() >= q.codes.data_ptr() + 5 * 8 * 128
+    at = c.pointers("x", 3, 640, cpu)
+    assert c.width == 640 and c.codes.shape == (3, 20, 2, 4, 32, 16) and c.scales.shape == (3, 640)
+    assert (c.codes.data_ptr(), c.scales.data_ptr()) == at and c.codes.numel() <= c.scales.data_ptr() - c.codes.data_ptr()
+    for wrong in ((7, 640), (8, 512)):
+        with pytest.raises(ValueError):
+            ops.BlockRows.empty(8, 640, cpu).pointers("x", *wrong, cpu)
+        with pytest.raises(ValueError):
+            q.pointers("x", *wrong, cpu)
+    other = torch.ones((8, 8))
+    q = ops.BlockRows.empty(8, 640, cpu)
+    q.scales = other
+    assert q.pointers("x", 8, 640, cpu) == (q.buffer.data_ptr(), other.data_ptr())
+    q.scales = other[:, :4]
+    with pytest.raises(ValueError):
+        q.pointers("x", 8, 640, cpu)
+    assert ops.BlockRows.empty(0, 128, cpu).codes.shape == (1, 0, 128)
+    w = moe.BlockWeights.empty(1, 128, 256, device="cpu")
+    with pytest.raises(ValueError):
+        moe.block_product(ops.BlockRows.empty(8, 640, cpu), w)
+
+
 def test_plain_forms_of_the_format():
     """The tests' own E4M3 rounding: every code is its value's code, midpoints go to the even code."""
     codes = np.array([c for c in range(256) if c & 0x7F != 0x7F], np.uint8)
