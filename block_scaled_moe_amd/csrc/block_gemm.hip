@@ -344,10 +344,11 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const BlockGemmArgs p) {
 // columns are too few to go round the CUs. A workgroup takes 32 columns of one tile of rows, its
 // four waves a quarter of the blocks each; weights go straight into registers, 16 bytes a lane from
 // 512 consecutive bytes an instruction's half, and the four partial sums meet in LDS in the waves'
-// order. Up to 16 rows have four blocks' loads ahead of the products, more rows share a turn's
-// weights in up to four pieces with fewer blocks ahead: 134 registers, three workgroups a CU (four
-// blocks ahead of two pieces or two ahead of four cost that and 5 %). One token through 8 of 64
-// experts, 5120 x 4096: 28 us for 168 MB (6.0 TB/s); 64 tokens, 96 of 384 experts: 202 us.
+// order. Up to 32 rows have two blocks' loads ahead of the products, more rows share a turn's
+// weights in four pieces with one block ahead: 134 registers, three workgroups a CU (four blocks
+// ahead of two pieces or two of four cost that and 5 %, four ahead of one piece 1 us of 28). One token
+// through 8 of 64 experts, 5120 x 4096: 26.7 us for 168 MB (6.3 TB/s); two tokens 48 us (7.0 TB/s); 64
+// tokens, 96 of 384 experts: 202 to 207 us.
 __global__ void __launch_bounds__(256, 3) stream_kernel(const BlockGemmArgs p) {
     __shared__ __attribute__((aligned(16))) float part[4][64][36];
     const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
@@ -438,7 +439,7 @@ __global__ void __launch_bounds__(256, 3) stream_kernel(const BlockGemmArgs p) {
     int m0 = 0;
     for (; rows - m0 > 32; m0 += 64) turn(m0, integral_constant<int, 4>{}, integral_constant<int, 1>{});
     if (rows - m0 > 16) turn(m0, integral_constant<int, 2>{}, integral_constant<int, 2>{});
-    else if (rows > m0) turn(m0, integral_constant<int, 1>{}, integral_constant<int, 4>{});
+    else if (rows > m0) turn(m0, integral_constant<int, 1>{}, integral_constant<int, 2>{});
 }
 
 }  // namespace

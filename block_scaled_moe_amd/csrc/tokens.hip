@@ -11,7 +11,7 @@
 // 16 bytes (one element where rows do not end on 16 bytes) of a token's row, finds the
 // token's positions, and touches all of its sorted rows; every output is written once by one
 // thread, without atomics, so results do not depend on the order of workgroups. 16384 tokens in
-// eight slots, 4096 bf16 values: 5.0 to 5.8 TB/s (below, at load_row); one token 3 us, a launch.
+// eight slots, 4096 bf16 values: 4.8 to 5.8 TB/s (below, at load_row); one token 3 us, a launch.
 #include "ops_internal.h"
 
 namespace moe {
@@ -43,8 +43,7 @@ struct alignas(sizeof(T) * V > 16 ? 16 : sizeof(T) * V) Piece {
 
 // Rows are read once and written once here, and the sorted ones of a long batch fill the caches many
 // times over: pieces of 16 bytes go past them (16384 tokens of 4096 bf16 values in eight slots:
-// gather 276 -> 240 us, join 290 -> 208 us, the gradient of combine 554 -> 476 us; with the sums' exchange
-// below 443 us: 5.0 to 5.8 TB/s).
+// gather 276 -> 240 us, join 290 -> 208 us, the gradient of combine 554 -> 476 us: 4.8 to 5.8 TB/s).
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 template <typename P>
 __device__ __forceinline__ P load_row(const P *p) {
@@ -195,7 +194,7 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(int32_t n_to
     if (lanes > 64) {
         const int wave = threadIdx.x >> 6, per = lanes >> 6;  // waves of one token
         // each of the first three steps gives half of the sums to the partner lane: ten exchanges, not 48
-        // (517 tokens of 1001 fp32 values 9.7 -> 8.0 us)
+        // (517 tokens of 1001 fp32 values 9.7 -> 8.0 us; long batches 478 -> 472 us)
 #pragma unroll
         for (int half = 4, off = 32; half > 0; half >>= 1, off >>= 1) {
             const bool upper = threadIdx.x & off;
