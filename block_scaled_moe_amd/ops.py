@@ -355,6 +355,12 @@ class BlockColumns(_Quantised):
         return (blocks, C // 32, 2, 4, 32, 16), (blocks, C)
 
 
+def _ask_form(what: str, q, form):
+    """One form's allocation is too small for the other's reads."""
+    if not isinstance(q, form):
+        raise ValueError(f"{what}: {type(q).__name__}, expected {form.__name__}")
+
+
 @dataclasses.dataclass
 class BlockWeights:
     """Expert weights [E, N, K] in E4M3 with an fp32 scale per 128 x 128 block: codes uint8
@@ -460,6 +466,7 @@ def quantize_block_both(x: torch.Tensor, g: Groups | None = None) -> tuple[Block
 
 
 def _product(x: BlockRows, w: BlockWeights, g: Groups | None, by_token: bool, transposed: bool, out):
+    _ask_form("x", x, BlockRows)
     R, C = (w.N, w.K) if transposed else (w.K, w.N)
     if g is not None:
         dev, n_x = g.device, g.T if by_token else g.rows
@@ -498,6 +505,8 @@ def block_weight_grad(dy: BlockColumns, x: BlockColumns, g: Groups | None = None
     the input (moe_block_wgrad). Without groups, `rows` says how many rows they hold."""
     if g is None and rows is None:
         raise ValueError("rows: needed without groups")
+    _ask_form("dy", dy, BlockColumns)
+    _ask_form("x", x, BlockColumns)
     dev = dy.place() if g is None else g.device
     R = rows if g is None else g.rows
     N, K, n = dy.width, x.width, 1 if g is None else g.n

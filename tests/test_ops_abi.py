@@ -208,6 +208,13 @@ def test_quantised_forms_in_one_allocation():
     w = moe.BlockWeights.empty(1, 128, 256, device="cpu")
     with pytest.raises(ValueError):
         moe.block_product(ops.BlockRows.empty(8, 640, cpu), w)
+    # one form in the other's place, of the same counts: one row and one run of rows of 256 columns
+    r, c = ops.BlockRows.empty(1, 256, cpu), ops.BlockColumns.empty(1, 256, cpu)
+    with pytest.raises(ValueError, match="expected BlockRows"):
+        moe.block_product(c, w)
+    for dy, x in ((r, c), (c, r)):
+        with pytest.raises(ValueError, match="expected BlockColumns"):
+            moe.block_weight_grad(dy, x, rows=100)
 
 
 def test_plain_forms_of_the_format():
