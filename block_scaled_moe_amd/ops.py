@@ -405,18 +405,22 @@ def quantize_block_weights(w: torch.Tensor, out: BlockWeights | None = None) -> 
 
 def pack_block_weights(codes: torch.Tensor, scales: torch.Tensor, out: BlockWeights | None = None) -> BlockWeights:
     """A checkpoint's E4M3 codes (uint8 or float8_e4m3fn [E, N, K], row-major) and fp32 scales
-    [E, N/128, K/128] -> BlockWeights (moe_block_pack_weights; the scales are kept, not copied)."""
+    [E, N/128, K/128] -> BlockWeights (moe_block_pack_weights). Without `out` the weights hold `scales` itself;
+    with it, the scales are copied into its buffer like the codes."""
     if codes.dim() != 3:
         raise ValueError(f"codes: shape {tuple(codes.shape)}, expected [E, N, K]")
     E, N, K = codes.shape
     _ask("codes", codes, (E, N, K), (torch.uint8, torch.float8_e4m3fn), codes.device)
     _ask("scales", scales, (E, N // 128, K // 128), torch.float32, codes.device)
-    out = BlockWeights.empty(E, N, K, device=codes.device) if out is None else out
+    if out is None:
+        out = BlockWeights.empty(E, N, K, device=codes.device)
+        out.scales = scales
     if (out.E, out.N, out.K) != (E, N, K):
         raise ValueError("out: weights of another shape")
-    out.scales = scales
     st = out.struct(codes.device)
     _call("moe_block_pack_weights", codes.device, codes.data_ptr(), E, N, K, st.codes)
+    if out.scales is not scales:
+        out.scales.copy_(scales)
     return out
 
 

@@ -566,3 +566,30 @@ def test_graph_replays_and_streams():
         for i in (0, 1):
             for n in FINAL:
                 assert torch.equal(got[i][n], want[i + 1][n]), n
+
+
+def test_pack_into_experts_of_a_longer_array():
+    """A checkpoint's experts packed into a view: the whole array has their codes and scales, and a product through a
+    captured graph, which holds the array's addresses, sees both."""
+    rng = np.random.default_rng(11)
+    w, x = values(rng, (4, 128, 256), "bf16"), values(rng, (40, 256), "bf16")
+    wc, ws = ref.weights(w)
+    whole = moe.quantize_block_weights(dev(values(rng, (4, 128, 256), "bf16"), torch.bfloat16))
+    idx = rng.integers(0, 4, 40).astype(np.int32)
+    off, ss, _ = ref.sort(idx, 0, 4)
+    g, q = moe.sort_tokens(dev(idx.reshape(40, 1)), 4), moe.quantize_block(dev(x, torch.bfloat16))
+    moe.block_product(q, whole, g, by_token=True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = moe.block_product(q, whole, g, by_token=True)
+    for a, b in ((1, 3), (0, 1), (3, 4)):
+        moe.pack_block_weights(dev(wc[a:b]), dev(ws[a:b]), out=whole.experts(a, b))
+    assert np.array_equal(host(whole.codes), ref.tile(wc)) and np.array_equal(host(whole.scales), ws)
+    want = ref.product(*ref.rows(x[ss]), wc, ws, idx[ss])
+    for _ in range(2):
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        check(num(y), *want, "replay")
+        check(num(moe.block_product(q, whole, g, by_token=True)), *want, "eager")

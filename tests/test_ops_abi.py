@@ -226,3 +226,25 @@ def test_plain_forms_of_the_format():
     want = np.where(np.arange(0x7E) % 2 == 0, np.arange(0x7E), np.arange(1, 0x7F))
     assert np.array_equal(ref.e4m3_code(mid), want)
     assert (ref.e4m3_code(np.array([460.0, 1e30], np.float32)) == 0x7E).all()
+
+
+def test_pack_fills_the_weights_it_is_given(monkeypatch):
+    """pack_block_weights(out=...) writes the scales into out's own buffer, which a longer array's view or a captured
+    graph holds, and nothing at all where the call is refused."""
+    all_w = moe.BlockWeights.empty(4, 128, 256, device="cpu")
+    all_w.scales.zero_()
+    codes = torch.zeros((2, 128, 256), dtype=torch.uint8)
+    scales = torch.tensor([[[1.0, 2.0]], [[3.0, 4.0]]])
+    view = all_w.experts(1, 3)
+    with pytest.raises(ValueError):  # no GPU
+        moe.pack_block_weights(codes, scales, out=view)
+    assert not all_w.scales.any() and view.scales.data_ptr() == all_w.scales[1:].data_ptr()
+    monkeypatch.setattr(ops, "_call", lambda *a: None)  # the codes' kernel
+    got = moe.pack_block_weights(codes, scales, out=view)
+    assert got is view and view.scales.data_ptr() == all_w.scales[1:].data_ptr()
+    assert torch.equal(all_w.scales[1:3], scales) and not all_w.scales[0].any() and not all_w.scales[3].any()
+    assert moe.pack_block_weights(codes, scales).scales is scales  # its own weights keep the caller's scales
+    assert moe.pack_block_weights(codes, view.scales, out=view).scales is view.scales
+    assert torch.equal(all_w.scales[1:3], scales)
+    with pytest.raises(ValueError):
+        moe.pack_block_weights(codes, scales, out=all_w)
