@@ -4,7 +4,8 @@ back, and the expert product in FP8 with a scale for each block of 128, each wit
 The functions marshal arguments like the package's other calls: torch provides device memory
 and the current stream of the tensors' device, every step runs in the library's kernels, and an
 argument the library refuses raises MoeError. Wrong dtypes, shapes, devices or strides raise
-ValueError before the call; tensors are contiguous.
+ValueError before the call; tensors are contiguous. Autograd does not see these calls: each gradient is a
+call of its own, and a tensor with requires_grad is refused unless gradients are off (torch.no_grad).
 
     g = sort_tokens(topk_idx, E)                       # after route()
     y = block_product(quantize_block(x), w, g, by_token=True)      # rows [T * k, N], sorted
@@ -102,7 +103,7 @@ def _call(name: str, device: torch.device, *args):
 
 
 def _ask(what: str, t: torch.Tensor, shape: tuple, dtype, device: torch.device):
-    """t has this shape, dtype (one or a collection of them) and device, and is contiguous."""
+    """t has this shape, dtype (one or a collection of them) and device, is contiguous, and autograd does not follow it."""
     if t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype is not dtype and (isinstance(dtype, torch.dtype) or t.dtype not in dtype):
@@ -111,6 +112,8 @@ def _ask(what: str, t: torch.Tensor, shape: tuple, dtype, device: torch.device):
         raise ValueError(f"{what}: on {t.device}, expected {device}")
     if not t.is_contiguous():
         raise ValueError(f"{what}: not contiguous")
+    if t.requires_grad and torch.is_grad_enabled():  # the result would have no history, and the gradient be lost
+        raise ValueError(f"{what}: asks autograd for a gradient; detach it, and use the operators' own gradients")
     return t
 
 

@@ -248,3 +248,40 @@ def test_pack_fills_the_weights_it_is_given(monkeypatch):
     assert torch.equal(all_w.scales[1:3], scales)
     with pytest.raises(ValueError):
         moe.pack_block_weights(codes, scales, out=all_w)
+
+
+def test_tensors_under_autograd_are_refused(monkeypatch):
+    """The results have no autograd history, so a tensor that asks for a gradient is refused in every argument, as torch's
+    own out= forms refuse it; without grad mode, or detached, it is taken."""
+    monkeypatch.setattr(ops, "_call", lambda *a: None)
+    g = moe.Groups.empty(4, 2, 8, 2, 6, device="cpu")
+    g.filled = True
+    x, rows, w = torch.zeros((4, 128)), torch.zeros((8, 128)), torch.zeros((4, 2))
+    xb, rb, wb = x.bfloat16(), rows.bfloat16(), torch.zeros((4, 128, 128), dtype=torch.bfloat16)
+    codes, ws = torch.zeros((4, 128, 128), dtype=torch.uint8), torch.ones((4, 1, 1))
+    form = lambda s: moe.BlockRows(torch.zeros((1, 8, 128), dtype=torch.uint8), s)
+    cols = lambda s: moe.BlockColumns(torch.zeros((4, 4, 2, 4, 32, 16), dtype=torch.uint8), s)
+    rs, cs = torch.ones((8, 4)), torch.ones((4, 128))
+    bw = moe.BlockWeights.empty(4, 128, 128, device="cpu")
+    weights = lambda s: moe.BlockWeights(4, 128, 128, bw.codes, s)
+    calls = [
+        (lambda x: moe.gather(g, x), x), (lambda o: moe.gather(g, x, out=o), rows),
+        (lambda d: moe.gather_backward(g, d), rows), (lambda y: moe.combine(g, y, w), rows),
+        (lambda w: moe.combine(g, rows, w), w), (lambda o: moe.combine(g, rows, w, out=o), x),
+        (lambda d: moe.combine_backward(g, d, rows, w), x), (lambda y: moe.combine_backward(g, x, y, w), rows),
+        (lambda w: moe.combine_backward(g, x, rows, w), w), (lambda d: moe.combine_backward(g, x, rows, w, dw=d), w),
+        (lambda x: moe.quantize_block(x), xb), (lambda x: moe.quantize_block_columns(x, g), rb),
+        (lambda x: moe.quantize_block_both(x, g), rb), (lambda w: moe.quantize_block_weights(w), wb),
+        (lambda s: moe.pack_block_weights(codes, s), ws), (lambda s: moe.block_product(form(s), bw, g), rs),
+        (lambda s: moe.block_product_grad(form(rs), weights(s), g), ws),
+        (lambda s: moe.block_weight_grad(cols(s), cols(cs), g), cs),
+        (lambda o: moe.block_weight_grad(cols(cs), cols(cs), g, out=o), wb)]
+    for call, t in calls:
+        call(t)
+        p = t.clone().requires_grad_()
+        for bad in (p, p * 1.0):  # a leaf, and one with a history
+            with pytest.raises(ValueError, match="gradient"):
+                call(bad)
+            call(bad.detach())
+            with torch.no_grad():
+                call(bad)
