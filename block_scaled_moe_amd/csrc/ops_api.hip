@@ -3,6 +3,8 @@
 // stream.
 #include "ops_internal.h"
 
+#include <initializer_list>
+
 using namespace moe;
 
 namespace moe {
@@ -68,18 +70,31 @@ int32_t check_rows(const moe_groups *g, int32_t D) {
     return g->T < (1 << 24) && D <= (1 << 30) ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
-// Buffers a and b of rows of D elements overlap.
-struct Rows {
+// A buffer of a call: n items of `item` bytes at p.
+struct Buffer {
     const void *p;
-    int64_t rows;
-    int32_t dtype;
+    int64_t n, item;
 };
-bool overlap(int32_t D, const Rows &a, const Rows &b) {
-    const auto end = [&](const Rows &r) { return (uintptr_t)r.p + (uintptr_t)r.rows * D * (r.dtype == MOE_DT_BF16 ? 2 : 4); };
-    return (uintptr_t)a.p < end(b) && (uintptr_t)b.p < end(a);
+bool overlap(const Buffer &a, const Buffer &b) {
+    typedef unsigned __int128 wide;  // sizes that no memory holds are compared too
+    const wide a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
+    return a0 < b0 + (wide)b.n * (wide)b.item && b0 < a0 + (wide)a.n * (wide)a.item;
+}
+// The output meets one of the buffers; a call refuses that (buffers not given are NULL).
+bool overlaps_any(const Buffer &out, std::initializer_list<Buffer> others) {
+    for (const Buffer &b : others)
+        if (out.p && b.p && overlap(out, b)) return true;
+    return false;
 }
 
+int64_t row_bytes(int32_t dtype, int32_t D) { return (int64_t)D * (dtype == MOE_DT_BF16 ? 2 : 4); }
+
 bool dtype_ok(int32_t d) { return d == MOE_DT_BF16 || d == MOE_DT_FP32; }
+
+// Blocks of a column form that a call touches at most: of g's slots, or of the one group of `rows` rows.
+int64_t column_blocks(const moe_groups *g, int32_t rows) {
+    return g ? moe_block_column_blocks(g->T * g->top_k, g->e_end - g->e_begin) : ((int64_t)rows + 127) / 128;
+}
 
 GroupView group_view(const moe_groups *g, int32_t rows) {
     GroupView v{};
@@ -158,7 +173,8 @@ int32_t moe_gather(const moe_groups *g, int32_t dtype, int32_t D, const void *x,
     if (g->T == 0) return MOE_OK;
     if (!x || !rows) return MOE_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(rows)) return MOE_ERR_ALIGNMENT;
-    if (overlap(D, {x, g->T, dtype}, {rows, (int64_t)g->T * g->top_k, dtype})) return MOE_ERR_INVALID_ARG;
+    const int64_t bytes = row_bytes(dtype, D);
+    if (overlaps_any({rows, (int64_t)g->T * g->top_k, bytes}, {{x, g->T, bytes}})) return MOE_ERR_INVALID_ARG;
     return to_status(launch_gather(*g, dtype, D, x, rows, (hipStream_t)stream));
 }
 
@@ -171,7 +187,8 @@ int32_t moe_gather_backward(const moe_groups *g, int32_t dtype, int32_t D, const
     if (g->T == 0) return MOE_OK;
     if (!d_rows || !dx) return MOE_ERR_INVALID_ARG;
     if (!aligned16(d_rows) || !aligned16(dx)) return MOE_ERR_ALIGNMENT;
-    if (overlap(D, {dx, g->T, dtype}, {d_rows, (int64_t)g->T * g->top_k, dtype})) return MOE_ERR_INVALID_ARG;
+    const int64_t bytes = row_bytes(dtype, D);
+    if (overlaps_any({dx, g->T, bytes}, {{d_rows, (int64_t)g->T * g->top_k, bytes}})) return MOE_ERR_INVALID_ARG;
     return to_status(launch_combine_rows(*g, dtype, dtype, D, d_rows, nullptr, dx, (hipStream_t)stream));
 }
 
@@ -185,7 +202,9 @@ int32_t moe_combine(const moe_groups *g, int32_t y_dtype, int32_t out_dtype, int
     if (g->T == 0) return MOE_OK;
     if (!y || !w || !out) return MOE_ERR_INVALID_ARG;
     if (!aligned16(y) || !aligned16(w) || !aligned16(out)) return MOE_ERR_ALIGNMENT;
-    if (overlap(D, {out, g->T, out_dtype}, {y, (int64_t)g->T * g->top_k, y_dtype})) return MOE_ERR_INVALID_ARG;
+    const int64_t slots = (int64_t)g->T * g->top_k;
+    if (overlaps_any({out, g->T, row_bytes(out_dtype, D)}, {{y, slots, row_bytes(y_dtype, D)}, {w, slots, 4}}))
+        return MOE_ERR_INVALID_ARG;
     return to_status(launch_combine_rows(*g, y_dtype, out_dtype, D, y, w, out, (hipStream_t)stream));
 }
 
@@ -201,7 +220,9 @@ int32_t moe_combine_backward(const moe_groups *g, int32_t y_dtype, int32_t out_d
     if (!aligned16(d_out) || !aligned16(y) || !aligned16(w) || !aligned16(d_y) || !aligned16(d_w))
         return MOE_ERR_ALIGNMENT;
     const int64_t slots = (int64_t)g->T * g->top_k;
-    if (overlap(D, {d_y, slots, y_dtype}, {y, slots, y_dtype}) || overlap(D, {d_y, slots, y_dtype}, {d_out, g->T, out_dtype}))
+    const Buffer bo = {d_out, g->T, row_bytes(out_dtype, D)}, by = {y, slots, row_bytes(y_dtype, D)}, bw = {w, slots, 4};
+    const Buffer bdy = {d_y, slots, by.item}, bdw = {d_w, slots, 4};
+    if (overlaps_any(bdy, {bo, by, bw, bdw}) || overlaps_any(bdw, {bo, by}) || (d_w != w && overlap(bdw, bw)))
         return MOE_ERR_INVALID_ARG;
     return to_status(launch_combine_backward(*g, y_dtype, out_dtype, D, d_out, y, w, d_y, d_w, (hipStream_t)stream));
 }
@@ -230,6 +251,12 @@ int32_t moe_block_quantize(const moe_block_quantize_args *q, void *stream) {
     if (!aligned16(q->x) || !aligned16(q->codes) || !aligned16(q->scales) || !aligned16(q->col_codes) ||
         !aligned16(q->col_scales))
         return MOE_ERR_ALIGNMENT;
+    const Buffer x = {q->x, q->rows, (int64_t)q->C * 2};
+    const Buffer c = {q->codes, q->rows, q->C}, s = {q->scales, q->rows, (int64_t)scale_stride(q->C) * 4};
+    const int64_t blocks = column_blocks(q->g, q->rows);
+    const Buffer cc = {q->col_codes, blocks, (int64_t)q->C * 128}, cs = {q->col_scales, blocks, (int64_t)q->C * 4};
+    if (overlaps_any(x, {c, s, cc, cs}) || overlaps_any(c, {s, cc, cs}) || overlaps_any(s, {cc, cs}) || overlaps_any(cc, {cs}))
+        return MOE_ERR_INVALID_ARG;
     BlockQuantArgs a{};
     a.offsets = q->g ? q->g->offsets : nullptr;
     a.sorted_slot = q->by_token ? q->g->sorted_slot : nullptr;
@@ -242,9 +269,13 @@ int32_t moe_block_quantize(const moe_block_quantize_args *q, void *stream) {
     a.scales = q->scales;
     a.col_codes = q->col_codes;
     a.col_scales = q->col_scales;
-    hipStream_t s = (hipStream_t)stream;
-    return to_status(by_columns ? launch_block_quant_columns(a, s) : launch_block_quant_rows(a, s));
+    hipStream_t hs = (hipStream_t)stream;
+    return to_status(by_columns ? launch_block_quant_columns(a, hs) : launch_block_quant_rows(a, hs));
 }
+
+// Codes and scales of weights [E][N][K].
+static Buffer weight_codes(const void *p, int32_t E, int32_t N, int32_t K) { return {p, E, (int64_t)N * K}; }
+static Buffer weight_scales(const void *p, int32_t E, int32_t N, int32_t K) { return {p, E, (int64_t)(N / 128) * (K / 128) * 4}; }
 
 // Sizes and buffers of weights [E][N][K].
 static int32_t check_weights(int32_t E, int32_t N, int32_t K, const void *codes, const void *scales) {
@@ -262,14 +293,17 @@ int32_t moe_block_quantize_weights(const uint16_t *w, int32_t E, int32_t N, int3
     if (rc != MOE_OK) return rc;
     if (!w) return MOE_ERR_INVALID_ARG;
     if (!aligned16(w)) return MOE_ERR_ALIGNMENT;
+    const Buffer c = weight_codes(codes, E, N, K), s = weight_scales(scales, E, N, K), x = {w, E, (int64_t)N * K * 2};
+    if (overlaps_any(x, {c, s}) || overlaps_any(c, {s})) return MOE_ERR_INVALID_ARG;
     return to_status(launch_block_quant_weights(w, E, N, K, codes, scales, (hipStream_t)stream));
 }
 
 int32_t moe_block_pack_weights(const uint8_t *rowmajor, int32_t E, int32_t N, int32_t K, uint8_t *codes, void *stream) {
     const int32_t rc = check_weights(E, N, K, codes, codes);
     if (rc != MOE_OK) return rc;
-    if (!rowmajor || rowmajor == codes) return MOE_ERR_INVALID_ARG;
+    if (!rowmajor) return MOE_ERR_INVALID_ARG;
     if (!aligned16(rowmajor)) return MOE_ERR_ALIGNMENT;
+    if (overlaps_any(weight_codes(codes, E, N, K), {weight_codes(rowmajor, E, N, K)})) return MOE_ERR_INVALID_ARG;
     return to_status(launch_pack_rowmajor(MOE_FMT_FP8, rowmajor, nullptr, E, N, K, codes, nullptr, (hipStream_t)stream));
 }
 
@@ -304,6 +338,11 @@ int32_t moe_block_gemm(const moe_block_gemm_args *a, void *stream) {
     p.w_expert_scales = (a->w.N / 128) * (a->w.K / 128);
     p.w_kb = a->w.K / 128;
     p.out = a->out;
+    const int64_t out_rows = a->g ? a->g->T * a->g->top_k : a->rows;
+    if (overlaps_any({a->out, out_rows, (int64_t)p.C * 2},
+                     {{a->x_codes, a->rows, p.R}, {a->x_scales, a->rows, (int64_t)scale_stride(p.R) * 4},
+                      weight_codes(a->w.codes, a->w.E, a->w.N, a->w.K), weight_scales(a->w.scales, a->w.E, a->w.N, a->w.K)}))
+        return MOE_ERR_INVALID_ARG;
     return to_status(launch_block_gemm(p, a->transposed != 0, (hipStream_t)stream));
 }
 
@@ -320,6 +359,11 @@ int32_t moe_block_wgrad(const moe_block_wgrad_args *a, void *stream) {
     if (!aligned16(a->dw) || !aligned16(a->g_codes) || !aligned16(a->g_scales) || !aligned16(a->x_codes) ||
         !aligned16(a->x_scales))
         return MOE_ERR_ALIGNMENT;
+    const int64_t blocks = column_blocks(a->g, a->rows);
+    if (overlaps_any({a->dw, a->g ? a->g->e_end - a->g->e_begin : 1, (int64_t)a->N * a->K * 2},
+                     {{a->g_codes, blocks, (int64_t)a->N * 128}, {a->g_scales, blocks, (int64_t)a->N * 4},
+                      {a->x_codes, blocks, (int64_t)a->K * 128}, {a->x_scales, blocks, (int64_t)a->K * 4}}))
+        return MOE_ERR_INVALID_ARG;
     BlockWgradArgs p{};
     p.offsets = a->g ? a->g->offsets : nullptr;
     p.rows = a->rows;

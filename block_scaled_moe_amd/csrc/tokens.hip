@@ -149,10 +149,10 @@ __global__ void __launch_bounds__(kThreads) join_kernel(int32_t n_tokens, int32_
 template <typename TY, typename TO, int V>
 __global__ void __launch_bounds__(kThreads) combine_backward_kernel(int32_t n_tokens, int32_t k, Span sp,
                                                                     const int32_t *__restrict__ slot_pos,
-                                                                    const float *__restrict__ w,
+                                                                    const float *w,  // may be d_w
                                                                     const TO *__restrict__ d_out,
                                                                     const TY *__restrict__ y, TY *__restrict__ d_y,
-                                                                    float *__restrict__ d_w) {
+                                                                    float *d_w) {
     using PY = Piece<TY, V>;
     using PO = Piece<TO, V>;
     __shared__ float part[kThreads / 64][8];

@@ -9,8 +9,11 @@
  * Conventions: those of moe.h (device pointers owned by the caller and 16-byte aligned, a
  * hipStream_t as void*, arguments checked on the host before anything is enqueued, nothing
  * synchronises, no allocation, no global state). `stream` must belong to the current
- * device. NaN and infinite inputs of the quantisers are outside the contract; the sort's
- * row operators pass them through to the rows and sums they belong to and to no others.
+ * device. An output that overlaps an input of its call or another output is refused
+ * (MOE_ERR_INVALID_ARG) unless the call allows it; the groups' own arrays, which nothing
+ * else may write, are not compared. NaN and infinite inputs of the quantisers are outside
+ * the contract; the sort's row operators pass them through to the rows and sums they belong
+ * to and to no others.
  */
 #ifndef BLOCK_SCALED_MOE_OPS_H
 #define BLOCK_SCALED_MOE_OPS_H
@@ -55,8 +58,7 @@ size_t moe_groups_plan_bytes(const moe_groups *g);
 int32_t moe_sort(const moe_groups *g, const int32_t *topk_idx, void *stream);
 
 /* rows[p] = x[sorted_slot[p] / top_k] for p < S. x [T][D], rows [T * top_k][D], both of
- * type dtype (MOE_DT_*). This call and the next three: T < 2^24, 1 <= D <= 2^30, and an
- * output that overlaps the rows it is made from is refused. */
+ * type dtype (MOE_DT_*). This call and the next three: T < 2^24, 1 <= D <= 2^30. */
 int32_t moe_gather(const moe_groups *g, int32_t dtype, int32_t D, const void *x, void *rows, void *stream);
 
 /* Gradient of moe_gather: dx[t] = sum over the token's local slots, j ascending, of
@@ -72,15 +74,14 @@ int32_t moe_combine(const moe_groups *g, int32_t y_dtype, int32_t out_dtype, int
 /* Gradient of moe_combine for d_out [T][D] of out_dtype:
  *   d_y[slot_pos] = w[t][j] * d_out[t]  (rounded once to y_dtype; rows behind S untouched)
  *   d_w[t][j]     = sum over D of d_out[t] * y[slot_pos], fp32; 0 for a slot not local.
- * d_y must not overlap y or d_out. */
+ * d_w may be w. */
 int32_t moe_combine_backward(const moe_groups *g, int32_t y_dtype, int32_t out_dtype, int32_t D, const void *d_out,
                              const void *y, const float *w, void *d_y, float *d_w, void *stream);
 
 /* ------------------------------------------------------------------ FP8, blocks of 128
  * E4M3 (OCP "FN") codes with one fp32 scale per block of 128: s = fl32(max |block| / 448),
  * 1 for an all-zero block; code = E4M3(fl32(x / s)), nearest, ties to even. The value is
- * code * s. All dimensions that blocks run along are multiples of 128 up to 2^24. Outputs
- * must not overlap inputs or each other.
+ * code * s. All dimensions that blocks run along are multiples of 128 up to 2^24.
  *   rows     codes [C/128][R][128] (the rows' first blocks, then their second ones, ..),
  *            scales [R][S], S = C/128 rounded up to a multiple of 4 (the rest of a row is
  *            neither written nor used): blocks of 1 x 128; R < 2^25 and R * S < 2^30
@@ -124,7 +125,7 @@ int32_t moe_block_quantize(const moe_block_quantize_args *a, void *stream);
 int32_t moe_block_quantize_weights(const uint16_t *w, int32_t E, int32_t N, int32_t K, uint8_t *codes, float *scales,
                                    void *stream);
 /* Codes of a checkpoint, row-major [E][N][K], into the tiled layout (scales stay as they
- * are). The two must not overlap. */
+ * are). */
 int32_t moe_block_pack_weights(const uint8_t *rowmajor, int32_t E, int32_t N, int32_t K, uint8_t *codes, void *stream);
 
 /* Grouped product with W: for sorted row p of expert e (g = NULL: every row, W's one expert)

@@ -593,3 +593,16 @@ def test_pack_into_experts_of_a_longer_array():
         torch.cuda.synchronize()
         check(num(y), *want, "replay")
         check(num(moe.block_product(q, whole, g, by_token=True)), *want, "eager")
+
+
+@pytest.mark.parametrize("D", [24, 4096, 1001])
+def test_weights_gradient_in_the_weights_place(D):
+    """dw over w itself: the same bits as beside it, for tokens that share a wave and for one over several."""
+    rng = np.random.default_rng(D)
+    idx = routing("dup", 77, 5, 9, rng)
+    g = moe.sort_tokens(dev(idx), 9)
+    d, y, w = dev(values(rng, (77, D))), dev(values(rng, (77 * 5, D))), dev(values(rng, (77, 5)))
+    dy, dw = moe.combine_backward(g, d, y, w)
+    w2 = w.clone()
+    dy2, dw2 = moe.combine_backward(g, d, y, w2, dw=w2)
+    assert dw2 is w2 and torch.equal(dw, dw2) and torch.equal(dy, dy2)

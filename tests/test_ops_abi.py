@@ -285,3 +285,56 @@ def test_tensors_under_autograd_are_refused(monkeypatch):
             call(bad.detach())
             with torch.no_grad():
                 call(bad)
+
+
+def test_overlapping_outputs_are_refused():
+    """An output on top of anything its call reads, or of another output, wholly or by its last bytes."""
+    lib, g = moe.lib(), groups()                 # 64 tokens of 8 slots, 96 of 384 experts
+    r, gp = ctypes.byref(g), ctypes.pointer(g)
+    far = lambda i: A + ((i + 1) << 32)          # places that do not meet
+
+    def each_pair(call, sizes, outputs, fits=()):
+        """`call` takes addresses of buffers of `sizes` bytes. Every output on top of every other buffer is refused, and so
+        is one whose first 16 bytes are the other's last, or the other way round; `fits` are the pairs that may be one."""
+        for o in outputs:
+            for b in range(len(sizes)):
+                if b == o:
+                    continue
+                for shift in (0, sizes[b] // 16 * 16 - 16, 16 - sizes[o] // 16 * 16):
+                    if shift == 0 and (o, b) in fits:
+                        continue
+                    at = [far(i) for i in range(len(sizes))]
+                    at[o] = at[b] + shift
+                    assert call(*at) == EINVAL, (o, b, shift)
+
+    t, s, w = 64 * 512 * 2, 512 * 512 * 2, 512 * 4   # token rows, sorted rows of 512 bf16 values; weights
+    each_pair(lambda x, rows: lib.moe_gather(r, 1, 512, x, rows, None), (t, s), (1,))
+    each_pair(lambda d, x: lib.moe_gather_backward(r, 1, 512, d, x, None), (s, t), (1,))
+    each_pair(lambda y, w, o: lib.moe_combine(r, 1, 1, 512, y, w, o, None), (s, w, t), (2,))
+    each_pair(lambda d, y, w, dy, dw: lib.moe_combine_backward(r, 1, 1, 512, d, y, w, dy, dw, None), (t, s, w, s, w), (3, 4),
+              fits=((4, 2),))
+    quant = lambda *a: lib.moe_block_quantize(ctypes.byref(ops.MoeBlockQuantizeArgs(*a)), None)
+    blocks = 512 // 128 + 96
+    each_pair(lambda x, c, sc, cc, cs: quant(512, 640, 0, gp, x, c, sc, cc, cs),
+              (512 * 640 * 2, 512 * 640, 512 * 8 * 4, blocks * 640 * 128, blocks * 640 * 4), (1, 2, 3, 4))
+    each_pair(lambda x, cc, cs: quant(64, 640, 1, gp, x, 0, 0, cc, cs), (64 * 640 * 2, blocks * 640 * 128, blocks * 640 * 4), (1, 2))
+    each_pair(lambda x, c, sc: quant(300, 640, 0, None, x, c, sc, 0, 0), (300 * 640 * 2, 300 * 640, 300 * 8 * 4), (1, 2))
+    each_pair(lambda x, cc, cs: quant(300, 640, 0, None, x, 0, 0, cc, cs), (300 * 640 * 2, 3 * 640 * 128, 3 * 640 * 4), (1, 2))
+    W = ops.MoeBlockWeights
+    gemm = lambda *a: lib.moe_block_gemm(ctypes.byref(ops.MoeBlockGemmArgs(*a)), None)
+    nw, ns = 96 * 256 * 640, 96 * 2 * 5 * 4
+    each_pair(lambda c, sc, wc, ws, o: gemm(512, 0, 0, gp, c, sc, W(96, 256, 640, wc, ws), o),
+              (512 * 640, 512 * 8 * 4, nw, ns, 512 * 256 * 2), (4,))
+    each_pair(lambda c, sc, wc, ws, o: gemm(64, 1, 0, gp, c, sc, W(96, 256, 640, wc, ws), o),
+              (64 * 640, 64 * 8 * 4, nw, ns, 512 * 256 * 2), (4,))
+    each_pair(lambda c, sc, wc, ws, o: gemm(512, 0, 1, gp, c, sc, W(96, 256, 640, wc, ws), o),
+              (512 * 256, 512 * 4 * 4, nw, ns, 512 * 640 * 2), (4,))
+    each_pair(lambda c, sc, wc, ws, o: gemm(40, 0, 0, None, c, sc, W(1, 256, 640, wc, ws), o),
+              (40 * 640, 40 * 8 * 4, 256 * 640, 2 * 5 * 4, 40 * 256 * 2), (4,))
+    wgrad = lambda *a: lib.moe_block_wgrad(ctypes.byref(ops.MoeBlockWgradArgs(*a)), None)
+    each_pair(lambda gc, gs, xc, xs, d: wgrad(512, 256, 640, gp, gc, gs, xc, xs, d),
+              (blocks * 256 * 128, blocks * 256 * 4, blocks * 640 * 128, blocks * 640 * 4, 2 * nw), (4,))
+    each_pair(lambda gc, gs, xc, xs, d: wgrad(300, 256, 640, None, gc, gs, xc, xs, d),
+              (3 * 256 * 128, 3 * 256 * 4, 3 * 640 * 128, 3 * 640 * 4, 2 * 256 * 640), (4,))
+    each_pair(lambda w, c, sc: lib.moe_block_quantize_weights(w, 96, 256, 640, c, sc, None), (2 * nw, nw, ns), (1, 2))
+    each_pair(lambda a, c: lib.moe_block_pack_weights(a, 96, 256, 640, c, None), (nw, nw), (1,))
