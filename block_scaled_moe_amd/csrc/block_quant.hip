@@ -23,7 +23,7 @@ struct Divisor {
     float s, r;
     bool fast;
     __device__ __forceinline__ explicit Divisor(float amax) {
-        s = amax > 0.0f ? amax / 448.0f : 1.0f;
+        s = amax != 0.0f ? amax / 448.0f : 1.0f;  // a NaN stays one
         fast = s >= 0x1p-60f && s <= 0x1p60f;
         r = fast ? 1.0f / s : 0.0f;
     }
@@ -38,6 +38,15 @@ __device__ __forceinline__ void widen(uint32_t w, float &lo, float &hi) {
     lo = __uint_as_float(w << 16);
     hi = __uint_as_float(w & 0xffff0000u);
 }
+
+// Maxima are taken of magnitudes as bit patterns, two bf16 values a word: they order like the values, and a
+// NaN or an infinity, above them all, reaches the scale (a maximum of floats drops a NaN).
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t magnitudes(uint32_t w) { return w & 0x7fff7fffu; }
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+__device__ __forceinline__ float max_of(uint32_t m) { return __uint_as_float(max(m & 0xffff0000u, m << 16)); }
 
 // ---- rows: 16 lanes per block, 8 values each. A workgroup takes four blocks of four rows at a
 // time: a wave reads 1 KiB of one row, and each block's plane of codes gets 512 bytes in a row.
@@ -57,12 +66,10 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const BlockQuantArgs a) 
         widen(u.y, x[2], x[3]);
         widen(u.z, x[4], x[5]);
         widen(u.w, x[6], x[7]);
-        float m = 0.0f;
+        uint32_t m = max2(max2(magnitudes(u.x), magnitudes(u.y)), max2(magnitudes(u.z), magnitudes(u.w)));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-#pragma unroll
-        for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
-        const Divisor d(m);
+        for (int off = 8; off > 0; off >>= 1) m = max2(m, __shfl_xor(m, off));
+        const Divisor d(max_of(m));
         uint2 c;
         c.x = codes4(d.quotient(x[0]), d.quotient(x[1]), d.quotient(x[2]), d.quotient(x[3]));
         c.y = codes4(d.quotient(x[4]), d.quotient(x[5]), d.quotient(x[6]), d.quotient(x[7]));
@@ -78,14 +85,14 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const BlockQuantArgs a) 
 // two divisions are done once, by one lane, and reach the others through LDS.
 constexpr int kColumnTiles = 4;
 
-// v[r] holds this lane's part of the maximum of row r over the 16 lanes of a DPP row; returns the
-// whole maximum of row (lane & 15). Each step gives half of its rows to a partner lane and takes
+// v[r] holds this lane's part of the maxima of row r (its even and its odd columns') over the 16 lanes of a
+// DPP row; returns the whole maxima of row (lane & 15). Each step gives half of its rows to a partner lane and takes
 // the partner's part of the other half: partners l ^ 8, l ^ 7, l ^ 2, l ^ 1 reach all 16 lanes.
-__device__ __forceinline__ float row_maxima(float (&v)[16], int lane) {
+__device__ __forceinline__ uint32_t row_maxima(uint32_t (&v)[16], int lane) {
 #define MOE_HALVE(COUNT, BIT, CTRL)                                                                               \
     _Pragma("unroll") for (int r = 0; r < COUNT; ++r) {                                                           \
-        const float keep = (lane & BIT) ? v[r + COUNT] : v[r], give = (lane & BIT) ? v[r] : v[r + COUNT];         \
-        v[r] = fmaxf(keep, __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(give), CTRL, 0xF, 0xF, true))); \
+        const uint32_t keep = (lane & BIT) ? v[r + COUNT] : v[r], give = (lane & BIT) ? v[r] : v[r + COUNT];      \
+        v[r] = max2(keep, __builtin_amdgcn_update_dpp(0, give, CTRL, 0xF, 0xF, true));                            \
     }
     MOE_HALVE(8, 8, 0x128)  // row_ror:8
     MOE_HALVE(4, 4, 0x141)  // row_half_mirror
@@ -106,7 +113,8 @@ __device__ __forceinline__ uint32_t quotient_codes(const float (&x)[4], float s,
 
 template <bool TOKEN, bool ROWS>
 __global__ void __launch_bounds__(kThreads, 3) columns_kernel(const BlockQuantArgs a) {
-    __shared__ __attribute__((aligned(16))) float col_max[8][128], col_s[128], col_r[128];
+    __shared__ __attribute__((aligned(16))) uint16_t col_max[8][128];  // magnitudes' bits
+    __shared__ __attribute__((aligned(16))) float col_s[128], col_r[128];
     __shared__ __attribute__((aligned(16))) float row_s[8][16], row_r[8][16];
     const int tid = threadIdx.x, q = tid & 31, h = tid >> 5;
     const int32_t run = blockIdx.x;
@@ -152,22 +160,20 @@ __global__ void __launch_bounds__(kThreads, 3) columns_kernel(const BlockQuantAr
 #pragma unroll
         for (int r = 0; r < 16; ++r) u[r] = next[r];
         if (ct + 1 < ct1) load(next, ct + 1);
-        float m[4] = {0.0f, 0.0f, 0.0f, 0.0f}, rm[16];
+        uint32_t m0 = 0, m1 = 0, rm[16];
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            float x[4];
-            widen(u[r].x, x[0], x[1]);
-            widen(u[r].y, x[2], x[3]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) m[c] = fmaxf(m[c], fabsf(x[c]));
-            rm[r] = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+            const uint32_t a0 = magnitudes(u[r].x), a1 = magnitudes(u[r].y);
+            m0 = max2(m0, a0);
+            m1 = max2(m1, a1);
+            rm[r] = max2(a0, a1);
         }
-        *reinterpret_cast<float4 *>(&col_max[h][4 * q]) = make_float4(m[0], m[1], m[2], m[3]);
+        *reinterpret_cast<uint2 *>(&col_max[h][4 * q]) = make_uint2(m0, m1);
         bool fast = true;
         if (ROWS) {  // the 32 threads of a row are half a wave
-            float top = row_maxima(rm, tid & 15);
-            top = fmaxf(top, __shfl_xor(top, 16));
-            const Divisor d(top);
+            uint32_t top = row_maxima(rm, tid & 15);
+            top = max2(top, __shfl_xor(top, 16));
+            const Divisor d(max_of(top));
             fast = __all(d.fast);
             if (q < 16) {
                 row_s[h][q] = d.s;
@@ -177,10 +183,10 @@ __global__ void __launch_bounds__(kThreads, 3) columns_kernel(const BlockQuantAr
         }
         __syncthreads();
         if (tid < 128) {
-            float cm = col_max[0][tid];
+            uint32_t cm = col_max[0][tid];
 #pragma unroll
-            for (int g = 1; g < 8; ++g) cm = fmaxf(cm, col_max[g][tid]);
-            const Divisor d(cm);
+            for (int g = 1; g < 8; ++g) cm = max(cm, (uint32_t)col_max[g][tid]);
+            const Divisor d(__uint_as_float(cm << 16));
             col_s[tid] = d.s;
             col_r[tid] = d.r;
             a.col_scales[(int64_t)run * a.C + ct * 128 + tid] = d.s;
@@ -233,36 +239,29 @@ __global__ void __launch_bounds__(kThreads, 3) columns_kernel(const BlockQuantAr
 // quarter row of a 32 x 64 tile) of rows r, r + 32, r + 64, r + 96.
 __global__ void __launch_bounds__(kThreads) weights_kernel(const uint16_t *__restrict__ w, int32_t N, int32_t K,
                                                            uint8_t *__restrict__ codes, float *__restrict__ scales) {
-    __shared__ float part[kThreads / 64];
+    __shared__ uint32_t part[kThreads / 64];
     const int tid = threadIdx.x, q = tid & 7, r = tid >> 3;
     const int kblocks = K / 128, nblocks = N / 128;
     const int64_t b = blockIdx.x;
     const int kb = (int)(b % kblocks), nb = (int)((b / kblocks) % nblocks);
     const int64_t e = b / ((int64_t)kblocks * nblocks);
     uint4 u[4][2];
-    float m = 0.0f;
+    uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint4 *src = reinterpret_cast<const uint4 *>(w + (e * N + nb * 128 + 32 * i + r) * K + kb * 128 + 16 * q);
         u[i][0] = src[0];
         u[i][1] = src[1];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t word[4] = {u[i][j].x, u[i][j].y, u[i][j].z, u[i][j].w};
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                float lo, hi;
-                widen(word[d], lo, hi);
-                m = fmaxf(m, fmaxf(fabsf(lo), fabsf(hi)));
-            }
-        }
+        for (int j = 0; j < 2; ++j)
+            m = max2(m, max2(max2(magnitudes(u[i][j].x), magnitudes(u[i][j].y)), max2(magnitudes(u[i][j].z), magnitudes(u[i][j].w))));
     }
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+    for (int off = 32; off > 0; off >>= 1) m = max2(m, __shfl_xor(m, off));
     if ((tid & 63) == 0) part[tid >> 6] = m;
     __syncthreads();
-    m = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-    const Divisor d(m);
+    m = max2(max2(part[0], part[1]), max2(part[2], part[3]));
+    const Divisor d(max_of(m));
     if (tid == 0) scales[b] = d.s;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

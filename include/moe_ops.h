@@ -11,9 +11,9 @@
  * synchronises, no allocation, no global state). `stream` must belong to the current
  * device. An output that overlaps an input of its call or another output is refused
  * (MOE_ERR_INVALID_ARG) unless the call allows it; the groups' own arrays, which nothing
- * else may write, are not compared. NaN and infinite inputs of the quantisers are outside
- * the contract; the sort's row operators pass them through to the rows and sums they belong
- * to and to no others.
+ * else may write, are not compared. The row operators pass NaN and infinite values through
+ * to the rows and sums they belong to and to no others; what they do to a quantised block
+ * stands at the format below.
  */
 #ifndef BLOCK_SCALED_MOE_OPS_H
 #define BLOCK_SCALED_MOE_OPS_H
@@ -81,7 +81,8 @@ int32_t moe_combine_backward(const moe_groups *g, int32_t y_dtype, int32_t out_d
 /* ------------------------------------------------------------------ FP8, blocks of 128
  * E4M3 (OCP "FN") codes with one fp32 scale per block of 128: s = fl32(max |block| / 448),
  * 1 for an all-zero block; code = E4M3(fl32(x / s)), nearest, ties to even. The value is
- * code * s. All dimensions that blocks run along are multiples of 128 up to 2^24.
+ * code * s. A NaN or an infinity makes its block's scale a NaN or an infinity (the codes are
+ * then not specified), and with it every result that the block enters. All dimensions that blocks run along are multiples of 128 up to 2^24.
  *   rows     codes [C/128][R][128] (the rows' first blocks, then their second ones, ..),
  *            scales [R][S], S = C/128 rounded up to a multiple of 4 (the rest of a row is
  *            neither written nor used): blocks of 1 x 128; R < 2^25 and R * S < 2^30

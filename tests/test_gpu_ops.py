@@ -606,3 +606,56 @@ def test_weights_gradient_in_the_weights_place(D):
     w2 = w.clone()
     dy2, dw2 = moe.combine_backward(g, d, y, w2, dw=w2)
     assert dw2 is w2 and torch.equal(dw, dw2) and torch.equal(dy, dy2)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_non_finite_values_reach_the_results(bad):
+    """A NaN or an infinity makes its block's scale, and every result that the block enters, not finite; all other codes,
+    scales and results keep their bits."""
+    rng = np.random.default_rng(8)
+    idx = exact_counts([200, 100])
+    g = moe.sort_tokens(dev(idx.reshape(-1, 1)), 2)
+    x, dy, w = values(rng, (300, 384), "bf16"), values(rng, (300, 256), "bf16"), values(rng, (2, 256, 384), "bf16")
+    t = lambda a: dev(a, torch.bfloat16)
+    put = lambda a, at: t(np.where(np.arange(a.size).reshape(a.shape) == np.ravel_multi_index(at, a.shape), np.float32(bad), a))
+    zero = lambda a, at: t(np.where(np.arange(a.size).reshape(a.shape) == np.ravel_multi_index(at, a.shape), np.float32(0), a))
+
+    def same_but(a, b, where, codes=False):
+        a, b = num(a) if a.is_floating_point() else host(a), num(b) if b.is_floating_point() else host(b)
+        hit = np.zeros(a.shape, bool)
+        hit[where] = True
+        assert np.array_equal(a[~hit], b[~hit])
+        assert codes or not np.isfinite(a[hit]).any()
+
+    wq = moe.quantize_block_weights(t(w))
+    # a row's value: row 5 is in block 1 of its row, in the first expert's first run
+    (q, c), (q0, c0) = moe.quantize_block_both(put(x, (5, 130)), g), moe.quantize_block_both(zero(x, (5, 130)), g)
+    one, one0 = moe.quantize_block(put(x, (5, 130))), moe.quantize_block(zero(x, (5, 130)))
+    only = moe.quantize_block_columns(put(x, (5, 130)), g)
+    for a, b in ((q, q0), (one, one0)):
+        same_but(a.scales[:, :3], b.scales[:, :3], (5, 1))
+        same_but(a.codes, b.codes, (1, 5), True)
+    runs = [0, 1, 2]  # offsets 0, 200: blocks 0, 1 of the first expert, 200 / 128 + 1 = 2 of the second
+    for a in (c, only):
+        same_but(a.scales[runs], c0.scales[runs], (0, 130))
+        same_but(a.codes[runs], c0.codes[runs], (0, 4, slice(None), slice(None), 2), True)
+    same_but(moe.block_product(q, wq, g), moe.block_product(q0, wq, g), 5)
+    gq, gc = moe.quantize_block_both(t(dy), g)
+    same_but(moe.block_weight_grad(gc, c, g), moe.block_weight_grad(gc, c0, g), (0, slice(None), 130))
+    # an output gradient's, in the second expert's rows
+    (q, c), (q0, c0) = moe.quantize_block_both(put(dy, (250, 7)), g), moe.quantize_block_both(zero(dy, (250, 7)), g)
+    same_but(moe.block_product_grad(q, wq, g), moe.block_product_grad(q0, wq, g), 250)
+    same_but(moe.block_weight_grad(c, only, g)[1:], moe.block_weight_grad(c0, only, g)[1:], (0, 7))
+    # a token's, seen through its one sorted row
+    row = int(np.nonzero(host(g.sorted_slot) == 17)[0][0])
+    a, b = (moe.quantize_block_columns(f(x, (17, 200)), g, by_token=True) for f in (put, zero))
+    run = row // 128 if row < 200 else 2
+    same_but(a.scales[runs], b.scales[runs], (run, 200))
+    # few rows: the kernel that streams the weights
+    a, b = (moe.block_product(moe.quantize_block(f(x, (5, 130))[:20]), wq.experts(0, 1)) for f in (put, zero))
+    same_but(a, b, 5)
+    # a weight's
+    a, b = (moe.quantize_block_weights(f(w, (1, 200, 300))) for f in (put, zero))
+    same_but(a.scales, b.scales, (1, 1, 2))
+    same_but(moe.block_product(one0, a, g), moe.block_product(one0, b, g), (slice(200, 300), slice(128, 256)))
+    same_but(moe.block_product_grad(gq, a, g), moe.block_product_grad(gq, b, g), (slice(200, 300), slice(256, 384)))
