@@ -344,6 +344,7 @@ class BlockRows(_Quantised):
 class BlockColumns(_Quantised):
     """Sorted rows in E4M3 with an fp32 scale per column of each run of 128 rows of an expert (the column
     form of include/moe_ops.h): codes uint8 [blocks, C / 32, 2, 4, 32, 16], scales [blocks, C]."""
+    height = None  # rows of the one group that it was made from, where known on the host
 
     @property
     def width(self) -> int:
@@ -447,6 +448,8 @@ def _quantize(x: torch.Tensor, g: Groups | None, by_token: bool, rows: bool, col
     if columns:
         n = (R if g is None else g.rows) // 128 + (1 if g is None else g.n)  # moe_block_column_blocks
         c = BlockColumns.empty(n, C, dev)
+        if g is None:
+            c.height = R
         cc = c.buffer.data_ptr()
         cs = cc + c.split
     _filled(g)
@@ -516,6 +519,9 @@ def block_weight_grad(dy: BlockColumns, x: BlockColumns, g: Groups | None = None
     _ask_form("x", x, BlockColumns)
     dev = dy.place() if g is None else g.device
     R = rows if g is None else g.rows
+    for q in (dy, x) if g is None else ():
+        if R < 0 or q.height not in (None, R):
+            raise ValueError(f"rows: {R}, but a column form holds {q.height}")
     N, K, n = dy.width, x.width, 1 if g is None else g.n
     _blocks_of_128("dy", N)
     _blocks_of_128("x", K)

@@ -338,3 +338,28 @@ def test_overlapping_outputs_are_refused():
               (3 * 256 * 128, 3 * 256 * 4, 3 * 640 * 128, 3 * 640 * 4, 2 * 256 * 640), (4,))
     each_pair(lambda w, c, sc: lib.moe_block_quantize_weights(w, 96, 256, 640, c, sc, None), (2 * nw, nw, ns), (1, 2))
     each_pair(lambda a, c: lib.moe_block_pack_weights(a, 96, 256, 640, c, None), (nw, nw), (1,))
+
+
+def test_weight_gradient_of_other_rows_is_refused(monkeypatch):
+    """Without groups, `rows` is checked against the rows that the column forms were made from: 256 of 300 rows have the
+    same blocks but lose the last run, and 260 of 256 would take in a run that nothing wrote."""
+    monkeypatch.setattr(ops, "_call", lambda *a: None)
+    x = lambda n: torch.zeros((n, 128), dtype=torch.bfloat16)
+    c = {n: moe.quantize_block_columns(x(n)) for n in (0, 256, 260, 300)}
+    for n in c:
+        moe.block_weight_grad(c[n], c[n], rows=n)
+    both = moe.quantize_block_both(x(300))[1]
+    for dy, other, rows in ((300, 300, 256), (300, 300, 260), (256, 256, 260), (300, 260, 300), (260, 300, 300), (260, 300, 260)):
+        with pytest.raises(ValueError, match="rows"):
+            moe.block_weight_grad(c[dy], c[other], rows=rows)
+    with pytest.raises(ValueError, match="rows"):
+        moe.block_weight_grad(c[300], both, rows=310)
+    with pytest.raises(ValueError, match="rows"):
+        moe.block_weight_grad(c[300], both, rows=-1)
+    plain = moe.BlockColumns(c[300].codes, c[300].scales)  # made of tensors: the caller knows
+    moe.block_weight_grad(plain, c[300], rows=300)
+    moe.block_weight_grad(plain, plain, rows=270)
+    # with groups the host does not know how many of the rows are local
+    g = moe.Groups.empty(150, 2, 1, device="cpu")
+    g.filled = True
+    moe.block_weight_grad(moe.quantize_block_columns(x(300), g), c[300], g)
