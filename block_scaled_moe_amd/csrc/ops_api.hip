@@ -42,13 +42,14 @@ GroupsPlan groups_plan(int32_t T, int32_t top_k, int32_t n) {
 namespace {
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+constexpr int32_t kMaxRows = INT32_MAX / 2;  // slots, or rows of one group: rounded up to runs they stay in 32 bits
 int32_t to_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 // The size fields of g.
 int32_t check_sizes(const moe_groups *g) {
     if (!g || g->T < 0 || g->top_k < 1 || g->top_k > 8 || g->E < 1 || g->E > 4096) return MOE_ERR_INVALID_ARG;
     if (g->e_begin < 0 || g->e_end <= g->e_begin || g->e_end > g->E) return MOE_ERR_INVALID_ARG;
-    if ((int64_t)g->T * g->top_k > INT32_MAX / 2) return MOE_ERR_INVALID_ARG;
+    if ((int64_t)g->T * g->top_k > kMaxRows) return MOE_ERR_INVALID_ARG;
     return MOE_OK;
 }
 
@@ -245,7 +246,7 @@ int32_t moe_block_quantize(const moe_block_quantize_args *q, void *stream) {
         if (rc != MOE_OK) return rc;
         if (q->rows != (q->by_token ? q->g->T : q->g->T * q->g->top_k)) return MOE_ERR_INVALID_ARG;
     }
-    if (by_rows && !rows_form_fits(q->rows, q->C)) return MOE_ERR_UNSUPPORTED;
+    if ((by_rows && !rows_form_fits(q->rows, q->C)) || q->rows > kMaxRows) return MOE_ERR_UNSUPPORTED;
     if (q->rows == 0) return MOE_OK;
     if (!q->x) return MOE_ERR_INVALID_ARG;
     if (!aligned16(q->x) || !aligned16(q->codes) || !aligned16(q->scales) || !aligned16(q->col_codes) ||
@@ -348,7 +349,8 @@ int32_t moe_block_gemm(const moe_block_gemm_args *a, void *stream) {
 
 int32_t moe_block_wgrad(const moe_block_wgrad_args *a, void *stream) {
     if (!a || a->rows < 0 || a->N < 1 || a->K < 1) return MOE_ERR_INVALID_ARG;
-    if (a->N % 128 || a->K % 128 || a->N > kMaxBlockDim || a->K > kMaxBlockDim) return MOE_ERR_UNSUPPORTED;
+    if (a->N % 128 || a->K % 128 || a->N > kMaxBlockDim || a->K > kMaxBlockDim || a->rows > kMaxRows)
+        return MOE_ERR_UNSUPPORTED;
     if (a->g) {
         const int32_t rc = check_groups(a->g);
         if (rc != MOE_OK) return rc;

@@ -107,9 +107,9 @@ typedef struct moe_block_weights {
 int64_t moe_block_column_blocks(int32_t rows, int32_t n);
 
 /* Quantise bf16 x [rows][C] by rows (codes, scales), by columns (col_codes, col_scales), or
- * both from one read. g = NULL: every row, one group. g given: rows = T * top_k sorted rows,
- * of which the S local ones are quantised; or, with by_token, x is [T][C] and sorted row p is
- * x[sorted_slot[p] / top_k] (columns only; rows = T). */
+ * both from one read. g = NULL: every row (fewer than 2^30), one group. g given: rows =
+ * T * top_k sorted rows, of which the S local ones are quantised; or, with by_token, x is
+ * [T][C] and sorted row p is x[sorted_slot[p] / top_k] (columns only; rows = T). */
 typedef struct moe_block_quantize_args {
     int32_t rows, C;          /* C % 128 == 0 */
     int32_t by_token;
@@ -155,7 +155,7 @@ int32_t moe_block_gemm(const moe_block_gemm_args *a, void *stream);
  * of the input (K columns) of the same sorted rows:
  *   dw[e][n][k] = sum over e's runs of 128 rows of sum over the run of cg * cx, times sg * sx
  * bf16 [E][N][K], accumulated in fp32 in ascending order; zeros for an expert without rows.
- * g = NULL: one group of `rows` rows (E = 1). N % 128 == 0, K % 128 == 0. */
+ * g = NULL: one group of `rows` < 2^30 rows (E = 1). N % 128 == 0, K % 128 == 0. */
 typedef struct moe_block_wgrad_args {
     int32_t rows;             /* T * top_k, or the rows of the one group */
     int32_t N, K;

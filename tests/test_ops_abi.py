@@ -363,3 +363,16 @@ def test_weight_gradient_of_other_rows_is_refused(monkeypatch):
     g = moe.Groups.empty(150, 2, 1, device="cpu")
     g.filled = True
     moe.block_weight_grad(moe.quantize_block_columns(x(300), g), c[300], g)
+
+
+def test_one_group_has_at_most_half_of_an_int_of_rows():
+    """Runs of 128 rows are counted in 32 bits: the number of rows next to the type's end overflowed there and gave an
+    empty gradient. One group has the bound that T * top_k has."""
+    lib, top = moe.lib(), 2 ** 31 - 1
+    at = [A + (i << 42) for i in range(5)]
+    for rows in (top, top - 127, top // 2 + 1):
+        w = ops.MoeBlockWgradArgs(rows, 128, 128, None, *at)
+        assert lib.moe_block_wgrad(ctypes.byref(w), None) == EUNSUP
+        q = ops.MoeBlockQuantizeArgs(rows, 128, 0, None, at[0], 0, 0, at[1], at[2])
+        assert lib.moe_block_quantize(ctypes.byref(q), None) == EUNSUP
+    assert lib.moe_block_wgrad(ctypes.byref(ops.MoeBlockWgradArgs(-1, 128, 128, None, *at)), None) == EINVAL
