@@ -659,3 +659,116 @@ def test_non_finite_values_reach_the_results(bad):
     same_but(a.scales, b.scales, (1, 1, 2))
     same_but(moe.block_product(one0, a, g), moe.block_product(one0, b, g), (slice(200, 300), slice(128, 256)))
     same_but(moe.block_product_grad(gq, a, g), moe.block_product_grad(gq, b, g), (slice(200, 300), slice(256, 384)))
+
+
+def sorted_by_definition(idx, e0, e1):
+    """ref.sort for many slots: a stable sort by expert, what is not local behind."""
+    flat = idx.reshape(-1).astype(np.int64) - e0
+    n = e1 - e0
+    key = np.where((flat >= 0) & (flat < n), flat, n)
+    order = np.argsort(key, kind="stable")
+    off = np.searchsorted(key[order], np.arange(n + 1))
+    S = off[-1]
+    ss, sp = np.full(flat.size, -1), np.full(flat.size, -1)
+    ss[:S] = order[:S]
+    sp[order[:S]] = np.arange(S)
+    return off, ss, sp.reshape(idx.shape)
+
+
+@pytest.mark.parametrize("kind", ["dup", "wild", "hot", "one"])
+@pytest.mark.parametrize("T,k,E,e0,e1", [
+    (1024, 1, 384, 0, 384), (1025, 1, 384, 0, 384),    # one and two passes of the one workgroup
+    (4095, 1, 384, 0, 384), (2048, 2, 384, 0, 384), (4097, 1, 384, 0, 384),  # one launch, two launches
+    (2500, 8, 384, 0, 384), (2500, 8, 700, 0, 700), (2500, 8, 1024, 0, 1024), (2500, 8, 1025, 0, 1025),
+    (2500, 8, 4096, 1000, 2024), (2500, 8, 65, 0, 65), (4096, 5, 513, 1, 513),
+    (33000, 8, 384, 0, 384), (33000, 8, 384, 96, 192), (66001, 8, 1024, 0, 1024)])  # several passes a chunk
+def test_sort_of_many_slots(kind, T, k, E, e0, e1):
+    """Every branch of the sort by size: passes of a workgroup, one launch or two, threads or waves or all of the
+    workgroup holding experts, chunks of more than one pass; against the definition, in full."""
+    rng = np.random.default_rng(T + E + e0)
+    if kind == "hot":  # most slots on a few experts, the rest anywhere
+        idx = np.where(rng.random((T, k)) < 0.9, rng.integers(0, 3, (T, k)) * (E // 3), rng.integers(0, E, (T, k))).astype(np.int32)
+    else:
+        idx = routing(kind, T, k, E, rng)
+    g = moe.sort_tokens(dev(idx), E, e0, e1)
+    off, ss, sp = sorted_by_definition(idx, e0, e1)
+    assert np.array_equal(host(g.offsets), off) and np.array_equal(host(g.slot_pos), sp) and np.array_equal(host(g.sorted_slot), ss)
+    # the tiles of the products, through one: a row's product with its expert's number in the scale
+    n = e1 - e0
+    w = moe.BlockWeights(n, 128, 128, torch.full((n, 4, 2, 4, 32, 16), 0x38, dtype=torch.uint8, device="cuda"),
+                         torch.arange(1, n + 1, device="cuda", dtype=torch.float32).reshape(n, 1, 1))
+    x = torch.zeros((T, 128), dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = 1.0
+    out = torch.full((T * k, 128), -1.0, dtype=torch.bfloat16, device="cuda")
+    moe.block_product(moe.quantize_block(x), w, g, by_token=True, out=out)
+    S = int(off[-1])
+    # 448 times fl32(1 / 448) times e + 1, rounded to bf16: within half a step of each of the three roundings
+    want = np.repeat(np.arange(1, n + 1), np.diff(off)).astype(np.float64)
+    got = num(out)
+    assert (np.abs(got[:S] - want[:, None]) <= want[:, None] * (ref.U_BF16 + 4 * ref.U24)).all() and (got[S:] == -1.0).all()
+
+
+def test_reference_sorts_agree():
+    rng = np.random.default_rng(0)
+    for kind in ("dup", "wild", "none"):
+        idx = routing(kind, 50, 3, 20, rng)
+        for a, b in zip(sorted_by_definition(idx, 4, 15), ref.sort(idx, 4, 15)):
+            assert np.array_equal(a, b)
+
+
+# Root mean square of the difference that a correct product may have; the largest single one (`check`) has room for a
+# worst case that sums of ordinary values come nowhere near.
+#  - rounding to bf16: for values not placed on purpose the error is spread evenly over half a step h to either side,
+#    h^2 / 3 in the mean (10 % for the spread of the sample: over 10^4 values its deviation is under 1 %);
+#  - the MFMA drops from each of a block's 128 products less than t = 2^-13 of the largest, the sign that of the product,
+#    which is as often positive as negative: 128 t^2 / 3 in the mean at most;
+#  - fp32: (blocks + 3) half steps of the sum of magnitudes, as in ops_ref.py, all in one direction.
+def rms_check(got, want, size, top2, blocks, what):
+    h = np.exp2(np.floor(np.log2(np.maximum(np.abs(want), 1e-30))) - 8)
+    mean = 1.1 ** 2 * (h ** 2 / 3).mean() + (128 / 3 * 2.0 ** -26 * top2).mean() + (((blocks + 3) * ref.U24 * size) ** 2).mean()
+    err = ((got - want) ** 2).mean()
+    assert got.size >= 10000 and err <= mean, f"{what}: rms {np.sqrt(err)}, expected up to {np.sqrt(mean)}"
+    assert np.sqrt(mean) <= 2.5e-3 * np.sqrt((want ** 2).mean())   # the bound itself is close to the rounding
+
+
+@pytest.mark.parametrize("counts,N,K", [([300, 130], 384, 4352), ([300, 130], 256, 128), ([2] * 16, 384, 2176), ([1] * 90, 128, 256),
+                                        ([90], 256, 2048), ([513], 512, 1152), ([128, 700], 256, 640)], ids=lambda v: str(v)[:20])
+def test_products_in_the_mean(counts, N, K):
+    """Product, its transposed form and the weight gradient on normal values, by the root mean square of their errors: a
+    factor wrong by a per cent anywhere in a sum shows."""
+    rng = np.random.default_rng(N + K + sum(counts))
+    T = sum(counts)
+    g = moe.sort_tokens(dev(np.repeat(np.arange(len(counts)), counts).astype(np.int32).reshape(T, 1)), len(counts))
+    x, dy, w = values(rng, (T, K), "bf16"), values(rng, (T, N), "bf16"), values(rng, (len(counts), N, K), "bf16")
+    wq, (wc, ws) = moe.quantize_block_weights(dev(w, torch.bfloat16)), ref.weights(w)
+    (xr, xcol), (gr, gcol) = (moe.quantize_block_both(dev(a, torch.bfloat16), g) for a in (x, dy))
+    off = np.concatenate([[0], np.cumsum(counts)])
+
+    def product(rows, transposed):
+        c, s = ref.rows(rows)
+        v = ref.e4m3_value(c) * np.repeat(s.astype(np.float64), 128, 1)
+        y, size, top2 = (np.zeros((T, K if transposed else N)) for _ in range(3))
+        for e in range(len(counts)):
+            at = slice(off[e], off[e + 1])
+            we = ref.e4m3_value(wc[e]) * np.repeat(np.repeat(ws[e].astype(np.float64), 128, 0), 128, 1)
+            we = we.T if transposed else we
+            y[at], size[at] = v[at] @ we.T, np.abs(v[at]) @ np.abs(we).T
+            top2[at] = ref.tops(v[at]) ** 2 @ (ref.tops(we) ** 2).T
+        return y, size, top2, rows.shape[1] // 128
+
+    rms_check(num(moe.block_product(xr, wq, g)), *product(x, False), "y")
+    rms_check(num(moe.block_product_grad(gr, wq, g)), *product(dy, True), "dx")
+    if len(counts) == 1:
+        rms_check(num(moe.block_product(moe.quantize_block(dev(x, torch.bfloat16)), wq)), *product(x, False), "y without groups")
+    got, cg, cx = num(moe.block_weight_grad(gcol, xcol, g)), ref.columns(dy, off), ref.columns(x, off)
+    value = lambda q: ref.e4m3_value(q[0].transpose(1, 2, 4, 0, 3).reshape(128, -1)) * q[1].astype(np.float64)
+    want, size, top2 = (np.zeros((len(counts), N, K)) for _ in range(3))
+    runs = 0
+    for b, r0, n in ref.column_blocks(off):
+        e = np.searchsorted(off, r0, side="right") - 1
+        u, v = value(cg[b]), value(cx[b])
+        want[e] += u.T @ v
+        size[e] += np.abs(u.T) @ np.abs(v)
+        top2[e] += np.outer(np.abs(u).max(0), np.abs(v).max(0)) ** 2
+        runs = max(runs, (counts[e] + 127) // 128)
+    rms_check(got, want, size, top2, runs, "dw")
