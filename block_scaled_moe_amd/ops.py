@@ -102,6 +102,12 @@ def _call(name: str, device: torch.device, *args):
         raise MoeError(name, rc)
 
 
+def _int32(what: str, v: int):
+    """ctypes passes the low 32 bits of a larger number on."""
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{what}: {v} does not fit 32 bits")
+
+
 def _ask(what: str, t: torch.Tensor, shape: tuple, dtype, device: torch.device):
     """t has this shape, dtype (one or a collection of them) and device, is contiguous, and autograd does not follow it."""
     if t.shape != shape:
@@ -184,6 +190,8 @@ class Groups:
 def _groups_layout(T: int, top_k: int, E: int, e_begin: int, e_end: int) -> tuple[int, int, int, int]:
     """Byte offsets of sorted_slot, slot_pos and the plan behind offsets, and the total, each a multiple of 256."""
     from . import MoeError
+    for v in (T, top_k, E, e_begin, e_end):
+        _int32("groups", v)
     st = MoeGroups(T, top_k, E, e_begin, e_end)
     n_plan = int(_function("moe_groups_plan_bytes")(ctypes.byref(st)))
     if n_plan == 0:
@@ -221,7 +229,10 @@ def _filled(g: Groups | None):
 def _row_width(what: str, t: torch.Tensor) -> int:
     if t.dim() != 2:
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected [rows, D]")
-    return t.shape[1]
+    rows, D = t.shape
+    if rows >= 2 ** 31 or D >= 2 ** 31:
+        _int32(what, max(rows, D))
+    return D
 
 
 def gather(g: Groups, x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:

@@ -376,3 +376,23 @@ def test_one_group_has_at_most_half_of_an_int_of_rows():
         q = ops.MoeBlockQuantizeArgs(rows, 128, 0, None, at[0], 0, 0, at[1], at[2])
         assert lib.moe_block_quantize(ctypes.byref(q), None) == EUNSUP
     assert lib.moe_block_wgrad(ctypes.byref(ops.MoeBlockWgradArgs(-1, 128, 128, None, *at)), None) == EINVAL
+
+
+def test_sizes_past_32_bits_are_refused(monkeypatch):
+    """The C ABI takes sizes in 32 bits, and ctypes would pass the low ones of a larger number on: a row of 2^32 + 8 values
+    would be moved as one of 8."""
+    monkeypatch.setattr(ops, "_call", lambda *a: None)
+    big = 2 ** 32
+    t = lambda *shape, dtype=torch.bfloat16: torch.empty(shape, dtype=dtype, device="meta")  # no memory behind it
+    g = moe.Groups.empty(1, 2, 8, device="meta")
+    g.filled = True
+    w = t(1, 2, dtype=torch.float32)
+    for call in (lambda: moe.gather(g, t(1, big + 8)), lambda: moe.gather_backward(g, t(2, big + 8)),
+                 lambda: moe.combine(g, t(2, big + 8), w), lambda: moe.combine_backward(g, t(1, big + 8), t(2, big + 8), w),
+                 lambda: moe.quantize_block(t(1, big + 128)), lambda: moe.quantize_block_columns(t(1, big + 128)),
+                 lambda: moe.quantize_block_both(t(big + 1, 128)), lambda: moe.quantize_block(t(1, 2 ** 31)),
+                 lambda: moe.sort_tokens(t(big + 1, 1, dtype=torch.int32), 8), lambda: moe.sort_tokens(t(1, 2, dtype=torch.int32), big + 8),
+                 lambda: moe.sort_tokens(t(1, 2, dtype=torch.int32), 8, big, big + 8), lambda: moe.Groups.empty(1, big + 2, 8, device="meta")):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+    assert moe.gather(g, t(1, 2 ** 31 - 1)).shape == (2, 2 ** 31 - 1)  # the library's own bounds come next
