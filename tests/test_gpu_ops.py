@@ -772,3 +772,27 @@ def test_products_in_the_mean(counts, N, K):
         top2[e] += np.outer(np.abs(u).max(0), np.abs(v).max(0)) ** 2
         runs = max(runs, (counts[e] + 127) // 128)
     rms_check(got, want, size, top2, runs, "dw")
+
+
+def test_rows_past_32_bit_bytes_of_a_plane():
+    """2^24 + 1000 rows of one block: their codes lie past 2^31 bytes of the block's plane. The last 1000 rows give the
+    bits that they give alone, by every form of the product, and so does a gradient that is zero before them."""
+    R, last = 2 ** 24 + 1000, 1000
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(2)
+    x = torch.randn((R, 128), dtype=torch.bfloat16, device="cuda", generator=gen)
+    w = moe.quantize_block_weights(torch.randn((1, 128, 128), dtype=torch.bfloat16, device="cuda", generator=gen))
+    xs = x[-last:].clone()
+    q, q1 = moe.quantize_block(x), moe.quantize_block(xs)
+    assert torch.equal(q.codes[:, -last:], q1.codes) and torch.equal(q.scales[-last:, :1], q1.scales[:, :1])
+    y = moe.block_product(q, w)
+    assert torch.equal(y[-last:], moe.block_product(q1, w))
+    g = moe.sort_tokens(torch.zeros((R, 1), dtype=torch.int32, device="cuda"), 1)
+    assert torch.equal(moe.block_product(q, w, g, by_token=True), y) and torch.equal(moe.block_product(q, w, g), y)
+    assert torch.equal(moe.block_product_grad(q, w)[-last:], moe.block_product_grad(q1, w))
+    c, c1 = moe.quantize_block_columns(x), moe.quantize_block_columns(xs)
+    assert torch.equal(c.codes[2 ** 24 // 128:], c1.codes) and torch.equal(c.scales[2 ** 24 // 128:], c1.scales)
+    both, cb = moe.quantize_block_both(x, g)
+    assert torch.equal(both.codes, q.codes) and torch.equal(cb.codes[2 ** 24 // 128:], c1.codes)
+    x[:-last] = 0.0
+    assert torch.equal(moe.block_weight_grad(moe.quantize_block_columns(x), c, rows=R), moe.block_weight_grad(c1, c1, rows=last))
