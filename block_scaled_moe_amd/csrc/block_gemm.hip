@@ -22,10 +22,10 @@
 // Transposed, the reduction runs along the weights' rows: the same bytes are copied, and the
 // operand is read with the transposing LDS read (8 rows x 16 columns per 16 lanes).
 //
-// One group of 8191 rows, 5120 x 4096: 177 us (1.94 PFLOP/s), of which the products alone take 130 us, the
-// barriers 8, the stores 15, the copies 24. 96 groups of about 170 rows, 5120 x 4096: 466 us (1.47 PFLOP/s,
+// One group of 8191 rows, 5120 x 4096: 176 us (1.95 PFLOP/s), of which the products alone take 130 us, the
+// barriers 8, the stores 15, the copies 24. 96 groups of about 170 rows, 5120 x 4096: 467 us (1.47 PFLOP/s,
 // 4.8 TB/s of weights, rows and results; a group's last tile is as long in copies as a full one). Transposed
-// on 16384 unevenly grouped rows, 4096 x 2560: 273 us.
+// on 17108 unevenly grouped rows, 4096 x 2560: 278 us.
 // stream_kernel below takes over where groups have few rows.
 #include "block_mma.h"
 #include "ops_internal.h"
@@ -347,8 +347,8 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const BlockGemmArgs p) {
 // order. Up to 32 rows have two blocks' loads ahead of the products, more rows share a turn's
 // weights in four pieces with one block ahead: 134 registers, three workgroups a CU (four blocks
 // ahead of two pieces or two of four cost that and 5 %, four ahead of one piece 1 us of 28). One token
-// through 8 of 64 experts, 5120 x 4096: 26.7 us for 168 MB (6.3 TB/s); two tokens 48 us (7.0 TB/s); 64
-// tokens, 96 of 384 experts: 202 to 207 us.
+// through 8 of 64 experts, 5120 x 4096: 27.7 us for 168 MB (6.1 TB/s); two tokens 52 us (6.4 TB/s); 64
+// tokens that meet 71 of 96 local experts of 384: 212 us for 1.49 GB (7.0 TB/s).
 __global__ void __launch_bounds__(256, 3) stream_kernel(const BlockGemmArgs p) {
     __shared__ __attribute__((aligned(16))) float part[4][64][36];
     const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
@@ -448,7 +448,9 @@ __global__ void __launch_bounds__(256, 3) stream_kernel(const BlockGemmArgs p) {
 // even routing: 64 tokens 202 : 243 us, 256 292 : 350, 384 303 : 347; but with a few hot experts (rows
 // of one group take turns over its weights) 256 tokens 295 : 292, 448 403 : 338, so the grouped limit
 // stays below the even crossing. One group: 16 rows 9.1 : 18.7, 64 17.3 : 25.9, 96 26.4 : 30.0, 128
-// 32.1 : 33.3.
+// 32.1 : 33.3. Both limits come from this one shape and go by rows alone: other shapes are not measured, and
+// a few experts of 6 to 96 rows each in groups take the tile kernel, which one such group alone loses by
+// (64 rows: 25.9 for 17.3 us). Transposed there is no kernel for few rows: one group of 16 takes 33 us, 64 42.
 constexpr int kStreamMean = 5, kStreamRows = 96;
 
 hipError_t launch_block_gemm(const BlockGemmArgs &a, bool transposed, hipStream_t s) {

@@ -3,9 +3,10 @@
 //
 // s = fl32(max |block| / 448) (1 for a zero block), code = E4M3(fl32(x / s)), nearest, ties to
 // even. All are bound by memory: 2 bytes read and 1 written per value (2 by rows and by
-// columns), one pass, the block's maximum taken in registers. 8191 x 4096 bf16: rows 20 us (5.0 TB/s),
-// columns 22 us (4.6), both 33 us (4.1); weights 32 x 4096 x 4096 292 us (5.5). Runs that are mostly
-// padding cost the whole run's time: 16384 rows in 96 uneven groups by both 97 us.
+// columns), one pass, the block's maximum taken in registers. 8191 x 4096 bf16: rows 23 to 25 us (4.1 to
+// 4.5 TB/s), columns 25 us (4.1), both 36 us (3.8); weights 32 x 4096 x 4096 302 us (5.3). Runs that are
+// mostly padding cost the whole run's time: 17108 rows of 4096 in 96 uneven groups by both 100 us, their
+// input's 2560 columns by token 46 us.
 #include "formats.h"
 #include "ops_internal.h"
 

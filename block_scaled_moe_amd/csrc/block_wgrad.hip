@@ -18,7 +18,7 @@
 // with its neighbour, so that every store instruction writes whole 128-byte lines, which go past
 // L2 (non-temporal) and leave the operands there.
 //
-// 96 experts of 4096 x 2560, 16384 rows unevenly routed: 508 us, of which the stores alone are 340 to
+// 96 experts of 4096 x 2560, 17108 rows unevenly routed: 504 us, of which the stores alone are 340 to
 // 380 us (2.0 GB, up to 5.9 TB/s), the copies alone 130 us and the products about 200 us (as many
 // cycles of the vector unit: each MFMA's four results take four products of scales and four multiply-adds).
 // Stores overlap with products, but hardly with copies of the same CU: stores spread over the next
@@ -49,8 +49,10 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(const BlockWgradArgs p)
     const int nbk = (K + kB - 1) / kB, tiles = (N + kB - 1) / kB * nbk;
 
     // An expert's tiles are split over `split` XCDs and the experts dealt to the 8 / split sets of
-    // XCDs, so that experts of very different size load them evenly; a part has four tiles or
-    // more, which share operands in the XCD's L2.
+    // XCDs, so that many experts of very different size load them evenly; a part has four tiles or
+    // more, which share operands in the XCD's L2. With fewer experts than sets the other sets have
+    // nothing to do, and few tiles in all leave most CUs idle: one group of 8192 rows takes 559 us
+    // at 512 x 512 (one workgroup works), 281 at 1024 x 1024 (eight), 160 at 4096 x 2560, 328 at 5120 x 4096.
     const int split = tiles >= 32 ? 8 : tiles >= 16 ? 4 : tiles >= 8 ? 2 : 1;
     const int xcd = blockIdx.x & 7, sets = 8 / split, part = (tiles + split - 1) / split;
     const int r0 = xcd % split * part, mine = min(part, tiles - r0), e0 = xcd / split;
