@@ -79,7 +79,7 @@ struct Buffer {
 bool overlap(const Buffer &a, const Buffer &b) {
     typedef unsigned __int128 wide;  // sizes that no memory holds are compared too
     const wide a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
-    return a0 < b0 + (wide)b.n * (wide)b.item && b0 < a0 + (wide)a.n * (wide)a.item;
+    return a.n && b.n && a0 < b0 + (wide)b.n * (wide)b.item && b0 < a0 + (wide)a.n * (wide)a.item;
 }
 // The output meets one of the buffers; a call refuses that (buffers not given are NULL).
 bool overlaps_any(const Buffer &out, std::initializer_list<Buffer> others) {

@@ -796,3 +796,17 @@ def test_rows_past_32_bit_bytes_of_a_plane():
     assert torch.equal(both.codes, q.codes) and torch.equal(cb.codes[2 ** 24 // 128:], c1.codes)
     x[:-last] = 0.0
     assert torch.equal(moe.block_weight_grad(moe.quantize_block_columns(x), c, rows=R), moe.block_weight_grad(c1, c1, rows=last))
+
+
+def test_weight_gradient_of_no_rows():
+    """Zeros without groups too; a buffer of no rows has no place that the output could overlap."""
+    import ctypes
+    from block_scaled_moe_amd import ops
+    c = moe.quantize_block_columns(torch.zeros((0, 256), dtype=torch.bfloat16, device="cuda"))
+    dw = torch.full((1, 256, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+    assert moe.block_weight_grad(c, c, rows=0, out=dw) is dw and not dw.any()
+    dw.fill_(7.0)
+    at = dw.data_ptr() + 256
+    a = ops.MoeBlockWgradArgs(0, 256, 256, None, at, at, at, at, dw.data_ptr())
+    ops._call("moe_block_wgrad", dw.device, ctypes.byref(a))
+    assert not dw.any()
