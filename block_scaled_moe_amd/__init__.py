@@ -12,7 +12,10 @@ shared expert, NVFP4 or MXFP8 experts with activations quantised to the same for
 
 Operators for programs that run or train their own experts next to it (include/moe_ops.h, ops.py):
 tokens grouped by expert and back (sort_tokens, gather, combine), the expert product in FP8 with a scale for
-each block of 128 (quantize_block, block_product), and the gradients of all of them.
+each block of 128 (quantize_block, block_product), and the gradients of all of them. What the router learns from
+(include/moe_router.h, router.py): its losses (router_losses), and the gradients from them and from the gate's weights back
+to the hidden states and the router's weight (logits_grad, route_backward). Expert products with 4-bit checkpoints
+(include/moe_w4.h, w4.py): pack_w4, w4_product.
 """
 from __future__ import annotations
 
@@ -22,7 +25,7 @@ import os
 
 import torch
 
-from . import ops
+from . import ops, router, w4
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
@@ -102,7 +105,7 @@ def lib():
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is not built; run __graft_entry__.build() first")
         handle = ctypes.CDLL(LIB_PATH)
-        for name, (args, res) in {**SIGNATURES, **ops.SIGNATURES}.items():
+        for name, (args, res) in {**SIGNATURES, **ops.SIGNATURES, **router.SIGNATURES, **w4.SIGNATURES}.items():
             fn = getattr(handle, name)
             fn.argtypes = args
             fn.restype = res
@@ -346,3 +349,5 @@ from .ops import (  # noqa: E402,F401
     BlockColumns, BlockRows, BlockWeights, Groups, block_product, block_product_grad, block_weight_grad, combine,
     combine_backward, gather, gather_backward, pack_block_weights, quantize_block, quantize_block_both,
     quantize_block_columns, quantize_block_weights, sort_tokens)
+from .router import RouterLosses, logits_grad, route_backward, route_backward_workspace, router_losses  # noqa: E402,F401
+from .w4 import W4Weights, pack_w4, w4_product  # noqa: E402,F401

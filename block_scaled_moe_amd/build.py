@@ -1,4 +1,4 @@
-"""Builds libmoe.so (the HIP kernels and the C ABI of include/moe.h and include/moe_ops.h) for gfx950.
+"""Builds libmoe.so (the HIP kernels and the C ABI of include/*.h) for gfx950.
 
 Each source compiles to an object in _build/ in parallel, then one shared library is
 linked next to this file. Flags: -ffp-contract=off, correctly rounded fp32 division
@@ -17,7 +17,8 @@ LIB = os.path.join(HERE, "libmoe.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["quant.hip", "route.hip", "permute.hip", "gemm.hip", "gemm_tile.hip", "gemm_stream.hip", "gemm_mx.hip",
            "gemm_fp8_wide.hip", "gemm_bf16_wide.hip", "combine.hip", "moe_api.hip", "sort.hip", "tokens.hip", "block_quant.hip",
-           "block_gemm.hip", "block_wgrad.hip", "ops_api.hip"]
+           "block_gemm.hip", "block_wgrad.hip", "ops_api.hip", "router_loss.hip", "router_grad.hip", "router_api.hip",
+           "w4_gemm.hip", "w4_api.hip"]
 FLAGS = ["-O3", "--offload-arch=gfx950", "-fPIC", "-std=c++17", "-ffp-contract=off",
          "-fhip-fp32-correctly-rounded-divide-sqrt", "-fno-gpu-flush-denormals-to-zero",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]

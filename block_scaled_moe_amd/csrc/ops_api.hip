@@ -97,6 +97,12 @@ int64_t column_blocks(const moe_groups *g, int32_t rows) {
     return g ? moe_block_column_blocks(g->T * g->top_k, g->e_end - g->e_begin) : ((int64_t)rows + 127) / 128;
 }
 
+}  // namespace
+
+namespace moe {
+
+int32_t check_filled_groups(const moe_groups *g) { return check_groups(g); }
+
 GroupView group_view(const moe_groups *g, int32_t rows) {
     GroupView v{};
     if (!g) {
@@ -123,7 +129,7 @@ GroupView group_view(const moe_groups *g, int32_t rows) {
     return v;
 }
 
-}  // namespace
+}  // namespace moe
 
 extern "C" {
 

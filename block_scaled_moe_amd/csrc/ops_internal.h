@@ -34,6 +34,10 @@ struct GroupView {
     int32_t rows, top_k, n, max_tiles;
     int32_t mean_rows;  // average rows of a group for an even routing (host's rule for the kernel)
 };
+// Status of g's fields (as moe_sort filled them), and the view of a batch of g's slots or, without g, of `rows` rows
+// (ops_api.hip).
+int32_t check_filled_groups(const moe_groups *g);
+GroupView group_view(const moe_groups *g, int32_t rows);
 
 // ---- sort (sort.hip), for up to kSortMaxLocal local experts: fills what launch_permute does
 constexpr int32_t kSortMaxLocal = 1024;
