@@ -18,7 +18,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["quant.hip", "route.hip", "permute.hip", "gemm.hip", "gemm_tile.hip", "gemm_stream.hip", "gemm_mx.hip",
            "gemm_fp8_wide.hip", "gemm_bf16_wide.hip", "combine.hip", "moe_api.hip", "sort.hip", "tokens.hip", "block_quant.hip",
            "block_gemm.hip", "block_wgrad.hip", "ops_api.hip", "router_loss.hip", "router_grad.hip", "router_api.hip",
-           "w4_gemm.hip", "w4_api.hip"]
+           "w4_pack.hip", "w4_stream.hip", "w4_tile.hip", "w4_api.hip"]
 FLAGS = ["-O3", "--offload-arch=gfx950", "-fPIC", "-std=c++17", "-ffp-contract=off",
          "-fhip-fp32-correctly-rounded-divide-sqrt", "-fno-gpu-flush-denormals-to-zero",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]

@@ -24,5 +24,6 @@ struct W4GemmArgs {
     void *out;
 };
 hipError_t launch_w4_gemm(const W4GemmArgs &a, hipStream_t s);
+hipError_t launch_w4_tile(const W4GemmArgs &a, hipStream_t s);  // groups of many rows
 
 }  // namespace moe

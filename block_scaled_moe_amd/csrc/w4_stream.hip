@@ -1,0 +1,219 @@
+// w4_stream.hip - product of few rows a group with 4-bit weights (include/moe_w4.h, moe_w4_gemm; the arithmetic stands in
+// w4_mma.h), and the choice between the kernels.
+//
+// Bound by the weights' bytes. A workgroup takes two column tiles of 16 (with swiglu one of the first half's columns and the
+// same of the second half's) of one tile of rows, its waves a part of the steps each, and their partial sums meet in
+// LDS in the waves' order. A wave's load of codes is 1 KiB in a row; those of the next step are in flight while the
+// current one is multiplied. Rows beyond those of one turn take another one over the same weights.
+#include "w4_mma.h"
+
+namespace moe {
+namespace {
+
+using namespace w4;
+
+// MOST: pieces of 16 rows in a turn at most
+template <int GROUP, bool HALF, bool ZEROS, int MOST, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES, MOST == 1 ? 4 : 2) stream_kernel(const W4GemmArgs p) {
+    constexpr int kGroups = kW4Step / GROUP;      // per step
+    constexpr int kWords = (kGroups + 1) / 2;     // of scales
+    constexpr int kZeroWords = (kGroups + 3) / 4;
+    __shared__ __attribute__((aligned(16))) float part[WAVES][16 * MOST][36];
+    const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
+    const int i16 = lane & 15, g = lane >> 4;
+    const int N = p.w.N, K = p.w.K;
+    const int nb = p.swiglu ? (p.C + 15) / 16 : (p.C + 31) / 32;
+    const int tile = blockIdx.x / nb, cb = blockIdx.x % nb;
+    int e = 0, p0 = tile * kGroupTile, rows = p.v.rows - p0;
+    if (p.v.offsets) {
+        // all at once: behind the last tile they are not used
+        const int n_tiles = scalar_load(&p.v.ctrl->n_tiles);
+        e = scalar_load(p.v.tile_expert + tile);
+        p0 = scalar_load(p.v.tile_row0 + tile);
+        if (tile >= n_tiles) return;
+        rows = scalar_load(p.v.offsets + e + 1) - p0;
+    }
+    const uint8_t *codes[2], *scales[2], *zeros[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        // this lane's weight row: past the end the last one, which is not stored
+        const int n = p.swiglu ? min(16 * cb + i16, p.C - 1) + q * p.C : min(32 * cb + 16 * q + i16, N - 1);
+        const int64_t at = ((int64_t)e * p.tiles + (n >> 4)) * p.steps, in = n & 15;
+        codes[q] = reinterpret_cast<const uint8_t *>(p.w.codes) + at * 2048 + (16 * g + in) * 16;
+        scales[q] = reinterpret_cast<const uint8_t *>(p.w.scales) + (at * 16 + in) * (2 * kGroups);
+        zeros[q] = ZEROS ? p.w.zeros + (at * 16 + in) * kGroups : nullptr;
+    }
+    const int s0 = wave * p.steps / WAVES, s1 = (wave + 1) * p.steps / WAVES;
+
+    struct Weights {
+        u32x4 c[2][2];
+        uint32_t s[2][kWords], z[2][kZeroWords];
+    };
+    auto load = [&](int s, Weights &w) __attribute__((always_inline)) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                w.c[q][h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(codes[q] + (int64_t)s * 2048 + h * 1024));
+            const uint8_t *sp = scales[q] + (int64_t)s * (32 * kGroups);
+            if constexpr (kWords == 1) {
+                w.s[q][0] = *reinterpret_cast<const uint32_t *>(sp);
+            } else if constexpr (kWords == 2) {
+                const u32x2 v = *reinterpret_cast<const u32x2 *>(sp);
+                w.s[q][0] = v.x, w.s[q][1] = v.y;
+            } else {
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(sp);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w.s[q][i] = v[i];
+            }
+            if constexpr (ZEROS) {
+                const uint8_t *zp = zeros[q] + (int64_t)s * (16 * kGroups);
+                if constexpr (kGroups == 2) {
+                    w.z[q][0] = *reinterpret_cast<const uint16_t *>(zp);
+                } else if constexpr (kGroups == 4) {
+                    w.z[q][0] = *reinterpret_cast<const uint32_t *>(zp);
+                } else {
+                    const u32x2 v = *reinterpret_cast<const u32x2 *>(zp);
+                    w.z[q][0] = v.x, w.z[q][1] = v.y;
+                }
+            }
+        }
+    };
+
+    Weights first;
+    if (s0 < s1) load(s0, first);
+    rows = min(rows, kGroupTile);
+
+    // MT pieces of 16 rows from m0 on
+    auto turn = [&](int m0, auto mt_c) __attribute__((always_inline)) {
+        constexpr int MT = decltype(mt_c)::value;
+        constexpr int kRuns = MT > 2 ? 4 : 8;  // of 32 columns whose rows are loaded together
+        const uint16_t *x[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int pos = p0 + min(m0 + 16 * m + i16, rows - 1);
+            const int64_t row = p.by_token ? p.v.sorted_slot[pos] / p.v.top_k : pos;
+            x[m] = p.x + row * K + 8 * g;
+        }
+        f4 acc[MT][2] = {};
+        Weights next = first;
+        if (m0 > 0 && s0 < s1) load(s0, next);
+        for (int s = s0; s < s1; ++s) {
+            const Weights w = next;
+#pragma unroll
+            for (int b = 0; b < 8 / kRuns; ++b) {
+                u32x4 xv[kRuns][MT];
+#pragma unroll
+                for (int i = 0; i < kRuns; ++i) {
+                    const int k = min(256 * s + 32 * (kRuns * b + i), K - 32);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) xv[i][m] = *reinterpret_cast<const u32x4 *>(x[m] + k);
+                }
+                if (b == 0) load(min(s + 1, s1 - 1), next);
+#pragma unroll
+                for (int gr = b * (32 * kRuns / GROUP); gr < (b + 1) * (32 * kRuns / GROUP); ++gr) {
+                    f4 sum[MT], d[MT][2];
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) sum[m] = d[m][0] = d[m][1] = (f4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int i = gr * (GROUP / 32); i < (gr + 1) * (GROUP / 32); ++i) {
+                        bf8 wv[2];
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) wv[q] = expand(w.c[q][i >> 2][i & 3]);
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            const bf8 xo = __builtin_bit_cast(bf8, xv[i % kRuns][m]);
+                            sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo, ones(), sum[m], 0, 0, 0);
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) d[m][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo, wv[q], d[m][q], 0, 0, 0);
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float f = scale_value<HALF>(w.s[q][gr / 2], gr & 1);
+                        const float off = ZEROS ? 16.0f + (float)((w.z[q][gr / 4] >> (8 * (gr & 3))) & 255u) : 24.0f;
+#pragma unroll
+                        for (int m = 0; m < MT; ++m)
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) acc[m][q][v] = fmaf(fmaf(-off, sum[m][v], d[m][q][v]), f, acc[m][q][v]);
+                    }
+                    if ((gr + 1) * GROUP % 128 == 0) __builtin_amdgcn_sched_barrier(0);  // else more is alive at once than registers hold
+                }
+            }
+        }
+        // accumulator v of (m, q): row 16 m + 4 g + v, column 16 q + i16
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) part[wave][16 * m + 4 * g + v][16 * q + i16] = acc[m][q][v];
+        __syncthreads();
+        for (int r = t >> 4; r < min(16 * MT, rows - m0); r += 4 * WAVES) {
+            float y[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int c = p.swiglu ? 16 * q + (t & 15) : 2 * (t & 15) + q;
+                y[q] = part[0][r][c];
+#pragma unroll
+                for (int k = 1; k < WAVES; ++k) y[q] += part[k][r][c];
+            }
+            const int64_t row = (int64_t)(p0 + m0 + r) * p.C;
+            if (p.swiglu) {
+                const int c = 16 * cb + (t & 15);
+                const float v = swiglu(y[0], y[1]);
+                if (c < p.C) {
+                    if (p.out_dtype == MOE_DT_BF16) static_cast<uint16_t *>(p.out)[row + c] = __builtin_bit_cast(uint16_t, (__bf16)v);
+                    else static_cast<float *>(p.out)[row + c] = v;
+                }
+            } else {
+                const int c = 32 * cb + 2 * (t & 15);
+                if (p.out_dtype == MOE_DT_BF16) {
+                    uint16_t *o = static_cast<uint16_t *>(p.out) + row + c;
+                    if (p.C % 2 == 0) {
+                        if (c < p.C) *reinterpret_cast<uint32_t *>(o) = bf16_pair(y[0], y[1]);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+                            if (c + q < p.C) o[q] = __builtin_bit_cast(uint16_t, (__bf16)y[q]);
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        if (c + q < p.C) static_cast<float *>(p.out)[row + c + q] = y[q];
+                }
+            }
+        }
+    };
+    using std::integral_constant;
+    if constexpr (MOST == 1) {
+        for (int m0 = 0; m0 < rows; m0 += 16) turn(m0, integral_constant<int, 1>{});
+    } else {
+        int m0 = 0;
+        for (; rows - m0 > 32; m0 += 64) turn(m0, integral_constant<int, 4>{});
+        if (rows > m0) turn(m0, integral_constant<int, 2>{});
+    }
+}
+
+}  // namespace
+
+hipError_t launch_w4_gemm(const W4GemmArgs &a, hipStream_t s) {
+    const int64_t nb = a.swiglu ? (a.C + 15) / 16 : (a.C + 31) / 32, groups = (int64_t)a.v.max_tiles * nb;
+    const int rows = a.v.mean_rows;
+    if (rows > (a.v.offsets ? 16 : 64)) return launch_w4_tile(a, s);
+    if (groups * 1024 >= 1ll << 32) return hipErrorInvalidValue;  // a grid's threads are 32 bits
+    by_form(a.w, [&](auto group, auto half, auto zeros) {
+        constexpr int kGroup = decltype(group)::value;
+        constexpr bool kHalf = decltype(half)::value, kZeros = decltype(zeros)::value;
+        auto go = [&](auto kernel, int waves) {
+            hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(64 * waves), 0, s, a);
+        };
+        if (rows > 16) go(stream_kernel<kGroup, kHalf, kZeros, 4, 8>, 8);
+        else if (groups < 512) go(stream_kernel<kGroup, kHalf, kZeros, 1, 16>, 16);
+        else go(stream_kernel<kGroup, kHalf, kZeros, 1, 4>, 4);
+    });
+    return hipGetLastError();
+}
+
+}  // namespace moe

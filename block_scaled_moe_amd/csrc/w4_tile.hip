@@ -1,0 +1,299 @@
+// w4_tile.hip - product of many rows a group with 4-bit weights (include/moe_w4.h, moe_w4_gemm; the arithmetic stands in
+// w4_mma.h).
+//
+// 128 rows x 64 NF columns a workgroup, 8 waves as 2 (rows) x 4 (columns), a wave up to 4 pieces of 16 rows (the tile's pieces
+// alternate between the two row waves, so that a partial tile splits evenly) x 16 NF columns; with swiglu half of a wave's
+// columns are the first half's and half the same ones of the second half, so that both meet in one lane.
+//  - Stages of 128 of the reduction. Rows (gathered by token) and codes go straight from memory into LDS, three buffers
+//    each, two stages ahead, scales and zero points into two buffers of 256 of the reduction; one barrier a stage covers
+//    everything. Both row waves read the same codes there.
+//  - The sums of x per row and group are the same for all columns: each wave forms those of one piece of 16 rows, a stage
+//    ahead, and leaves them in LDS.
+#include "w4_mma.h"
+
+namespace moe {
+namespace {
+
+using namespace w4;
+
+constexpr int kThreads = 512, kBM = 128, kStage = 128;
+constexpr int kX = kBM * kStage * 2;  // LDS bytes of a stage's rows
+
+// copy_to_lds from any address
+__device__ __forceinline__ void copy_from(const void *src, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(uniform((int)dst)), "v"(src) : "memory");
+}
+
+template <int GROUP, bool HALF, bool ZEROS, int NF>
+__global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
+    constexpr int kBN = 64 * NF;
+    constexpr int kTiles = kBN / 16 + (NF == 2 ? 1 : 0);      // packed tiles: a second half may start inside one
+    constexpr int kGroups = kW4Step / GROUP, kIn = kStage / GROUP;  // groups per step, per stage
+    constexpr int kW = kTiles * 1024;                         // LDS bytes of a stage's codes
+    constexpr int kS = kTiles * 32 * kGroups, kZ = ZEROS ? kS / 2 : 0;  // of a step's scales and zero points
+    constexpr int kLds = 3 * (kX + kW) + 2 * (kS + kZ) + 2 * kIn * kBM * 4;
+    constexpr int kWCopies = kBN / 16 / 8;  // of codes by every wave in a stage (the first one: perhaps one more)
+    constexpr int kSWaves = (kS + 1023) / 1024, kZWaves = (kZ + 1023) / 1024;
+    static_assert(kLds <= 160 * 1024 && kBM * (kBN + 8) * 2 <= 3 * kX && kSWaves + kZWaves <= 8, "LDS");
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
+    uint8_t *const xb = lds, *const wb = lds + 3 * kX, *const sb = wb + 3 * kW, *const zb = sb + 2 * kS;
+    float *const sums = reinterpret_cast<float *>(zb + 2 * kZ);
+
+    const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
+    const int i16 = lane & 15, g = lane >> 4, wm = wave >> 2, wn = wave & 3;
+    const int K = p.w.K, stages = (K + kStage - 1) / kStage;
+    const int width = p.swiglu ? kBN / 2 : kBN;  // output columns a workgroup
+    const int nb = (p.C + width - 1) / width;
+
+    // ---- work item: each XCD (workgroups 8 apart) takes a range of the experts' tiles, whose rows then meet in one L2; both
+    // parts of a tile of the groups' list next to each other
+    int e = 0, p0, rows, cb;
+    {
+        const int parts = p.v.offsets ? 2 : 1;
+        const int n_tiles = p.v.offsets ? scalar_load(&p.v.ctrl->n_tiles) : (p.v.rows + kBM - 1) / kBM;
+        const int items = n_tiles * nb * parts, per = (items + 7) / 8, i = blockIdx.x >> 3;
+        const int item = (blockIdx.x & 7) * per + i;
+        if (i >= per || item >= items) return;
+        const int tile = item / (nb * parts), rest = item % (nb * parts);
+        cb = rest / parts;
+        if (p.v.offsets) {
+            e = scalar_load(p.v.tile_expert + tile);
+            p0 = scalar_load(p.v.tile_row0 + tile);
+            rows = min(scalar_load(p.v.offsets + e + 1) - p0, kGroupTile) - kBM * (rest % 2);
+            p0 += kBM * (rest % 2);
+            if (rows <= 0) return;
+        } else {
+            p0 = tile * kBM;
+            rows = p.v.rows - p0;
+        }
+        rows = min(rows, kBM);
+    }
+
+    // ---- sources. Rows: copies wave + 8 j of four rows of 256 bytes; a row's 16-byte pieces are swapped by the row's last
+    // four bits, so that sixteen rows' pieces of one place lie in different banks.
+    const int n_sub = (rows + 15) / 16;
+    const uint16_t *x[4];
+    const int x_at = ((lane & 15) ^ ((4 * wave + (lane >> 4)) & 15)) * 8;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int pos = p0 + min(4 * (wave + 8 * j) + (lane >> 4), rows - 1);
+        const int64_t row = p.by_token ? p.v.sorted_slot[pos] / p.v.top_k : pos;
+        x[j] = p.x + row * K;
+    }
+    // Packed tiles in LDS order; past the end the last one, whose columns are not stored.
+    auto packed_tile = [&](int j) __attribute__((always_inline)) -> int64_t {
+        int tile = cb * (width / 16) + j;
+        if (p.swiglu && j >= kBN / 32) tile = (p.C + cb * width) / 16 + j - kBN / 32;
+        return ((int64_t)e * p.tiles + min(tile, p.tiles - 1)) * p.steps;
+    };
+    const uint8_t *codes[kWCopies + 1];
+#pragma unroll
+    for (int j = 0; j <= kWCopies; ++j)
+        codes[j] = uniform(reinterpret_cast<const uint8_t *>(p.w.codes) + packed_tile(min(wave + 8 * j, kTiles - 1)) * 2048);
+    // 16 bytes a lane of the step's scales (waves from 0 on) or zero points (the next ones)
+    const bool side_z = wave >= kSWaves;
+    const int side_lane = (side_z ? wave - kSWaves : wave) * 64 + lane;
+    const bool side_on = side_lane < (side_z ? kZ : kS) / 16;
+    const int side_bytes = side_z ? 16 * kGroups : 32 * kGroups;  // of a tile
+    const uint8_t *side = side_z ? p.w.zeros : reinterpret_cast<const uint8_t *>(p.w.scales);
+    if (side_on) side += packed_tile(side_lane * 16 / side_bytes) * side_bytes + side_lane * 16 % side_bytes;
+
+    const uint32_t x_lds = lds_address(xb) + wave * 1024, w_lds = lds_address(wb) + wave * 1024;
+    const uint32_t side_lds = lds_address(side_z ? zb : sb) + (side_z ? wave - kSWaves : wave) * 1024;
+    auto copy_side = [&](int step) __attribute__((always_inline)) {
+        if (side_on) copy_from(side + (int64_t)step * side_bytes, side_lds + (step & 1) * (side_z ? kZ : kS));
+    };
+    auto copy_x = [&](int s, int buffer) __attribute__((always_inline)) {
+        const int k = min(s * kStage + x_at, K - 8);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (wave + 8 * j < 4 * n_sub) copy_from(x[j] + k, x_lds + buffer * kX + j * 8192);
+    };
+    auto copy_w = [&](int s, int buffer) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j <= kWCopies; ++j)
+            if (wave + 8 * j < kTiles && (j < kWCopies || p.swiglu))
+                copy_to_lds(codes[j] + (int64_t)s * 1024, lane * 16, w_lds + buffer * kW + j * 8192);
+    };
+
+    // ---- this lane's columns: row of the packed tiles in LDS
+    int w_row[NF];
+#pragma unroll
+    for (int q = 0; q < NF; ++q) {
+        w_row[q] = (wn * NF + q) * 16 + i16;
+        if (p.swiglu) {
+            const int in = (wn * (NF / 2) + q % (NF / 2)) * 16 + i16;
+            w_row[q] = q < NF / 2 ? in : kBN / 2 + ((p.C + cb * width) & 15) + in;
+        }
+    }
+
+    // sums of x over the groups of stage s for the 16 rows of piece `wave`
+    auto row_sums = [&](int s, int buffer) __attribute__((always_inline)) {
+        if (wave >= n_sub) return;
+        const uint8_t *row = xb + buffer * kX + (16 * wave + i16) * 256;
+#pragma unroll
+        for (int gr = 0; gr < kIn; ++gr) {
+            f4 d = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int r = gr * (GROUP / 32); r < (gr + 1) * (GROUP / 32); ++r)
+                d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf8, *reinterpret_cast<const u32x4 *>(row + ((4 * r + g) ^ i16) * 16)), ones(), d, 0, 0, 0);
+            if (i16 == 0) *reinterpret_cast<f4 *>(sums + ((s & 1) * kIn + gr) * kBM + 16 * wave + 4 * g) = d;
+        }
+    };
+
+    copy_side(0);
+    copy_x(0, 0);
+    copy_w(0, 0);
+    if (stages > 1) {
+        copy_x(1, 1);
+        copy_w(1, 1);
+    }
+    wait_copies<0>();
+    lds_barrier();
+    row_sums(0, 0);
+
+    auto run = [&](auto mf_c) __attribute__((always_inline)) {
+        constexpr int MF = decltype(mf_c)::value;  // this wave's pieces of 16 rows
+        f4 acc[MF][NF];
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+#pragma unroll
+            for (int q = 0; q < NF; ++q) acc[i][q] = (f4){0.0f, 0.0f, 0.0f, 0.0f};
+        int b0 = 0, b1 = 1, b2 = 2;  // buffers of stages s, s + 1, s + 2
+#pragma clang loop unroll(disable)
+        for (int s = 0; s < stages; ++s) {
+            // everything but the codes of stage s + 1 has arrived; every wave is done with stage s - 1 and has left the
+            // sums of stage s
+            if (s + 1 < stages) wait_copies<kWCopies>();
+            else wait_copies<0>();
+            lds_barrier();
+            if (s + 2 < stages) {
+                if ((s & 1) == 0) copy_side(s / 2 + 1);
+                copy_x(s + 2, b2);
+                copy_w(s + 2, b2);
+            }
+            if (s + 1 < stages) row_sums(s + 1, b1);
+            u32x4 raw[NF];
+            float f[NF][kIn], off[NF][kIn];
+#pragma unroll
+            for (int q = 0; q < NF; ++q) {
+                raw[q] = *reinterpret_cast<const u32x4 *>(wb + b0 * kW + (w_row[q] >> 4) * 1024 + (16 * g + (w_row[q] & 15)) * 16);
+                const uint8_t *sp = sb + ((s >> 1) & 1) * kS + w_row[q] * (2 * kGroups) + (s & 1) * (2 * kIn);
+                uint32_t word[(kIn + 1) / 2];
+                if constexpr (kIn == 1) word[0] = *reinterpret_cast<const uint16_t *>(sp);
+                else if constexpr (kIn == 2) word[0] = *reinterpret_cast<const uint32_t *>(sp);
+                else word[0] = reinterpret_cast<const u32x2 *>(sp)->x, word[1] = reinterpret_cast<const u32x2 *>(sp)->y;
+#pragma unroll
+                for (int gr = 0; gr < kIn; ++gr) {
+                    f[q][gr] = scale_value<HALF>(word[gr / 2], gr & 1);
+                    off[q][gr] = 24.0f;
+                }
+                if constexpr (ZEROS) {
+                    const uint8_t *zp = zb + ((s >> 1) & 1) * kZ + w_row[q] * kGroups + (s & 1) * kIn;
+                    uint32_t z;
+                    if constexpr (kIn == 1) z = *zp;
+                    else if constexpr (kIn == 2) z = *reinterpret_cast<const uint16_t *>(zp);
+                    else z = *reinterpret_cast<const uint32_t *>(zp);
+#pragma unroll
+                    for (int gr = 0; gr < kIn; ++gr) off[q][gr] = 16.0f + (float)((z >> (8 * gr)) & 255u);
+                }
+            }
+            const uint8_t *row = xb + b0 * kX + (16 * wm + i16) * 256;
+#pragma unroll
+            for (int gr = 0; gr < kIn; ++gr) {
+                f4 d[MF][NF];
+#pragma unroll
+                for (int i = 0; i < MF; ++i)
+#pragma unroll
+                    for (int q = 0; q < NF; ++q) d[i][q] = (f4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int r = gr * (GROUP / 32); r < (gr + 1) * (GROUP / 32); ++r) {
+                    bf8 w[NF];
+#pragma unroll
+                    for (int q = 0; q < NF; ++q) w[q] = expand(raw[q][r]);
+#pragma unroll
+                    for (int i = 0; i < MF; ++i) {
+                        const bf8 xo = __builtin_bit_cast(bf8, *reinterpret_cast<const u32x4 *>(row + i * 8192 + ((4 * r + g) ^ i16) * 16));
+#pragma unroll
+                        for (int q = 0; q < NF; ++q) d[i][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo, w[q], d[i][q], 0, 0, 0);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < MF; ++i) {
+                    const f4 sum = *reinterpret_cast<const f4 *>(sums + ((s & 1) * kIn + gr) * kBM + 16 * (2 * i + wm) + 4 * g);
+#pragma unroll
+                    for (int q = 0; q < NF; ++q)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            acc[i][q][v] = fmaf(fmaf(-off[q][gr], sum[v], d[i][q][v]), f[q][gr], acc[i][q][v]);
+                }
+            }
+            const int b = b0;
+            b0 = b1, b1 = b2, b2 = b;
+        }
+
+        // ---- outputs: accumulator v of (i, q): row 16 (2 i + wm) + 4 g + v. fp32 from the lanes, bf16 by way of LDS as
+        // whole runs of a row
+        const int out_frags = p.swiglu ? NF / 2 : NF, c0 = cb * width, pitch = width + 8;
+        lds_barrier();  // every wave is done with the buffers
+        uint16_t *const ob = reinterpret_cast<uint16_t *>(lds);
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+#pragma unroll
+            for (int q = 0; q < NF; ++q) {
+                if (q >= out_frags) continue;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    float y = acc[i][q][v];
+                    if constexpr (NF > 1)
+                        if (p.swiglu) y = swiglu(y, acc[i][(q + NF / 2) % NF][v]);
+                    const int m = 16 * (2 * i + wm) + 4 * g + v, c = (wn * out_frags + q) * 16 + i16;
+                    if (p.out_dtype == MOE_DT_BF16) ob[m * pitch + c] = __builtin_bit_cast(uint16_t, (__bf16)y);
+                    else if (m < rows && c0 + c < p.C) static_cast<float *>(p.out)[(int64_t)(p0 + m) * p.C + c0 + c] = y;
+                }
+            }
+        if (p.out_dtype != MOE_DT_BF16) return;
+        lds_barrier();
+        uint16_t *out = static_cast<uint16_t *>(p.out) + (int64_t)p0 * p.C + c0;
+        if (p.C % 8 == 0) {
+            const int pieces = width / 8;
+            for (int j = t; j < rows * pieces; j += kThreads) {
+                const int m = j / pieces, c = j % pieces * 8;
+                if (c0 + c < p.C) *reinterpret_cast<u32x4 *>(out + (int64_t)m * p.C + c) = *reinterpret_cast<const u32x4 *>(ob + m * pitch + c);
+            }
+        } else {
+            for (int j = t; j < rows * width; j += kThreads) {
+                const int m = j / width, c = j % width;
+                if (c0 + c < p.C) out[(int64_t)m * p.C + c] = ob[m * pitch + c];
+            }
+        }
+    };
+    using std::integral_constant;
+    switch ((n_sub - wm + 1) / 2) {
+        case 4: run(integral_constant<int, 4>{}); break;
+        case 3: run(integral_constant<int, 3>{}); break;
+        case 2: run(integral_constant<int, 2>{}); break;
+        default: run(integral_constant<int, 1>{}); break;  // none: beside the other waves, nothing of it is stored
+    }
+}
+
+}  // namespace
+
+hipError_t launch_w4_tile(const W4GemmArgs &a, hipStream_t s) {
+    const int64_t tiles = a.v.offsets ? 2 * (int64_t)a.v.max_tiles : (a.v.rows + kBM - 1) / kBM;
+    auto items = [&](int columns) { return tiles * ((a.C + columns - 1) / columns); };
+    // a second half that starts inside a packed tile needs one more of them, for which only the narrow tile has room
+    const bool narrow = (a.swiglu && a.C % 16) || items(a.swiglu ? 128 : 256) < 512;
+    const int64_t grid = (items(narrow ? (a.swiglu ? 64 : 128) : (a.swiglu ? 128 : 256)) + 7) / 8 * 8;
+    if (grid >= 1 << 23) return hipErrorInvalidValue;  // a grid's threads are 32 bits
+    w4::by_form(a.w, [&](auto group, auto half, auto zeros) {
+        constexpr int kGroup = decltype(group)::value;
+        constexpr bool kHalf = decltype(half)::value, kZeros = decltype(zeros)::value;
+        if (narrow) hipLaunchKernelGGL((tile_kernel<kGroup, kHalf, kZeros, 2>), dim3((unsigned)grid), dim3(kThreads), 0, s, a);
+        else hipLaunchKernelGGL((tile_kernel<kGroup, kHalf, kZeros, 4>), dim3((unsigned)grid), dim3(kThreads), 0, s, a);
+    });
+    return hipGetLastError();
+}
+
+}  // namespace moe
