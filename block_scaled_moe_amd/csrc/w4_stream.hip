@@ -1,10 +1,9 @@
 // w4_stream.hip - product of few rows a group with 4-bit weights (include/moe_w4.h, moe_w4_gemm; the arithmetic stands in
 // w4_mma.h), and the choice between the kernels.
 //
-// Bound by the weights' bytes. A workgroup takes two column tiles of 16 (with swiglu one of the first half's columns and the
-// same of the second half's) of one tile of rows, its waves a part of the steps each, and their partial sums meet in
-// LDS in the waves' order. A wave's load of codes is 1 KiB in a row; those of the next step are in flight while the
-// current one is multiplied. Rows beyond those of one turn take another one over the same weights.
+// Bound by the weights' bytes. A wave takes two column tiles of 16 (with swiglu one of the first half's columns and the same of
+// the second half's) of one tile of rows; its load of codes is 1 KiB in a row, and those of the next step are in flight
+// while the current one is multiplied.
 #include "w4_mma.h"
 
 namespace moe {
@@ -12,9 +11,193 @@ namespace {
 
 using namespace w4;
 
-// MOST: pieces of 16 rows in a turn at most
+// Up to 16 rows a turn: they go into LDS once for the workgroup's eight waves (in parts of the reduction where they
+// do not fit), and KS waves share two column tiles, each with a part of the steps; their sums meet in LDS in the waves' order.
+// 16 + z is a bf16 as 16 + q is, so it is taken off by a second MFMA on the same rows, which leaves four multiply-adds
+// for four results and group.
+constexpr int kStreamWaves = 8, kStreamX = 60 * 1024;  // waves, LDS bytes of rows of a workgroup: two of them a CU
+template <int GROUP, bool HALF, bool ZEROS, int KS>
+__global__ void __launch_bounds__(64 * kStreamWaves, 4) stream_kernel(const W4GemmArgs p) {
+    constexpr int kGroups = kW4Step / GROUP;      // per step
+    constexpr int kWords = (kGroups + 1) / 2;     // of scales
+    constexpr int kZeroWords = (kGroups + 3) / 4;
+    constexpr int kBlocks = kStreamWaves / KS;    // of two column tiles a workgroup
+    __shared__ __attribute__((aligned(16))) uint8_t xs[kStreamX];
+    __shared__ __attribute__((aligned(16))) float part[KS > 1 ? kStreamWaves : 1][KS > 1 ? 16 : 1][36];
+    const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
+    const int i16 = lane & 15, g = lane >> 4, ks = wave % KS;
+    const int K = p.w.K, steps = p.steps;
+    const int nb = p.swiglu ? (p.C + 15) / 16 : (p.C + 31) / 32, per_tile = (nb + kBlocks - 1) / kBlocks;
+    const int tile = blockIdx.x / per_tile, cb = blockIdx.x % per_tile * kBlocks + wave / KS;
+    int e = 0, p0 = tile * kGroupTile, rows = p.v.rows - p0;
+    if (p.v.offsets) {
+        // all at once: behind the last tile they are not used
+        const int n_tiles = scalar_load(&p.v.ctrl->n_tiles);
+        e = scalar_load(p.v.tile_expert + tile);
+        p0 = scalar_load(p.v.tile_row0 + tile);
+        if (tile >= n_tiles) return;
+        rows = scalar_load(p.v.offsets + e + 1) - p0;
+    }
+    rows = min(rows, kGroupTile);
+
+    const uint8_t *codes[2], *scales[2], *zeros[2];  // of the column tile's first row
+    uint32_t code_at[2], scale_at[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        // this lane's weight row: past the end the last one, which is not stored
+        const int last = p.swiglu ? (q + 1) * p.C - 1 : p.C - 1;
+        const int n0 = min(p.swiglu ? 16 * cb + q * p.C : 32 * cb + 16 * q, last), n = min(n0 + i16, last);
+        const int64_t at = ((int64_t)e * p.tiles + (n0 >> 4)) * steps;
+        const uint32_t next = (n >> 4) - (n0 >> 4), in = n & 15;  // the row may lie in the next packed tile
+        codes[q] = uniform(reinterpret_cast<const uint8_t *>(p.w.codes) + at * 2048);
+        code_at[q] = next * steps * 2048 + (16 * g + in) * 16;
+        scales[q] = uniform(reinterpret_cast<const uint8_t *>(p.w.scales) + at * 32 * kGroups);
+        zeros[q] = ZEROS ? uniform(p.w.zeros + at * 16 * kGroups) : nullptr;
+        scale_at[q] = (next * steps * 16 + in) * (2 * kGroups);
+    }
+
+    struct Weights {
+        u32x4 c[2][2];
+        uint32_t s[2][kWords], z[2][kZeroWords];
+    };
+    auto load = [&](int s, Weights &w) __attribute__((always_inline)) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const uint8_t *cp = codes[q] + (int64_t)s * 2048;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                w.c[q][h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(cp + (code_at[q] + h * 1024)));
+            const uint8_t *sp = scales[q] + (int64_t)s * (32 * kGroups);
+            if constexpr (kWords == 1) {
+                w.s[q][0] = *reinterpret_cast<const uint32_t *>(sp + scale_at[q]);
+            } else if constexpr (kWords == 2) {
+                const u32x2 v = *reinterpret_cast<const u32x2 *>(sp + scale_at[q]);
+                w.s[q][0] = v.x, w.s[q][1] = v.y;
+            } else {
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(sp + scale_at[q]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w.s[q][i] = v[i];
+            }
+            if constexpr (ZEROS) {
+                const uint8_t *zp = zeros[q] + (int64_t)s * (16 * kGroups);
+                const uint32_t at = scale_at[q] / 2;
+                if constexpr (kGroups == 2) {
+                    w.z[q][0] = *reinterpret_cast<const uint16_t *>(zp + at);
+                } else if constexpr (kGroups == 4) {
+                    w.z[q][0] = *reinterpret_cast<const uint32_t *>(zp + at);
+                } else {
+                    const u32x2 v = *reinterpret_cast<const u32x2 *>(zp + at);
+                    w.z[q][0] = v.x, w.z[q][1] = v.y;
+                }
+            }
+        }
+    };
+
+    for (int m0 = 0; m0 < rows; m0 += 16) {
+        const int have = min(rows - m0, 16);
+        const int chunk = min(steps, (kStreamX / have - 16) / 512), pitch = chunk * 512 + 16;  // steps in LDS, bytes of a row
+        // steps of this wave in the chunk that begins at c
+        auto first = [&](int c) __attribute__((always_inline)) { return c + ks * min(chunk, steps - c) / KS; };
+        auto behind = [&](int c) __attribute__((always_inline)) { return c + (ks + 1) * min(chunk, steps - c) / KS; };
+        Weights next;
+        bool loaded = first(0) < behind(0);
+        if (loaded) load(first(0), next);
+        f4 acc[2] = {};
+        const uint8_t *row = xs + min(i16, have - 1) * pitch + 16 * g;
+        for (int c = 0; c < steps; c += chunk) {
+            if (c > 0 || m0 > 0) __syncthreads();
+            {
+                const int k0 = c * 256, pieces = min(chunk, steps - c) * 32;  // of 16 bytes; past the end the last ones
+                for (int r = wave; r < have; r += kStreamWaves) {
+                    const int pos = p0 + m0 + r;
+                    const int64_t src = p.by_token ? p.v.sorted_slot[pos] / p.v.top_k : pos;
+                    for (int i = lane; i < pieces; i += 64)
+                        *reinterpret_cast<u32x4 *>(xs + r * pitch + i * 16) =
+                            *reinterpret_cast<const u32x4 *>(p.x + src * K + min(k0 + 8 * i, K - 8));
+                }
+            }
+            __syncthreads();
+            const int c2 = c + chunk, s_end = behind(c);
+            const bool more = c2 < steps && first(c2) < behind(c2);
+            if (!loaded && first(c) < s_end) load(first(c), next);
+            loaded = more && first(c) < s_end;
+            for (int s = first(c); s < s_end; ++s) {
+                const Weights w = next;
+                load(s + 1 < s_end ? s + 1 : more ? first(c2) : s, next);
+                const uint8_t *at = row + (s - c) * 512;
+#pragma unroll
+                for (int gr = 0; gr < kGroups; ++gr) {
+                    f4 d[2] = {};
+                    uint32_t off[2];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {  // minus 16 minus the zero point, twice
+                        const uint32_t z = ZEROS ? (w.z[q][gr / 4] >> (8 * (gr & 3))) & 255u : 8u;
+                        off[q] = 0xC180C180u | z << 3 | z << 19;
+                    }
+#pragma unroll
+                    for (int i = gr * (GROUP / 32); i < (gr + 1) * (GROUP / 32); ++i) {
+                        const bf8 xo = __builtin_bit_cast(bf8, *reinterpret_cast<const u32x4 *>(at + 64 * i));
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            d[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo, expand(w.c[q][i >> 2][i & 3]), d[q], 0, 0, 0);
+                            d[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                xo, __builtin_bit_cast(bf8, (u32x4){off[q], off[q], off[q], off[q]}), d[q], 0, 0, 0);
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float f = scale_value<HALF>(w.s[q][gr / 2], gr & 1);
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) acc[q][v] = fmaf(d[q][v], f, acc[q][v]);
+                    }
+                }
+            }
+        }
+        // accumulator v of q: row 4 g + v, column 16 q + i16
+        if constexpr (KS > 1) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) part[wave][4 * g + v][16 * q + i16] = acc[q][v];
+            __syncthreads();
+            // a block's waves take the rows 4 g + v of its sums in turn: a wave's lanes are 16 columns of four rows
+            if (ks >= 4) continue;
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    float y = part[wave - ks][4 * g + v][16 * q + i16];
+#pragma unroll
+                    for (int k = 1; k < KS; ++k) y += part[wave - ks + k][4 * g + v][16 * q + i16];
+                    acc[q][v] = y;
+                }
+        }
+        if (cb < nb) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int m = 4 * g + v;
+                if (m >= have || (KS > 1 && ks != v)) continue;
+                const int64_t out = (int64_t)(p0 + m0 + m) * p.C;
+                auto store = [&](int c, float y) __attribute__((always_inline)) {
+                    if (c >= p.C) return;
+                    if (p.out_dtype == MOE_DT_BF16) static_cast<uint16_t *>(p.out)[out + c] = __builtin_bit_cast(uint16_t, (__bf16)y);
+                    else static_cast<float *>(p.out)[out + c] = y;
+                };
+                if (p.swiglu) {
+                    store(16 * cb + i16, swiglu(acc[0][v], acc[1][v]));
+                } else {
+                    store(32 * cb + i16, acc[0][v]);
+                    store(32 * cb + 16 + i16, acc[1][v]);
+                }
+            }
+        }
+    }
+}
+
+// 17 to 64 rows of one group: a workgroup takes two column tiles, its waves a part of the steps each, and their partial sums
+// meet in LDS in the waves' order. MOST: pieces of 16 rows in a turn at most.
 template <int GROUP, bool HALF, bool ZEROS, int MOST, int WAVES>
-__global__ void __launch_bounds__(64 * WAVES, MOST == 1 ? 4 : 2) stream_kernel(const W4GemmArgs p) {
+__global__ void __launch_bounds__(64 * WAVES, 2) wide_stream_kernel(const W4GemmArgs p) {
     constexpr int kGroups = kW4Step / GROUP;      // per step
     constexpr int kWords = (kGroups + 1) / 2;     // of scales
     constexpr int kZeroWords = (kGroups + 3) / 4;
@@ -187,31 +370,28 @@ __global__ void __launch_bounds__(64 * WAVES, MOST == 1 ? 4 : 2) stream_kernel(c
         }
     };
     using std::integral_constant;
-    if constexpr (MOST == 1) {
-        for (int m0 = 0; m0 < rows; m0 += 16) turn(m0, integral_constant<int, 1>{});
-    } else {
-        int m0 = 0;
-        for (; rows - m0 > 32; m0 += 64) turn(m0, integral_constant<int, 4>{});
-        if (rows > m0) turn(m0, integral_constant<int, 2>{});
-    }
+    int m0 = 0;
+    for (; rows - m0 > 32; m0 += 64) turn(m0, integral_constant<int, 4>{});
+    if (rows > m0) turn(m0, integral_constant<int, 2>{});
 }
 
 }  // namespace
 
 hipError_t launch_w4_gemm(const W4GemmArgs &a, hipStream_t s) {
-    const int64_t nb = a.swiglu ? (a.C + 15) / 16 : (a.C + 31) / 32, groups = (int64_t)a.v.max_tiles * nb;
     const int rows = a.v.mean_rows;
     if (rows > (a.v.offsets ? 16 : 64)) return launch_w4_tile(a, s);
-    if (groups * 1024 >= 1ll << 32) return hipErrorInvalidValue;  // a grid's threads are 32 bits
+    const int64_t nb = a.swiglu ? (a.C + 15) / 16 : (a.C + 31) / 32, blocks = (int64_t)a.v.max_tiles * nb;
+    if (blocks >= 1 << 22) return hipErrorInvalidValue;  // a grid's threads are 32 bits
     by_form(a.w, [&](auto group, auto half, auto zeros) {
         constexpr int kGroup = decltype(group)::value;
         constexpr bool kHalf = decltype(half)::value, kZeros = decltype(zeros)::value;
-        auto go = [&](auto kernel, int waves) {
-            hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(64 * waves), 0, s, a);
+        auto go = [&](auto kernel, int per_group) {
+            hipLaunchKernelGGL(kernel, dim3((unsigned)(a.v.max_tiles * ((nb + per_group - 1) / per_group))), dim3(512), 0, s, a);
         };
-        if (rows > 16) go(stream_kernel<kGroup, kHalf, kZeros, 4, 8>, 8);
-        else if (groups < 512) go(stream_kernel<kGroup, kHalf, kZeros, 1, 16>, 16);
-        else go(stream_kernel<kGroup, kHalf, kZeros, 1, 4>, 4);
+        if (rows > 16) go(wide_stream_kernel<kGroup, kHalf, kZeros, 4, 8>, 1);
+        else if (blocks >= 4096) go(stream_kernel<kGroup, kHalf, kZeros, 1>, 8);
+        else if (blocks >= 1024) go(stream_kernel<kGroup, kHalf, kZeros, 4>, 2);
+        else go(stream_kernel<kGroup, kHalf, kZeros, 8>, 1);
     });
     return hipGetLastError();
 }
