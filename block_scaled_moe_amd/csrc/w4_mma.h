@@ -22,16 +22,23 @@ using namespace block;
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// eight codes as 16 + q
-__device__ __forceinline__ bf8 expand(uint32_t w) {
-    const uint32_t mask = 0x00780078u, base = 0x41804180u;
-    u32x4 r;
-    r[0] = (w & mask) | base;
-    r[1] = ((w >> 4) & mask) | base;
-    r[2] = ((w >> 8) & mask) | base;
-    r[3] = (__builtin_rotateright32(w, 12) & mask) | base;
-    return __builtin_bit_cast(bf8, r);
-}
+// eight codes as 16 + q, by one AND-OR of each pair. The constants are held in registers: as literals they cannot go into that
+// instruction, and the compiler takes it apart into two.
+struct Expander {
+    uint32_t mask, base;
+    __device__ __forceinline__ Expander() {
+        asm("s_mov_b32 %0, 0x00780078" : "=s"(mask));
+        asm("v_mov_b32 %0, 0x41804180" : "=v"(base));
+    }
+    __device__ __forceinline__ bf8 operator()(uint32_t w) const {
+        u32x4 r;
+        r[0] = (w & mask) | base;
+        r[1] = ((w >> 4) & mask) | base;
+        r[2] = ((w >> 8) & mask) | base;
+        r[3] = (__builtin_rotateright32(w, 12) & mask) | base;
+        return __builtin_bit_cast(bf8, r);
+    }
+};
 
 template <bool HALF>
 __device__ __forceinline__ float scale_value(uint32_t word, int upper) {

@@ -24,6 +24,7 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) stream_kernel(const W4Ge
     constexpr int kBlocks = kStreamWaves / KS;    // of two column tiles a workgroup
     __shared__ __attribute__((aligned(16))) uint8_t xs[kStreamX];
     __shared__ __attribute__((aligned(16))) float part[KS > 1 ? kStreamWaves : 1][KS > 1 ? 16 : 1][36];
+    const Expander expand;
     const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
     const int i16 = lane & 15, g = lane >> 4, ks = wave % KS;
     const int K = p.w.K, steps = p.steps;
@@ -202,6 +203,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) wide_stream_kernel(const W4Gemm
     constexpr int kWords = (kGroups + 1) / 2;     // of scales
     constexpr int kZeroWords = (kGroups + 3) / 4;
     __shared__ __attribute__((aligned(16))) float part[WAVES][16 * MOST][36];
+    const Expander expand;
     const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
     const int i16 = lane & 15, g = lane >> 4;
     const int N = p.w.N, K = p.w.K;

@@ -17,6 +17,7 @@ namespace {
 using namespace w4;
 
 constexpr int kThreads = 512, kBM = 128, kStage = 128;
+constexpr int kGrid = 256;  // workgroups: one a CU
 constexpr int kX = kBM * kStage * 2;  // LDS bytes of a stage's rows
 
 // copy_to_lds from any address
@@ -39,35 +40,27 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
     uint8_t *const xb = lds, *const wb = lds + 3 * kX, *const sb = wb + 3 * kW, *const zb = sb + 2 * kS;
     float *const sums = reinterpret_cast<float *>(zb + 2 * kZ);
 
+    const Expander expand;
     const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
     const int i16 = lane & 15, g = lane >> 4, wm = wave >> 2, wn = wave & 3;
     const int K = p.w.K, stages = (K + kStage - 1) / kStage;
     const int width = p.swiglu ? kBN / 2 : kBN;  // output columns a workgroup
     const int nb = (p.C + width - 1) / width;
 
-    // ---- work item: each XCD (workgroups 8 apart) takes a range of the experts' tiles, whose rows then meet in one L2; both
-    // parts of a tile of the groups' list next to each other
-    int e = 0, p0, rows, cb;
-    {
-        const int parts = p.v.offsets ? 2 : 1;
-        const int n_tiles = p.v.offsets ? scalar_load(&p.v.ctrl->n_tiles) : (p.v.rows + kBM - 1) / kBM;
-        const int items = n_tiles * nb * parts, per = (items + 7) / 8, i = blockIdx.x >> 3;
-        const int item = (blockIdx.x & 7) * per + i;
-        if (i >= per || item >= items) return;
-        const int tile = item / (nb * parts), rest = item % (nb * parts);
-        cb = rest / parts;
-        if (p.v.offsets) {
-            e = scalar_load(p.v.tile_expert + tile);
-            p0 = scalar_load(p.v.tile_row0 + tile);
-            rows = min(scalar_load(p.v.offsets + e + 1) - p0, kGroupTile) - kBM * (rest % 2);
-            p0 += kBM * (rest % 2);
-            if (rows <= 0) return;
-        } else {
-            p0 = tile * kBM;
-            rows = p.v.rows - p0;
-        }
-        rows = min(rows, kBM);
+    // ---- work items: each XCD (workgroups 8 apart) takes a range of the experts' tiles, whose rows then meet in one L2; a tile
+    // of the groups' list is up to two of 128 rows
+    const int n_tiles = p.v.offsets ? scalar_load(&p.v.ctrl->n_tiles) : (p.v.rows + kBM - 1) / kBM;
+    const int items = n_tiles * nb, per = (items + 7) / 8, item_end = min((int)(blockIdx.x & 7) * per + per, items);
+    for (int item = (blockIdx.x & 7) * per + (blockIdx.x >> 3); item < item_end; item += gridDim.x >> 3) {
+    const int tile = item / nb, cb = item % nb;
+    int e = 0, row0 = tile * kBM, row_end = min(row0 + kBM, p.v.rows);
+    if (p.v.offsets) {
+        e = scalar_load(p.v.tile_expert + tile);
+        row0 = scalar_load(p.v.tile_row0 + tile);
+        row_end = min(scalar_load(p.v.offsets + e + 1), row0 + kGroupTile);
     }
+    for (int p0 = row0; p0 < row_end; p0 += kBM) {
+    const int rows = min(row_end - p0, kBM);
 
     // ---- sources. Rows: copies wave + 8 j of four rows of 256 bytes; a row's 16-byte pieces are swapped by the row's last
     // four bits, so that sixteen rows' pieces of one place lie in different banks.
@@ -276,17 +269,21 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
         case 2: run(integral_constant<int, 2>{}); break;
         default: run(integral_constant<int, 1>{}); break;  // none: beside the other waves, nothing of it is stored
     }
+    lds_barrier();  // the buffers are the next item's
+    }
+    }
 }
 
 }  // namespace
 
 hipError_t launch_w4_tile(const W4GemmArgs &a, hipStream_t s) {
-    const int64_t tiles = a.v.offsets ? 2 * (int64_t)a.v.max_tiles : (a.v.rows + kBM - 1) / kBM;
+    const int64_t tiles = a.v.offsets ? a.v.max_tiles : (a.v.rows + kBM - 1) / kBM;
     auto items = [&](int columns) { return tiles * ((a.C + columns - 1) / columns); };
     // a second half that starts inside a packed tile needs one more of them, for which only the narrow tile has room
     const bool narrow = (a.swiglu && a.C % 16) || items(a.swiglu ? 128 : 256) < 512;
-    const int64_t grid = (items(narrow ? (a.swiglu ? 64 : 128) : (a.swiglu ? 128 : 256)) + 7) / 8 * 8;
-    if (grid >= 1 << 23) return hipErrorInvalidValue;  // a grid's threads are 32 bits
+    const int64_t n = (items(narrow ? (a.swiglu ? 64 : 128) : (a.swiglu ? 128 : 256)) + 7) / 8 * 8;
+    if (n > INT32_MAX) return hipErrorInvalidValue;
+    const int64_t grid = n < kGrid ? n : kGrid;
     w4::by_form(a.w, [&](auto group, auto half, auto zeros) {
         constexpr int kGroup = decltype(group)::value;
         constexpr bool kHalf = decltype(half)::value, kZeros = decltype(zeros)::value;
