@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
     };
 
     // ---- this lane's columns: row of the packed tiles in LDS
-    int w_row[NF];
+    int w_row[NF], w_at[NF];  // and place in its codes
 #pragma unroll
     for (int q = 0; q < NF; ++q) {
         w_row[q] = (wn * NF + q) * 16 + i16;
@@ -118,9 +118,10 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
             const int in = (wn * (NF / 2) + q % (NF / 2)) * 16 + i16;
             w_row[q] = q < NF / 2 ? in : kBN / 2 + ((p.C + cb * width) & 15) + in;
         }
+        w_at[q] = (w_row[q] >> 4) * 1024 + (16 * g + (w_row[q] & 15)) * 16;
     }
 
-    // sums of x over the groups of stage s for the 16 rows of piece `wave`
+    // sums of x over the groups of stage s for the 16 rows of piece `wave`, negative, without zero points times 24
     auto row_sums = [&](int s, int buffer) __attribute__((always_inline)) {
         if (wave >= n_sub) return;
         const uint8_t *row = xb + buffer * kX + (16 * wave + i16) * 256;
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
             for (int r = gr * (GROUP / 32); r < (gr + 1) * (GROUP / 32); ++r)
                 d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                     __builtin_bit_cast(bf8, *reinterpret_cast<const u32x4 *>(row + ((4 * r + g) ^ i16) * 16)), ones(), d, 0, 0, 0);
-            if (i16 == 0) *reinterpret_cast<f4 *>(sums + ((s & 1) * kIn + gr) * kBM + 16 * wave + 4 * g) = d;
+            if (i16 == 0) *reinterpret_cast<f4 *>(sums + ((s & 1) * kIn + gr) * kBM + 16 * wave + 4 * g) = d * (ZEROS ? -1.0f : -24.0f);
         }
     };
 
@@ -153,6 +154,14 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
         for (int i = 0; i < MF; ++i)
 #pragma unroll
             for (int q = 0; q < NF; ++q) acc[i][q] = (f4){0.0f, 0.0f, 0.0f, 0.0f};
+        f4 d[MF][NF];  // of the group that is summed
+        float f_last[NF];  // and its scales
+#pragma unroll
+        for (int q = 0; q < NF; ++q) {
+            f_last[q] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < MF; ++i) d[i][q] = (f4){0.0f, 0.0f, 0.0f, 0.0f};
+        }
         int b0 = 0, b1 = 1, b2 = 2;  // buffers of stages s, s + 1, s + 2
 #pragma clang loop unroll(disable)
         for (int s = 0; s < stages; ++s) {
@@ -171,17 +180,14 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
             float f[NF][kIn], off[NF][kIn];
 #pragma unroll
             for (int q = 0; q < NF; ++q) {
-                raw[q] = *reinterpret_cast<const u32x4 *>(wb + b0 * kW + (w_row[q] >> 4) * 1024 + (16 * g + (w_row[q] & 15)) * 16);
+                raw[q] = *reinterpret_cast<const u32x4 *>(wb + b0 * kW + w_at[q]);
                 const uint8_t *sp = sb + ((s >> 1) & 1) * kS + w_row[q] * (2 * kGroups) + (s & 1) * (2 * kIn);
                 uint32_t word[(kIn + 1) / 2];
                 if constexpr (kIn == 1) word[0] = *reinterpret_cast<const uint16_t *>(sp);
                 else if constexpr (kIn == 2) word[0] = *reinterpret_cast<const uint32_t *>(sp);
                 else word[0] = reinterpret_cast<const u32x2 *>(sp)->x, word[1] = reinterpret_cast<const u32x2 *>(sp)->y;
 #pragma unroll
-                for (int gr = 0; gr < kIn; ++gr) {
-                    f[q][gr] = scale_value<HALF>(word[gr / 2], gr & 1);
-                    off[q][gr] = 24.0f;
-                }
+                for (int gr = 0; gr < kIn; ++gr) f[q][gr] = scale_value<HALF>(word[gr / 2], gr & 1);
                 if constexpr (ZEROS) {
                     const uint8_t *zp = zb + ((s >> 1) & 1) * kZ + w_row[q] * kGroups + (s & 1) * kIn;
                     uint32_t z;
@@ -193,38 +199,45 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
                 }
             }
             const uint8_t *row = xb + b0 * kX + (16 * wm + i16) * 256;
+            const float *sum_at = sums + (s & 1) * kIn * kBM + 16 * wm + 4 * g;
 #pragma unroll
-            for (int gr = 0; gr < kIn; ++gr) {
-                f4 d[MF][NF];
+            for (int r = 0; r < 4; ++r) {
+                constexpr int kRuns = GROUP / 32;
+                const int gr = r / kRuns;
+                bf8 w[NF];
 #pragma unroll
-                for (int i = 0; i < MF; ++i)
-#pragma unroll
-                    for (int q = 0; q < NF; ++q) d[i][q] = (f4){0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int r = gr * (GROUP / 32); r < (gr + 1) * (GROUP / 32); ++r) {
-                    bf8 w[NF];
-#pragma unroll
-                    for (int q = 0; q < NF; ++q) w[q] = expand(raw[q][r]);
-#pragma unroll
-                    for (int i = 0; i < MF; ++i) {
-                        const bf8 xo = __builtin_bit_cast(bf8, *reinterpret_cast<const u32x4 *>(row + i * 8192 + ((4 * r + g) ^ i16) * 16));
-#pragma unroll
-                        for (int q = 0; q < NF; ++q) d[i][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo, w[q], d[i][q], 0, 0, 0);
-                    }
-                }
+                for (int q = 0; q < NF; ++q) w[q] = expand(raw[q][r]);
 #pragma unroll
                 for (int i = 0; i < MF; ++i) {
-                    const f4 sum = *reinterpret_cast<const f4 *>(sums + ((s & 1) * kIn + gr) * kBM + 16 * (2 * i + wm) + 4 * g);
+                    const bf8 xo = __builtin_bit_cast(bf8, *reinterpret_cast<const u32x4 *>(row + i * 8192 + ((4 * r + g) ^ i16) * 16));
+                    f4 sum;
+                    if (r % kRuns == 0) sum = *reinterpret_cast<const f4 *>(sum_at + gr * kBM + 32 * i);
 #pragma unroll
-                    for (int q = 0; q < NF; ++q)
+                    for (int q = 0; q < NF; ++q) {
+                        f4 c = d[i][q];
+                        if (r % kRuns == 0) {
+                            // the group before is done: its sum goes to the accumulator behind this group's first MFMAs
 #pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            acc[i][q][v] = fmaf(fmaf(-off[q][gr], sum[v], d[i][q][v]), f[q][gr], acc[i][q][v]);
+                            for (int v = 0; v < 4; ++v) acc[i][q][v] = fmaf(c[v], f_last[q], acc[i][q][v]);
+                            c = ZEROS ? sum * off[q][gr] : sum;
+                        }
+                        d[i][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo, w[q], c, 0, 0, 0);
+                    }
+                }
+                if (r % kRuns == 0) {
+#pragma unroll
+                    for (int q = 0; q < NF; ++q) f_last[q] = f[q][gr];
                 }
             }
             const int b = b0;
             b0 = b1, b1 = b2, b2 = b;
         }
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+#pragma unroll
+            for (int q = 0; q < NF; ++q)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[i][q][v] = fmaf(d[i][q][v], f_last[q], acc[i][q][v]);
 
         // ---- outputs: accumulator v of (i, q): row 16 (2 i + wm) + 4 g + v. fp32 from the lanes, bf16 by way of LDS as
         // whole runs of a row
