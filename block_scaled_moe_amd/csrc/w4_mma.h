@@ -30,13 +30,12 @@ struct Expander {
         asm("s_mov_b32 %0, 0x00780078" : "=s"(mask));
         asm("v_mov_b32 %0, 0x41804180" : "=v"(base));
     }
+    // codes 2 i and 2 i + 1
+    __device__ __forceinline__ uint32_t pair(uint32_t w, int i) const {
+        return ((i == 0 ? w : i < 3 ? w >> (4 * i) : __builtin_rotateright32(w, 12)) & mask) | base;
+    }
     __device__ __forceinline__ bf8 operator()(uint32_t w) const {
-        u32x4 r;
-        r[0] = (w & mask) | base;
-        r[1] = ((w >> 4) & mask) | base;
-        r[2] = ((w >> 8) & mask) | base;
-        r[3] = (__builtin_rotateright32(w, 12) & mask) | base;
-        return __builtin_bit_cast(bf8, r);
+        return __builtin_bit_cast(bf8, (u32x4){pair(w, 0), pair(w, 1), pair(w, 2), pair(w, 3)});
     }
 };
 

@@ -5,10 +5,13 @@
 // alternate between the two row waves, so that a partial tile splits evenly) x 16 NF columns; with swiglu half of a wave's
 // columns are the first half's and half the same ones of the second half, so that both meet in one lane.
 //  - Stages of 128 of the reduction. Rows (gathered by token) and codes go straight from memory into LDS, three buffers
-//    each, two stages ahead, scales and zero points into two buffers of 256 of the reduction; one barrier a stage covers
-//    everything. Both row waves read the same codes there.
-//  - The sums of x per row and group are the same for all columns: each wave forms those of one piece of 16 rows, a stage
-//    ahead, and leaves them in LDS.
+//    each, scales and zero points into two buffers of 256 of the reduction; one barrier a stage covers everything. It
+//    stands before the last quarter of a stage's products, whose operands are in registers by then: its buffers take the stage
+//    three ahead at once, and the next stage's operands are read and expanded behind those products.
+//  - The sums of x per row and group are the same for all columns: each wave forms those of one piece of 16 rows, two stages
+//    ahead, and leaves them in LDS, from where they are the products' first addends.
+//  - MFMAs (16 clocks) and vector instructions (4 clocks) are about as much work, so each MFMA stands beside the
+//    instructions that expand a later operand or add an earlier group's sum.
 #include "w4_mma.h"
 
 namespace moe {
@@ -32,7 +35,7 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
     constexpr int kGroups = kW4Step / GROUP, kIn = kStage / GROUP;  // groups per step, per stage
     constexpr int kW = kTiles * 1024;                         // LDS bytes of a stage's codes
     constexpr int kS = kTiles * 32 * kGroups, kZ = ZEROS ? kS / 2 : 0;  // of a step's scales and zero points
-    constexpr int kLds = 3 * (kX + kW) + 2 * (kS + kZ) + 2 * kIn * kBM * 4;
+    constexpr int kLds = 3 * (kX + kW) + 2 * (kS + kZ) + 3 * kIn * kBM * 4;
     constexpr int kWCopies = kBN / 16 / 8;  // of codes by every wave in a stage (the first one: perhaps one more)
     constexpr int kSWaves = (kS + 1023) / 1024, kZWaves = (kZ + 1023) / 1024;
     static_assert(kLds <= 160 * 1024 && kBM * (kBN + 8) * 2 <= 3 * kX && kSWaves + kZWaves <= 8, "LDS");
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
     }
 
     // sums of x over the groups of stage s for the 16 rows of piece `wave`, negative, without zero points times 24
-    auto row_sums = [&](int s, int buffer) __attribute__((always_inline)) {
+    auto row_sums = [&](int buffer) __attribute__((always_inline)) {
         if (wave >= n_sub) return;
         const uint8_t *row = xb + buffer * kX + (16 * wave + i16) * 256;
 #pragma unroll
@@ -132,103 +135,140 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
             for (int r = gr * (GROUP / 32); r < (gr + 1) * (GROUP / 32); ++r)
                 d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                     __builtin_bit_cast(bf8, *reinterpret_cast<const u32x4 *>(row + ((4 * r + g) ^ i16) * 16)), ones(), d, 0, 0, 0);
-            if (i16 == 0) *reinterpret_cast<f4 *>(sums + ((s & 1) * kIn + gr) * kBM + 16 * wave + 4 * g) = d * (ZEROS ? -1.0f : -24.0f);
+            if (i16 == 0) *reinterpret_cast<f4 *>(sums + (buffer * kIn + gr) * kBM + 16 * wave + 4 * g) = d * (ZEROS ? -1.0f : -24.0f);
         }
     };
 
     copy_side(0);
+    if (stages > 2) copy_side(1);
     copy_x(0, 0);
     copy_w(0, 0);
     if (stages > 1) {
         copy_x(1, 1);
         copy_w(1, 1);
     }
+    if (stages > 2) {
+        copy_x(2, 2);
+        copy_w(2, 2);
+    }
     wait_copies<0>();
     lds_barrier();
-    row_sums(0, 0);
+    row_sums(0);
+    if (stages > 1) row_sums(1);
+    lds_barrier();
 
     auto run = [&](auto mf_c) __attribute__((always_inline)) {
-        constexpr int MF = decltype(mf_c)::value;  // this wave's pieces of 16 rows
-        f4 acc[MF][NF];
-#pragma unroll
-        for (int i = 0; i < MF; ++i)
-#pragma unroll
-            for (int q = 0; q < NF; ++q) acc[i][q] = (f4){0.0f, 0.0f, 0.0f, 0.0f};
-        f4 d[MF][NF];  // of the group that is summed
-        float f_last[NF];  // and its scales
+        constexpr int MF = decltype(mf_c)::value, kRuns = GROUP / 32;  // this wave's pieces of 16 rows; MFMAs in a row of a group
+        f4 acc[MF][NF], d[MF][NF];  // d: of the group that is summed
+        float f_last[NF];           // and its scales
 #pragma unroll
         for (int q = 0; q < NF; ++q) {
             f_last[q] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < MF; ++i) d[i][q] = (f4){0.0f, 0.0f, 0.0f, 0.0f};
+            for (int i = 0; i < MF; ++i) acc[i][q] = d[i][q] = (f4){0.0f, 0.0f, 0.0f, 0.0f};
         }
-        int b0 = 0, b1 = 1, b2 = 2;  // buffers of stages s, s + 1, s + 2
-#pragma clang loop unroll(disable)
-        for (int s = 0; s < stages; ++s) {
-            // everything but the codes of stage s + 1 has arrived; every wave is done with stage s - 1 and has left the
-            // sums of stage s
-            if (s + 1 < stages) wait_copies<kWCopies>();
-            else wait_copies<0>();
-            lds_barrier();
-            if (s + 2 < stages) {
-                if ((s & 1) == 0) copy_side(s / 2 + 1);
-                copy_x(s + 2, b2);
-                copy_w(s + 2, b2);
-            }
-            if (s + 1 < stages) row_sums(s + 1, b1);
+        // what a stage's products need of its columns
+        struct Columns {
             u32x4 raw[NF];
-            float f[NF][kIn], off[NF][kIn];
+            uint32_t s[NF][(kIn + 1) / 2], z[NF];
+        };
+        auto read_columns = [&](int s, int buffer, Columns &c) __attribute__((always_inline)) {
 #pragma unroll
             for (int q = 0; q < NF; ++q) {
-                raw[q] = *reinterpret_cast<const u32x4 *>(wb + b0 * kW + w_at[q]);
+                c.raw[q] = *reinterpret_cast<const u32x4 *>(wb + buffer * kW + w_at[q]);
                 const uint8_t *sp = sb + ((s >> 1) & 1) * kS + w_row[q] * (2 * kGroups) + (s & 1) * (2 * kIn);
-                uint32_t word[(kIn + 1) / 2];
-                if constexpr (kIn == 1) word[0] = *reinterpret_cast<const uint16_t *>(sp);
-                else if constexpr (kIn == 2) word[0] = *reinterpret_cast<const uint32_t *>(sp);
-                else word[0] = reinterpret_cast<const u32x2 *>(sp)->x, word[1] = reinterpret_cast<const u32x2 *>(sp)->y;
-#pragma unroll
-                for (int gr = 0; gr < kIn; ++gr) f[q][gr] = scale_value<HALF>(word[gr / 2], gr & 1);
+                if constexpr (kIn == 1) c.s[q][0] = *reinterpret_cast<const uint16_t *>(sp);
+                else if constexpr (kIn == 2) c.s[q][0] = *reinterpret_cast<const uint32_t *>(sp);
+                else c.s[q][0] = reinterpret_cast<const u32x2 *>(sp)->x, c.s[q][1] = reinterpret_cast<const u32x2 *>(sp)->y;
                 if constexpr (ZEROS) {
                     const uint8_t *zp = zb + ((s >> 1) & 1) * kZ + w_row[q] * kGroups + (s & 1) * kIn;
-                    uint32_t z;
-                    if constexpr (kIn == 1) z = *zp;
-                    else if constexpr (kIn == 2) z = *reinterpret_cast<const uint16_t *>(zp);
-                    else z = *reinterpret_cast<const uint32_t *>(zp);
-#pragma unroll
-                    for (int gr = 0; gr < kIn; ++gr) off[q][gr] = 16.0f + (float)((z >> (8 * gr)) & 255u);
+                    if constexpr (kIn == 1) c.z[q] = *zp;
+                    else if constexpr (kIn == 2) c.z[q] = *reinterpret_cast<const uint16_t *>(zp);
+                    else c.z[q] = *reinterpret_cast<const uint32_t *>(zp);
                 }
             }
-            const uint8_t *row = xb + b0 * kX + (16 * wm + i16) * 256;
-            const float *sum_at = sums + (s & 1) * kIn * kBM + 16 * wm + 4 * g;
+        };
+        const uint8_t *const rows_at = xb + (16 * wm + i16) * 256;
+        // operand n = MF r + i of the stage in `buffer`: rows of piece i, columns 32 r ..
+        auto read_rows = [&](int buffer, int n) __attribute__((always_inline)) -> bf8 {
+            return __builtin_bit_cast(bf8, *reinterpret_cast<const u32x4 *>(rows_at + buffer * kX + n % MF * 8192 + ((4 * (n / MF) + g) ^ i16) * 16));
+        };
+        Columns c, cn;
+        bf8 x0 = read_rows(0, 0), x1 = read_rows(0, 1);
+        u32x4 w[NF];
+        read_columns(0, 0, c);
+#pragma unroll
+        for (int q = 0; q < NF; ++q) w[q] = __builtin_bit_cast(u32x4, expand(c.raw[q][0]));
+        int b0 = 0, b1 = 1, b2 = 2;  // buffers of stages s (and s + 3), s + 1, s + 2
+#pragma clang loop unroll(disable)
+        for (int s = 0; s < stages; ++s) {
+            const float *sum_at = sums + b0 * kIn * kBM + 16 * wm + 4 * g;
+            bf8 x[4 * MF];
+            u32x4 wn[NF];
+            x[0] = x0, x[1] = x1;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                constexpr int kRuns = GROUP / 32;
                 const int gr = r / kRuns;
-                bf8 w[NF];
-#pragma unroll
-                for (int q = 0; q < NF; ++q) w[q] = expand(raw[q][r]);
-#pragma unroll
-                for (int i = 0; i < MF; ++i) {
-                    const bf8 xo = __builtin_bit_cast(bf8, *reinterpret_cast<const u32x4 *>(row + i * 8192 + ((4 * r + g) ^ i16) * 16));
-                    f4 sum;
-                    if (r % kRuns == 0) sum = *reinterpret_cast<const f4 *>(sum_at + gr * kBM + 32 * i);
-#pragma unroll
-                    for (int q = 0; q < NF; ++q) {
-                        f4 c = d[i][q];
-                        if (r % kRuns == 0) {
-                            // the group before is done: its sum goes to the accumulator behind this group's first MFMAs
-#pragma unroll
-                            for (int v = 0; v < 4; ++v) acc[i][q][v] = fmaf(c[v], f_last[q], acc[i][q][v]);
-                            c = ZEROS ? sum * off[q][gr] : sum;
-                        }
-                        d[i][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo, w[q], c, 0, 0, 0);
+                if (r == 3) {
+                    // everything but the codes of stage s + 2 has arrived, and every wave is done with the buffers of stage s
+                    if (s + 2 < stages) wait_copies<kWCopies>();
+                    else wait_copies<0>();
+                    lds_barrier();
+                    if (s + 3 < stages) {
+                        if (s & 1) copy_side((s + 3) / 2);
+                        copy_x(s + 3, b0);
+                        copy_w(s + 3, b0);
                     }
+                    read_columns(s + 1, b1, cn);  // behind the last stage what is there, unused
+                    x0 = read_rows(b1, 0), x1 = read_rows(b1, 1);
                 }
+                float f[NF], off[NF];
                 if (r % kRuns == 0) {
 #pragma unroll
-                    for (int q = 0; q < NF; ++q) f_last[q] = f[q][gr];
+                    for (int q = 0; q < NF; ++q) {
+                        f[q] = scale_value<HALF>(c.s[q][gr / 2], gr & 1);
+                        if constexpr (ZEROS) off[q] = 16.0f + (float)((c.z[q] >> (8 * gr)) & 255u);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < MF; ++i) {
+                    const int n = MF * r + i;
+                    if (n + 2 < 3 * MF) x[n + 2] = read_rows(b0, n + 2);
+                    if (r == 2) x[3 * MF + i] = read_rows(b0, 3 * MF + i);
+                    f4 sum;
+                    if (r % kRuns == 0) sum = *reinterpret_cast<const f4 *>(sum_at + gr * kBM + 32 * i);
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int q = 0; q < NF; ++q) {
+                        const f4 last = d[i][q];
+                        d[i][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            x[n], __builtin_bit_cast(bf8, w[q]), r % kRuns != 0 ? last : ZEROS ? sum * off[q] : sum, 0, 0, 0);
+                        pin(d[i][q]);
+                        __builtin_amdgcn_sched_barrier(0);  // what follows behind the MFMA, not before it
+                        if (r % kRuns == 0) {               // the group before is done
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) acc[i][q][v] = fmaf(last[v], f_last[q], acc[i][q][v]);
+                            pin(acc[i][q]);
+                        }
+                        // the next operands of the columns, in equal parts
+                        const int slot = i * NF + q;
+#pragma unroll
+                        for (int e = 0; e < 4 * NF; ++e)
+                            if (e >= slot * 4 / MF && e < (slot + 1) * 4 / MF) {
+                                wn[e / 4][e % 4] = expand.pair(r < 3 ? c.raw[e / 4][r < 3 ? r + 1 : 0] : cn.raw[e / 4][0], e % 4);
+                                asm volatile("" ::"v"(wn[e / 4][e % 4]));
+                            }
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < NF; ++q) {
+                    w[q] = wn[q];
+                    if (r % kRuns == 0) f_last[q] = f[q];
                 }
             }
+            if (s + 2 < stages) row_sums(b2);
+            c = cn;
             const int b = b0;
             b0 = b1, b1 = b2, b2 = b;
         }
@@ -292,16 +332,22 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
 hipError_t launch_w4_tile(const W4GemmArgs &a, hipStream_t s) {
     const int64_t tiles = a.v.offsets ? a.v.max_tiles : (a.v.rows + kBM - 1) / kBM;
     auto items = [&](int columns) { return tiles * ((a.C + columns - 1) / columns); };
-    // a second half that starts inside a packed tile needs one more of them, for which only the narrow tile has room
-    const bool narrow = (a.swiglu && a.C % 16) || items(a.swiglu ? 128 : 256) < 512;
+    // a second half that starts inside a packed tile needs one more of them, for which only the narrow tile has room, as for the
+    // sums of groups of 32
+    const bool narrow = a.w.group == 32 || (a.swiglu && a.C % 16) || items(a.swiglu ? 128 : 256) < 512;
     const int64_t n = (items(narrow ? (a.swiglu ? 64 : 128) : (a.swiglu ? 128 : 256)) + 7) / 8 * 8;
     if (n > INT32_MAX) return hipErrorInvalidValue;
     const int64_t grid = n < kGrid ? n : kGrid;
     w4::by_form(a.w, [&](auto group, auto half, auto zeros) {
         constexpr int kGroup = decltype(group)::value;
         constexpr bool kHalf = decltype(half)::value, kZeros = decltype(zeros)::value;
-        if (narrow) hipLaunchKernelGGL((tile_kernel<kGroup, kHalf, kZeros, 2>), dim3((unsigned)grid), dim3(kThreads), 0, s, a);
-        else hipLaunchKernelGGL((tile_kernel<kGroup, kHalf, kZeros, 4>), dim3((unsigned)grid), dim3(kThreads), 0, s, a);
+        if constexpr (kGroup > 32) {
+            if (!narrow) {
+                hipLaunchKernelGGL((tile_kernel<kGroup, kHalf, kZeros, 4>), dim3((unsigned)grid), dim3(kThreads), 0, s, a);
+                return;
+            }
+        }
+        hipLaunchKernelGGL((tile_kernel<kGroup, kHalf, kZeros, 2>), dim3((unsigned)grid), dim3(kThreads), 0, s, a);
     });
     return hipGetLastError();
 }
