@@ -14,11 +14,11 @@ refused while gradients are on).
 from __future__ import annotations
 
 import ctypes
-import dataclasses
+import functools
 
 import torch
 
-from .ops import DTYPES, _ask, _call, _function, _int32, _out
+from .ops import DTYPES, _ask, _call, _function, _int32, _once, _out
 
 
 class MoeLosses(ctypes.Structure):
@@ -58,9 +58,10 @@ SIGNATURES = {
 def _matrix(what: str, t: torch.Tensor) -> tuple[int, int]:
     if t.dim() != 2:
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected two dimensions")
-    for n in t.shape:
-        _int32(what, n)
-    return t.shape
+    rows, columns = t.shape
+    if rows >= 2 ** 31 or columns >= 2 ** 31:
+        _int32(what, max(rows, columns))
+    return rows, columns
 
 
 def _ptr(t: torch.Tensor | None):
@@ -72,48 +73,101 @@ def _refuse(name: str, status: int = -1):
     raise MoeError(name, status)
 
 
-@dataclasses.dataclass
+@functools.lru_cache(maxsize=256)
+def _losses_layout(T: int, E: int, top_k: int, B: int, seq: bool) -> tuple[int, ...]:
+    """Places of prob_sums, lse, counts, tokens, balance, z and the workspace in RouterLosses.buffer, in 4-byte words, each a
+    multiple of 64, and its words in all; the workspace's bytes."""
+    for v in (T, E, top_k, B):
+        _int32("losses", v)
+    st = MoeLosses(T, E, top_k, B, 256 if seq else None)
+    n = int(_function("moe_router_losses_workspace_bytes")(ctypes.byref(st)))
+    if n == 0:
+        _refuse("moe_router_losses_workspace_bytes")
+    up = lambda words: (words + 63) // 64 * 64
+    at = [0]
+    for words in (B * E, T, B * E, B, B, B, (n + 3) // 4):
+        at.append(at[-1] + up(words))
+    return (*at, n)
+
+
 class RouterLosses:
-    """Losses of the B sequences of a batch, with what their gradient reads (moe_losses). counts and tokens may hold the
-    sums over several batches or ranks when the gradient is asked for."""
-    balance: torch.Tensor    # fp32 [B]
-    z: torch.Tensor          # fp32 [B]
-    counts: torch.Tensor     # int32 [B, E] slots of every expert
-    tokens: torch.Tensor     # int32 [B] tokens that count
-    prob_sums: torch.Tensor  # fp32 [B, E]
-    lse: torch.Tensor        # fp32 [T]; -inf: the token does not count
-    top_k: int
-    seq: torch.Tensor | None = None  # int32 [B + 1], or None: one sequence of all tokens
+    """Losses of the B sequences of a batch, with what their gradient reads (moe_losses; filled by router_losses). The
+    arrays share one allocation, of which they are views. counts and tokens may be added to (sums over several batches or
+    ranks) before the gradient is asked for; they are changed in place, not replaced."""
+
+    def __init__(self, T: int, E: int, top_k: int, seq: torch.Tensor | None = None, device="cuda"):
+        if seq is not None and (seq.dim() != 1 or seq.shape[0] < 2):
+            raise ValueError(f"seq: shape {tuple(seq.shape)}, expected [B + 1], B > 0")
+        self.T, self.E, self.top_k = T, E, top_k
+        self.B = 1 if seq is None else seq.shape[0] - 1
+        self._at = at = _losses_layout(T, E, top_k, self.B, seq is not None)
+        self.buffer = torch.empty(at[7], dtype=torch.float32, device=device)
+        self.device = self.buffer.device
+        if seq is not None:
+            _ask("seq", seq, (self.B + 1,), torch.int32, self.device)
+        self.seq = seq  # int32 [B + 1], or None: one sequence of all tokens
+        self.filled = False  # by router_losses
+        base = self.buffer.data_ptr()
+        self.struct = MoeLosses(T, E, top_k, self.B, _ptr(seq), base + 4 * at[4], base + 4 * at[5], base + 4 * at[2], base + 4 * at[3],
+                                base, base + 4 * at[1])
+        self.workspace = base + 4 * at[6]
+        self.ref = ctypes.byref(self.struct)
 
     @staticmethod
     def empty(T: int, E: int, top_k: int, seq: torch.Tensor | None = None, device="cuda") -> "RouterLosses":
-        if seq is not None and seq.dim() != 1:
-            raise ValueError(f"seq: shape {tuple(seq.shape)}, expected [B + 1]")
-        B = 1 if seq is None else seq.shape[0] - 1
-        if B < 1:
-            raise ValueError("seq: no sequence")
-        f = lambda *shape: torch.empty(shape, dtype=torch.float32, device=device)
-        i = lambda *shape: torch.empty(shape, dtype=torch.int32, device=device)
-        return RouterLosses(f(B), f(B), i(B, E), i(B), f(B, E), f(T), top_k, seq)
+        return RouterLosses(T, E, top_k, seq, device)
 
-    def struct(self, T: int, E: int, device: torch.device) -> MoeLosses:
-        B = self.balance.shape[0] if self.balance.dim() == 1 else -1
-        if self.seq is not None:
-            _ask("seq", self.seq, (B + 1,), torch.int32, device)
-        elif B != 1:
-            raise ValueError(f"losses of {B} sequences without seq")
-        f, i = torch.float32, torch.int32
-        at = [_ask("losses", t, shape, dtype, device).data_ptr() for t, shape, dtype in (
-            (self.balance, (B,), f), (self.z, (B,), f), (self.counts, (B, E), i), (self.tokens, (B,), i),
-            (self.prob_sums, (B, E), f), (self.lse, (T,), f))]
-        return MoeLosses(T, E, self.top_k, B, _ptr(self.seq), *at)
+    @_once
+    def pointer(self):
+        return ctypes.pointer(self.struct)
+
+    @_once
+    def _words(self) -> torch.Tensor:
+        return self.buffer.view(torch.int32)
+
+    @_once
+    def balance(self) -> torch.Tensor:
+        """fp32 [B]"""
+        return self.buffer.as_strided((self.B,), (1,), self._at[4])
+
+    @_once
+    def z(self) -> torch.Tensor:
+        """fp32 [B]"""
+        return self.buffer.as_strided((self.B,), (1,), self._at[5])
+
+    @_once
+    def counts(self) -> torch.Tensor:
+        """int32 [B, E]: slots of every expert."""
+        return self._words.as_strided((self.B, self.E), (self.E, 1), self._at[2])
+
+    @_once
+    def tokens(self) -> torch.Tensor:
+        """int32 [B]: tokens that count."""
+        return self._words.as_strided((self.B,), (1,), self._at[3])
+
+    @_once
+    def prob_sums(self) -> torch.Tensor:
+        """fp32 [B, E]"""
+        return self.buffer.as_strided((self.B, self.E), (self.E, 1), 0)
+
+    @_once
+    def lse(self) -> torch.Tensor:
+        """fp32 [T]; -inf: the token does not count."""
+        return self.buffer.as_strided((self.T,), (1,), self._at[1])
+
+    def check(self):
+        """Somebody put another tensor in an array's place: the library would not see it."""
+        own = self.__dict__
+        for name, at in (("counts", 2), ("tokens", 3), ("lse", 1)):
+            if name in own and own[name].data_ptr() != self.buffer.data_ptr() + 4 * self._at[at] and own[name].numel():
+                raise ValueError(f"losses: {name} was replaced; it is changed in place")
 
 
 def router_losses(logits: torch.Tensor, topk_idx: torch.Tensor, valid: torch.Tensor | None = None,
                   seq: torch.Tensor | None = None, out: RouterLosses | None = None) -> RouterLosses:
     """logits [T, E] (fp32 or bf16) and topk_idx int32 [T, k] -> RouterLosses (moe_router_losses). valid: bool or uint8 [T],
     the tokens that count (default: all). seq: int32 [B + 1] starts of packed sequences, each with losses of its own
-    (default: one sequence). `out`: losses of the same sizes to fill again, with its own seq unless one is given."""
+    (default: one sequence). `out`: losses of the same sizes to fill again, which hold their own seq."""
     T, E = _matrix("logits", logits)
     k = _matrix("topk_idx", topk_idx)[1]
     dev = logits.device
@@ -122,16 +176,13 @@ def router_losses(logits: torch.Tensor, topk_idx: torch.Tensor, valid: torch.Ten
     if valid is not None:
         _ask("valid", valid, (T,), (torch.bool, torch.uint8), dev)
     if out is None:
-        out = RouterLosses.empty(T, E, k, seq, dev)
-    elif seq is not None:
-        out.seq = seq
-    if out.top_k != k:
-        raise ValueError(f"out: losses of {out.top_k} slots a token, expected {k}")
-    st = out.struct(T, E, dev)
-    n = int(_function("moe_router_losses_workspace_bytes")(ctypes.byref(st)))
-    workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-    _call("moe_router_losses", dev, ctypes.byref(st), DTYPES[logits.dtype], logits.data_ptr(), topk_idx.data_ptr(), _ptr(valid),
-          _ptr(workspace), n)
+        out = RouterLosses(T, E, k, seq, dev)
+    elif (out.T, out.E, out.top_k, out.device) != (T, E, k, dev) or (seq is not None and seq is not out.seq):
+        raise ValueError("out: losses of other sizes, sequences or on another device")
+    out.check()
+    _call("moe_router_losses", dev, out.ref, DTYPES[logits.dtype], logits.data_ptr(), topk_idx.data_ptr(), _ptr(valid),
+          out.workspace, out._at[8])
+    out.filled = True
     return out
 
 
@@ -156,13 +207,15 @@ def logits_grad(logits: torch.Tensor, topk_idx: torch.Tensor, losses: RouterLoss
             _ask(what, t, (T, k), torch.float32, dev)
     l = None
     if losses is not None:
-        if losses.top_k != k:
-            raise ValueError(f"losses of {losses.top_k} slots a token, expected {k}")
-        st = losses.struct(T, E, dev)
-        l = ctypes.pointer(st)
+        if (losses.T, losses.E, losses.top_k, losses.device) != (T, E, k, dev):
+            raise ValueError("losses: of other sizes or on another device")
+        if not losses.filled:
+            raise ValueError("losses that router_losses has not filled")
+        losses.check()
+        l = losses.pointer
         for what, t in (("d_balance", d_balance), ("d_z", d_z)):
             if t is not None:
-                _ask(what, t, (st.B,), torch.float32, dev)
+                _ask(what, t, (losses.B,), torch.float32, dev)
     out = _out("out", out, (T, E), torch.float32, dev)
     a = MoeLogitsGradArgs(T, E, k, DTYPES[logits.dtype], l, logits.data_ptr(), _ptr(d_balance), _ptr(d_z), topk_idx.data_ptr(),
                           _ptr(topk_w), _ptr(d_topk_w), out.data_ptr())

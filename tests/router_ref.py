@@ -114,10 +114,10 @@ def close(got, want, bound, what):
     """got within bound of want; NaN and infinities in the same places, where a value past fp32's largest (by half a step or
     more) is an infinity in fp32."""
     got, want, bound = np.asarray(got, np.float64), np.asarray(want, np.float64), np.broadcast_to(bound, np.shape(want))
-    want = np.where(np.abs(want) >= 2.0 ** 128 * (1 - U24 / 2), np.sign(want) * INF, want)
+    want = np.where(np.abs(want) >= 2.0 ** 128 * (1 - U24 / 2), np.copysign(INF, want), want)
     fine = np.isfinite(want)
     assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(got[~fine & ~np.isnan(want)], want[~fine & ~np.isnan(want)]), what
-    err = np.abs(got - want)[fine]
+    err = np.abs(got[fine] - want[fine])
     assert (err <= bound[fine]).all(), f"{what}: off by {err.max()}, at most {(err / np.maximum(bound[fine], 1e-300)).max()} of the bound"
 
 

@@ -246,7 +246,7 @@ def test_summed_counts_of_several_batches():
     x, idx = rng.standard_normal((90, 40)).astype(np.float32), routing(rng, 90, 40, 2)
     l = moe.router_losses(dev(x), dev(idx))
     other = moe.router_losses(dev(x[::-1].copy()), dev(routing(rng, 90, 40, 2)))
-    l.counts += other.counts
+    l.counts.add_(other.counts)
     l.tokens += other.tokens
     got = {n: num(getattr(l, n)) for n in ("counts", "tokens", "lse")}
     d = moe.logits_grad(dev(x), dev(idx), l, d_balance=torch.ones(1, device="cuda"))
@@ -353,7 +353,7 @@ def test_training_step():
         counts = torch.bincount(idx64[seq[b]:seq[b + 1]].flatten(), minlength=E).double()
         balance = E / (k * n * n) * (counts * torch.softmax(r, 1).sum(0)).sum()
         z = (torch.logsumexp(r, 1) ** 2).mean()
-        assert abs(float(l.balance[b]) - float(balance)) <= 1e-5 * float(balance) and abs(float(l.z[b]) - float(z)) <= 1e-5 * float(z)
+        assert abs(float(l.balance[b]) - balance.item()) <= 1e-5 * balance.item() and abs(float(l.z[b]) - z.item()) <= 1e-5 * z.item()
         loss = loss + 0.5 * balance + 0.1 * z
     loss.backward()
     # each step is within some hundred roundings of its terms' size; the terms of a gradient here are about as large as the
