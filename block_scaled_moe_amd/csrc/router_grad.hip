@@ -4,12 +4,13 @@
 //
 // Both are products of a fp32 matrix with a bf16 one whose rows run along the reduction, so one kernel does both. The
 // fp32 one, which is the smaller, goes through the bf16 MFMA in pieces: its value is the sum of its upper 8 bits, the next 8
-// and the last 8, each a bf16 exactly. split_kernel cuts it once into the order in which the MFMA takes it, for either
-// product: tiles of 128 rows, steps of 32 of the reduction, pieces, 16 rows, lanes; a tile's step is one contiguous copy.
+// and the last 8, each a bf16 exactly. Where many column tiles share it, split_kernel cuts it once into the order in which
+// the MFMA takes it, for either product: tiles of 128 rows, steps of 32 of the reduction, pieces, 16 rows, lanes; a tile's
+// step is one contiguous copy. Where few do, a launch costs more than cutting it in every workgroup.
 //
-// product_kernel: 128 rows x 256 columns a workgroup, 4 waves of 64 x 128, two workgroups a CU, a step of 32 of the
-// reduction in one LDS buffer while the next one arrives in the other. The bf16 matrix comes as it is and is turned over
-// by the transposing LDS read (4 rows x 16 columns per 16 lanes), the same operand for all pieces.
+// product_kernel: BM rows x 256 columns a workgroup of 4 waves, two workgroups a CU, a step of 32 of the reduction in one LDS
+// buffer while the next one arrives in the other. The bf16 matrix comes as it is and is turned over by the transposing
+// LDS read (4 rows x 16 columns per 16 lanes), the same operand for all pieces.
 #include "block_mma.h"
 #include "router_internal.h"
 
@@ -23,7 +24,7 @@ using namespace block;
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 
-constexpr int kThreads = 256, kBM = 128, kBN = 256, kStep = 32;
+constexpr int kThreads = 256, kBM = 128, kFusedBM = 64, kBN = 256, kStep = 32;
 
 // v in pieces of bf16: cut off at 8 bits each, which nothing can overflow; the last of two is rounded
 template <int P>
@@ -40,9 +41,10 @@ __device__ __forceinline__ void split(float v, uint16_t (&out)[P]) {
     }
 }
 
-// One lane's operand of a 16 x 32 piece: row r of 16, values k = 4 g .. 4 g + 3 and 16 + 4 g .. 16 + 4 g + 3
+// One lane's operand of a 16 x 32 piece: row r of 16, values k = 4 g .. 4 g + 3 and 16 + 4 g .. 16 + 4 g + 3; the pieces lie
+// `stride` operands apart.
 template <int P>
-__device__ __forceinline__ void write_operand(const float (&v)[8], u32x4 *dst, int lane) {
+__device__ __forceinline__ void write_operand(const float (&v)[8], u32x4 *dst, int lane, int stride = 8) {
     uint16_t x[8][P];
 #pragma unroll
     for (int i = 0; i < 8; ++i) split<P>(v[i], x[i]);
@@ -51,7 +53,7 @@ __device__ __forceinline__ void write_operand(const float (&v)[8], u32x4 *dst, i
         u32x4 o;
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = (uint32_t)x[2 * i][p] | (uint32_t)x[2 * i + 1][p] << 16;
-        dst[p * 8 * 64 + lane] = o;
+        dst[p * stride * 64 + lane] = o;
     }
 }
 
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const float *__restrict
 
 // One product: out[m][n] = sum over k of a[m][k] b[k][n], M x D, K of the reduction.
 struct Product {
-    const u32x4 *a;         // operands, tiles x steps
+    const u32x4 *a;         // operands, tiles x steps; or (not cut beforehand) NULL
     const uint16_t *b;      // bf16 [K][D]
     void *out;              // [M][D] of out_dtype, or fp32 [splits][M][D]
     float *bias;            // fp32 [splits][M] sums of a's rows, or NULL
@@ -109,17 +111,23 @@ struct Product {
 };
 struct ProductArgs {
     Product w, h;
-    int32_t D, n_tiles;
+    const float *g;
+    int32_t T, E, D, n_tiles;
     int32_t w_items, h_items;
 };
 
-template <int P>
-__device__ __forceinline__ void product(const Product &p, int D, int n_tiles, int item, uint8_t *lds) {
-    constexpr int kA = P * 8192, kB = kStep * kBN * 2, kBuffer = kA + kB;
+// OUTER: a's rows run along g's columns (dwr); CUT: a was cut beforehand
+template <int P, int BM, bool OUTER, bool CUT>
+__device__ __forceinline__ void product(const ProductArgs &args, const Product &p, int item, uint8_t *lds) {
+    constexpr int kSub = BM / 16;                        // pieces of 16 rows
+    constexpr int kWM = BM / 64, kJ = 16 / (4 / kWM);    // row waves; column tiles of 16 a wave
+    constexpr int kA = P * kSub * 1024, kB = kStep * kBN * 2, kBuffer = kA + kB;
+    static_assert(!CUT || BM == kBM, "tiles of split_kernel");
+    const int D = args.D, n_tiles = args.n_tiles, T = args.T, E = args.E;
     const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
-    const int i16 = lane & 15, g = lane >> 4, wm = wave >> 1, wn = wave & 1;
+    const int i16 = lane & 15, g = lane >> 4, wm = wave / (4 / kWM), wn = wave % (4 / kWM);
     // items of one part of the reduction together, its row tiles innermost: they share b's columns
-    const int split = item / (p.m_tiles * n_tiles), rest = item % (p.m_tiles * n_tiles);
+    const int part = item / (p.m_tiles * n_tiles), rest = item % (p.m_tiles * n_tiles);
     int mt, nt;
     if (p.splits > 1 || p.m_tiles < n_tiles) {
         mt = rest % p.m_tiles;
@@ -128,9 +136,9 @@ __device__ __forceinline__ void product(const Product &p, int D, int n_tiles, in
         mt = rest / n_tiles;
         nt = rest % n_tiles;
     }
-    const int s0 = split * p.steps_per_split, s1 = min(s0 + p.steps_per_split, p.steps);
+    const int s0 = part * p.steps_per_split, s1 = min(s0 + p.steps_per_split, p.steps);
     const int n0 = nt * kBN;
-    const u32x4 *a = p.a + (int64_t)mt * p.steps * (P * 512);
+    const u32x4 *a = CUT ? p.a + (int64_t)mt * p.steps * (kA / 16) : nullptr;
     const uint32_t base = lds_address(lds) + wave * 1024;
 
     // copy c of 16 of b's step: rows 2 c and 2 c + 1 of 512 bytes; the 32-byte pieces of a row are swapped by the row's
@@ -143,9 +151,11 @@ __device__ __forceinline__ void product(const Product &p, int D, int n_tiles, in
     }
     auto copy = [&](int s) __attribute__((always_inline)) {
         const uint32_t dst = base + (s & 1) * kBuffer;
-        const uint8_t *src = reinterpret_cast<const uint8_t *>(a + (int64_t)s * (P * 512));
+        if constexpr (CUT) {
+            const uint8_t *src = reinterpret_cast<const uint8_t *>(a + (int64_t)s * (kA / 16));
 #pragma unroll
-        for (int j = 0; j < 2 * P; ++j) copy_to_lds(src + (wave + 4 * j) * 1024, lane * 16, dst + j * 4096);
+            for (int j = 0; j < P * kSub / 4; ++j) copy_to_lds(src + (wave + 4 * j) * 1024, lane * 16, dst + j * 4096);
+        }
         const uint8_t *rows = reinterpret_cast<const uint8_t *>(p.b) + (int64_t)s * kStep * D * 2;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -153,34 +163,59 @@ __device__ __forceinline__ void product(const Product &p, int D, int n_tiles, in
             copy_to_lds(rows, (uint32_t)r * (uint32_t)D * 2 + b_col, dst + kA + j * 4096);
         }
     };
+    // not cut beforehand: the operands that this lane writes, of rows 16 (wave + 4 i) + i16
+    constexpr int kOwn = CUT ? 1 : kSub / 4;
+    float v[kOwn][8];
+    auto load = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            const int m = mt * BM + 16 * (wave + 4 * i) + i16;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int k = s * kStep + (j >> 2) * 16 + 4 * g + (j & 3);
+                const int row = OUTER ? k : m, col = OUTER ? m : k;
+                v[i][j] = row < T && col < E ? args.g[(int64_t)row * E + col] : 0.0f;
+            }
+        }
+    };
 
-    f4 acc[4][8];
+    f4 acc[4][kJ];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j] = (f4){0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < kJ; ++j) acc[i][j] = (f4){0.0f, 0.0f, 0.0f, 0.0f};
     f4 bias[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) bias[i] = (f4){0.0f, 0.0f, 0.0f, 0.0f};
-    const bool want_bias = p.bias && nt == 0 && wn == 0;
+    const bool want_bias = OUTER && p.bias && nt == 0 && wn == 0;
 
-    if (s0 < s1) copy(s0);
+    if (s0 < s1) {
+        copy(s0);
+        if constexpr (!CUT) load(s0);
+    }
     for (int s = s0; s < s1; ++s) {
+        uint8_t *buf = lds + (s & 1) * kBuffer;
+        if constexpr (!CUT) {
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) write_operand<P>(v[i], reinterpret_cast<u32x4 *>(buf) + (wave + 4 * i) * 64, lane, kSub);
+        }
         wait_copies<0>();
         lds_barrier();
-        if (s + 1 < s1) copy(s + 1);
-        const uint8_t *buf = lds + (s & 1) * kBuffer;
+        if (s + 1 < s1) {
+            copy(s + 1);
+            if constexpr (!CUT) load(s + 1);
+        }
         bf8 x[P][4];
 #pragma unroll
         for (int q = 0; q < P; ++q)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                x[q][i] = __builtin_bit_cast(bf8, *reinterpret_cast<const u32x4 *>(buf + (q * 8 + 4 * wm + i) * 1024 + lane * 16));
+                x[q][i] = __builtin_bit_cast(bf8, *reinterpret_cast<const u32x4 *>(buf + (q * kSub + 4 * wm + i) * 1024 + lane * 16));
         const int r = 4 * g + (i16 >> 2);
         const uint8_t *row = buf + kA + r * 512 + (i16 & 3) * 8;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint8_t *at = row + ((8 * wn + j) ^ (r & 7)) * 32;
+        for (int j = 0; j < kJ; ++j) {
+            const uint8_t *at = row + ((kJ * wn + j) ^ (r & 7)) * 32;
             const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4 *)at);
             const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4 *)(at + 16 * 512));
             const bf8 y = __builtin_bit_cast(bf8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -200,34 +235,35 @@ __device__ __forceinline__ void product(const Product &p, int D, int n_tiles, in
 
     // accumulator v of (i, j): row 16 i + i16, column 16 j + 4 g + v of the wave's
     const bool narrow = p.splits == 1 && p.out_dtype == MOE_DT_BF16;
+    const int c0 = n0 + 16 * kJ * wn;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int m = mt * kBM + 64 * wm + 16 * i + i16;
-        if (want_bias && g == 0 && m < p.M) p.bias[(int64_t)split * p.M + m] = bias[i][0];
-        const int64_t at = ((int64_t)split * p.M + m) * D + n0 + 128 * wn;
+        const int m = mt * BM + 64 * wm + 16 * i + i16;
+        if (want_bias && g == 0 && m < p.M) p.bias[(int64_t)part * p.M + m] = bias[i][0];
+        const int64_t at = ((int64_t)part * p.M + m) * D + c0;
         if (narrow) {
             uint16_t *o = static_cast<uint16_t *>(p.out) + at;
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {
+            for (int j = 0; j < kJ; j += 2) {
                 const uint2 c = make_uint2(bf16_pair(acc[i][j][0], acc[i][j][1]), bf16_pair(acc[i][j][2], acc[i][j][3]));
                 const uint2 d = make_uint2(bf16_pair(acc[i][j + 1][0], acc[i][j + 1][1]), bf16_pair(acc[i][j + 1][2], acc[i][j + 1][3]));
                 const u32x4 v = swap_groups(c, d);
                 const int col = 16 * (j + (g & 1)) + 8 * (g >> 1);
-                if (m < p.M && n0 + 128 * wn + col < D) *reinterpret_cast<u32x4 *>(o + col) = v;
+                if (m < p.M && c0 + col < D) *reinterpret_cast<u32x4 *>(o + col) = v;
             }
         } else {
             float *o = static_cast<float *>(p.out) + at;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (m < p.M && n0 + 128 * wn + 16 * j < D) *reinterpret_cast<f4 *>(o + 16 * j + 4 * g) = acc[i][j];
+            for (int j = 0; j < kJ; ++j)
+                if (m < p.M && c0 + 16 * j < D) *reinterpret_cast<f4 *>(o + 16 * j + 4 * g) = acc[i][j];
         }
     }
 }
 
-template <int PH, int PW>
+template <int PH, int PW, bool CUT>
 __global__ void __launch_bounds__(kThreads, 2) product_kernel(const ProductArgs a) {
-    constexpr int P = PH > PW ? PH : PW;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * (P * 8192 + kStep * kBN * 2)];
+    constexpr int P = PH > PW ? PH : PW, BM = CUT ? kBM : kFusedBM;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * (P * BM * 64 + kStep * kBN * 2)];
     // each XCD (workgroups 8 apart) takes a range of either product's items
     auto mine = [](int b, int items) __attribute__((always_inline)) {
         const int per = (items + 7) / 8, x = b & 7, i = b >> 3;
@@ -238,12 +274,12 @@ __global__ void __launch_bounds__(kThreads, 2) product_kernel(const ProductArgs 
     if ((int)blockIdx.x < w_groups) {
         if constexpr (PW > 0) {
             const int item = mine(blockIdx.x, a.w_items);
-            if (item >= 0) product<PW>(a.w, a.D, a.n_tiles, item, lds);
+            if (item >= 0) product<PW, BM, true, CUT>(a, a.w, item, lds);
         }
     } else {
         if constexpr (PH > 0) {
             const int item = mine(blockIdx.x - w_groups, a.h_items);
-            if (item >= 0) product<PH>(a.h, a.D, a.n_tiles, item, lds);
+            if (item >= 0) product<PH, BM, false, CUT>(a, a.h, item, lds);
         }
     }
 }
@@ -251,25 +287,33 @@ __global__ void __launch_bounds__(kThreads, 2) product_kernel(const ProductArgs 
 // Sums of the parts of dwr's and dbias's reduction, in their order; no parts: zeros (no tokens).
 __global__ void __launch_bounds__(256) parts_kernel(const float *__restrict__ parts, const float *__restrict__ bias_parts,
                                                     int32_t splits, int32_t E, int64_t n, void *out, int32_t dtype, float *dbias) {
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2;
     if (out && i < n) {
-        f4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-        for (int k = 0; k < splits; ++k) s += *reinterpret_cast<const f4 *>(parts + k * n + i);
-        if (dtype == MOE_DT_BF16)
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + i) = make_uint2(bf16_pair(s[0], s[1]), bf16_pair(s[2], s[3]));
-        else
-            *reinterpret_cast<f4 *>(static_cast<float *>(out) + i) = s;
+        float s[2] = {0.0f, 0.0f};
+#pragma unroll 8
+        for (int k = 0; k < splits; ++k) {
+            const f2 v = *reinterpret_cast<const f2 *>(parts + k * n + i);
+            s[0] += v[0];
+            s[1] += v[1];
+        }
+        if (dtype == MOE_DT_BF16) *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(out) + i) = bf16_pair(s[0], s[1]);
+        else *reinterpret_cast<f2 *>(static_cast<float *>(out) + i) = (f2){s[0], s[1]};
     }
     if (dbias) {
         const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
         if (e < E) {
             float s = 0.0f;
+#pragma unroll 8
             for (int k = 0; k < splits; ++k) s += bias_parts[(int64_t)k * E + e];
             dbias[e] = s;
         }
     }
 }
+
+// Values of g times column tiles from which on g is cut beforehand. Cutting takes a launch and 8 to 18 us, cutting it anew for every
+// column tile 1.4 us for each 2^20 of these: 5003 x 61, 1088 columns (1.5 million) 25 us in the workgroups, 33 us beforehand;
+// 16384 x 384, 4096 columns (101 million) 356 and 215 us.
+constexpr int64_t kCutFrom = 1 << 23;
 
 }  // namespace
 
@@ -277,12 +321,15 @@ RouteBackwardPlan route_backward_plan(const moe_route_backward_args &a) {
     RouteBackwardPlan p{};
     if (a.dh) p.planes_h = a.dh_dtype == MOE_DT_BF16 ? 2 : 3;
     if (a.dwr || a.dbias) p.planes_w = (a.dwr && a.dwr_dtype == MOE_DT_FP32) || a.dbias ? 3 : 2;
-    p.t_tiles = (a.T + kBM - 1) / kBM;
-    p.e_tiles = (a.E + kBM - 1) / kBM;
+    const int64_t n_tiles = (a.D + kBN - 1) / kBN;
+    p.cut = (int64_t)a.T * a.E * n_tiles >= kCutFrom;
+    const int32_t bm = p.cut ? kBM : kFusedBM;
+    p.t_tiles = (a.T + bm - 1) / bm;
+    p.e_tiles = (a.E + bm - 1) / bm;
     p.t_steps = (a.T + kStep - 1) / kStep;
     p.e_steps = (a.E + kStep - 1) / kStep;
     // dwr has few tiles: its reduction is cut so that they fill the CUs once, in parts of 256 tokens at least
-    const int64_t tiles = (int64_t)p.e_tiles * ((a.D + kBN - 1) / kBN);
+    const int64_t tiles = p.e_tiles * n_tiles;
     p.splits = 1;
     if (p.planes_w && tiles < 256) {
         const int64_t most = p.t_steps / 8;
@@ -297,10 +344,10 @@ RouteBackwardPlan route_backward_plan(const moe_route_backward_args &a) {
         off += (bytes + 255) & ~(size_t)255;
         return at;
     };
-    p.a_h = take((size_t)p.planes_h * 8192 * (size_t)p.t_tiles * p.e_steps);
-    p.a_w = take((size_t)p.planes_w * 8192 * (size_t)p.e_tiles * p.t_steps);
+    p.a_h = take(p.cut ? (size_t)p.planes_h * 8192 * (size_t)p.t_tiles * p.e_steps : 0);
+    p.a_w = take(p.cut ? (size_t)p.planes_w * 8192 * (size_t)p.e_tiles * p.t_steps : 0);
     p.parts = take(p.splits > 1 && a.dwr ? 4 * (size_t)p.splits * a.E * (size_t)a.D : 0);
-    p.bias_parts = take(a.dbias ? 4 * (size_t)p.splits * a.E : 0);
+    p.bias_parts = take(p.splits > 1 && a.dbias ? 4 * (size_t)p.splits * a.E : 0);
     p.total = off > 0 ? off : 256;
     return p;
 }
@@ -309,12 +356,15 @@ hipError_t launch_route_backward(const moe_route_backward_args &a, const RouteBa
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
     u32x4 *a_h = reinterpret_cast<u32x4 *>(ws + p.a_h), *a_w = reinterpret_cast<u32x4 *>(ws + p.a_w);
     float *parts = reinterpret_cast<float *>(ws + p.parts), *bias_parts = reinterpret_cast<float *>(ws + p.bias_parts);
+    const bool parted = p.splits > 1 || a.T == 0;
     ProductArgs q{};
+    q.g = a.d_logits;
+    q.T = a.T;
+    q.E = a.E;
     q.D = a.D;
     q.n_tiles = (a.D + kBN - 1) / kBN;
     if (p.planes_w) {
-        // the bias alone takes the first column tile's workgroups, whose product is then not stored
-        q.w = {a_w, a.h, p.splits > 1 ? parts : a.dwr, a.dbias ? bias_parts : nullptr, a.E, a.T, a.dwr_dtype,
+        q.w = {a_w, a.h, parted ? parts : a.dwr, a.dbias && parted ? bias_parts : a.dbias, a.E, a.T, a.dwr_dtype,
                p.e_tiles, p.t_steps, p.splits, p.steps_per_split};
         q.w_items = p.e_tiles * q.n_tiles * p.splits;
     }
@@ -324,12 +374,16 @@ hipError_t launch_route_backward(const moe_route_backward_args &a, const RouteBa
     }
     auto run = [&](auto ph, auto pw) {
         constexpr int PH = decltype(ph)::value, PW = decltype(pw)::value;
-        // with experts as rows the last tile is filled up to 128
-        const unsigned e_blocks = (unsigned)(PW > 0 ? 4 * p.e_tiles : p.e_steps);
-        hipLaunchKernelGGL((split_kernel<PH, PW>), dim3((unsigned)p.t_tiles, e_blocks), dim3(kThreads), 0, s, a.d_logits,
-                           a.T, a.E, p.e_steps, p.t_steps, a_h, a_w);
         const unsigned grid = (unsigned)((q.w_items + 7) / 8 * 8 + (q.h_items + 7) / 8 * 8);
-        hipLaunchKernelGGL((product_kernel<PH, PW>), dim3(grid), dim3(kThreads), 0, s, q);
+        if (p.cut) {
+            // with experts as rows the last tile is filled up to 128
+            const unsigned e_blocks = (unsigned)(PW > 0 ? 4 * p.e_tiles : p.e_steps);
+            hipLaunchKernelGGL((split_kernel<PH, PW>), dim3((unsigned)p.t_tiles, e_blocks), dim3(kThreads), 0, s, a.d_logits,
+                               a.T, a.E, p.e_steps, p.t_steps, a_h, a_w);
+            hipLaunchKernelGGL((product_kernel<PH, PW, true>), dim3(grid), dim3(kThreads), 0, s, q);
+        } else {
+            hipLaunchKernelGGL((product_kernel<PH, PW, false>), dim3(grid), dim3(kThreads), 0, s, q);
+        }
     };
     using std::integral_constant;
     auto by_w = [&](auto ph) {
@@ -343,11 +397,10 @@ hipError_t launch_route_backward(const moe_route_backward_args &a, const RouteBa
         else if (p.planes_h == 2) by_w(integral_constant<int, 2>{});
         else by_w(integral_constant<int, 3>{});
     }
-    const bool parted = p.splits > 1 || a.T == 0;
-    if ((a.dwr && parted) || a.dbias) {
-        const int64_t n = (int64_t)a.E * a.D, threads = a.dwr && parted ? (n / 4 > a.E ? n / 4 : a.E) : a.E;
+    if (parted && a.dwr) {
+        const int64_t n = (int64_t)a.E * a.D, threads = n / 2;  // D >= 64: more than dbias has
         hipLaunchKernelGGL(parts_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, parts, bias_parts,
-                           a.T == 0 ? 0 : p.splits, a.E, n, parted ? a.dwr : nullptr, a.dwr_dtype, a.dbias);
+                           a.T == 0 ? 0 : p.splits, a.E, n, a.dwr, a.dwr_dtype, a.dbias);
     }
     return hipGetLastError();
 }

@@ -78,15 +78,19 @@ __device__ __forceinline__ bool find_run(const int32_t *seq, int32_t T, int32_t 
     int32_t lo = 0, hi = T;
     r.s = 0;
     if (seq) {
-        int32_t a = 0, b = B;  // the last sequence whose first run is not behind `run`
-        while (b - a > 1) {
-            const int32_t m = (a + b) >> 1;
-            if ((int64_t)(start_of(seq, m, T) >> log_rows) + m <= run) a = m;
-            else b = m;
+        // the last sequence whose first run is not behind `run`: a wave's lanes look at 64 of them at a time
+        int32_t a = 0, n = B;
+        for (;;) {
+            const int32_t step = (n + 63) / 64, at = a + (threadIdx.x & 63) * step;
+            const bool before = at < a + n && (int64_t)(start_of(seq, min(at, B), T) >> log_rows) + at <= run;
+            const int32_t last = max(__popcll(__ballot(before)), 1) - 1;
+            a += last * step;
+            if (step == 1) break;
+            n = min(step, n - last * step);
         }
-        r.s = a;
-        lo = start_of(seq, a, T);
-        hi = start_of(seq, a + 1, T);
+        r.s = __builtin_amdgcn_readfirstlane(a);
+        lo = start_of(seq, r.s, T);
+        hi = start_of(seq, r.s + 1, T);
     }
     const int64_t first = (int64_t)lo + ((run - ((lo >> log_rows) + r.s)) << log_rows);
     if (first < lo || first >= hi) return false;
@@ -105,7 +109,7 @@ struct LossArgs {
     int32_t *counts;    // [run][E]
     double *squares;    // [run]
     int32_t *tokens;    // [run]
-    double *parts;      // [B][ceil(E / 64)] of the balance loss
+    double *parts;      // [B][workgroups] of the balance loss
     uint32_t *arrived;  // [B] workgroups that have left their part
 };
 
@@ -126,8 +130,6 @@ __global__ void __launch_bounds__(kThreads) loss_kernel(const LossArgs a) {
         if (!ONE) return;
         r = {0, 0, 0};
     }
-    for (int e = t; e < kRow; e += kThreads) hist[e] = 0;
-    __syncthreads();
     f4 acc[NP];
 #pragma unroll
     for (int p = 0; p < NP; ++p) acc[p] = (f4){0.0f, 0.0f, 0.0f, 0.0f};
@@ -148,6 +150,8 @@ __global__ void __launch_bounds__(kThreads) loss_kernel(const LossArgs a) {
     };
     Row next;
     load(r.row0 + group, next);
+    for (int e = t; e < kRow; e += kThreads) hist[e] = 0;
+    __syncthreads();
     for (int row = r.row0 + group; row < r.row1; row += kThreads / L) {
         const Row x = next;
         load(row + kThreads / L, next);
@@ -233,18 +237,19 @@ __global__ void __launch_bounds__(kThreads) loss_kernel(const LossArgs a) {
     }
 }
 
-// The sums of 64 experts of one sequence over its runs, sixteen runs at a time; the workgroup that comes last for a
-// sequence adds the parts of its balance loss, in the order of the experts.
-constexpr int kJoinExperts = 64, kJoinRuns = 16;
-__global__ void __launch_bounds__(kJoinExperts *kJoinRuns) join_kernel(const LossArgs a) {
-    __shared__ double sum[kJoinRuns][kJoinExperts];
-    __shared__ int32_t count[kJoinRuns][kJoinExperts];
-    __shared__ double squares[kJoinRuns];
-    __shared__ int32_t tokens[kJoinRuns];
-    const int E = a.l.E, ne = (E + kJoinExperts - 1) / kJoinExperts;
-    const int s = blockIdx.x / ne, eb = blockIdx.x % ne;
-    const int lane = threadIdx.x % kJoinExperts, w = threadIdx.x / kJoinExperts;
-    const int e = eb * kJoinExperts + lane;
+// The sums of EXPERTS experts of one sequence over its runs, 1024 / EXPERTS runs at a time. Where that is not all of them, the
+// workgroup that comes last for a sequence adds the parts of its balance loss, in the order of the experts.
+constexpr int kJoinThreads = 1024, kJoinWaves = kJoinThreads / 64;
+template <int EXPERTS>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const LossArgs a) {
+    constexpr int kRunsAtATime = kJoinThreads / EXPERTS;
+    __shared__ double sum[kJoinWaves][EXPERTS];
+    __shared__ int32_t count[kJoinWaves][EXPERTS];
+    __shared__ double squares[kJoinWaves];
+    __shared__ int32_t tokens[kJoinWaves];
+    const int E = a.l.E, ne = (E + EXPERTS - 1) / EXPERTS;
+    const int s = blockIdx.x / ne, eb = blockIdx.x % ne, t = threadIdx.x;
+    const int e = eb * EXPERTS + t % EXPERTS;
     int32_t lo = 0, hi = a.l.T;
     if (a.l.seq) {
         lo = start_of(a.l.seq, s, a.l.T);
@@ -256,42 +261,54 @@ __global__ void __launch_bounds__(kJoinExperts *kJoinRuns) join_kernel(const Los
     int32_t c = 0, m = 0;
     if (e < E) {
 #pragma unroll 8
-        for (int i = w; i < n; i += kJoinRuns) {
+        for (int i = t / EXPERTS; i < n; i += kRunsAtATime) {
             p += a.sums[(first + i) * E + e];
             c += a.counts[(first + i) * E + e];
         }
     }
-    for (int i = w + kJoinRuns * lane; i < n; i += kJoinRuns * kJoinExperts) {
+    for (int i = t; i < n; i += kJoinThreads) {
         z += a.squares[first + i];
         m += a.tokens[first + i];
     }
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) {
+        if (off >= EXPERTS) {
+            p += __shfl_xor(p, off);
+            c += __shfl_xor(c, off);
+        }
         z += __shfl_xor(z, off);
         m += __shfl_xor(m, off);
     }
-    sum[w][lane] = p;
-    count[w][lane] = c;
-    if (lane == 0) {
-        squares[w] = z;
-        tokens[w] = m;
+    if (t % 64 < EXPERTS) {
+        sum[t / 64][t % 64] = p;
+        count[t / 64][t % 64] = c;
+    }
+    if (t % 64 == 0) {
+        squares[t / 64] = z;
+        tokens[t / 64] = m;
     }
     __syncthreads();
-    if (w != 0) return;
-    for (int i = 1; i < kJoinRuns; ++i) {
-        p += sum[i][lane];
-        c += count[i][lane];
-        z += squares[i];  // lane 0's
-        m += tokens[i];
-    }
-    if (e < E) {
+    if (t >= 64) return;
+    double part = 0.0;
+    if (t < EXPERTS && e < E) {
+        p = sum[0][t];
+        c = count[0][t];
+#pragma unroll
+        for (int i = 1; i < kJoinWaves; ++i) {
+            p += sum[i][t];
+            c += count[i][t];
+        }
         a.l.prob_sums[(int64_t)s * E + e] = (float)p;
         a.l.counts[(int64_t)s * E + e] = c;
+        part = p * c;
     }
-    double part = e < E ? p * c : 0.0;
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) part += __shfl_xor(part, off);
-    if (lane != 0) return;
+    if (t != 0) return;
+    for (int i = 1; i < kJoinWaves; ++i) {
+        z += squares[i];
+        m += tokens[i];
+    }
     if (eb == 0) {
         a.l.tokens[s] = m;
         a.l.z[s] = m ? (float)(z / m) : 0.0f;
@@ -302,6 +319,7 @@ __global__ void __launch_bounds__(kJoinExperts *kJoinRuns) join_kernel(const Los
         const uint32_t before = __hip_atomic_fetch_add(a.arrived + s, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
         if (before + 1 != (uint32_t)ne) return;
         part = 0.0;
+#pragma unroll 8
         for (int i = 0; i < ne; ++i) part += __hip_atomic_load(parts + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     a.l.balance[s] = m ? (float)(part * E / ((double)a.l.top_k * m * m)) : 0.0f;
@@ -325,23 +343,6 @@ __global__ void __launch_bounds__(kGradThreads) logits_grad_kernel(const GradArg
     const int E = g.a.E, k = g.a.top_k;
     Run r;
     if (!find_run(LOSS ? g.l.seq : nullptr, g.a.T, LOSS ? g.l.B : 1, g.log_rows, blockIdx.x, r)) return;
-    f4 f[NP];
-    float b = 0.0f;
-    if constexpr (LOSS) {
-        const int32_t n = g.l.tokens[r.s];
-        float a = 0.0f;
-        if (n != 0) {
-            if (g.a.d_balance) a = (float)((double)g.a.d_balance[r.s] * E / ((double)k * n * n));
-            if (g.a.d_z) b = (float)(2.0 * (double)g.a.d_z[r.s] / n);
-        }
-#pragma unroll
-        for (int p = 0; p < NP; ++p)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int e = 4 * (p * L + lane) + i;
-                f[p][i] = e < E && g.a.d_balance ? a * (float)g.l.counts[(int64_t)r.s * E + e] : 0.0f;
-            }
-    }
     if constexpr (GATE) {
 #pragma unroll
         for (int p = 0; p < NP; ++p) *reinterpret_cast<f4 *>(&gate[group][4 * (p * L + lane)]) = (f4){0.0f, 0.0f, 0.0f, 0.0f};
@@ -368,6 +369,23 @@ __global__ void __launch_bounds__(kGradThreads) logits_grad_kernel(const GradArg
     };
     Row next;
     load(r.row0 + group, next);
+    f4 f[NP];
+    float b = 0.0f;
+    if constexpr (LOSS) {
+        const int32_t n = g.l.tokens[r.s];
+        float a = 0.0f;
+        if (n != 0) {
+            if (g.a.d_balance) a = (float)((double)g.a.d_balance[r.s] * E / ((double)k * n * n));
+            if (g.a.d_z) b = (float)(2.0 * (double)g.a.d_z[r.s] / n);
+        }
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = 4 * (p * L + lane) + i;
+                f[p][i] = e < E && g.a.d_balance ? a * (float)g.l.counts[(int64_t)r.s * E + e] : 0.0f;
+            }
+    }
     for (int row = r.row0 + group; row < r.row1; row += kGroups) {
         const Row x = next;
         load(row + kGroups, next);
@@ -467,7 +485,7 @@ LossPlan loss_plan(int32_t T, int32_t E, int32_t B) {
     p.counts = take(4 * (size_t)p.runs.n * E);
     p.squares = take(8 * (size_t)p.runs.n);
     p.tokens = take(4 * (size_t)p.runs.n);
-    p.parts = take(8 * (size_t)B * ((E + kJoinExperts - 1) / kJoinExperts));
+    p.parts = take(8 * (size_t)B * ((E + 15) / 16));
     p.arrived = take(4 * (size_t)B);
     p.total = off > 0 ? off : 256;
     return p;
@@ -504,15 +522,17 @@ hipError_t launch_router_losses(const moe_losses &l, int32_t dtype, const void *
         }
     });
     if (!one) {
-        const int64_t ne = (l.E + kJoinExperts - 1) / kJoinExperts;
-        hipLaunchKernelGGL(join_kernel, dim3((unsigned)(l.B * ne)), dim3(kJoinExperts * kJoinRuns), 0, s, a);
+        // 16 experts a workgroup read the runs in fewer turns, 64 are done without the exchange between workgroups
+        const int experts = l.E <= 64 && p.runs.n <= 128ll * l.B ? 64 : 16;
+        const unsigned groups = (unsigned)(l.B * ((l.E + experts - 1) / experts));
+        hipLaunchKernelGGL(experts == 64 ? join_kernel<64> : join_kernel<16>, dim3(groups), dim3(kJoinThreads), 0, s, a);
     }
     return hipGetLastError();
 }
 
 hipError_t launch_logits_grad(const moe_logits_grad_args &args, hipStream_t s) {
     const int32_t B = args.l ? args.l->B : 1;
-    const RunSplit runs = run_split(args.T, B, kGradThreads / row_lanes(args.E), 2048);
+    const RunSplit runs = run_split(args.T, B, kGradThreads / row_lanes(args.E), 1024);
     GradArgs g{};
     g.a = args;
     if (args.l) g.l = *args.l;

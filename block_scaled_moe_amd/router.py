@@ -229,16 +229,22 @@ def _backward_args(T, D, E, dh_dtype, dwr_dtype, want_dh, want_dwr, want_bias) -
                                 mark(want_dwr), mark(want_bias), None, 0)
 
 
-def route_backward_workspace(T: int, D: int, E: int, dh_dtype: torch.dtype = torch.bfloat16,
-                             dwr_dtype: torch.dtype = torch.float32, want_dh: bool = True, want_dwr: bool = True,
-                             want_bias: bool = False, device="cuda") -> torch.Tensor:
-    """Device scratch for route_backward with these arguments (reusable across calls that do not overlap)."""
+@functools.lru_cache(maxsize=256)
+def _backward_bytes(T: int, D: int, E: int, dh_dtype, dwr_dtype, want_dh: bool, want_dwr: bool, want_bias: bool) -> int:
     for v in (T, D, E):
         _int32("sizes", v)
     a = _backward_args(T, D, E, dh_dtype, dwr_dtype, want_dh, want_dwr, want_bias)
     n = int(_function("moe_route_backward_workspace_bytes")(ctypes.byref(a)))
     if n == 0:
         _refuse("moe_route_backward_workspace_bytes")
+    return n
+
+
+def route_backward_workspace(T: int, D: int, E: int, dh_dtype: torch.dtype = torch.bfloat16,
+                             dwr_dtype: torch.dtype = torch.float32, want_dh: bool = True, want_dwr: bool = True,
+                             want_bias: bool = False, device="cuda") -> torch.Tensor:
+    """Device scratch for route_backward with these arguments (reusable across calls that do not overlap)."""
+    n = _backward_bytes(T, D, E, dh_dtype, dwr_dtype, want_dh, want_dwr, want_bias)
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
@@ -268,8 +274,7 @@ def route_backward(h: torch.Tensor, wr: torch.Tensor, d_logits: torch.Tensor, dh
     dbias = torch.empty(E, dtype=torch.float32, device=dev) if want_bias else None
     a = _backward_args(T, D, E, dh_dtype, dwr_dtype, want_dh, want_dwr, want_bias)
     if workspace is None:
-        n = int(_function("moe_route_backward_workspace_bytes")(ctypes.byref(a)))
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(_backward_bytes(T, D, E, dh_dtype, dwr_dtype, want_dh, want_dwr, want_bias), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace: on another device, or not contiguous")
     a.h, a.wr, a.d_logits = h.data_ptr(), wr.data_ptr(), d_logits.data_ptr()

@@ -42,7 +42,7 @@ def run_losses(dtype=2, logits=A + 10 * FAR, idx=A + 11 * FAR, valid=A + 12 * FA
 
 @pytest.mark.parametrize("over,status", [
     (dict(T=-1), EINVAL), (dict(T=1 << 30), EUNSUP), (dict(E=0), EINVAL), (dict(E=4097), EINVAL), (dict(top_k=0), EINVAL), (dict(top_k=9), EINVAL),
-    (dict(B=0), EINVAL), (dict(B=1 << 16), EUNSUP), (dict(seq=0), EINVAL), (dict(balance=0), EINVAL), (dict(z=0), EINVAL), (dict(counts=0), EINVAL),
+    (dict(B=0), EINVAL), (dict(B=1 << 14), EUNSUP), (dict(seq=0), EINVAL), (dict(balance=0), EINVAL), (dict(z=0), EINVAL), (dict(counts=0), EINVAL),
     (dict(tokens=0), EINVAL), (dict(prob_sums=0), EINVAL), (dict(lse=0), EINVAL), (dict(logits=0), EINVAL), (dict(idx=0), EINVAL), (dict(dtype=3), EINVAL),
     (dict(ws=0), EWS), (dict(n=64), EWS), (dict(ws=A + 13 * FAR + 8), EALIGN), (dict(logits=A + 4), EALIGN), (dict(lse=A + 4), EALIGN),
     (dict(counts=A + 8), EALIGN), (dict(seq=A + 4), EALIGN), (dict(z=A + FAR + 32, balance=A + FAR + 32), EINVAL), (dict(lse=A + 10 * FAR + 64), EINVAL),
@@ -86,7 +86,7 @@ def test_logits_grad_of_no_tokens():
 
 
 def backward(**over):
-    a = router.MoeRouteBackwardArgs(100, 128, 64, 1, 2, *(A + i * FAR for i in range(7)), 1 << 30)
+    a = router.MoeRouteBackwardArgs(20000, 1024, 128, 1, 2, *(A + i * FAR for i in range(7)), 1 << 30)
     for k, v in over.items():
         setattr(a, k, v)
     return a
@@ -104,7 +104,7 @@ def test_route_backward_refuses(over, status):
 
 def test_route_backward_workspace():
     f = lambda **o: moe.lib().moe_route_backward_workspace_bytes(ctypes.byref(backward(**o)))
-    assert f() > 0 and f(T=0) > 0 and f(T=10000) > f() and f(dwr=0, dbias=0) < f() and f(dh=0) < f() and f(dwr=0) == 0 and f(D=100) == 0
+    assert f() > 0 and f(T=0) > 0 and f(T=40000) > f() and f(dwr=0, dbias=0) < f() and f(dh=0) < f() and f(dwr=0) == 0 and f(D=100) == 0
     assert moe.lib().moe_route_backward(ctypes.byref(backward(T=0, dwr=0, dbias=0, d_logits=0, h=0, wr=0)), None) == OK
 
 
