@@ -20,7 +20,7 @@ __global__ void __launch_bounds__(256) pack_codes_kernel(const uint8_t *__restri
     }
 }
 
-// scales (two bytes) or zero points (one): [E][N][groups] -> [E][N/16][K/256][16][per_step]
+// scales (two bytes) or zero points (one, as the lower byte of the bf16 16 + zero): [E][N][groups] -> [E][N/16][K/256][16][per_step]
 template <typename T>
 __global__ void __launch_bounds__(256) pack_groups_kernel(const T *__restrict__ src, int32_t N, int32_t groups, int32_t per_step,
                                                           int32_t tiles, int32_t steps, int64_t n_out, T *__restrict__ dst) {
@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(256) pack_groups_kernel(const T *__restrict__ 
         const int64_t n = 16 * tile + row, k = step * per_step + g;
         T v = 0;
         if (n < N && k < groups) v = src[(e * N + n) * groups + k];
-        if constexpr (sizeof(T) == 1) v &= 15;
+        if constexpr (sizeof(T) == 1) v = 0x80 | (v & 15) << 3;
         dst[i] = v;
     }
 }

@@ -131,10 +131,8 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) stream_kernel(const W4Ge
                     f4 d[2] = {};
                     uint32_t off[2];
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {  // minus 16 minus the zero point, twice
-                        const uint32_t z = ZEROS ? (w.z[q][gr / 4] >> (8 * (gr & 3))) & 255u : 8u;
-                        off[q] = 0xC180C180u | z << 3 | z << 19;
-                    }
+                    for (int q = 0; q < 2; ++q)  // minus 16 minus the zero point, twice: its lower byte as it is stored, 0xC1
+                        off[q] = ZEROS ? __builtin_amdgcn_perm(0xC1C1C1C1u, w.z[q][gr / 4], 0x04000400u | (gr & 3) * 0x00010001u) : 0xC1C0C1C0u;
 #pragma unroll
                     for (int i = gr * (GROUP / 32); i < (gr + 1) * (GROUP / 32); ++i) {
                         const bf8 xo = __builtin_bit_cast(bf8, *reinterpret_cast<const u32x4 *>(at + 64 * i));
@@ -316,7 +314,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) wide_stream_kernel(const W4Gemm
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         const float f = scale_value<HALF>(w.s[q][gr / 2], gr & 1);
-                        const float off = ZEROS ? 16.0f + (float)((w.z[q][gr / 4] >> (8 * (gr & 3))) & 255u) : 24.0f;
+                        const float off = ZEROS ? 0.125f * (float)((w.z[q][gr / 4] >> (8 * (gr & 3))) & 255u) : 24.0f;
 #pragma unroll
                         for (int m = 0; m < MT; ++m)
 #pragma unroll

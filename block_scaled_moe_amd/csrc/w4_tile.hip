@@ -124,7 +124,8 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
         w_at[q] = (w_row[q] >> 4) * 1024 + (16 * g + (w_row[q] & 15)) * 16;
     }
 
-    // sums of x over the groups of stage s for the 16 rows of piece `wave`, negative, without zero points times 24
+    // sums of x over the groups of stage s for the 16 rows of piece `wave`, times minus 24, or with zero points, which
+    // are read times 8, times minus 1 / 8
     auto row_sums = [&](int buffer) __attribute__((always_inline)) {
         if (wave >= n_sub) return;
         const uint8_t *row = xb + buffer * kX + (16 * wave + i16) * 256;
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
             for (int r = gr * (GROUP / 32); r < (gr + 1) * (GROUP / 32); ++r)
                 d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                     __builtin_bit_cast(bf8, *reinterpret_cast<const u32x4 *>(row + ((4 * r + g) ^ i16) * 16)), ones(), d, 0, 0, 0);
-            if (i16 == 0) *reinterpret_cast<f4 *>(sums + (buffer * kIn + gr) * kBM + 16 * wave + 4 * g) = d * (ZEROS ? -1.0f : -24.0f);
+            if (i16 == 0) *reinterpret_cast<f4 *>(sums + (buffer * kIn + gr) * kBM + 16 * wave + 4 * g) = d * (ZEROS ? -0.125f : -24.0f);
         }
     };
 
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
 #pragma unroll
                     for (int q = 0; q < NF; ++q) {
                         f[q] = scale_value<HALF>(c.s[q][gr / 2], gr & 1);
-                        if constexpr (ZEROS) off[q] = 16.0f + (float)((c.z[q] >> (8 * gr)) & 255u);
+                        if constexpr (ZEROS) off[q] = (float)((c.z[q] >> (8 * gr)) & 255u);  // times 8
                     }
                 }
 #pragma unroll

@@ -48,8 +48,8 @@ SIGNATURES = {
 @dataclasses.dataclass
 class W4Weights:
     """Packed weights [E, N, K] = scale * (code - zero): codes int32 [E, N/16, K/256, 2, 64, 4], scales bf16 or fp16
-    [E, N/16, K/256, 16, 256/group], zeros uint8 of the scales' shape or None (8 everywhere); divisions rounded up, the
-    order that include/moe_w4.h gives."""
+    [E, N/16, K/256, 16, 256/group], zeros uint8 of the scales' shape or None (8 everywhere); divisions rounded up, in the
+    order and with the values that include/moe_w4.h gives."""
     E: int
     N: int
     K: int

@@ -34,7 +34,7 @@ int32_t moe_w4_abi_version(void);
  *   codes  [E][N/16][K/256][2][64][4] 32-bit words: the step's halves of 128 columns; in half c lane 16 g + i
  *          has, in word j, row i's columns 128 c + 32 j + 8 g .. + 7: with r the word rotated right by 3 bits, value 2 m
  *          in bits 4 m .. 4 m + 3 of r, value 2 m + 1 in bits 16 + 4 m .. (m < 4)
- *   scales [E][N/16][K/256][16][256/group], zeros bytes in the same order
+ *   scales [E][N/16][K/256][16][256/group]; zeros in the same order, a byte 0x80 + 8 * zero point each
  * (divisions rounded up). What fills up are zero codes, scales and zero points.
  */
 typedef struct moe_w4_weights {

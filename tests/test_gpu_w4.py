@@ -80,6 +80,8 @@ def test_packing(E, N, K, G, zeros):
     for packed, src in ((w.scales, s),) + (((w.zeros, z),) if zeros else ()):
         full = np.zeros((E, q.shape[1], q.shape[2] // G), np.float64)
         full[:, :N, :K // G] = num(src)
+        if src is z:
+            full = 0x80 + 8 * full
         want = full.reshape(E, -1, 16, q.shape[2] // 256, per).transpose(0, 1, 3, 2, 4)
         assert np.array_equal(num(packed), want)
 
