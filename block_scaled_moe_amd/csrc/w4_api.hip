@@ -74,6 +74,7 @@ int32_t moe_w4_gemm(const moe_w4_gemm_args *a, void *stream) {
     p.tiles = (int32_t)w4_tiles(a->w);
     p.steps = (int32_t)w4_steps(a->w);
     p.C = a->swiglu ? a->w.N / 2 : a->w.N;
+    p.slot_factor = (uint32_t)(((1ull << 31) + p.v.top_k - 1) / p.v.top_k);
     p.out = a->out;
     const int64_t out_rows = a->g ? a->g->T * a->g->top_k : a->rows;
     if (outputs_meet({{a->out, out_rows, p.C * type_bytes(a->out_dtype)}},

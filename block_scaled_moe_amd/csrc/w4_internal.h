@@ -21,8 +21,12 @@ struct W4GemmArgs {
     moe_w4_weights w;
     int32_t tiles, steps;  // of the packed form
     int32_t C;             // columns of out
+    uint32_t slot_factor;  // 2^31 / top_k rounded up
     void *out;
 };
+// Token of a slot below 2^28 (x has fewer than 2^25 rows): the factor is less than 8 / 2^31 too large, relative to 1 / top_k,
+// which does not reach the next whole number.
+__device__ __forceinline__ uint32_t token_of(uint32_t slot, const W4GemmArgs &a) { return __umulhi(2 * slot, a.slot_factor); }
 hipError_t launch_w4_gemm(const W4GemmArgs &a, hipStream_t s);
 hipError_t launch_w4_tile(const W4GemmArgs &a, hipStream_t s);  // groups of many rows
 

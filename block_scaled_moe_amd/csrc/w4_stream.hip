@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) stream_kernel(const W4Ge
                 const int k0 = c * 256, pieces = min(chunk, steps - c) * 32;  // of 16 bytes; past the end the last ones
                 for (int r = wave; r < have; r += kStreamWaves) {
                     const int pos = p0 + m0 + r;
-                    const int64_t src = p.by_token ? p.v.sorted_slot[pos] / p.v.top_k : pos;
+                    const int64_t src = p.by_token ? token_of(p.v.sorted_slot[pos], p) : pos;
                     for (int i = lane; i < pieces; i += 64)
                         *reinterpret_cast<u32x4 *>(xs + r * pitch + i * 16) =
                             *reinterpret_cast<const u32x4 *>(p.x + src * K + min(k0 + 8 * i, K - 8));
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) wide_stream_kernel(const W4Gemm
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             const int pos = p0 + min(m0 + 16 * m + i16, rows - 1);
-            const int64_t row = p.by_token ? p.v.sorted_slot[pos] / p.v.top_k : pos;
+            const int64_t row = p.by_token ? token_of(p.v.sorted_slot[pos], p) : pos;
             x[m] = p.x + row * K + 8 * g;
         }
         f4 acc[MT][2] = {};

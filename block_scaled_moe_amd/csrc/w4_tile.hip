@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
     constexpr int kLds = 3 * (kX + kW) + 2 * (kS + kZ) + 3 * kIn * kBM * 4;
     constexpr int kWCopies = kBN / 16 / 8;  // of codes by every wave in a stage (the first one: perhaps one more)
     constexpr int kSWaves = (kS + 1023) / 1024, kZWaves = (kZ + 1023) / 1024;
-    static_assert(kLds <= 160 * 1024 && kBM * (kBN + 8) * 2 <= 3 * kX && kSWaves + kZWaves <= 8, "LDS");
+    static_assert(kLds <= 160 * 1024 && kSWaves + kZWaves <= 8, "LDS");
     __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
     uint8_t *const xb = lds, *const wb = lds + 3 * kX, *const sb = wb + 3 * kW, *const zb = sb + 2 * kS;
     float *const sums = reinterpret_cast<float *>(zb + 2 * kZ);
@@ -73,8 +73,8 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int pos = p0 + min(4 * (wave + 8 * j) + (lane >> 4), rows - 1);
-        const int64_t row = p.by_token ? p.v.sorted_slot[pos] / p.v.top_k : pos;
-        x[j] = p.x + row * K;
+        const uint32_t row = p.by_token ? token_of(p.v.sorted_slot[pos], p) : pos;
+        x[j] = p.x + (int64_t)row * K;
     }
     // Packed tiles in LDS order; past the end the last one, whose columns are not stored.
     auto packed_tile = [&](int j) __attribute__((always_inline)) -> int64_t {
@@ -142,17 +142,14 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
 
     copy_side(0);
     if (stages > 2) copy_side(1);
-    copy_x(0, 0);
-    copy_w(0, 0);
-    if (stages > 1) {
-        copy_x(1, 1);
-        copy_w(1, 1);
-    }
-    if (stages > 2) {
-        copy_x(2, 2);
-        copy_w(2, 2);
-    }
-    wait_copies<0>();
+#pragma unroll
+    for (int s = 0; s < 3; ++s)
+        if (s < stages) copy_x(s, s);
+#pragma unroll
+    for (int s = 0; s < 3; ++s)
+        if (s < stages) copy_w(s, s);
+    if (stages > 2) wait_copies<2 * kWCopies>();
+    else wait_copies<0>();
     lds_barrier();
     row_sums(0);
     if (stages > 1) row_sums(1);
@@ -280,41 +277,67 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
 #pragma unroll
                 for (int v = 0; v < 4; ++v) acc[i][q][v] = fmaf(d[i][q][v], f_last[q], acc[i][q][v]);
 
-        // ---- outputs: accumulator v of (i, q): row 16 (2 i + wm) + 4 g + v. fp32 from the lanes, bf16 by way of LDS as
-        // whole runs of a row
-        const int out_frags = p.swiglu ? NF / 2 : NF, c0 = cb * width, pitch = width + 8;
-        lds_barrier();  // every wave is done with the buffers
-        uint16_t *const ob = reinterpret_cast<uint16_t *>(lds);
+        // ---- outputs: accumulator v of (i, q): row 16 (2 i + wm) + 4 g + v, column 16 q + i16
+        auto store = [&](auto swiglu_c) __attribute__((always_inline)) {
+            constexpr bool kSwiglu = decltype(swiglu_c)::value;
+            constexpr int kOut = kSwiglu ? NF / 2 : NF;
+            const int c0 = cb * (kSwiglu ? kBN / 2 : kBN) + wn * kOut * 16;  // the wave's first column
+            auto value = [&](int i, int q) __attribute__((always_inline)) -> f4 {
+                f4 y = acc[i][q];
+                if constexpr (kSwiglu) {
 #pragma unroll
-        for (int i = 0; i < MF; ++i)
+                    for (int v = 0; v < 4; ++v) y[v] = swiglu(y[v], acc[i][q + kOut][v]);
+                }
+                return y;
+            };
+            if (p.out_dtype != MOE_DT_BF16) {
 #pragma unroll
-            for (int q = 0; q < NF; ++q) {
-                if (q >= out_frags) continue;
+                for (int i = 0; i < MF; ++i) {
+                    const int m = 16 * (2 * i + wm) + 4 * g;
+                    float *o = static_cast<float *>(p.out) + (int64_t)(p0 + m) * p.C + c0 + i16;
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    float y = acc[i][q][v];
-                    if constexpr (NF > 1)
-                        if (p.swiglu) y = swiglu(y, acc[i][(q + NF / 2) % NF][v]);
-                    const int m = 16 * (2 * i + wm) + 4 * g + v, c = (wn * out_frags + q) * 16 + i16;
-                    if (p.out_dtype == MOE_DT_BF16) ob[m * pitch + c] = __builtin_bit_cast(uint16_t, (__bf16)y);
-                    else if (m < rows && c0 + c < p.C) static_cast<float *>(p.out)[(int64_t)(p0 + m) * p.C + c0 + c] = y;
+                    for (int q = 0; q < kOut; ++q) {
+                        const f4 y = value(i, q);
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            if (m + v < rows && c0 + 16 * q + i16 < p.C) o[(int64_t)v * p.C + 16 * q] = y[v];
+                    }
+                }
+                return;
+            }
+            // four lanes exchange their four rows of four columns: each then stores four columns of one row
+            const bool odd = i16 & 1, upper = i16 & 2;
+            const int col = c0 + (i16 & ~3);
+#pragma unroll
+            for (int i = 0; i < MF; ++i) {
+                const int m = 16 * (2 * i + wm) + 4 * g + (i16 & 3);
+                uint16_t *o = static_cast<uint16_t *>(p.out) + (int64_t)(p0 + m) * p.C + col;
+#pragma unroll
+                for (int q = 0; q < kOut; ++q) {
+                    const f4 y = value(i, q);
+                    uint32_t pair[2];  // columns 2 (i16 / 2), + 1 of rows 2 h + i16 % 2
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float give = odd ? y[2 * h] : y[2 * h + 1];
+                        const float got = __uint_as_float(
+                            __builtin_amdgcn_update_dpp(0, __float_as_uint(give), 0xB1, 0xF, 0xF, true));  // quad_perm 1, 0, 3, 2
+                        pair[h] = bf16_pair(odd ? got : y[2 * h], odd ? y[2 * h + 1] : got);
+                    }
+                    const uint32_t got = __builtin_amdgcn_update_dpp(0, upper ? pair[0] : pair[1], 0x4E, 0xF, 0xF, true);  // 2, 3, 0, 1
+                    const u32x2 out = upper ? (u32x2){got, pair[1]} : (u32x2){pair[0], got};
+                    if (m >= rows) continue;
+                    if (p.C % 4 == 0) {
+                        if (col + 16 * q < p.C) *reinterpret_cast<u32x2 *>(o + 16 * q) = out;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (col + 16 * q + j < p.C) o[16 * q + j] = (uint16_t)(out[j / 2] >> (16 * (j & 1)));
+                    }
                 }
             }
-        if (p.out_dtype != MOE_DT_BF16) return;
-        lds_barrier();
-        uint16_t *out = static_cast<uint16_t *>(p.out) + (int64_t)p0 * p.C + c0;
-        if (p.C % 8 == 0) {
-            const int pieces = width / 8;
-            for (int j = t; j < rows * pieces; j += kThreads) {
-                const int m = j / pieces, c = j % pieces * 8;
-                if (c0 + c < p.C) *reinterpret_cast<u32x4 *>(out + (int64_t)m * p.C + c) = *reinterpret_cast<const u32x4 *>(ob + m * pitch + c);
-            }
-        } else {
-            for (int j = t; j < rows * width; j += kThreads) {
-                const int m = j / width, c = j % width;
-                if (c0 + c < p.C) out[(int64_t)m * p.C + c] = ob[m * pitch + c];
-            }
-        }
+        };
+        if (p.swiglu) store(std::integral_constant<bool, true>{});
+        else store(std::integral_constant<bool, false>{});
     };
     using std::integral_constant;
     switch ((n_sub - wm + 1) / 2) {
@@ -323,7 +346,7 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
         case 2: run(integral_constant<int, 2>{}); break;
         default: run(integral_constant<int, 1>{}); break;  // none: beside the other waves, nothing of it is stored
     }
-    lds_barrier();  // the buffers are the next item's
+    lds_barrier();  // every wave is done with the buffers
     }
     }
 }

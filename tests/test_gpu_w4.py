@@ -141,6 +141,21 @@ def test_grouped(T, k, E, e0, e1, kind, N, K, G, scale, zeros, swiglu, out, by_t
     assert (num(y)[S:] == 77.0).all()
 
 
+@pytest.mark.parametrize("k", [1, 2, 3, 5, 6, 7, 8])
+def test_token_of_a_slot(k):
+    """Every token's row is its own, for every number of slots a token, in both kernels."""
+    T, E = 400, 2
+    for t, e in ((40, 40), (T, E)):
+        idx = np.arange(t * k, dtype=np.int32).reshape(t, k) % e
+        g = moe.sort_tokens(dev(idx), e)
+        w = moe.pack_w4(torch.full((e, 16, 192), 0x99, dtype=torch.uint8, device="cuda"), torch.ones((e, 16, 3), dtype=BF16, device="cuda"))
+        x = torch.zeros((t, 384), dtype=BF16, device="cuda")
+        x[:, 0], x[:, 200] = torch.arange(t) % 16, 256 * torch.arange(t).div(16, rounding_mode="floor") / 16
+        y = moe.w4_product(x, w, g, by_token=True, out_dtype=FP32)   # the sum of the row: weights of one
+        want = host(g.sorted_slot) // k
+        assert np.array_equal(host(y), np.repeat((want % 16 + want // 16 * 16).astype(np.float32)[:, None], 16, 1))
+
+
 def test_products_in_the_mean():
     """By the root mean square: a scale, zero point or factor that is off by a per cent anywhere shows. The rounding to bf16 is
     spread evenly over half a step h to either side: h^2 / 3 in the mean, 10 % for the sample; the rest is far below it."""
