@@ -21,6 +21,7 @@ struct W4GemmArgs {
     moe_w4_weights w;
     int32_t tiles, steps;  // of the packed form
     int32_t C;             // columns of out
+    int32_t shares;        // workgroups that share the turns over a tile's rows (set by the launcher)
     uint32_t slot_factor;  // 2^31 / top_k rounded up
     void *out;
 };

@@ -11,7 +11,7 @@ namespace {
 
 using namespace w4;
 
-// Up to 16 rows a turn: they go into LDS once for the workgroup's eight waves (in parts of the reduction where they
+// Up to 16 or 32 rows a turn: they go into LDS once for the workgroup's eight waves (in parts of the reduction where they
 // do not fit), and KS waves share two column tiles, each with a part of the steps; their sums meet in LDS in the waves' order.
 // 16 + z is a bf16 as 16 + q is, so it is taken off by a second MFMA on the same rows, which leaves four multiply-adds
 // for four results and group.
@@ -22,6 +22,9 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) stream_kernel(const W4Ge
     constexpr int kWords = (kGroups + 1) / 2;     // of scales
     constexpr int kZeroWords = (kGroups + 3) / 4;
     constexpr int kBlocks = kStreamWaves / KS;    // of two column tiles a workgroup
+    // two pieces of 16 rows share the expanded codes where registers (not beside finest groups or zero points) and LDS (not
+    // beside shared columns) allow it
+    constexpr int kUnit = KS == 1 && GROUP > 32 && !ZEROS ? 32 : 16;
     __shared__ __attribute__((aligned(16))) uint8_t xs[kStreamX];
     __shared__ __attribute__((aligned(16))) float part[KS > 1 ? kStreamWaves : 1][KS > 1 ? 16 : 1][36];
     const Expander expand;
@@ -29,7 +32,9 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) stream_kernel(const W4Ge
     const int i16 = lane & 15, g = lane >> 4, ks = wave % KS;
     const int K = p.w.K, steps = p.steps;
     const int nb = p.swiglu ? (p.C + 15) / 16 : (p.C + 31) / 32, per_tile = (nb + kBlocks - 1) / kBlocks;
-    const int tile = blockIdx.x / per_tile, cb = blockIdx.x % per_tile * kBlocks + wave / KS;
+    // the later shares first: most are empty and leave at once, the others take longest
+    const int share = p.shares - 1 - blockIdx.x / (p.v.max_tiles * per_tile), tile = blockIdx.x % (p.v.max_tiles * per_tile) / per_tile;
+    const int cb = blockIdx.x % per_tile * kBlocks + wave / KS;
     int e = 0, p0 = tile * kGroupTile, rows = p.v.rows - p0;
     if (p.v.offsets) {
         // all at once: behind the last tile they are not used
@@ -40,6 +45,7 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) stream_kernel(const W4Ge
         rows = scalar_load(p.v.offsets + e + 1) - p0;
     }
     rows = min(rows, kGroupTile);
+    if (share * kUnit >= rows) return;
 
     const uint8_t *codes[2], *scales[2], *zeros[2];  // of the column tile's first row
     uint32_t code_at[2], scale_at[2];
@@ -94,8 +100,10 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) stream_kernel(const W4Ge
         }
     };
 
-    for (int m0 = 0; m0 < rows; m0 += 16) {
-        const int have = min(rows - m0, 16);
+    // MT pieces of 16 rows from m0 on
+    auto turn = [&](int m0, auto mt_c) __attribute__((always_inline)) {
+        constexpr int MT = decltype(mt_c)::value;
+        const int have = min(rows - m0, 16 * MT);
         const int chunk = min(steps, (kStreamX / have - 16) / 512), pitch = chunk * 512 + 16;  // steps in LDS, bytes of a row
         // steps of this wave in the chunk that begins at c
         auto first = [&](int c) __attribute__((always_inline)) { return c + ks * min(chunk, steps - c) / KS; };
@@ -103,10 +111,12 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) stream_kernel(const W4Ge
         Weights next;
         bool loaded = first(0) < behind(0);
         if (loaded) load(first(0), next);
-        f4 acc[2] = {};
-        const uint8_t *row = xs + min(i16, have - 1) * pitch + 16 * g;
+        f4 acc[MT][2] = {};
+        uint32_t row[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) row[m] = min(16 * m + i16, have - 1) * pitch + 16 * g;
         for (int c = 0; c < steps; c += chunk) {
-            if (c > 0 || m0 > 0) __syncthreads();
+            if (c > 0 || m0 > share * kUnit) __syncthreads();
             {
                 const int k0 = c * 256, pieces = min(chunk, steps - c) * 32;  // of 16 bytes; past the end the last ones
                 for (int r = wave; r < have; r += kStreamWaves) {
@@ -125,42 +135,51 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) stream_kernel(const W4Ge
             for (int s = first(c); s < s_end; ++s) {
                 const Weights w = next;
                 load(s + 1 < s_end ? s + 1 : more ? first(c2) : s, next);
-                const uint8_t *at = row + (s - c) * 512;
+                const uint8_t *at = xs + (s - c) * 512;
 #pragma unroll
                 for (int gr = 0; gr < kGroups; ++gr) {
-                    f4 d[2] = {};
+                    f4 d[MT][2] = {};
                     uint32_t off[2];
 #pragma unroll
                     for (int q = 0; q < 2; ++q)  // minus 16 minus the zero point, twice: its lower byte as it is stored, 0xC1
                         off[q] = ZEROS ? __builtin_amdgcn_perm(0xC1C1C1C1u, w.z[q][gr / 4], 0x04000400u | (gr & 3) * 0x00010001u) : 0xC1C0C1C0u;
 #pragma unroll
                     for (int i = gr * (GROUP / 32); i < (gr + 1) * (GROUP / 32); ++i) {
-                        const bf8 xo = __builtin_bit_cast(bf8, *reinterpret_cast<const u32x4 *>(at + 64 * i));
+                        bf8 w_op[2];
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            d[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo, expand(w.c[q][i >> 2][i & 3]), d[q], 0, 0, 0);
-                            d[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                xo, __builtin_bit_cast(bf8, (u32x4){off[q], off[q], off[q], off[q]}), d[q], 0, 0, 0);
+                        for (int q = 0; q < 2; ++q) w_op[q] = expand(w.c[q][i >> 2][i & 3]);
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            const bf8 xo = __builtin_bit_cast(bf8, *reinterpret_cast<const u32x4 *>(at + row[m] + 64 * i));
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                d[m][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xo, w_op[q], d[m][q], 0, 0, 0);
+                                d[m][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                    xo, __builtin_bit_cast(bf8, (u32x4){off[q], off[q], off[q], off[q]}), d[m][q], 0, 0, 0);
+                            }
                         }
                     }
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         const float f = scale_value<HALF>(w.s[q][gr / 2], gr & 1);
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) acc[q][v] = fmaf(d[q][v], f, acc[q][v]);
+                        for (int m = 0; m < MT; ++m)
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) acc[m][q][v] = fmaf(d[m][q][v], f, acc[m][q][v]);
                     }
+                    if constexpr (MT > 1) __builtin_amdgcn_sched_barrier(0);  // one group's operands at a time: registers
                 }
             }
         }
-        // accumulator v of q: row 4 g + v, column 16 q + i16
+        // accumulator v of (m, q): row 16 m + 4 g + v, column 16 q + i16
         if constexpr (KS > 1) {
 #pragma unroll
             for (int q = 0; q < 2; ++q)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) part[wave][4 * g + v][16 * q + i16] = acc[q][v];
+                for (int v = 0; v < 4; ++v) part[wave][4 * g + v][16 * q + i16] = acc[0][q][v];
             __syncthreads();
             // a block's waves take the rows 4 g + v of its sums in turn: a wave's lanes are 16 columns of four rows
-            if (ks >= 4) continue;
+            if (ks >= 4) return;
 #pragma unroll
             for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -168,28 +187,34 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) stream_kernel(const W4Ge
                     float y = part[wave - ks][4 * g + v][16 * q + i16];
 #pragma unroll
                     for (int k = 1; k < KS; ++k) y += part[wave - ks + k][4 * g + v][16 * q + i16];
-                    acc[q][v] = y;
+                    acc[0][q][v] = y;
                 }
         }
-        if (cb < nb) {
+        if (cb >= nb) return;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                const int m = 4 * g + v;
-                if (m >= have || (KS > 1 && ks != v)) continue;
-                const int64_t out = (int64_t)(p0 + m0 + m) * p.C;
+                const int r = 16 * m + 4 * g + v;
+                if (r >= have || (KS > 1 && ks != v)) continue;
+                const int64_t out = (int64_t)(p0 + m0 + r) * p.C;
                 auto store = [&](int c, float y) __attribute__((always_inline)) {
                     if (c >= p.C) return;
                     if (p.out_dtype == MOE_DT_BF16) static_cast<uint16_t *>(p.out)[out + c] = __builtin_bit_cast(uint16_t, (__bf16)y);
                     else static_cast<float *>(p.out)[out + c] = y;
                 };
                 if (p.swiglu) {
-                    store(16 * cb + i16, swiglu(acc[0][v], acc[1][v]));
+                    store(16 * cb + i16, swiglu(acc[m][0][v], acc[m][1][v]));
                 } else {
-                    store(32 * cb + i16, acc[0][v]);
-                    store(32 * cb + 16 + i16, acc[1][v]);
+                    store(32 * cb + i16, acc[m][0][v]);
+                    store(32 * cb + 16 + i16, acc[m][1][v]);
                 }
             }
-        }
+    };
+    using std::integral_constant;
+    for (int m0 = share * kUnit; m0 < rows; m0 += p.shares * kUnit) {
+        if (kUnit > 16 && rows - m0 > 16) turn(m0, integral_constant<int, kUnit / 16>{});
+        else turn(m0, integral_constant<int, 1>{});
     }
 }
 
@@ -377,18 +402,29 @@ __global__ void __launch_bounds__(64 * WAVES, 2) wide_stream_kernel(const W4Gemm
 
 }  // namespace
 
-hipError_t launch_w4_gemm(const W4GemmArgs &a, hipStream_t s) {
+// Kernels by the rows of a group (for an even routing, or of the one group). One group, 5120 x 4096, groups of 128, us of this
+// kernel, the wide one and the tiles: 16 rows 10.0, 11.6, 24.8; 32 rows 17.0, 13.9, 25.9; 128 rows 58, 38, 46; 192 rows 90, 55, 47.
+// 4096 x 2560, groups of 32 and zero points: 16 rows 8.2, 10.6, 24.3; 192 rows 66, 44, 54; 256 rows 78, 53, 54. Evenly routed
+// over 96 experts, this one and the tiles: 16 rows each 235, 303 and 171, 292; 21 rows 258, 306 and 220, 300; 32 rows 390, 343 and
+// 289, 334; with one expert of twenty times the mean 10 rows 227, 308 and 161, 272; 21 rows 297, 403 and 300, 537.
+constexpr int kStreamMean = 24, kStreamRows = 16, kWideRows = 160;
+
+hipError_t launch_w4_gemm(const W4GemmArgs &args, hipStream_t s) {
+    W4GemmArgs a = args;
     const int rows = a.v.mean_rows;
-    if (rows > (a.v.offsets ? 16 : 64)) return launch_w4_tile(a, s);
+    if (rows > (a.v.offsets ? kStreamMean : kWideRows)) return launch_w4_tile(a, s);
     const int64_t nb = a.swiglu ? (a.C + 15) / 16 : (a.C + 31) / 32, blocks = (int64_t)a.v.max_tiles * nb;
+    // An expert that far more tokens chose than the others takes several turns: four workgroups share them (256 tokens, 161 of
+    // them for one expert of 60, 5120 x 4096: 284 -> 186 us; evenly routed, where most of them are empty, 202 -> 208 us).
+    a.shares = a.v.offsets && a.v.rows / a.v.top_k > 64 ? 4 : 1;
     if (blocks >= 1 << 22) return hipErrorInvalidValue;  // a grid's threads are 32 bits
     by_form(a.w, [&](auto group, auto half, auto zeros) {
         constexpr int kGroup = decltype(group)::value;
         constexpr bool kHalf = decltype(half)::value, kZeros = decltype(zeros)::value;
         auto go = [&](auto kernel, int per_group) {
-            hipLaunchKernelGGL(kernel, dim3((unsigned)(a.v.max_tiles * ((nb + per_group - 1) / per_group))), dim3(512), 0, s, a);
+            hipLaunchKernelGGL(kernel, dim3((unsigned)(a.v.max_tiles * a.shares * ((nb + per_group - 1) / per_group))), dim3(512), 0, s, a);
         };
-        if (rows > 16) go(wide_stream_kernel<kGroup, kHalf, kZeros, 4, 8>, 1);
+        if (!a.v.offsets && rows > kStreamRows) go(wide_stream_kernel<kGroup, kHalf, kZeros, 4, 8>, 1);
         else if (blocks >= 4096) go(stream_kernel<kGroup, kHalf, kZeros, 1>, 8);
         else if (blocks >= 1024) go(stream_kernel<kGroup, kHalf, kZeros, 4>, 2);
         else go(stream_kernel<kGroup, kHalf, kZeros, 8>, 1);
