@@ -412,12 +412,12 @@ constexpr int kStreamMean = 24, kStreamRows = 16, kWideRows = 160;
 hipError_t launch_w4_gemm(const W4GemmArgs &args, hipStream_t s) {
     W4GemmArgs a = args;
     const int rows = a.v.mean_rows;
-    if (rows > (a.v.offsets ? kStreamMean : kWideRows)) return launch_w4_tile(a, s);
     const int64_t nb = a.swiglu ? (a.C + 15) / 16 : (a.C + 31) / 32, blocks = (int64_t)a.v.max_tiles * nb;
+    // a grid's threads are 32 bits; the tiles' grid is one workgroup a CU
+    if (rows > (a.v.offsets ? kStreamMean : kWideRows) || blocks >= 1 << 22) return launch_w4_tile(a, s);
     // An expert that far more tokens chose than the others takes several turns: four workgroups share them (256 tokens, 161 of
     // them for one expert of 60, 5120 x 4096: 284 -> 186 us; evenly routed, where most of them are empty, 202 -> 208 us).
     a.shares = a.v.offsets && a.v.rows / a.v.top_k > 64 ? 4 : 1;
-    if (blocks >= 1 << 22) return hipErrorInvalidValue;  // a grid's threads are 32 bits
     by_form(a.w, [&](auto group, auto half, auto zeros) {
         constexpr int kGroup = decltype(group)::value;
         constexpr bool kHalf = decltype(half)::value, kZeros = decltype(zeros)::value;

@@ -61,7 +61,8 @@ int32_t moe_w4_pack(const uint8_t *codes, const uint16_t *scales, const uint8_t 
  * x bf16 of rows of K; out [rows][N or N/2] of out_dtype (MOE_DT_*). Sums are fp32, rounded once.
  * by_token: x has T rows and sorted row p reads row sorted_slot[p] / top_k; otherwise rows = T * top_k, already
  * sorted. W has n experts (the local ones); rows behind the last local one are left as they are. A NaN or an infinity
- * makes every result that it enters not finite; they enter none of other rows.
+ * makes every result that it enters not finite; they enter none of other rows. So may, on the way, values of x from
+ * 2^116 on.
  * rows < 2^25, N and K up to 2^20; rows * K and N * K below 2^36 each. */
 typedef struct moe_w4_gemm_args {
     int32_t rows;             /* rows of x */

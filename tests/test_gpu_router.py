@@ -395,3 +395,44 @@ def test_streams_and_graph_replays():
         torch.cuda.synchronize()
         kept = [t.clone() for t in out]
         assert all(torch.equal(a, b) for a, b in zip(kept, step()))
+
+
+def test_more_than_32_bits_of_logits():
+    """Logits numbered past 2^31: 64 rows again and again, the last two repetitions sequences of their own."""
+    rng = np.random.default_rng(14)
+    E, k, T = 4096, 8, 2 ** 19 + 192
+    base, idx = bf16(rng, (64, E)), routing(rng, 64, E, k)
+    logits = base.repeat(T // 64, 1)
+    many = dev(idx).repeat(T // 64, 1)
+    l = moe.router_losses(logits, many, seq=dev(np.array([0, T - 128, T - 64, T], np.int32)))
+    want, bound, _, _ = ref.losses(num(base), idx, None, None, k)
+    for s in (1, 2):
+        assert np.array_equal(num(l.counts)[s], want["counts"][0]) and num(l.tokens)[s] == 64
+        for n in ("balance", "z", "prob_sums"):
+            ref.close(num(getattr(l, n))[s:s + 1], want[n], bound[n], n)
+    assert np.array_equal(num(l.counts)[0], want["counts"][0] * (T // 64 - 2))
+    ref.close(num(l.lse)[-64:], want["lse"], bound["lse"], "lse")
+    assert bool((l.lse.view(-1, 64) == l.lse[:64]).all())
+    db, dz = np.array([0.5, -2.0, 3.0], np.float32), np.array([1.0, 0.5, -1.5], np.float32)
+    w, dw = gate(rng, 64, k)
+    d = moe.logits_grad(logits, many, l, dev(db), dev(dz), dev(w).repeat(T // 64, 1), dev(dw).repeat(T // 64, 1))
+    for s, rows in ((1, slice(T - 128, T - 64)), (2, slice(T - 64, T))):
+        got = {"counts": num(l.counts)[s:s + 1], "tokens": num(l.tokens)[s:s + 1], "lse": num(l.lse)[rows]}
+        want_d, bound_d = ref.logits_grad(num(base), idx, got, db[s:s + 1], dz[s:s + 1], w, dw, None, k)
+        ref.close(num(d[rows]), want_d, bound_d, f"d_logits of {s}")
+    for i in range(0, T - 128, 1 << 16):
+        rows = d[i:min(i + (1 << 16), T - 128)].view(-1, 64, E)
+        assert bool((rows == d[:64]).all())
+
+
+def test_more_than_32_bits_of_hidden_states():
+    """h and dh numbered past 2^31, of small whole numbers: every sum is exact, in whatever order."""
+    rng = np.random.default_rng(15)
+    T, D, E = 2 ** 19 + 192, 4096, 9
+    h, wr, g = (rng.integers(-a, a + 1, s).astype(np.float32) for a, s in ((2, (64, D)), (2, (E, D)), (1, (64, E))))
+    n = T // 64
+    dh, dwr, dbias = moe.route_backward(dev(h, BF16).repeat(n, 1), dev(wr, BF16), dev(g).repeat(n, 1), want_bias=True)
+    assert np.array_equal(num(dwr), n * (g.T @ h)) and np.array_equal(num(dbias), n * g.sum(0))
+    want = dev(g @ wr, BF16)
+    for i in range(0, T, 1 << 16):
+        assert bool((dh[i:i + (1 << 16)].view(-1, 64, D) == want).all()), f"rows from {i} on"

@@ -263,3 +263,44 @@ def test_decode_step():
                 size[t] += w[t, j] * (np.abs(w2[idx[t, j]]) @ np.abs(a))
         # a and the second product are rounded to bf16, everything else is fp32
         assert (np.abs(out - want) <= (2 * U_BF16 + 2000 * U24) * size).all()
+
+
+def far(got, want, bound, period, chunk=1 << 17):
+    """Rows repeat with a period, and so do their expected values; compared on the device, where they are too many for the host."""
+    want, bound = dev(want), dev(bound)
+    for i in range(0, len(got), chunk):
+        g = got[i:i + chunk].view(-1, period, got.shape[1]).float()
+        assert bool(((g - want.float()).abs() <= bound.float() + 2 * U24 * want.float().abs()).all()), f"rows from {i} on"
+
+
+@pytest.mark.parametrize("rows,N,K", [(2 ** 19 + 320, 16, 4096), (2 ** 20 + 128, 2050, 32)], ids=["rows", "results"])
+def test_more_than_32_bits_of_elements(rows, N, K):
+    """Rows of x, or of the result, whose elements are numbered past 2^31."""
+    rng = np.random.default_rng(8)
+    codes, s, _, w, size = checkpoint(rng, 1, N, K, 32)
+    x = dev(rng.standard_normal((64, K)).astype(np.float32), BF16)
+    y, bound = expect(num(x).astype(np.float64), w[0], size[0], 32, False, True)
+    out = torch.full((rows, N), float("nan"), dtype=BF16, device="cuda")
+    moe.w4_product(x.repeat(rows // 64, 1), moe.pack_w4(codes, s), out=out)
+    far(out, y, bound, 64)
+
+
+def test_more_than_32_bits_of_codes():
+    """Weights of 17 GB, and more column tiles than the grid of a workgroup each can have."""
+    E, N, K, T, k = 128, 2 ** 20, 32, 16, 8
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    codes = torch.randint(0, 256, (E, N, K // 2), dtype=torch.uint8, device="cuda", generator=gen)
+    s = (torch.rand((E, N, 1), device="cuda", generator=gen) * 0.1 + 0.01).to(BF16)
+    w = moe.pack_w4(codes, s)
+    idx = torch.arange(T * k, dtype=torch.int32, device="cuda").flip(0).view(T, k).contiguous()
+    x = torch.randn((T, K), device="cuda", generator=gen).to(BF16)
+    g = moe.sort_tokens(idx, E)
+    out = moe.w4_product(x, w, g, by_token=True)
+    for e in (0, 1, 63, 64, 126, 127):
+        q = torch.stack((codes[e] & 15, codes[e] >> 4), 2).view(N, K).double()
+        v = x[(T * k - 1 - e) // k].double()
+        sv = s[e].double()[:, 0]
+        y, ay = ((q - 8) @ v) * sv, (((q - 8).abs() @ v.abs()) * sv)
+        bound = (2 * K + 8) * 2 * U24 * ((40 + q) @ v.abs()) * sv + (K // 32 + 8) * 2 * U24 * ay  # as in expect
+        err = (out[e].double() - y).abs()
+        assert bool((err <= bound + U_BF16 * (y.abs() + bound) + 1e-37).all()), f"expert {e}"
