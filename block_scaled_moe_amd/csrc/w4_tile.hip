@@ -12,6 +12,12 @@
 //    ahead, and leaves them in LDS, from where they are the products' first addends.
 //  - MFMAs (16 clocks) and vector instructions (4 clocks) are about as much work, so each MFMA stands beside the
 //    instructions that expand a later operand or add an earlier group's sum.
+//  - A workgroup a CU (155 KiB of LDS) walks its items. Where the next part's rows are is found out while this one's first
+//    stages arrive: three loads in a row, each of which needs the one before, no longer begin a part.
+// Bound by what a CU issues: of a stage's 3600 clocks at 85 rows about 2000 are MFMAs and vector instructions, the rest are waits
+// for LDS and barriers that two waves a SIMD do not hide; about 8 us of an item are its beginning and end. 8192 rows of 96
+// experts, 5120 x 4096, groups of 128: 506 us (0.68 PFLOP/s; 1920 items, of which a workgroup takes seven or eight). Fewer
+// rows are bound by the latency of a stage's rows, 0.8 us a stage.
 #include "w4_mma.h"
 
 namespace moe {
@@ -28,6 +34,11 @@ __device__ __forceinline__ void copy_from(const void *src, uint32_t dst) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(uniform((int)dst)), "v"(src) : "memory");
 }
 
+// a word a lane
+__device__ __forceinline__ void copy_words(const void *src, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, off" ::"s"(uniform((int)dst)), "v"(src) : "memory");
+}
+
 template <int GROUP, bool HALF, bool ZEROS, int NF>
 __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
     constexpr int kBN = 64 * NF;
@@ -35,13 +46,14 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
     constexpr int kGroups = kW4Step / GROUP, kIn = kStage / GROUP;  // groups per step, per stage
     constexpr int kW = kTiles * 1024;                         // LDS bytes of a stage's codes
     constexpr int kS = kTiles * 32 * kGroups, kZ = ZEROS ? kS / 2 : 0;  // of a step's scales and zero points
-    constexpr int kLds = 3 * (kX + kW) + 2 * (kS + kZ) + 3 * kIn * kBM * 4;
+    constexpr int kLds = 3 * (kX + kW) + 2 * (kS + kZ) + 3 * kIn * kBM * 4 + 2 * kBM * 4;
     constexpr int kWCopies = kBN / 16 / 8;  // of codes by every wave in a stage (the first one: perhaps one more)
     constexpr int kSWaves = (kS + 1023) / 1024, kZWaves = (kZ + 1023) / 1024;
     static_assert(kLds <= 160 * 1024 && kSWaves + kZWaves <= 8, "LDS");
     __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
     uint8_t *const xb = lds, *const wb = lds + 3 * kX, *const sb = wb + 3 * kW, *const zb = sb + 2 * kS;
     float *const sums = reinterpret_cast<float *>(zb + 2 * kZ);
+    int32_t *const slots = reinterpret_cast<int32_t *>(sums + 3 * kIn * kBM);  // of the rows of this part and of the next one
 
     const Expander expand;
     const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
@@ -50,20 +62,64 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
     const int width = p.swiglu ? kBN / 2 : kBN;  // output columns a workgroup
     const int nb = (p.C + width - 1) / width;
 
-    // ---- work items: each XCD (workgroups 8 apart) takes a range of the experts' tiles, whose rows then meet in one L2; a tile
-    // of the groups' list is up to two of 128 rows
+    // ---- work items: a tile of the groups' list is up to two parts of 128 rows. Up to two tiles' items in a row, whose rows
+    // and codes then meet in one L2, go to each XCD (workgroups 8 apart) in turn, each time from another one on: experts with
+    // many rows, which often stand together, are spread over all of them.
     const int n_tiles = p.v.offsets ? scalar_load(&p.v.ctrl->n_tiles) : (p.v.rows + kBM - 1) / kBM;
-    const int items = n_tiles * nb, per = (items + 7) / 8, item_end = min((int)(blockIdx.x & 7) * per + per, items);
-    for (int item = (blockIdx.x & 7) * per + (blockIdx.x >> 3); item < item_end; item += gridDim.x >> 3) {
-    const int tile = item / nb, cb = item % nb;
-    int e = 0, row0 = tile * kBM, row_end = min(row0 + kBM, p.v.rows);
-    if (p.v.offsets) {
-        e = scalar_load(p.v.tile_expert + tile);
-        row0 = scalar_load(p.v.tile_row0 + tile);
-        row_end = min(scalar_load(p.v.offsets + e + 1), row0 + kGroupTile);
+    const int items = n_tiles * nb, unit = min(2 * nb, max(items / 32, 1));
+    // this workgroup's j-th item, -1: none, but there may be more; items: no more
+    auto item_of = [&](int j) __attribute__((always_inline)) -> int {
+        const int turn = j / unit;
+        if (turn * 8 * unit >= items) return items;
+        const int item = (8 * turn + ((blockIdx.x - turn) & 7)) * unit + j % unit;
+        return item < items ? item : -1;
+    };
+    struct Part {
+        int item, e, p0, end;  // expert; first row, the one behind the tile's last
+    } part, next;
+    auto first_of = [&](int item, Part &q) __attribute__((always_inline)) {
+        const int tile = item / nb;
+        q.item = item;
+        if (p.v.offsets) {
+            q.e = scalar_load(p.v.tile_expert + tile);
+            q.p0 = scalar_load(p.v.tile_row0 + tile);
+        } else {
+            q.e = 0, q.p0 = tile * kBM;
+        }
+    };
+    auto end_of = [&](Part &q) __attribute__((always_inline)) {
+        q.end = p.v.offsets ? min(scalar_load(p.v.offsets + q.e + 1), q.p0 + kGroupTile) : min(q.p0 + kBM, p.v.rows);
+    };
+    auto copy_slots = [&](const Part &q, int buffer) __attribute__((always_inline)) {
+        if (p.by_token && wave < kBM / 64)
+            copy_words(p.v.sorted_slot + min(q.p0 + 64 * wave + lane, q.end - 1), lds_address(slots + buffer * kBM + 64 * wave));
+    };
+    auto following = [&](int &j) __attribute__((always_inline)) -> int {
+        int item;
+        do {
+            item = item_of(j);
+            j += gridDim.x >> 3;
+        } while (item < 0);
+        return item;
+    };
+    int j_next = blockIdx.x >> 3, parity = 0;
+    part.item = following(j_next);
+    if (part.item >= items) return;
+    first_of(part.item, part);
+    end_of(part);
+    copy_slots(part, 0);
+    wait_copies<0>();
+    lds_barrier();
+    for (;;) {
+    // the next part: of this tile, or the first one of the next item; what says where its rows are arrives beside this one's
+    const bool same = part.p0 + kBM < part.end;
+    next = part;
+    next.p0 += kBM;
+    if (!same) {
+        next.item = following(j_next);
+        if (next.item < items) first_of(next.item, next);
     }
-    for (int p0 = row0; p0 < row_end; p0 += kBM) {
-    const int rows = min(row_end - p0, kBM);
+    const int e = part.e, cb = part.item % nb, p0 = part.p0, rows = min(part.end - p0, kBM);
 
     // ---- sources. Rows: copies wave + 8 j of four rows of 256 bytes; a row's 16-byte pieces are swapped by the row's last
     // four bits, so that sixteen rows' pieces of one place lie in different banks.
@@ -72,8 +128,8 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
     const int x_at = ((lane & 15) ^ ((4 * wave + (lane >> 4)) & 15)) * 8;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const int pos = p0 + min(4 * (wave + 8 * j) + (lane >> 4), rows - 1);
-        const uint32_t row = p.by_token ? token_of(p.v.sorted_slot[pos], p) : pos;
+        const int in = min(4 * (wave + 8 * j) + (lane >> 4), rows - 1);
+        const uint32_t row = p.by_token ? token_of(slots[parity * kBM + in], p) : p0 + in;
         x[j] = p.x + (int64_t)row * K;
     }
     // Packed tiles in LDS order; past the end the last one, whose columns are not stored.
@@ -148,9 +204,15 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
 #pragma unroll
     for (int s = 0; s < 3; ++s)
         if (s < stages) copy_w(s, s);
+    if (!same && next.item < items) {
+        asm volatile("" : "+s"(next.e), "+s"(next.p0));
+        end_of(next);
+        asm volatile("" : "+s"(next.end));
+    }
     if (stages > 2) wait_copies<2 * kWCopies>();
     else wait_copies<0>();
     lds_barrier();
+    if (next.item < items) copy_slots(next, parity ^ 1);
     row_sums(0);
     if (stages > 1) row_sums(1);
     lds_barrier();
@@ -347,7 +409,9 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
         default: run(integral_constant<int, 1>{}); break;  // none: beside the other waves, nothing of it is stored
     }
     lds_barrier();  // every wave is done with the buffers
-    }
+    if (next.item >= items) return;
+    part = next;
+    parity ^= 1;
     }
 }
 
