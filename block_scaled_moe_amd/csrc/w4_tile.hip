@@ -12,12 +12,13 @@
 //    ahead, and leaves them in LDS, from where they are the products' first addends.
 //  - MFMAs (16 clocks) and vector instructions (4 clocks) are about as much work, so each MFMA stands beside the
 //    instructions that expand a later operand or add an earlier group's sum.
-//  - A workgroup a CU (155 KiB of LDS) walks its items. Where the next part's rows are is found out while this one's first
-//    stages arrive: three loads in a row, each of which needs the one before, no longer begin a part.
+//  - A workgroup a CU (157 KiB of LDS) walks its items, parts with many rows first. Where the next part's rows are is found out
+//    while this one's first stages arrive: three loads in a row, each of which needs the one before, no longer begin a part.
 // Bound by what a CU issues: of a stage's 3600 clocks at 85 rows about 2000 are MFMAs and vector instructions, the rest are waits
 // for LDS and barriers that two waves a SIMD do not hide; about 8 us of an item are its beginning and end. 8192 rows of 96
-// experts, 5120 x 4096, groups of 128: 506 us (0.68 PFLOP/s; 1920 items, of which a workgroup takes seven or eight). Fewer
-// rows are bound by the latency of a stage's rows, 0.8 us a stage.
+// experts, 5120 x 4096, groups of 128: 510 us (0.67 PFLOP/s; 1920 items, of which a workgroup takes seven or eight). 3003 rows of
+// 60 experts (1 to 553 each), 1002 x 2592, groups of 32: 98 us; 126 with the parts in the list's order, 116 once they
+// are spread over the XCDs. Evenly routed the order costs 2%.
 #include "w4_mma.h"
 
 namespace moe {
@@ -46,7 +47,7 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
     constexpr int kGroups = kW4Step / GROUP, kIn = kStage / GROUP;  // groups per step, per stage
     constexpr int kW = kTiles * 1024;                         // LDS bytes of a stage's codes
     constexpr int kS = kTiles * 32 * kGroups, kZ = ZEROS ? kS / 2 : 0;  // of a step's scales and zero points
-    constexpr int kLds = 3 * (kX + kW) + 2 * (kS + kZ) + 3 * kIn * kBM * 4 + 2 * kBM * 4;
+    constexpr int kLds = 3 * (kX + kW) + 2 * (kS + kZ) + 3 * kIn * kBM * 4 + 2 * kBM * 4 + 4 * kThreads;
     constexpr int kWCopies = kBN / 16 / 8;  // of codes by every wave in a stage (the first one: perhaps one more)
     constexpr int kSWaves = (kS + 1023) / 1024, kZWaves = (kZ + 1023) / 1024;
     static_assert(kLds <= 160 * 1024 && kSWaves + kZWaves <= 8, "LDS");
@@ -54,6 +55,7 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
     uint8_t *const xb = lds, *const wb = lds + 3 * kX, *const sb = wb + 3 * kW, *const zb = sb + 2 * kS;
     float *const sums = reinterpret_cast<float *>(zb + 2 * kZ);
     int32_t *const slots = reinterpret_cast<int32_t *>(sums + 3 * kIn * kBM);  // of the rows of this part and of the next one
+    uint16_t *const order = reinterpret_cast<uint16_t *>(slots + 2 * kBM);
 
     const Expander expand;
     const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
@@ -62,11 +64,55 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
     const int width = p.swiglu ? kBN / 2 : kBN;  // output columns a workgroup
     const int nb = (p.C + width - 1) / width;
 
-    // ---- work items: a tile of the groups' list is up to two parts of 128 rows. Up to two tiles' items in a row, whose rows
-    // and codes then meet in one L2, go to each XCD (workgroups 8 apart) in turn, each time from another one on: experts with
-    // many rows, which often stand together, are spread over all of them.
+    // ---- work items: parts of 128 rows (a tile of the groups' list is one or two) times column blocks, those with most rows
+    // first: workgroups then take about as much work each, however uneven the groups are. kThreads tiles of the list are brought
+    // into that order at a time: its parts by the number of their pieces, in `order` as 2 * tile + part.
     const int n_tiles = p.v.offsets ? scalar_load(&p.v.ctrl->n_tiles) : (p.v.rows + kBM - 1) / kBM;
-    const int items = n_tiles * nb, unit = min(2 * nb, max(items / 32, 1));
+    auto sort_parts = [&](int tile0) __attribute__((always_inline)) -> int {
+        int *const count = reinterpret_cast<int *>(sums), *const place = count + 64;  // by pieces (8 first), then waves
+        int pieces[2] = {0, 0};  // of this thread's tile's parts
+        if (tile0 + t < n_tiles) {
+            const int rows = min(p.v.offsets[p.v.tile_expert[tile0 + t] + 1] - p.v.tile_row0[tile0 + t], kGroupTile);
+            pieces[0] = (min(rows, kBM) + 15) / 16;
+            pieces[1] = (max(rows - kBM, 0) + 15) / 16;
+        }
+        int before[2] = {0, 0};  // parts of as many pieces before it in its wave
+        const uint64_t lower = (1ull << lane) - 1;
+#pragma unroll
+        for (int n = 1; n <= 8; ++n) {
+            const uint64_t b0 = __ballot(pieces[0] == n), b1 = __ballot(pieces[1] == n);
+            if (pieces[0] == n) before[0] = __popcll(b0 & lower);
+            if (pieces[1] == n) before[1] = __popcll(b0) + __popcll(b1 & lower);
+            if (lane == 0) count[(8 - n) * 8 + wave] = __popcll(b0) + __popcll(b1);
+        }
+        __syncthreads();
+        if (wave == 0) {
+            const int own = count[lane];
+            int sum = own;
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) {
+                const int v = __shfl_up(sum, off);
+                if (lane >= off) sum += v;
+            }
+            place[lane] = sum - own;
+            if (lane == 63) place[64] = sum;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (pieces[i] > 0) order[place[(8 - pieces[i]) * 8 + wave] + before[i]] = (uint16_t)(2 * t + i);
+        const int n = uniform(place[64]);
+        __syncthreads();
+        return n;
+    };
+    struct Part {
+        int item, e, p0, end;  // expert; first row, the one behind the last
+    };
+    int parity = 0;
+    for (int tile0 = 0; tile0 < n_tiles; tile0 += p.v.offsets ? kThreads : n_tiles) {
+    // Up to two parts' items in a row, whose rows and codes then meet in one L2, go to each XCD (workgroups 8 apart) in turn, each
+    // time from another one on.
+    const int items = (p.v.offsets ? sort_parts(tile0) : n_tiles) * nb, unit = min(2 * nb, max(items / 32, 1));
     // this workgroup's j-th item, -1: none, but there may be more; items: no more
     auto item_of = [&](int j) __attribute__((always_inline)) -> int {
         const int turn = j / unit;
@@ -74,21 +120,18 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
         const int item = (8 * turn + ((blockIdx.x - turn) & 7)) * unit + j % unit;
         return item < items ? item : -1;
     };
-    struct Part {
-        int item, e, p0, end;  // expert; first row, the one behind the tile's last
-    } part, next;
     auto first_of = [&](int item, Part &q) __attribute__((always_inline)) {
-        const int tile = item / nb;
         q.item = item;
         if (p.v.offsets) {
+            const int at = uniform((int)order[item / nb]), tile = tile0 + at / 2;
             q.e = scalar_load(p.v.tile_expert + tile);
-            q.p0 = scalar_load(p.v.tile_row0 + tile);
+            q.p0 = scalar_load(p.v.tile_row0 + tile) + at % 2 * kBM;
         } else {
-            q.e = 0, q.p0 = tile * kBM;
+            q.e = 0, q.p0 = item / nb * kBM;
         }
     };
     auto end_of = [&](Part &q) __attribute__((always_inline)) {
-        q.end = p.v.offsets ? min(scalar_load(p.v.offsets + q.e + 1), q.p0 + kGroupTile) : min(q.p0 + kBM, p.v.rows);
+        q.end = min(p.v.offsets ? scalar_load(p.v.offsets + q.e + 1) : p.v.rows, q.p0 + kBM);
     };
     auto copy_slots = [&](const Part &q, int buffer) __attribute__((always_inline)) {
         if (p.by_token && wave < kBM / 64)
@@ -102,24 +145,20 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
         } while (item < 0);
         return item;
     };
-    int j_next = blockIdx.x >> 3, parity = 0;
+    int j_next = blockIdx.x >> 3;
+    Part part, next;
     part.item = following(j_next);
-    if (part.item >= items) return;
+    if (part.item >= items) continue;
     first_of(part.item, part);
     end_of(part);
-    copy_slots(part, 0);
+    copy_slots(part, parity);
     wait_copies<0>();
     lds_barrier();
     for (;;) {
-    // the next part: of this tile, or the first one of the next item; what says where its rows are arrives beside this one's
-    const bool same = part.p0 + kBM < part.end;
-    next = part;
-    next.p0 += kBM;
-    if (!same) {
-        next.item = following(j_next);
-        if (next.item < items) first_of(next.item, next);
-    }
-    const int e = part.e, cb = part.item % nb, p0 = part.p0, rows = min(part.end - p0, kBM);
+    // what says where the next part's rows are arrives beside this one's rows
+    next.item = following(j_next);
+    if (next.item < items) first_of(next.item, next);
+    const int e = part.e, cb = part.item % nb, p0 = part.p0, rows = part.end - p0;
 
     // ---- sources. Rows: copies wave + 8 j of four rows of 256 bytes; a row's 16-byte pieces are swapped by the row's last
     // four bits, so that sixteen rows' pieces of one place lie in different banks.
@@ -204,7 +243,7 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
 #pragma unroll
     for (int s = 0; s < 3; ++s)
         if (s < stages) copy_w(s, s);
-    if (!same && next.item < items) {
+    if (next.item < items) {
         asm volatile("" : "+s"(next.e), "+s"(next.p0));
         end_of(next);
         asm volatile("" : "+s"(next.end));
@@ -409,9 +448,10 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
         default: run(integral_constant<int, 1>{}); break;  // none: beside the other waves, nothing of it is stored
     }
     lds_barrier();  // every wave is done with the buffers
-    if (next.item >= items) return;
-    part = next;
     parity ^= 1;
+    if (next.item >= items) break;
+    part = next;
+    }
     }
 }
 
@@ -423,7 +463,7 @@ hipError_t launch_w4_tile(const W4GemmArgs &a, hipStream_t s) {
     // a second half that starts inside a packed tile needs one more of them, for which only the narrow tile has room, as for the
     // sums of groups of 32
     const bool narrow = a.w.group == 32 || (a.swiglu && a.C % 16) || items(a.swiglu ? 128 : 256) < 512;
-    const int64_t n = (items(narrow ? (a.swiglu ? 64 : 128) : (a.swiglu ? 128 : 256)) + 7) / 8 * 8;
+    const int64_t n = ((a.v.offsets ? 2 : 1) * items(narrow ? (a.swiglu ? 64 : 128) : (a.swiglu ? 128 : 256)) + 7) / 8 * 8;
     if (n > INT32_MAX) return hipErrorInvalidValue;
     const int64_t grid = n < kGrid ? n : kGrid;
     w4::by_form(a.w, [&](auto group, auto half, auto zeros) {

@@ -141,6 +141,13 @@ def test_grouped(T, k, E, e0, e1, kind, N, K, G, scale, zeros, swiglu, out, by_t
     assert (num(y)[S:] == 77.0).all()
 
 
+@pytest.mark.parametrize("T,k,E,e0,e1,kind", [(13000, 3, 1300, 50, 1300, "dup"), (9000, 4, 700, 0, 700, "hot"), (2000, 8, 520, 3, 517, "wild")])
+@pytest.mark.parametrize("by_token", [False, True])
+def test_many_groups(T, k, E, e0, e1, kind, by_token):
+    """More tiles than are brought into order at a time, even and uneven ones."""
+    test_grouped(T, k, E, e0, e1, kind, 20, 64, 32, BF16, False, True, BF16, by_token)
+
+
 @pytest.mark.parametrize("k", [1, 2, 3, 5, 6, 7, 8])
 def test_token_of_a_slot(k):
     """Every token's row is its own, for every number of slots a token, in both kernels."""
