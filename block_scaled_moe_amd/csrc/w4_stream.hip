@@ -3,7 +3,9 @@
 //
 // Bound by the weights' bytes. A wave takes two column tiles of 16 (with swiglu one of the first half's columns and the same of
 // the second half's) of one tile of rows; its load of codes is 1 KiB in a row, and those of the next step are in flight
-// while the current one is multiplied.
+// while the current one is multiplied. 64 tokens on 96 of 384 experts, 5120 x 4096, groups of 32 with zero points: 148 us, 6.0
+// TB/s. One token, eight experts 4096 x 2560, groups of 128: 11.1 to 12.8 us for 41 MB; one row, 5120 x 4096: 7.8 us for 11.5 MB:
+// a load's latency, the rows' way into LDS and the launch.
 #include "w4_mma.h"
 
 namespace moe {
@@ -405,8 +407,9 @@ __global__ void __launch_bounds__(64 * WAVES, 2) wide_stream_kernel(const W4Gemm
 // Kernels by the rows of a group (for an even routing, or of the one group). One group, 5120 x 4096, groups of 128, us of this
 // kernel, the wide one and the tiles: 16 rows 10.0, 11.6, 24.8; 32 rows 17.0, 13.9, 25.9; 128 rows 58, 38, 46; 192 rows 90, 55, 47.
 // 4096 x 2560, groups of 32 and zero points: 16 rows 8.2, 10.6, 24.3; 192 rows 66, 44, 54; 256 rows 78, 53, 54. Evenly routed
-// over 96 experts, this one and the tiles: 16 rows each 235, 303 and 171, 292; 21 rows 258, 306 and 220, 300; 32 rows 390, 343 and
-// 289, 334; with one expert of twenty times the mean 10 rows 227, 308 and 161, 272; 21 rows 297, 403 and 300, 537.
+// over 96 experts, this one and the tiles: 16 rows each 241, 300 and 183, 290; 21 rows 256, 302 and 219, 294; 32 rows 345, 322 and
+// 304, 342; 42 rows 474, 352 and 373, 378; unevenly (the largest group of five to thirty times the mean) 10 rows 220, 273 and 167,
+// 270; 21 rows 322, 348 and 187, 294; 42 rows 444, 424 and 311, 360.
 constexpr int kStreamMean = 24, kStreamRows = 16, kWideRows = 160;
 
 hipError_t launch_w4_gemm(const W4GemmArgs &args, hipStream_t s) {
