@@ -4,7 +4,8 @@
 //
 // Both are products of a fp32 matrix with a bf16 one whose rows run along the reduction, so one kernel does both. The
 // fp32 one, which is the smaller, goes through the bf16 MFMA in pieces: its value is the sum of its upper 8 bits, the next 8
-// and the last 8, each a bf16 exactly. Where many column tiles share it, split_kernel cuts it once into the order in which
+// and the last 8, each a bf16 exactly. All three are needed for bf16 results too: a row of g sums to nearly nothing, so what
+// the experts' weights have in common cancels, and the leading bits with it. Where many column tiles share it, split_kernel cuts it once into the order in which
 // the MFMA takes it, for either product: tiles of 128 rows, steps of 32 of the reduction, pieces, 16 rows, lanes; a tile's
 // step is one contiguous copy. Where few do, a launch costs more than cutting it in every workgroup.
 //
@@ -12,8 +13,8 @@
 // buffer while the next one arrives in the other. The bf16 matrix comes as it is and is turned over by the transposing
 // LDS read (4 rows x 16 columns per 16 lanes), the same operand for all pieces.
 //
-// Bound by the MFMAs where they are many: 16384 x 384, 4096 columns, bf16 results (two pieces): split 19, both products 172 to
-// 178 (206 GFLOP of pieces, 1.18 PFLOP/s), joining dwr's parts 7.8 us. 5003 x 61, 1088 columns, fp32 results with the bias's: 18.8
+// Bound by the MFMAs where they are many: 16384 x 384, 4096 columns, bf16 results: 272 us a call (309 GFLOP of pieces; 212 with
+// two pieces, whose results were up to 2^-15 of each value of g off). 5003 x 61, 1088 columns, fp32 results with the bias's: 18.8
 // and 4.1 us. 300 x 64, 256 columns: 11.8 us, two steps' latency and the launch.
 #include "block_mma.h"
 #include "router_internal.h"
@@ -30,30 +31,25 @@ typedef short s4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256, kBM = 128, kFusedBM = 64, kBN = 256, kStep = 32;
 
-// v in pieces of bf16: cut off at 8 bits each, which nothing can overflow; the last of two is rounded
-template <int P>
-__device__ __forceinline__ void split(float v, uint16_t (&out)[P]) {
+// v in pieces of bf16: cut off at 8 bits each, which nothing can overflow
+constexpr int kPieces = 3;
+__device__ __forceinline__ void split(float v, uint16_t (&out)[kPieces]) {
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-        if (P == 2 && p == 1) {
-            out[p] = __builtin_bit_cast(uint16_t, (__bf16)v);
-        } else {
-            const uint32_t u = __float_as_uint(v) & 0xFFFF0000u;
-            out[p] = (uint16_t)(u >> 16);
-            v -= __uint_as_float(u);
-        }
+    for (int p = 0; p < kPieces; ++p) {
+        const uint32_t u = __float_as_uint(v) & 0xFFFF0000u;
+        out[p] = (uint16_t)(u >> 16);
+        v -= __uint_as_float(u);
     }
 }
 
 // One lane's operand of a 16 x 32 piece: row r of 16, values k = 4 g .. 4 g + 3 and 16 + 4 g .. 16 + 4 g + 3; the pieces lie
 // `stride` operands apart.
-template <int P>
 __device__ __forceinline__ void write_operand(const float (&v)[8], u32x4 *dst, int lane, int stride = 8) {
-    uint16_t x[8][P];
+    uint16_t x[8][kPieces];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) split<P>(v[i], x[i]);
+    for (int i = 0; i < 8; ++i) split(v[i], x[i]);
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
+    for (int p = 0; p < kPieces; ++p) {
         u32x4 o;
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = (uint32_t)x[2 * i][p] | (uint32_t)x[2 * i + 1][p] << 16;
@@ -63,7 +59,7 @@ __device__ __forceinline__ void write_operand(const float (&v)[8], u32x4 *dst, i
 
 // A block of 128 tokens x 32 experts of g: its operands with tokens as rows (dh), and with experts as rows (dwr).
 // Both forms are filled up with zeros to whole tiles and steps.
-template <int PH, int PW>
+template <bool H, bool W>
 __global__ void __launch_bounds__(kThreads) split_kernel(const float *__restrict__ g, int32_t T, int32_t E, int32_t e_steps,
                                                          int32_t t_steps, u32x4 *__restrict__ a_h, u32x4 *__restrict__ a_w) {
     __shared__ float v[128][33];
@@ -75,30 +71,30 @@ __global__ void __launch_bounds__(kThreads) split_kernel(const float *__restrict
         v[r][c] = t0 + r < T && e0 + c < E ? g[(int64_t)(t0 + r) * E + e0 + c] : 0.0f;
     }
     __syncthreads();
-    if constexpr (PH > 0) {
+    if constexpr (H) {
         if (e0 / 32 < e_steps) {
-            u32x4 *tile = a_h + ((int64_t)blockIdx.x * e_steps + blockIdx.y) * (PH * 512);
+            u32x4 *tile = a_h + ((int64_t)blockIdx.x * e_steps + blockIdx.y) * (kPieces * 512);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int m = wave + 4 * j;  // 16 tokens
                 float x[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] = v[16 * m + i16][(i >> 2) * 16 + 4 * q + (i & 3)];
-                write_operand<PH>(x, tile + m * 64, lane);
+                write_operand(x, tile + m * 64, lane);
             }
         }
     }
-    if constexpr (PW > 0) {
+    if constexpr (W) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int m = 2 * (blockIdx.y & 3) + j;            // 16 experts of the tile
             const int step = blockIdx.x * 4 + wave;            // 32 tokens
             if (step < t_steps) {
-                u32x4 *tile = a_w + ((int64_t)(blockIdx.y >> 2) * t_steps + step) * (PW * 512);
+                u32x4 *tile = a_w + ((int64_t)(blockIdx.y >> 2) * t_steps + step) * (kPieces * 512);
                 float x[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] = v[32 * wave + (i >> 2) * 16 + 4 * q + (i & 3)][16 * j + i16];
-                write_operand<PW>(x, tile + m * 64, lane);
+                write_operand(x, tile + m * 64, lane);
             }
         }
     }
@@ -121,11 +117,11 @@ struct ProductArgs {
 };
 
 // OUTER: a's rows run along g's columns (dwr); CUT: a was cut beforehand
-template <int P, int BM, bool OUTER, bool CUT>
+template <int BM, bool OUTER, bool CUT>
 __device__ __forceinline__ void product(const ProductArgs &args, const Product &p, int item, uint8_t *lds) {
     constexpr int kSub = BM / 16;                        // pieces of 16 rows
     constexpr int kWM = BM / 64, kJ = 16 / (4 / kWM);    // row waves; column tiles of 16 a wave
-    constexpr int kA = P * kSub * 1024, kB = kStep * kBN * 2, kBuffer = kA + kB;
+    constexpr int kA = kPieces * kSub * 1024, kB = kStep * kBN * 2, kBuffer = kA + kB;
     static_assert(!CUT || BM == kBM, "tiles of split_kernel");
     const int D = args.D, n_tiles = args.n_tiles, T = args.T, E = args.E;
     const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
@@ -158,7 +154,7 @@ __device__ __forceinline__ void product(const ProductArgs &args, const Product &
         if constexpr (CUT) {
             const uint8_t *src = reinterpret_cast<const uint8_t *>(a + (int64_t)s * (kA / 16));
 #pragma unroll
-            for (int j = 0; j < P * kSub / 4; ++j) copy_to_lds(src + (wave + 4 * j) * 1024, lane * 16, dst + j * 4096);
+            for (int j = 0; j < kPieces * kSub / 4; ++j) copy_to_lds(src + (wave + 4 * j) * 1024, lane * 16, dst + j * 4096);
         }
         const uint8_t *rows = reinterpret_cast<const uint8_t *>(p.b) + (int64_t)s * kStep * D * 2;
 #pragma unroll
@@ -201,7 +197,7 @@ __device__ __forceinline__ void product(const ProductArgs &args, const Product &
         uint8_t *buf = lds + (s & 1) * kBuffer;
         if constexpr (!CUT) {
 #pragma unroll
-            for (int i = 0; i < kOwn; ++i) write_operand<P>(v[i], reinterpret_cast<u32x4 *>(buf) + (wave + 4 * i) * 64, lane, kSub);
+            for (int i = 0; i < kOwn; ++i) write_operand(v[i], reinterpret_cast<u32x4 *>(buf) + (wave + 4 * i) * 64, lane, kSub);
         }
         wait_copies<0>();
         lds_barrier();
@@ -209,9 +205,9 @@ __device__ __forceinline__ void product(const ProductArgs &args, const Product &
             copy(s + 1);
             if constexpr (!CUT) load(s + 1);
         }
-        bf8 x[P][4];
+        bf8 x[kPieces][4];
 #pragma unroll
-        for (int q = 0; q < P; ++q)
+        for (int q = 0; q < kPieces; ++q)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 x[q][i] = __builtin_bit_cast(bf8, *reinterpret_cast<const u32x4 *>(buf + (q * kSub + 4 * wm + i) * 1024 + lane * 16));
@@ -224,14 +220,14 @@ __device__ __forceinline__ void product(const ProductArgs &args, const Product &
             const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4 *)(at + 16 * 512));
             const bf8 y = __builtin_bit_cast(bf8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
-            for (int q = 0; q < P; ++q)
+            for (int q = 0; q < kPieces; ++q)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y, x[q][i], acc[i][j], 0, 0, 0);
         }
         if (want_bias) {
             const bf8 one = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
 #pragma unroll
-            for (int q = 0; q < P; ++q)
+            for (int q = 0; q < kPieces; ++q)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) bias[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(one, x[q][i], bias[i], 0, 0, 0);
         }
@@ -264,10 +260,10 @@ __device__ __forceinline__ void product(const ProductArgs &args, const Product &
     }
 }
 
-template <int PH, int PW, bool CUT>
+template <bool H, bool W, bool CUT>
 __global__ void __launch_bounds__(kThreads, 2) product_kernel(const ProductArgs a) {
-    constexpr int P = PH > PW ? PH : PW, BM = CUT ? kBM : kFusedBM;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * (P * BM * 64 + kStep * kBN * 2)];
+    constexpr int BM = CUT ? kBM : kFusedBM;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * (kPieces * BM * 64 + kStep * kBN * 2)];
     // each XCD (workgroups 8 apart) takes a range of either product's items
     auto mine = [](int b, int items) __attribute__((always_inline)) {
         const int per = (items + 7) / 8, x = b & 7, i = b >> 3;
@@ -276,14 +272,14 @@ __global__ void __launch_bounds__(kThreads, 2) product_kernel(const ProductArgs 
     };
     const int w_groups = (a.w_items + 7) / 8 * 8;
     if ((int)blockIdx.x < w_groups) {
-        if constexpr (PW > 0) {
+        if constexpr (W) {
             const int item = mine(blockIdx.x, a.w_items);
-            if (item >= 0) product<PW, BM, true, CUT>(a, a.w, item, lds);
+            if (item >= 0) product<BM, true, CUT>(a, a.w, item, lds);
         }
     } else {
-        if constexpr (PH > 0) {
+        if constexpr (H) {
             const int item = mine(blockIdx.x - w_groups, a.h_items);
-            if (item >= 0) product<PH, BM, false, CUT>(a, a.h, item, lds);
+            if (item >= 0) product<BM, false, CUT>(a, a.h, item, lds);
         }
     }
 }
@@ -323,8 +319,6 @@ constexpr int64_t kCutFrom = 1 << 23;
 
 RouteBackwardPlan route_backward_plan(const moe_route_backward_args &a) {
     RouteBackwardPlan p{};
-    if (a.dh) p.planes_h = a.dh_dtype == MOE_DT_BF16 ? 2 : 3;
-    if (a.dwr || a.dbias) p.planes_w = (a.dwr && a.dwr_dtype == MOE_DT_FP32) || a.dbias ? 3 : 2;
     const int64_t n_tiles = (a.D + kBN - 1) / kBN;
     p.cut = (int64_t)a.T * a.E * n_tiles >= kCutFrom;
     const int32_t bm = p.cut ? kBM : kFusedBM;
@@ -335,7 +329,7 @@ RouteBackwardPlan route_backward_plan(const moe_route_backward_args &a) {
     // dwr has few tiles: its reduction is cut so that they fill the CUs once, in parts of 256 tokens at least
     const int64_t tiles = p.e_tiles * n_tiles;
     p.splits = 1;
-    if (p.planes_w && tiles < 256) {
+    if (a.dwr && tiles < 256) {
         const int64_t most = p.t_steps / 8;
         p.splits = (int32_t)(256 / tiles < most ? 256 / tiles : most);
         if (p.splits < 1) p.splits = 1;
@@ -348,8 +342,8 @@ RouteBackwardPlan route_backward_plan(const moe_route_backward_args &a) {
         off += (bytes + 255) & ~(size_t)255;
         return at;
     };
-    p.a_h = take(p.cut ? (size_t)p.planes_h * 8192 * (size_t)p.t_tiles * p.e_steps : 0);
-    p.a_w = take(p.cut ? (size_t)p.planes_w * 8192 * (size_t)p.e_tiles * p.t_steps : 0);
+    p.a_h = take(p.cut && a.dh ? (size_t)kPieces * 8192 * (size_t)p.t_tiles * p.e_steps : 0);
+    p.a_w = take(p.cut && a.dwr ? (size_t)kPieces * 8192 * (size_t)p.e_tiles * p.t_steps : 0);
     p.parts = take(p.splits > 1 && a.dwr ? 4 * (size_t)p.splits * a.E * (size_t)a.D : 0);
     p.bias_parts = take(p.splits > 1 && a.dbias ? 4 * (size_t)p.splits * a.E : 0);
     p.total = off > 0 ? off : 256;
@@ -367,39 +361,33 @@ hipError_t launch_route_backward(const moe_route_backward_args &a, const RouteBa
     q.E = a.E;
     q.D = a.D;
     q.n_tiles = (a.D + kBN - 1) / kBN;
-    if (p.planes_w) {
+    if (a.dwr) {
         q.w = {a_w, a.h, parted ? parts : a.dwr, a.dbias && parted ? bias_parts : a.dbias, a.E, a.T, a.dwr_dtype,
                p.e_tiles, p.t_steps, p.splits, p.steps_per_split};
         q.w_items = p.e_tiles * q.n_tiles * p.splits;
     }
-    if (p.planes_h) {
+    if (a.dh) {
         q.h = {a_h, a.wr, a.dh, nullptr, a.T, a.E, a.dh_dtype, p.t_tiles, p.e_steps, 1, p.e_steps};
         q.h_items = p.t_tiles * q.n_tiles;
     }
-    auto run = [&](auto ph, auto pw) {
-        constexpr int PH = decltype(ph)::value, PW = decltype(pw)::value;
+    auto run = [&](auto h, auto w) {
+        constexpr bool H = decltype(h)::value, W = decltype(w)::value;
         const unsigned grid = (unsigned)((q.w_items + 7) / 8 * 8 + (q.h_items + 7) / 8 * 8);
         if (p.cut) {
             // with experts as rows the last tile is filled up to 128
-            const unsigned e_blocks = (unsigned)(PW > 0 ? 4 * p.e_tiles : p.e_steps);
-            hipLaunchKernelGGL((split_kernel<PH, PW>), dim3((unsigned)p.t_tiles, e_blocks), dim3(kThreads), 0, s, a.d_logits,
+            const unsigned e_blocks = (unsigned)(W ? 4 * p.e_tiles : p.e_steps);
+            hipLaunchKernelGGL((split_kernel<H, W>), dim3((unsigned)p.t_tiles, e_blocks), dim3(kThreads), 0, s, a.d_logits,
                                a.T, a.E, p.e_steps, p.t_steps, a_h, a_w);
-            hipLaunchKernelGGL((product_kernel<PH, PW, true>), dim3(grid), dim3(kThreads), 0, s, q);
+            hipLaunchKernelGGL((product_kernel<H, W, true>), dim3(grid), dim3(kThreads), 0, s, q);
         } else {
-            hipLaunchKernelGGL((product_kernel<PH, PW, false>), dim3(grid), dim3(kThreads), 0, s, q);
+            hipLaunchKernelGGL((product_kernel<H, W, false>), dim3(grid), dim3(kThreads), 0, s, q);
         }
     };
     using std::integral_constant;
-    auto by_w = [&](auto ph) {
-        if (p.planes_w == 0) {
-            if constexpr (decltype(ph)::value > 0) run(ph, integral_constant<int, 0>{});
-        } else if (p.planes_w == 2) run(ph, integral_constant<int, 2>{});
-        else run(ph, integral_constant<int, 3>{});
-    };
     if (a.T > 0) {
-        if (p.planes_h == 0) by_w(integral_constant<int, 0>{});
-        else if (p.planes_h == 2) by_w(integral_constant<int, 2>{});
-        else by_w(integral_constant<int, 3>{});
+        if (a.dh && a.dwr) run(integral_constant<bool, true>{}, integral_constant<bool, true>{});
+        else if (a.dh) run(integral_constant<bool, true>{}, integral_constant<bool, false>{});
+        else run(integral_constant<bool, false>{}, integral_constant<bool, true>{});
     }
     if (parted && a.dwr) {
         const int64_t n = (int64_t)a.E * a.D, threads = n / 2;  // D >= 64: more than dbias has

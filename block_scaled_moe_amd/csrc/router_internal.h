@@ -27,8 +27,7 @@ hipError_t launch_logits_grad(const moe_logits_grad_args &a, hipStream_t s);
 
 // Workspace and work of moe_route_backward.
 struct RouteBackwardPlan {
-    int32_t planes_h, planes_w;         // pieces of d_logits for dh, and for dwr and dbias
-    bool cut;                           // into pieces beforehand
+    bool cut;                           // d_logits into pieces beforehand
     int32_t t_tiles, e_tiles;           // of 128 rows, 64 if not cut beforehand
     int32_t t_steps, e_steps;           // of 32 along the reduction
     int32_t splits, steps_per_split;    // of dwr's reduction

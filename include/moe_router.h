@@ -79,8 +79,8 @@ int32_t moe_logits_grad(const moe_logits_grad_args *a, void *stream);
 /* Gradients of the router's product logits = h wr^T + bias:
  *   dh [T][D] = d_logits wr,  dwr [E][D] = d_logits^T h,  dbias[e] = sum over t of d_logits[t][e]
  * dh or dwr may be NULL (not computed), dbias is computed beside dwr only. h [T][D] and wr [E][D] are bf16, d_logits fp32; dh and dwr are of the
- * given types. d_logits enters the bf16 MFMA in pieces of 8 bits: for a bf16 result two (off by up to 2^-15 of each value, far
- * below the result's own rounding), for fp32 and for dbias three, which hold it exactly. Sums are fp32, those over
+ * given types. d_logits enters the bf16 MFMA in three pieces of 8 bits, which hold it exactly: what all experts share cancels in dh,
+ * so that a result may be made of the last bits. Sums are fp32, those over
  * long T in parts that are then added in order. D % 64 == 0, D < 2^24, T < 2^24, E <= 4096 (moe_route: 1024); T * D
  * below 2^38, E * D below 2^32.
  * A NaN or an infinity makes every result that it enters not finite. */
