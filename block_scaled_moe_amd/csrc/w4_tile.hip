@@ -20,13 +20,14 @@
 // 60 experts (1 to 553 each), 1002 x 2592, groups of 32: 98 us; 126 with the parts in the list's order, 116 once they
 // are spread over the XCDs. Evenly routed the order costs 2%.
 #include "w4_mma.h"
+#include "w4_parts.h"
 
 namespace moe {
 namespace {
 
 using namespace w4;
 
-constexpr int kThreads = 512, kBM = 128, kStage = 128;
+constexpr int kThreads = 512, kBM = kW4PartRows, kStage = 128;
 constexpr int kGrid = 256;  // workgroups: one a CU
 constexpr int kX = kBM * kStage * 2;  // LDS bytes of a stage's rows
 
@@ -72,9 +73,9 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
         int *const count = reinterpret_cast<int *>(sums), *const place = count + 64;  // by pieces (8 first), then waves
         int pieces[2] = {0, 0};  // of this thread's tile's parts
         if (tile0 + t < n_tiles) {
-            const int rows = min(p.v.offsets[p.v.tile_expert[tile0 + t] + 1] - p.v.tile_row0[tile0 + t], kGroupTile);
-            pieces[0] = (min(rows, kBM) + 15) / 16;
-            pieces[1] = (max(rows - kBM, 0) + 15) / 16;
+            const int left = p.v.offsets[p.v.tile_expert[tile0 + t] + 1] - p.v.tile_row0[tile0 + t];
+            pieces[0] = (w4_part_rows(left, kGroupTile, 0) + 15) / 16;
+            pieces[1] = (w4_part_rows(left, kGroupTile, 1) + 15) / 16;
         }
         int before[2] = {0, 0};  // parts of as many pieces before it in its wave
         const uint64_t lower = (1ull << lane) - 1;
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
         return n;
     };
     struct Part {
-        int item, e, p0, end;  // expert; first row, the one behind the last
+        int item, e, part, p0, end;  // expert; which of its tile; first row, the one behind the last
     };
     int parity = 0;
     for (int tile0 = 0; tile0 < n_tiles; tile0 += p.v.offsets ? kThreads : n_tiles) {
@@ -125,13 +126,15 @@ __global__ void __launch_bounds__(kThreads) tile_kernel(const W4GemmArgs p) {
         if (p.v.offsets) {
             const int at = uniform((int)order[item / nb]), tile = tile0 + at / 2;
             q.e = scalar_load(p.v.tile_expert + tile);
-            q.p0 = scalar_load(p.v.tile_row0 + tile) + at % 2 * kBM;
+            q.part = at % 2;
+            q.p0 = scalar_load(p.v.tile_row0 + tile) + q.part * kBM;
         } else {
-            q.e = 0, q.p0 = item / nb * kBM;
+            q.e = q.part = 0, q.p0 = item / nb * kBM;
         }
     };
     auto end_of = [&](Part &q) __attribute__((always_inline)) {
-        q.end = min(p.v.offsets ? scalar_load(p.v.offsets + q.e + 1) : p.v.rows, q.p0 + kBM);
+        const int left = (p.v.offsets ? scalar_load(p.v.offsets + q.e + 1) : p.v.rows) - (q.p0 - q.part * kBM);
+        q.end = uniform(q.p0 + w4_part_rows(left, kGroupTile, q.part));
     };
     auto copy_slots = [&](const Part &q, int buffer) __attribute__((always_inline)) {
         if (p.by_token && wave < kBM / 64)
