@@ -97,3 +97,71 @@ def test_groups_longer_than_a_tile(T, k, E, kind, N, K, G, swiglu):
     """Groups of several tiles of 224 rows, cut into parts of 128 and 96."""
     assert form(T, k, E, E, N, G, swiglu)[0] == "tile"
     run(T, k, E, 0, E, kind, N, K, G, BF16, True, swiglu, BF16)
+
+
+WIDE = [  # K of one, two, three and more stages of 128
+    (1600, 64, 64, BF16, False, False, BF16), (1605, 192, 64, FP16, True, False, BF16), (1602, 320, 64, BF16, True, False, FP32),
+    (1664, 1088, 64, FP16, False, True, BF16), (1600, 320, 64, BF16, True, True, FP32), (1601, 128, 128, FP16, False, False, BF16),
+    (1600, 256, 128, BF16, True, False, BF16), (1664, 384, 128, BF16, False, True, BF16), (1632, 640, 128, FP16, True, True, BF16),
+    (1700, 1152, 128, BF16, False, False, FP32), (1696, 128, 128, FP16, True, True, FP32), (1603, 1152, 128, FP16, True, False, BF16)]
+
+
+@pytest.mark.parametrize("T,k,E,e0,e1,kind", [(400, 8, 64, 0, 64, "even"), (900, 8, 128, 40, 104, "wild"), (420, 8, 64, 0, 64, "hot"),
+                                              (410, 8, 64, 0, 64, "steps")])
+@pytest.mark.parametrize("N,K,G,scale,zeros,swiglu,out", WIDE)
+def test_wide_tiles(T, k, E, e0, e1, kind, N, K, G, scale, zeros, swiglu, out):
+    """A prompt's product: tiles of 256 columns, with the activation 128 of either half, parts of every number of pieces of 16 rows."""
+    assert form(T, k, E, e1 - e0, N, G, swiglu) == ("tile", 4, 1)
+    run(T, k, E, e0, e1, kind, N, K, G, scale, zeros, swiglu, out, by_token=K % 3 != 0)
+
+
+@pytest.mark.parametrize("rows", [700, 3000])
+@pytest.mark.parametrize("N,K,G,scale,zeros,swiglu,out", [(21888, 320, 64, BF16, True, False, BF16), (25600, 256, 128, FP16, False, True, BF16)])
+def test_wide_tiles_of_one_weight(rows, N, K, G, scale, zeros, swiglu, out):
+    assert form(rows, 1, 0, 1, N, G, swiglu) == ("tile", 4, 1)
+    run(rows, 1, 0, 0, 1, "", N, K, G, scale, zeros, swiglu, out)
+
+
+# ---------------------------------------------------------------- few rows
+
+FORMS = [(G, scale, zeros, swiglu, out) for G, scale, zeros, swiglu, out in (
+    (32, BF16, False, False, BF16), (32, FP16, True, True, BF16), (64, FP16, False, True, FP32), (64, BF16, True, False, BF16),
+    (128, BF16, False, False, BF16), (128, BF16, False, True, BF16), (128, FP16, True, False, FP32))]
+
+
+@pytest.mark.parametrize("waves,N,K", [(8, 134, 2688), (4, 602, 1152), (4, 620, 128), (1, 2050, 1152), (1, 2054, 2048), (1, 2070, 384)])
+@pytest.mark.parametrize("T,kind", [(64, "even"), (64, "hot"), (60, "steps"), (100, "even"), (110, "hot"), (180, "wild"), (190, "steps")])
+@pytest.mark.parametrize("G,scale,zeros,swiglu,out", FORMS)
+def test_few_rows_a_group(waves, N, K, T, kind, G, scale, zeros, swiglu, out):
+    """Each number of waves that share a column tile; turns of up to 16 rows and (one wave, groups of 64 or 128 without zero points)
+    of 32, several for the hot expert and several parts of the reduction in LDS; one or four workgroups that share the turns."""
+    k, E = 8, 64
+    if swiglu:
+        N += N % 2
+    assert form(T, k, E, E, N, G, swiglu) == ("stream", waves, 4 if T > 64 else 1)
+    run(T, k, E, 0, E, kind, N, K, G, scale, zeros, swiglu, out, by_token=T % 20 == 0 or T == 64)
+
+
+@pytest.mark.parametrize("T", [1, 3])
+@pytest.mark.parametrize("N,K,G,scale,zeros,swiglu", [(4096, 2560, 128, BF16, False, False), (5120, 1536, 32, FP16, True, True), (5101, 640, 64, BF16, True, False)])
+def test_one_token(T, N, K, G, scale, zeros, swiglu):
+    """Eight experts, some with the same row twice."""
+    assert form(T, 8, 64, 64, N, G, swiglu) == ("stream", 4, 1)
+    run(T, 8, 64, 0, 64, "even", N, K, G, scale, zeros, swiglu, BF16)
+
+
+@pytest.mark.parametrize("rows", [1, 5, 16])
+@pytest.mark.parametrize("waves,N", [(8, 4100), (4, 32800), (1, 131110)])
+@pytest.mark.parametrize("K,G,scale,zeros,swiglu,out", [(96, 32, BF16, True, False, BF16), (640, 128, FP16, False, True, BF16), (2112, 64, BF16, False, False, FP32)])
+def test_few_rows_of_one_weight(rows, waves, N, K, G, scale, zeros, swiglu, out):
+    assert form(rows, 1, 0, 1, N, G, swiglu) == ("stream", waves, 1)
+    run(rows, 1, 0, 0, 1, "", N, K, G, scale, zeros, swiglu, out)
+
+
+@pytest.mark.parametrize("rows", [17, 32, 33, 64, 65, 97, 128, 129, 160])
+@pytest.mark.parametrize("N,K,G,scale,zeros,swiglu,out", [
+    (67, 96, 32, FP16, True, False, BF16), (130, 2592, 32, BF16, False, True, BF16), (96, 1088, 64, BF16, True, True, FP32), (101, 640, 64, FP16, False, False, FP32),
+    (64, 256, 128, BF16, True, False, BF16), (2, 128, 128, FP16, False, True, BF16)])
+def test_some_rows_of_one_weight(rows, N, K, G, scale, zeros, swiglu, out):
+    assert form(rows, 1, 0, 1, N, G, swiglu) == ("wide", 8, 1)
+    run(rows, 1, 0, 0, 1, "", N, K, G, scale, zeros, swiglu, out)
