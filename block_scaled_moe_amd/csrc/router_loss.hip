@@ -34,6 +34,14 @@ __device__ __forceinline__ float exp_neg(float x) {
     return fmaf(e, r * kLn2, e);
 }
 
+// m + log(sum), rounded once: a logarithm of several units would add a rounding of its own
+__device__ __forceinline__ float log_sum_exp(float m, float sum) {
+    constexpr double kLn2 = 0.693147180559945309;
+    int k;
+    const float f = frexpf(sum, &k);
+    return (float)((double)m + fma((double)k, kLn2, (double)logf(f)));
+}
+
 template <int L>
 __device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
@@ -167,14 +175,14 @@ __global__ void __launch_bounds__(kThreads) loss_kernel(const LossArgs a) {
         m = lanes_max<L>(m);
         if (m == kNegInf) m = 0.0f;  // nothing above -inf: the sum is 0, or a NaN
         f4 ex[NP];
-        float sum = 0.0f;
+        f4 four = {0.0f, 0.0f, 0.0f, 0.0f};  // four chains: shorter ones round less
 #pragma unroll
         for (int p = 0; p < NP; ++p)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sum += ex[p][i] = exp_neg(x.v[p][i] - m);
-        sum = lanes_sum<L>(sum);
+            for (int i = 0; i < 4; ++i) four[i] += ex[p][i] = exp_neg(x.v[p][i] - m);
+        const float sum = lanes_sum<L>((four[0] + four[1]) + (four[2] + four[3]));
         const bool counted = x.valid && sum != 0.0f;
-        const float lse = counted ? m + logf(sum) : kNegInf;
+        const float lse = counted ? log_sum_exp(m, sum) : kNegInf;
         if (lane == 0) a.l.lse[row] = lse;
         if (counted) {
             const float inv = 1.0f / sum;
@@ -412,19 +420,30 @@ __global__ void __launch_bounds__(kGradThreads) logits_grad_kernel(const GradArg
         }
         if constexpr (LOSS) {
             if (x.lse != kNegInf) {
+                // by the row's own maximum and sum, as the losses have them: beside a maximum far from zero, lse has few bits left
+                // of the sum's logarithm, or none
+                float m = kNegInf;
+#pragma unroll
+                for (int p = 0; p < NP; ++p)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) m = fmaxf(m, x.v[p][i]);
+                m = lanes_max<L>(m);
                 float dot = 0.0f;
+                f4 sum = {0.0f, 0.0f, 0.0f, 0.0f};  // four chains: shorter ones round less
 #pragma unroll
                 for (int p = 0; p < NP; ++p)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        d[p][i] = exp_neg(x.v[p][i] - x.lse);
+                        d[p][i] = exp_neg(x.v[p][i] - m);
+                        sum[i] += d[p][i];
                         dot = fmaf(d[p][i], f[p][i], dot);
                     }
-                dot = lanes_sum<L>(dot) - (g.a.d_z ? b * x.lse : 0.0f);
+                const float inv = 1.0f / lanes_sum<L>((sum[0] + sum[1]) + (sum[2] + sum[3]));
+                dot = lanes_sum<L>(dot) * inv - (g.a.d_z ? b * x.lse : 0.0f);
 #pragma unroll
                 for (int p = 0; p < NP; ++p)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) d[p][i] *= f[p][i] - dot;
+                    for (int i = 0; i < 4; ++i) d[p][i] *= inv * (f[p][i] - dot);
             }
         }
         float *out = g.a.d_logits + (int64_t)row * E;

@@ -32,8 +32,8 @@ int32_t moe_router_abi_version(void);
  *   prob_sums[s][e] = sum of p[t][e],  tokens[s] = n
  *   balance[s]   = E / (top_k n^2) * sum over e of counts * prob_sums     (1 if both are even)
  *   z[s]         = 1 / n * sum of lse[t]^2
- * and both losses are 0 for n = 0. Probabilities, their sums over some tokens and lse are fp32, squares and the sums over
- * those and over experts 64-bit, rounded once. NaN and infinite logits of a token that counts reach the losses and
+ * and both losses are 0 for n = 0. Probabilities, a row's sum and sums over some tokens are fp32, the logarithm added to the maximum,
+ * squares and the sums over those and over experts 64-bit, rounded once. NaN and infinite logits of a token that counts reach the losses and
  * prob_sums of its own sequence only. */
 typedef struct moe_losses {
     int32_t T, E;             /* tokens, 0 <= T < 2^30; experts, 1 <= E <= 4096   */
@@ -55,8 +55,9 @@ int32_t moe_router_losses(const moe_losses *l, int32_t dtype, const void *logits
                           const uint8_t *valid, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Gradient of the logits, fp32 [T][E]: the sum of
- *   losses (l given): for each token that counts (lse[t] > -inf or a NaN), with the counts, tokens and lse of l (a
- *     program that balances over several batches or ranks puts their sums into counts and tokens) and a[e] =
+ *   losses (l given): for each token that counts (lse[t] > -inf or a NaN), with p the softmax of its logits (from the row itself, by
+ *     its maximum and sum: not from lse, which is rounded), the counts, tokens and lse of l (a program that
+ *     balances over several batches or ranks puts their sums into counts and tokens) and a[e] =
  *     d_balance[s] E / (top_k tokens[s]^2) counts[s][e], which no gradient passes through:
  *       p[t][e] (a[e] - sum over i of p[t][i] a[i])  +  2 d_z[s] / tokens[s] * lse[t] p[t][e]
  *   gate (topk_w given): at e = topk_idx[t][j], for w the softmax over the token's chosen logits that moe_route
