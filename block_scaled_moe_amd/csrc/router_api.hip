@@ -36,41 +36,7 @@ int32_t check_route_backward_sizes(const moe_route_backward_args *a) {
     return (int64_t)a->T * a->D < (1ll << 38) && (int64_t)a->E * a->D < (1ll << 32) ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
-}  // namespace
-
-extern "C" {
-
-int32_t moe_router_abi_version(void) { return MOE_ROUTER_ABI_VERSION; }
-
-size_t moe_router_losses_workspace_bytes(const moe_losses *l) {
-    return check_losses_sizes(l) == MOE_OK ? loss_plan(l->T, l->E, l->B).total : 0;
-}
-
-int32_t moe_router_losses(const moe_losses *l, int32_t dtype, const void *logits, const int32_t *topk_idx,
-                          const uint8_t *valid, void *workspace, size_t workspace_bytes, void *stream) {
-    int32_t rc = check_losses_sizes(l);
-    if (rc != MOE_OK) return rc;
-    if (!type_ok(dtype) || !l->balance || !l->z || !l->prob_sums) return MOE_ERR_INVALID_ARG;
-    rc = check_losses_read(l);
-    if (rc != MOE_OK) return rc;
-    if (l->T > 0 && (!logits || !topk_idx)) return MOE_ERR_INVALID_ARG;
-    if (!aligned(l->balance, 16) || !aligned(l->z, 16) || !aligned(l->prob_sums, 16) || !aligned(logits, 16) ||
-        !aligned(topk_idx, 16))
-        return MOE_ERR_ALIGNMENT;
-    const size_t need = loss_plan(l->T, l->E, l->B).total;
-    if (!workspace || workspace_bytes < need) return MOE_ERR_WORKSPACE;
-    if (!aligned(workspace, 16)) return MOE_ERR_ALIGNMENT;
-    const int64_t be = (int64_t)l->B * l->E;
-    if (outputs_meet({{l->balance, l->B, 4}, {l->z, l->B, 4}, {l->counts, be, 4}, {l->tokens, l->B, 4}, {l->prob_sums, be, 4},
-                      {l->lse, l->T, 4}, {workspace, 1, (int64_t)need}},
-                     {{logits, l->T, type_bytes(dtype) * l->E}, {topk_idx, l->T, 4 * (int64_t)l->top_k}, {valid, l->T, 1},
-                      {l->seq, (int64_t)l->B + 1, 4}}))
-        return MOE_ERR_INVALID_ARG;
-    return status_of(launch_router_losses(*l, dtype, logits, topk_idx, valid, static_cast<uint8_t *>(workspace),
-                                          (hipStream_t)stream));
-}
-
-int32_t moe_logits_grad(const moe_logits_grad_args *a, void *stream) {
+int32_t logits_grad(const moe_logits_grad_args *a, bool all, void *stream) {
     if (!a) return MOE_ERR_INVALID_ARG;
     int32_t rc = check_sizes(a->T, a->E, a->top_k);
     if (rc != MOE_OK) return rc;
@@ -97,8 +63,45 @@ int32_t moe_logits_grad(const moe_logits_grad_args *a, void *stream) {
                                  {l.seq, (int64_t)l.B + 1, 4}, {l.counts, l.B, 4 * row}, {l.tokens, l.B, 4}, {l.lse, a->T, 4}}))
             return MOE_ERR_INVALID_ARG;
     }
-    return status_of(launch_logits_grad(*a, (hipStream_t)stream));
+    return status_of(launch_logits_grad(*a, all, (hipStream_t)stream));
 }
+
+}  // namespace
+
+extern "C" {
+
+int32_t moe_router_abi_version(void) { return MOE_ROUTER_ABI_VERSION; }
+
+size_t moe_router_losses_workspace_bytes(const moe_losses *l) {
+    return check_losses_sizes(l) == MOE_OK ? loss_plan(l->T, l->E, l->B, l->seq).total : 0;
+}
+
+int32_t moe_router_losses(const moe_losses *l, int32_t dtype, const void *logits, const int32_t *topk_idx,
+                          const uint8_t *valid, void *workspace, size_t workspace_bytes, void *stream) {
+    int32_t rc = check_losses_sizes(l);
+    if (rc != MOE_OK) return rc;
+    if (!type_ok(dtype) || !l->balance || !l->z || !l->prob_sums) return MOE_ERR_INVALID_ARG;
+    rc = check_losses_read(l);
+    if (rc != MOE_OK) return rc;
+    if (l->T > 0 && (!logits || !topk_idx)) return MOE_ERR_INVALID_ARG;
+    if (!aligned(l->balance, 16) || !aligned(l->z, 16) || !aligned(l->prob_sums, 16) || !aligned(logits, 16) ||
+        !aligned(topk_idx, 16))
+        return MOE_ERR_ALIGNMENT;
+    const size_t need = loss_plan(l->T, l->E, l->B, l->seq).total;
+    if (!workspace || workspace_bytes < need) return MOE_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return MOE_ERR_ALIGNMENT;
+    const int64_t be = (int64_t)l->B * l->E;
+    if (outputs_meet({{l->balance, l->B, 4}, {l->z, l->B, 4}, {l->counts, be, 4}, {l->tokens, l->B, 4}, {l->prob_sums, be, 4},
+                      {l->lse, l->T, 4}, {workspace, 1, (int64_t)need}},
+                     {{logits, l->T, type_bytes(dtype) * l->E}, {topk_idx, l->T, 4 * (int64_t)l->top_k}, {valid, l->T, 1},
+                      {l->seq, (int64_t)l->B + 1, 4}}))
+        return MOE_ERR_INVALID_ARG;
+    return status_of(launch_router_losses(*l, dtype, logits, topk_idx, valid, static_cast<uint8_t *>(workspace),
+                                          (hipStream_t)stream));
+}
+
+int32_t moe_logits_grad(const moe_logits_grad_args *a, void *stream) { return logits_grad(a, false, stream); }
+int32_t moe_logits_grad_all(const moe_logits_grad_args *a, void *stream) { return logits_grad(a, true, stream); }
 
 size_t moe_route_backward_workspace_bytes(const moe_route_backward_args *a) {
     return check_route_backward_sizes(a) == MOE_OK ? route_backward_plan(*a).total : 0;

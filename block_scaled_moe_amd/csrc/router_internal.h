@@ -7,23 +7,24 @@
 
 namespace moe {
 
-// Runs of up to 2^log_rows tokens of one sequence. Run i of sequence s has number (seq[s] >> log_rows) + s + i: no two
-// runs share one, and they are fewer than (T >> log_rows) + B.
+// Runs of up to 2^log_rows tokens of one sequence. Without `seq` they are numbered in a row. Else the tokens before seq[0] and those
+// from seq[B] on count as sequences -1 and B, and run i of sequence s has number (its first token >> log_rows) + s + 1 + i: no
+// two runs share one, and they are fewer than (T >> log_rows) + B + 2.
 struct RunSplit {
     int32_t log_rows;
     int64_t n;
 };
-RunSplit run_split(int32_t T, int32_t B, int32_t rows_at_least, int32_t runs_at_most);
+RunSplit run_split(int32_t T, int32_t B, bool seq, int32_t rows_at_least, int32_t runs_at_most);
 
 // Byte offsets inside the workspace of moe_router_losses.
 struct LossPlan {
     RunSplit runs;
     size_t sums, counts, squares, tokens, parts, arrived, total;
 };
-LossPlan loss_plan(int32_t T, int32_t E, int32_t B);
+LossPlan loss_plan(int32_t T, int32_t E, int32_t B, bool seq);
 hipError_t launch_router_losses(const moe_losses &l, int32_t dtype, const void *logits, const int32_t *topk_idx,
                                 const uint8_t *valid, uint8_t *workspace, hipStream_t s);
-hipError_t launch_logits_grad(const moe_logits_grad_args &a, hipStream_t s);
+hipError_t launch_logits_grad(const moe_logits_grad_args &a, bool all, hipStream_t s);  // all: rows of tokens in no sequence too
 
 // Workspace and work of moe_route_backward.
 struct RouteBackwardPlan {

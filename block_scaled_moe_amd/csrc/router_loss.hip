@@ -81,30 +81,36 @@ __device__ __forceinline__ f4 load_piece(const T *row, int e, int E, bool whole)
     return v;
 }
 
-// Tokens row0 .. row1 - 1 of sequence s: run `run` of the batch. false: there is no such run.
+// Tokens row0 .. row1 - 1 of sequence s, or (s = -1 or B) of those before the first one or behind the last: run `run` of the batch.
+// false: there is no such run.
 struct Run {
     int32_t s, row0, row1;
 };
-__device__ __forceinline__ int32_t start_of(const int32_t *seq, int32_t s, int32_t T) { return min(max(seq[s], 0), T); }
+// First token of sequence s of -1 .. B + 1, the outer ones being the tokens in none and the end.
+__device__ __forceinline__ int32_t start_of(const int32_t *seq, int32_t s, int32_t T, int32_t B) {
+    return s < 0 ? 0 : s > B ? T : min(max(seq[s], 0), T);
+}
 __device__ __forceinline__ bool find_run(const int32_t *seq, int32_t T, int32_t B, int32_t log_rows, int64_t run, Run &r) {
     int32_t lo = 0, hi = T;
     r.s = 0;
     if (seq) {
         // the last sequence whose first run is not behind `run`: a wave's lanes look at 64 of them at a time
-        int32_t a = 0, n = B;
+        int32_t a = 0, n = B + 2;  // numbered from -1 on
         for (;;) {
             const int32_t step = (n + 63) / 64, at = a + (threadIdx.x & 63) * step;
-            const bool before = at < a + n && (int64_t)(start_of(seq, min(at, B), T) >> log_rows) + at <= run;
+            const bool before = at < a + n && (int64_t)(start_of(seq, min(at, B + 1) - 1, T, B) >> log_rows) + at <= run;
             const int32_t last = max(__popcll(__ballot(before)), 1) - 1;
             a += last * step;
             if (step == 1) break;
             n = min(step, n - last * step);
         }
-        r.s = __builtin_amdgcn_readfirstlane(a);
-        lo = start_of(seq, r.s, T);
-        hi = start_of(seq, r.s + 1, T);
+        a = __builtin_amdgcn_readfirstlane(a);
+        r.s = a - 1;
+        lo = start_of(seq, r.s, T, B);
+        hi = start_of(seq, r.s + 1, T, B);
+        run -= a;
     }
-    const int64_t first = (int64_t)lo + ((run - ((lo >> log_rows) + r.s)) << log_rows);
+    const int64_t first = (int64_t)lo + ((run - (lo >> log_rows)) << log_rows);
     if (first < lo || first >= hi) return false;
     r.row0 = (int32_t)first;
     r.row1 = (int32_t)min((int64_t)hi, first + (1 << log_rows));
@@ -137,10 +143,17 @@ __global__ void __launch_bounds__(kThreads) loss_kernel(const LossArgs a) {
     const int t = threadIdx.x, lane = t % L, group = t / L;
     const int E = a.l.E, k = a.l.top_k;
     if (!ONE && t == 0 && (int)blockIdx.x < a.l.B) a.arrived[blockIdx.x] = 0;
-    Run r;
-    if (!find_run(a.l.seq, a.l.T, a.l.B, a.log_rows, blockIdx.x, r)) {
-        if (!ONE) return;
-        r = {0, 0, 0};
+    Run r = {0, 0, a.l.T};
+    if constexpr (ONE) {
+        if (a.l.seq) r = {0, start_of(a.l.seq, 0, a.l.T, 1), start_of(a.l.seq, 1, a.l.T, 1)};
+        for (int row = t; row < a.l.T; row += kThreads)
+            if (row < r.row0 || row >= r.row1) a.l.lse[row] = kNegInf;
+    } else {
+        if (!find_run(a.l.seq, a.l.T, a.l.B, a.log_rows, blockIdx.x, r)) return;
+        if (r.s < 0 || r.s == a.l.B) {  // in no sequence
+            for (int row = r.row0 + t; row < r.row1; row += kThreads) a.l.lse[row] = kNegInf;
+            return;
+        }
     }
     f4 acc[NP];
 #pragma unroll
@@ -263,11 +276,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LossArgs a) {
     const int s = blockIdx.x / ne, eb = blockIdx.x % ne, t = threadIdx.x;
     const int e = eb * EXPERTS + t % EXPERTS;
     int32_t lo = 0, hi = a.l.T;
+    int64_t first = 0;
     if (a.l.seq) {
-        lo = start_of(a.l.seq, s, a.l.T);
-        hi = start_of(a.l.seq, s + 1, a.l.T);
+        lo = start_of(a.l.seq, s, a.l.T, a.l.B);
+        hi = start_of(a.l.seq, s + 1, a.l.T, a.l.B);
+        first = (lo >> a.log_rows) + s + 1;
     }
-    const int64_t first = (lo >> a.log_rows) + s;
     const int n = hi > lo ? (hi - lo + (1 << a.log_rows) - 1) >> a.log_rows : 0;
     double p = 0.0, z = 0.0;
     int32_t c = 0, m = 0;
@@ -343,6 +357,7 @@ struct GradArgs {
     moe_logits_grad_args a;
     moe_losses l;
     int32_t log_rows, whole;
+    int32_t all;  // rows of tokens in no sequence too
 };
 
 // LOSS: the gradients of the losses; GATE: those of the gate's weights, put into their places of a row in LDS, from where the
@@ -355,6 +370,8 @@ __global__ void __launch_bounds__(kGradThreads) logits_grad_kernel(const GradArg
     const int E = g.a.E, k = g.a.top_k;
     Run r;
     if (!find_run(LOSS ? g.l.seq : nullptr, g.a.T, LOSS ? g.l.B : 1, g.log_rows, blockIdx.x, r)) return;
+    const bool outside = LOSS && (r.s < 0 || r.s == g.l.B);  // in no sequence
+    if (outside && !g.all) return;
     if constexpr (GATE) {
 #pragma unroll
         for (int p = 0; p < NP; ++p) *reinterpret_cast<f4 *>(&gate[group][4 * (p * L + lane)]) = (f4){0.0f, 0.0f, 0.0f, 0.0f};
@@ -374,7 +391,7 @@ __global__ void __launch_bounds__(kGradThreads) logits_grad_kernel(const GradArg
             x.dw = slot ? g.a.d_topk_w[(int64_t)row * k + lane] : 0.0f;
         }
         if constexpr (LOSS) {
-            x.lse = g.l.lse[row];
+            x.lse = outside ? kNegInf : g.l.lse[row];
 #pragma unroll
             for (int p = 0; p < NP; ++p) x.v[p] = load_piece(logits + (int64_t)row * E, 4 * (p * L + lane), E, g.whole);
         }
@@ -384,7 +401,7 @@ __global__ void __launch_bounds__(kGradThreads) logits_grad_kernel(const GradArg
     f4 f[NP];
     float b = 0.0f;
     if constexpr (LOSS) {
-        const int32_t n = g.l.tokens[r.s];
+        const int32_t n = outside ? 0 : g.l.tokens[r.s];
         float a = 0.0f;
         if (n != 0) {
             if (g.a.d_balance) a = (float)((double)g.a.d_balance[r.s] * E / ((double)k * n * n));
@@ -395,7 +412,7 @@ __global__ void __launch_bounds__(kGradThreads) logits_grad_kernel(const GradArg
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int e = 4 * (p * L + lane) + i;
-                f[p][i] = e < E && g.a.d_balance ? a * (float)g.l.counts[(int64_t)r.s * E + e] : 0.0f;
+                f[p][i] = e < E && g.a.d_balance && !outside ? a * (float)g.l.counts[(int64_t)r.s * E + e] : 0.0f;
             }
     }
     for (int row = r.row0 + group; row < r.row1; row += kGroups) {
@@ -487,17 +504,17 @@ int32_t row_lanes(int32_t E) { return E <= 256 ? 16 : E <= 512 ? 32 : 64; }
 
 }  // namespace
 
-RunSplit run_split(int32_t T, int32_t B, int32_t rows_at_least, int32_t runs_at_most) {
+RunSplit run_split(int32_t T, int32_t B, bool seq, int32_t rows_at_least, int32_t runs_at_most) {
     RunSplit r{};
     while ((1 << r.log_rows) < rows_at_least) ++r.log_rows;
     while ((T >> r.log_rows) > runs_at_most) ++r.log_rows;
-    r.n = B == 1 ? ((int64_t)T + (1 << r.log_rows) - 1) >> r.log_rows : ((int64_t)T >> r.log_rows) + B;
+    r.n = seq ? ((int64_t)T >> r.log_rows) + B + 2 : ((int64_t)T + (1 << r.log_rows) - 1) >> r.log_rows;
     return r;
 }
 
-LossPlan loss_plan(int32_t T, int32_t E, int32_t B) {
+LossPlan loss_plan(int32_t T, int32_t E, int32_t B, bool seq) {
     LossPlan p{};
-    p.runs = run_split(T, B, 2 * kThreads / row_lanes(E), 512);
+    p.runs = run_split(T, B, seq, 2 * kThreads / row_lanes(E), 512);
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -516,7 +533,7 @@ LossPlan loss_plan(int32_t T, int32_t E, int32_t B) {
 
 hipError_t launch_router_losses(const moe_losses &l, int32_t dtype, const void *logits, const int32_t *topk_idx,
                                 const uint8_t *valid, uint8_t *workspace, hipStream_t s) {
-    const LossPlan p = loss_plan(l.T, l.E, l.B);
+    const LossPlan p = loss_plan(l.T, l.E, l.B, l.seq);
     LossArgs a{};
     a.l = l;
     a.log_rows = p.runs.log_rows;
@@ -530,7 +547,7 @@ hipError_t launch_router_losses(const moe_losses &l, int32_t dtype, const void *
     a.tokens = reinterpret_cast<int32_t *>(workspace + p.tokens);
     a.parts = reinterpret_cast<double *>(workspace + p.parts);
     a.arrived = reinterpret_cast<uint32_t *>(workspace + p.arrived);
-    const bool one = l.B == 1 && p.runs.n <= 1;
+    const bool one = l.B == 1 && l.T <= 1 << p.runs.log_rows;
     by_row(l.E, [&](auto L, auto NP) {
         constexpr int kL = decltype(L)::value, kNP = decltype(NP)::value;
         auto go = [&](auto kernel) {
@@ -553,12 +570,13 @@ hipError_t launch_router_losses(const moe_losses &l, int32_t dtype, const void *
     return hipGetLastError();
 }
 
-hipError_t launch_logits_grad(const moe_logits_grad_args &args, hipStream_t s) {
+hipError_t launch_logits_grad(const moe_logits_grad_args &args, bool all, hipStream_t s) {
     const int32_t B = args.l ? args.l->B : 1;
-    const RunSplit runs = run_split(args.T, B, kGradThreads / row_lanes(args.E), 1024);
+    const RunSplit runs = run_split(args.T, B, args.l && args.l->seq, kGradThreads / row_lanes(args.E), 1024);
     GradArgs g{};
     g.a = args;
     if (args.l) g.l = *args.l;
+    g.all = all;
     g.log_rows = runs.log_rows;
     g.whole = args.E % 4 == 0;
     by_row(args.E, [&](auto L, auto NP) {

@@ -50,6 +50,7 @@ SIGNATURES = {
     "moe_router_losses_workspace_bytes": ([_L], _Z),
     "moe_router_losses": ([_L, _I, _P, _P, _P, _P, _Z, _P], _I),
     "moe_logits_grad": ([ctypes.POINTER(MoeLogitsGradArgs), _P], _I),
+    "moe_logits_grad_all": ([ctypes.POINTER(MoeLogitsGradArgs), _P], _I),
     "moe_route_backward_workspace_bytes": ([_B], _Z),
     "moe_route_backward": ([_B, _P], _I),
 }
@@ -152,7 +153,7 @@ class RouterLosses:
 
     @_once
     def lse(self) -> torch.Tensor:
-        """fp32 [T]; -inf: the token does not count."""
+        """fp32 [T]; -inf: the token does not count, or lies in no sequence."""
         return self.buffer.as_strided((self.T,), (1,), self._at[1])
 
     def check(self):
@@ -167,7 +168,7 @@ def router_losses(logits: torch.Tensor, topk_idx: torch.Tensor, valid: torch.Ten
                   seq: torch.Tensor | None = None, out: RouterLosses | None = None) -> RouterLosses:
     """logits [T, E] (fp32 or bf16) and topk_idx int32 [T, k] -> RouterLosses (moe_router_losses). valid: bool or uint8 [T],
     the tokens that count (default: all). seq: int32 [B + 1] starts of packed sequences, each with losses of its own
-    (default: one sequence). `out`: losses of the same sizes to fill again, which hold their own seq."""
+    (default: one sequence); tokens before the first one or from the last start on count nowhere. `out`: losses of the same sizes to fill again, which hold their own seq."""
     T, E = _matrix("logits", logits)
     k = _matrix("topk_idx", topk_idx)[1]
     dev = logits.device
@@ -190,7 +191,9 @@ def logits_grad(logits: torch.Tensor, topk_idx: torch.Tensor, losses: RouterLoss
                 d_balance: torch.Tensor | None = None, d_z: torch.Tensor | None = None, topk_w: torch.Tensor | None = None,
                 d_topk_w: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
     """Gradient of the logits, fp32 [T, E] (moe_logits_grad): of the losses (d_balance and d_z fp32 [B], None: no
-    gradient), of the gate's weights (topk_w and d_topk_w fp32 [T, k]; without `losses` of them alone), or of both."""
+    gradient), of the gate's weights (topk_w and d_topk_w fp32 [T, k]; without `losses` of them alone), or of both. Tokens
+    that do not count or lie in no sequence have the gate's gradient alone, or zeros. In a given `out` the rows of tokens in no
+    sequence keep what they hold."""
     T, E = _matrix("logits", logits)
     k = _matrix("topk_idx", topk_idx)[1]
     dev = logits.device
@@ -216,10 +219,11 @@ def logits_grad(logits: torch.Tensor, topk_idx: torch.Tensor, losses: RouterLoss
         for what, t in (("d_balance", d_balance), ("d_z", d_z)):
             if t is not None:
                 _ask(what, t, (losses.B,), torch.float32, dev)
+    name = "moe_logits_grad_all" if out is None else "moe_logits_grad"
     out = _out("out", out, (T, E), torch.float32, dev)
     a = MoeLogitsGradArgs(T, E, k, DTYPES[logits.dtype], l, logits.data_ptr(), _ptr(d_balance), _ptr(d_z), topk_idx.data_ptr(),
                           _ptr(topk_w), _ptr(d_topk_w), out.data_ptr())
-    _call("moe_logits_grad", dev, ctypes.byref(a))
+    _call(name, dev, ctypes.byref(a))
     return out
 
 

@@ -24,7 +24,7 @@ int32_t moe_router_abi_version(void);
 /* Losses of the B sequences of a batch of T tokens. Sequence s holds tokens seq[s] .. seq[s + 1] - 1
  * (0 <= seq[0] <= .. <= seq[B] <= T, on the device; values outside 0 .. T are taken as the nearer end, and other
  * orders give wrong sums, never a wrong access). A sequence may be empty, and tokens before seq[0] or from seq[B] on
- * are in none: their rows of lse and of d_logits keep what they hold.
+ * are in none: they count nowhere, and their lse is -inf.
  * A token counts if valid[t] != 0 (valid NULL: every token) and any of its logits is above -inf or a
  * NaN; the rows of others may hold anything. Over the tokens of s that count, with n their number:
  *   p[t][e]      = exp(l[t][e] - lse[t]),  lse[t] = log sum over e of exp(l[t][e])   (-inf: does not count)
@@ -63,8 +63,9 @@ int32_t moe_router_losses(const moe_losses *l, int32_t dtype, const void *logits
  *   gate (topk_w given): at e = topk_idx[t][j], for w the softmax over the token's chosen logits that moe_route
  *     returns, g[j] = topk_w[t][j] (d_topk_w[t][j] - sum over i of topk_w[t][i] d_topk_w[t][i]); slots whose index
  *     is outside 0 .. E - 1 take part in nothing, several slots of one expert add up.
- * d_balance, d_z: fp32 [B] gradients of the losses, 4-byte aligned; NULL: that loss has none. With l, rows of tokens in no sequence
- * keep what they hold; without, logits is not read (may be NULL) and every row is written. */
+ * d_balance, d_z: fp32 [B] gradients of the losses, 4-byte aligned; NULL: that loss has none. With l, moe_logits_grad leaves the rows of
+ * tokens in no sequence as they are, and moe_logits_grad_all writes every row: theirs are the gate's gradient alone, zeros
+ * without it. Without l, logits is not read (may be NULL) and either writes every row. */
 typedef struct moe_logits_grad_args {
     int32_t T, E, top_k;      /* as in moe_losses */
     int32_t dtype;            /* of logits */
@@ -76,6 +77,7 @@ typedef struct moe_logits_grad_args {
     float *d_logits;          /* [T][E] */
 } moe_logits_grad_args;
 int32_t moe_logits_grad(const moe_logits_grad_args *a, void *stream);
+int32_t moe_logits_grad_all(const moe_logits_grad_args *a, void *stream);
 
 /* Gradients of the router's product logits = h wr^T + bias:
  *   dh [T][D] = d_logits wr,  dwr [E][D] = d_logits^T h,  dbias[e] = sum over t of d_logits[t][e]

@@ -146,3 +146,93 @@ def test_log_sum_exp_is_rounded_once(E):
     # a lane's values, their exchanges; log(f) of f in 1/2 .. 1 is below one: a unit and a half of its last place at most
     off = (ex * ref.exp_error(l - m)).sum(1) / ex.sum(1) + ((E + 63) // 64 + 6) * U24 + 2 * U24
     assert (np.abs(got - want) <= off + U24 * np.exp2(np.ceil(np.log2(np.abs(want))))).all()
+
+
+def poison(*shapes):
+    """Leaves NaN in memory that the allocator will hand out next."""
+    kept = [torch.full(s, float("nan"), device="cuda") for s in shapes for _ in range(3)]
+    torch.cuda.synchronize()
+    del kept
+
+
+OUTSIDE = {"both": (700, [90, 300, 300, 610]), "behind": (1000, [0, 400, 940]), "before": (300, [299, 300, 300]), "one": (200, [150, 190]),
+           "one small": (14, [3, 9]), "one of none": (100, [40, 40]), "small of none": (12, [5, 5]), "none": (50, [0, 0, 0]), "end": (60, [60, 60, 60]),
+           "many": (5000, sorted(np.random.default_rng(0).integers(700, 4200, 300).tolist())), "outside": (80, [-5, 20, 95]), "long": (70000, [33000, 33100, 66000])}
+
+
+@pytest.mark.parametrize("name", OUTSIDE)
+@pytest.mark.parametrize("E,dtype", [(60, FP32), (61, BF16), (384, FP32), (1100, FP32)])
+@pytest.mark.parametrize("with_gate", [False, True])
+def test_tokens_in_no_sequence(name, E, dtype, with_gate):
+    """They count nowhere: lse is -inf, and their rows of a new gradient are the gate's alone, or zeros."""
+    T, seq = OUTSIDE[name]
+    k = 4
+    rng = np.random.default_rng(T + E)
+    x = rng.standard_normal((T, E)).astype(np.float32) * 2
+    of = ref.sequence_of(seq, T)
+    x[of < 0] = np.nan  # not looked at
+    t, idx = dev(x, dtype), slots(rng, T, E, k)
+    B = len(seq) - 1
+    db, dz = rng.standard_normal(B).astype(np.float32), rng.standard_normal(B).astype(np.float32)
+    w, dw = (rng.random((T, k)).astype(np.float32), rng.standard_normal((T, k)).astype(np.float32)) if with_gate else (None, None)
+    opt = lambda a: None if a is None else dev(a)
+    args = (t, dev(idx), dev(np.array(seq, np.int32)), dev(db), dev(dz), opt(w), opt(dw))
+    poison((T,), (T, E), (4 * T + 64 * E,))
+    l = moe.router_losses(args[0], args[1], seq=args[2])
+    d = moe.logits_grad(args[0], args[1], l, *args[3:])
+    values, bounds, _, _ = ref.losses(np.where(of[:, None] < 0, 0.0, num(t)), idx, None, seq, k)
+    assert np.isneginf(host(l.lse)[of < 0]).all()
+    ref.close(host(l.lse), values["lse"], np.where(of < 0, 0.0, bounds["lse"]), "lse")
+    assert np.array_equal(host(l.counts), values["counts"]) and np.array_equal(host(l.tokens), values["tokens"])
+    for n in ("balance", "z", "prob_sums"):
+        ref.close(host(getattr(l, n)), values[n], bounds[n], n)
+    want, bound, _ = gradient(np.where(of[:, None] < 0, 0.0, num(t)), idx, None, seq, k, db.astype(np.float64), dz.astype(np.float64))
+    if with_gate:
+        gate, off = ref.logits_grad(np.zeros((T, E)), idx, None, None, None, w, dw, None, k)
+        want, bound = want + gate, bound + off + 2 * U24 * np.abs(want + gate)
+    else:
+        assert not host(d)[of < 0].any()
+    ref.close(host(d), want, bound, "d_logits")
+    kept = torch.full((T, E), 77.0, device="cuda")  # a given buffer keeps those rows
+    assert moe.logits_grad(args[0], args[1], l, *args[3:], out=kept) is kept
+    assert (host(kept)[of < 0] == 77.0).all() and torch.equal(kept[dev(of >= 0)], d[dev(of >= 0)])
+
+
+def test_router_gradient_of_a_padded_batch():
+    """router_losses, logits_grad, route_backward: padding before the first and behind the last sequence adds nothing."""
+    rng = np.random.default_rng(9)
+    T, E, D, k, seq = 300, 48, 128, 3, [20, 100, 250]
+    h, wr = dev(rng.standard_normal((T, D)).astype(np.float32), BF16), dev(rng.standard_normal((E, D)).astype(np.float32), BF16)
+    x, idx = dev(rng.standard_normal((T, E)).astype(np.float32)), dev(slots(rng, T, E, k))
+    ones = torch.ones(2, device="cuda")
+    poison((T,), (T, E), (4 * T + 16 * E,))
+    l = moe.router_losses(x, idx, seq=dev(np.array(seq, np.int32)))
+    d = moe.logits_grad(x, idx, l, ones, ones)
+    dh, dwr, dbias = moe.route_backward(h, wr, d, dh_dtype=FP32, want_bias=True)
+    d64 = num(d).astype(np.float64)
+    assert not d64[:20].any() and not d64[250:].any() and not dh[:20].any() and not dh[250:].any()
+    y, bound, _ = ref.product(np.ascontiguousarray(d64[20:250].T), num(h)[20:250].astype(np.float64), False, 3, 256)
+    ref.close(num(dwr), y, bound, "dwr")
+    assert np.isfinite(num(dbias)).all()
+
+
+def test_sequences_that_move_between_calls():
+    """The starts are read when the calls run: a token that left its sequence has no lse and no gradient of the losses any more."""
+    rng = np.random.default_rng(10)
+    T, E = 400, 64
+    x, idx = dev(rng.standard_normal((T, E)).astype(np.float32)), dev(slots(rng, T, E, 2))
+    seq = dev(np.array([0, 200, 400], np.int32))
+    l, ones = moe.router_losses(x, idx, seq=seq), torch.ones(2, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.router_losses(x, idx, out=l)
+        d = moe.logits_grad(x, idx, l, ones, ones)
+    for starts in ([0, 200, 400], [100, 150, 300], [0, 0, 50], [390, 400, 400], [0, 399, 400]):
+        seq.copy_(dev(np.array(starts, np.int32)))
+        graph.replay()
+        torch.cuda.synchronize()
+        kept = [t.clone() for t in (d, l.lse, l.balance, l.counts)]
+        again = moe.router_losses(x, idx, seq=seq)
+        eager = [moe.logits_grad(x, idx, again, ones, ones), again.lse, again.balance, again.counts]
+        assert all(torch.equal(a, b) for a, b in zip(kept, eager)), starts
+        assert bool(torch.isneginf(l.lse[:starts[0]]).all()) and bool(torch.isneginf(l.lse[starts[2]:]).all())

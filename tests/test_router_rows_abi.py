@@ -1,0 +1,37 @@
+"""moe_logits_grad_all of include/moe_router.h on the host (no GPU needed): the refusals of moe_logits_grad, before anything is
+enqueued."""
+import ctypes
+
+import pytest
+
+import block_scaled_moe_amd as moe
+from block_scaled_moe_amd import router
+
+OK, EINVAL, EUNSUP, EALIGN = 0, -1, -2, -3
+A, FAR = 1 << 40, 1 << 36  # fake, aligned "device" addresses, never dereferenced on these paths
+NO_L = ctypes.POINTER(router.MoeLosses)()
+
+
+def run(name, over_l=(), **over):
+    l = router.MoeLosses(100, 64, 4, 3, *(A + i * FAR for i in range(7)))
+    for k, v in dict(over_l).items():
+        setattr(l, k, v)
+    a = router.MoeLogitsGradArgs(100, 64, 4, 2, ctypes.pointer(l), *(A + i * FAR for i in range(10, 17)))
+    for k, v in over.items():
+        setattr(a, k, v)
+    return getattr(moe.lib(), name)(ctypes.byref(a), None)
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(T=-1), EINVAL), (dict(T=1 << 30), EUNSUP), (dict(T=99), EINVAL), (dict(E=65), EINVAL), (dict(dtype=0), EINVAL), (dict(logits=0), EINVAL),
+    (dict(topk_w=0), EINVAL), (dict(topk_idx=0), EINVAL), (dict(d_logits=0), EINVAL), (dict(l=NO_L), EINVAL), (dict(logits=A + 2), EALIGN),
+    (dict(d_logits=A + 8), EALIGN), (dict(d_logits=A + 10 * FAR), EINVAL), (dict(d_logits=A + 6 * FAR), EINVAL), (dict(over_l=dict(lse=0)), EINVAL),
+    (dict(over_l=dict(T=0), T=0, d_logits=0, logits=0), OK)])
+def test_both_forms_refuse_alike(over, status):
+    assert run("moe_logits_grad_all", **over) == run("moe_logits_grad", **over) == status
+    assert moe.lib().moe_logits_grad_all(None, None) == EINVAL
+
+
+def test_a_batch_of_sequences_needs_lines_for_what_is_in_none():
+    size = lambda seq: moe.lib().moe_router_losses_workspace_bytes(ctypes.byref(router.MoeLosses(100, 64, 4, 1, seq)))
+    assert size(A) > size(0) > 0
