@@ -18,6 +18,7 @@ int32_t check_losses_sizes(const moe_losses *l) {
     const int32_t rc = check_sizes(l->T, l->E, l->top_k);
     if (rc != MOE_OK) return rc;
     if (l->B < 1 || (!l->seq && l->B != 1)) return MOE_ERR_INVALID_ARG;
+    if ((int64_t)l->T * l->top_k > INT32_MAX) return MOE_ERR_UNSUPPORTED;  // one expert may have every slot
     return l->B < (1 << 14) ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 

@@ -37,7 +37,7 @@ int32_t moe_router_abi_version(void);
  * prob_sums of its own sequence only. */
 typedef struct moe_losses {
     int32_t T, E;             /* tokens, 0 <= T < 2^30; experts, 1 <= E <= 4096   */
-    int32_t top_k, B;         /* 1 <= top_k <= 8; sequences, 1 <= B < 2^14        */
+    int32_t top_k, B;         /* 1 <= top_k <= 8, T * top_k < 2^31; sequences, 1 <= B < 2^14 */
     const int32_t *seq;       /* [B + 1], or NULL: one sequence of all tokens (B = 1) */
     float *balance, *z;       /* [B] */
     int32_t *counts;          /* [B][E] */

@@ -35,3 +35,13 @@ def test_both_forms_refuse_alike(over, status):
 def test_a_batch_of_sequences_needs_lines_for_what_is_in_none():
     size = lambda seq: moe.lib().moe_router_losses_workspace_bytes(ctypes.byref(router.MoeLosses(100, 64, 4, 1, seq)))
     assert size(A) > size(0) > 0
+
+
+@pytest.mark.parametrize("T,top_k,fits", [((1 << 28) - 1, 8, True), (1 << 28, 8, False), ((1 << 30) - 1, 2, True), ((1 << 30) - 1, 3, False), ((1 << 30) - 1, 1, True)])
+def test_counts_of_slots_fit_their_type(T, top_k, fits):
+    """All slots may be of one expert, whose count is a 32-bit number."""
+    l = router.MoeLosses(T, 64, top_k, 3, *(A + i * 16 * FAR for i in range(7)))
+    assert (moe.lib().moe_router_losses_workspace_bytes(ctypes.byref(l)) > 0) == fits
+    if not fits:
+        call = moe.lib().moe_router_losses(ctypes.byref(l), 2, A + 200 * FAR, A + 220 * FAR, None, A + 240 * FAR, 1 << 34, None)
+        assert call == EUNSUP and run("moe_logits_grad", dict(T=T, top_k=top_k), T=T, top_k=top_k) == EUNSUP
