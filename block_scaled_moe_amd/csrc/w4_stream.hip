@@ -220,40 +220,32 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) stream_kernel(const W4Ge
     }
 }
 
-// 17 to 64 rows of one group: a workgroup takes two column tiles, its waves a part of the steps each, and their partial sums
-// meet in LDS in the waves' order. MOST: pieces of 16 rows in a turn at most.
-template <int GROUP, bool HALF, bool ZEROS, int MOST, int WAVES>
-__global__ void __launch_bounds__(64 * WAVES, 2) wide_stream_kernel(const W4GemmArgs p) {
+// 17 to kWideRows rows of the one weight there is (no groups, so x's rows are in order): a workgroup takes two column tiles, its waves a
+// part of the steps each, and their partial sums meet in LDS in the waves' order. Turns of up to 64 rows, each of which reads the weights.
+constexpr int kWideWaves = 8, kWidePieces = 4;  // of 16 rows in a turn
+template <int GROUP, bool HALF, bool ZEROS>
+__global__ void __launch_bounds__(64 * kWideWaves, 2) wide_stream_kernel(const W4GemmArgs p) {
     constexpr int kGroups = kW4Step / GROUP;      // per step
     constexpr int kWords = (kGroups + 1) / 2;     // of scales
     constexpr int kZeroWords = (kGroups + 3) / 4;
-    __shared__ __attribute__((aligned(16))) float part[WAVES][16 * MOST][36];
+    __shared__ __attribute__((aligned(16))) float part[kWideWaves][16 * kWidePieces][36];
     const Expander expand;
     const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
     const int i16 = lane & 15, g = lane >> 4;
     const int N = p.w.N, K = p.w.K;
     const int nb = p.swiglu ? (p.C + 15) / 16 : (p.C + 31) / 32;
-    const int tile = blockIdx.x / nb, cb = blockIdx.x % nb;
-    int e = 0, p0 = tile * kGroupTile, rows = p.v.rows - p0;
-    if (p.v.offsets) {
-        // all at once: behind the last tile they are not used
-        const int n_tiles = scalar_load(&p.v.ctrl->n_tiles);
-        e = scalar_load(p.v.tile_expert + tile);
-        p0 = scalar_load(p.v.tile_row0 + tile);
-        if (tile >= n_tiles) return;
-        rows = scalar_load(p.v.offsets + e + 1) - p0;
-    }
+    const int cb = blockIdx.x, rows = p.v.rows;
     const uint8_t *codes[2], *scales[2], *zeros[2];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         // this lane's weight row: past the end the last one, which is not stored
         const int n = p.swiglu ? min(16 * cb + i16, p.C - 1) + q * p.C : min(32 * cb + 16 * q + i16, N - 1);
-        const int64_t at = ((int64_t)e * p.tiles + (n >> 4)) * p.steps, in = n & 15;
+        const int64_t at = (int64_t)(n >> 4) * p.steps, in = n & 15;
         codes[q] = reinterpret_cast<const uint8_t *>(p.w.codes) + at * 2048 + (16 * g + in) * 16;
         scales[q] = reinterpret_cast<const uint8_t *>(p.w.scales) + (at * 16 + in) * (2 * kGroups);
         zeros[q] = ZEROS ? p.w.zeros + (at * 16 + in) * kGroups : nullptr;
     }
-    const int s0 = wave * p.steps / WAVES, s1 = (wave + 1) * p.steps / WAVES;
+    const int s0 = wave * p.steps / kWideWaves, s1 = (wave + 1) * p.steps / kWideWaves;
 
     struct Weights {
         u32x4 c[2][2];
@@ -292,7 +284,6 @@ __global__ void __launch_bounds__(64 * WAVES, 2) wide_stream_kernel(const W4Gemm
 
     Weights first;
     if (s0 < s1) load(s0, first);
-    rows = min(rows, kGroupTile);
 
     // MT pieces of 16 rows from m0 on
     auto turn = [&](int m0, auto mt_c) __attribute__((always_inline)) {
@@ -300,11 +291,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) wide_stream_kernel(const W4Gemm
         constexpr int kRuns = MT > 2 ? 4 : 8;  // of 32 columns whose rows are loaded together
         const uint16_t *x[MT];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const int pos = p0 + min(m0 + 16 * m + i16, rows - 1);
-            const int64_t row = p.by_token ? token_of(p.v.sorted_slot[pos], p) : pos;
-            x[m] = p.x + row * K + 8 * g;
-        }
+        for (int m = 0; m < MT; ++m) x[m] = p.x + (int64_t)min(m0 + 16 * m + i16, rows - 1) * K + 8 * g;
         f4 acc[MT][2] = {};
         Weights next = first;
         if (m0 > 0 && s0 < s1) load(s0, next);
@@ -360,16 +347,16 @@ __global__ void __launch_bounds__(64 * WAVES, 2) wide_stream_kernel(const W4Gemm
 #pragma unroll
                 for (int v = 0; v < 4; ++v) part[wave][16 * m + 4 * g + v][16 * q + i16] = acc[m][q][v];
         __syncthreads();
-        for (int r = t >> 4; r < min(16 * MT, rows - m0); r += 4 * WAVES) {
+        for (int r = t >> 4; r < min(16 * MT, rows - m0); r += 4 * kWideWaves) {
             float y[2];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const int c = p.swiglu ? 16 * q + (t & 15) : 2 * (t & 15) + q;
                 y[q] = part[0][r][c];
 #pragma unroll
-                for (int k = 1; k < WAVES; ++k) y[q] += part[k][r][c];
+                for (int k = 1; k < kWideWaves; ++k) y[q] += part[k][r][c];
             }
-            const int64_t row = (int64_t)(p0 + m0 + r) * p.C;
+            const int64_t row = (int64_t)(m0 + r) * p.C;
             if (p.swiglu) {
                 const int c = 16 * cb + (t & 15);
                 const float v = swiglu(y[0], y[1]);
@@ -427,7 +414,7 @@ hipError_t launch_w4_gemm(const W4GemmArgs &args, hipStream_t s) {
         auto go = [&](auto kernel, int per_group) {
             hipLaunchKernelGGL(kernel, dim3((unsigned)(a.v.max_tiles * a.shares * ((nb + per_group - 1) / per_group))), dim3(512), 0, s, a);
         };
-        if (!a.v.offsets && rows > kStreamRows) go(wide_stream_kernel<kGroup, kHalf, kZeros, 4, 8>, 1);
+        if (!a.v.offsets && rows > kStreamRows) go(wide_stream_kernel<kGroup, kHalf, kZeros>, 1);
         else if (blocks >= 4096) go(stream_kernel<kGroup, kHalf, kZeros, 1>, 8);
         else if (blocks >= 1024) go(stream_kernel<kGroup, kHalf, kZeros, 4>, 2);
         else go(stream_kernel<kGroup, kHalf, kZeros, 8>, 1);
