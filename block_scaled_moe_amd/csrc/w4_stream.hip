@@ -13,6 +13,42 @@ namespace {
 
 using namespace w4;
 
+// A step of 256 columns of one weight row as a lane holds it: four words of codes of each half, the groups' scales and zero points.
+template <int GROUP, bool ZEROS>
+struct Step {
+    static constexpr int kGroups = kW4Step / GROUP, kWords = (kGroups + 1) / 2, kZeroWords = (kGroups + 3) / 4;
+    u32x4 c[2];
+    uint32_t s[kWords], z[kZeroWords];
+    // from the step's places in the packed arrays, and this lane's in them
+    __device__ __forceinline__ void load(const uint8_t *codes, uint32_t code_at, const uint8_t *scales, const uint8_t *zeros, uint32_t scale_at) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            c[h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(codes + (code_at + h * 1024)));
+        const uint8_t *sp = scales + scale_at;
+        if constexpr (kWords == 1) {
+            s[0] = *reinterpret_cast<const uint32_t *>(sp);
+        } else if constexpr (kWords == 2) {
+            const u32x2 v = *reinterpret_cast<const u32x2 *>(sp);
+            s[0] = v.x, s[1] = v.y;
+        } else {
+            const u32x4 v = *reinterpret_cast<const u32x4 *>(sp);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i] = v[i];
+        }
+        if constexpr (ZEROS) {
+            const uint8_t *zp = zeros + scale_at / 2;
+            if constexpr (kGroups == 2) {
+                z[0] = *reinterpret_cast<const uint16_t *>(zp);
+            } else if constexpr (kGroups == 4) {
+                z[0] = *reinterpret_cast<const uint32_t *>(zp);
+            } else {
+                const u32x2 v = *reinterpret_cast<const u32x2 *>(zp);
+                z[0] = v.x, z[1] = v.y;
+            }
+        }
+    }
+};
+
 // Up to 16 or 32 rows a turn: they go into LDS once for the workgroup's eight waves (in parts of the reduction where they
 // do not fit), and KS waves share two column tiles, each with a part of the steps; their sums meet in LDS in the waves' order.
 // 16 + z is a bf16 as 16 + q is, so it is taken off by a second MFMA on the same rows, which leaves four multiply-adds
@@ -21,8 +57,6 @@ constexpr int kStreamWaves = 8, kStreamX = 60 * 1024;  // waves, LDS bytes of ro
 template <int GROUP, bool HALF, bool ZEROS, int KS>
 __global__ void __launch_bounds__(64 * kStreamWaves, 4) stream_kernel(const W4GemmArgs p) {
     constexpr int kGroups = kW4Step / GROUP;      // per step
-    constexpr int kWords = (kGroups + 1) / 2;     // of scales
-    constexpr int kZeroWords = (kGroups + 3) / 4;
     constexpr int kBlocks = kStreamWaves / KS;    // of two column tiles a workgroup
     // two pieces of 16 rows share the expanded codes where registers (not beside finest groups or zero points) and LDS (not
     // beside shared columns) allow it
@@ -65,41 +99,12 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) stream_kernel(const W4Ge
         scale_at[q] = (next * steps * 16 + in) * (2 * kGroups);
     }
 
-    struct Weights {
-        u32x4 c[2][2];
-        uint32_t s[2][kWords], z[2][kZeroWords];
-    };
+    typedef Step<GROUP, ZEROS> Weights[2];
     auto load = [&](int s, Weights &w) __attribute__((always_inline)) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const uint8_t *cp = codes[q] + (int64_t)s * 2048;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                w.c[q][h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(cp + (code_at[q] + h * 1024)));
-            const uint8_t *sp = scales[q] + (int64_t)s * (32 * kGroups);
-            if constexpr (kWords == 1) {
-                w.s[q][0] = *reinterpret_cast<const uint32_t *>(sp + scale_at[q]);
-            } else if constexpr (kWords == 2) {
-                const u32x2 v = *reinterpret_cast<const u32x2 *>(sp + scale_at[q]);
-                w.s[q][0] = v.x, w.s[q][1] = v.y;
-            } else {
-                const u32x4 v = *reinterpret_cast<const u32x4 *>(sp + scale_at[q]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w.s[q][i] = v[i];
-            }
-            if constexpr (ZEROS) {
-                const uint8_t *zp = zeros[q] + (int64_t)s * (16 * kGroups);
-                const uint32_t at = scale_at[q] / 2;
-                if constexpr (kGroups == 2) {
-                    w.z[q][0] = *reinterpret_cast<const uint16_t *>(zp + at);
-                } else if constexpr (kGroups == 4) {
-                    w.z[q][0] = *reinterpret_cast<const uint32_t *>(zp + at);
-                } else {
-                    const u32x2 v = *reinterpret_cast<const u32x2 *>(zp + at);
-                    w.z[q][0] = v.x, w.z[q][1] = v.y;
-                }
-            }
-        }
+        for (int q = 0; q < 2; ++q)
+            w[q].load(codes[q] + (int64_t)s * 2048, code_at[q], scales[q] + (int64_t)s * (32 * kGroups),
+                      ZEROS ? zeros[q] + (int64_t)s * (16 * kGroups) : nullptr, scale_at[q]);
     };
 
     // MT pieces of 16 rows from m0 on
@@ -135,7 +140,7 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) stream_kernel(const W4Ge
             if (!loaded && first(c) < s_end) load(first(c), next);
             loaded = more && first(c) < s_end;
             for (int s = first(c); s < s_end; ++s) {
-                const Weights w = next;
+                const Step<GROUP, ZEROS> w[2] = {next[0], next[1]};
                 load(s + 1 < s_end ? s + 1 : more ? first(c2) : s, next);
                 const uint8_t *at = xs + (s - c) * 512;
 #pragma unroll
@@ -144,12 +149,12 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) stream_kernel(const W4Ge
                     uint32_t off[2];
 #pragma unroll
                     for (int q = 0; q < 2; ++q)  // minus 16 minus the zero point, twice: its lower byte as it is stored, 0xC1
-                        off[q] = ZEROS ? __builtin_amdgcn_perm(0xC1C1C1C1u, w.z[q][gr / 4], 0x04000400u | (gr & 3) * 0x00010001u) : 0xC1C0C1C0u;
+                        off[q] = ZEROS ? __builtin_amdgcn_perm(0xC1C1C1C1u, w[q].z[gr / 4], 0x04000400u | (gr & 3) * 0x00010001u) : 0xC1C0C1C0u;
 #pragma unroll
                     for (int i = gr * (GROUP / 32); i < (gr + 1) * (GROUP / 32); ++i) {
                         bf8 w_op[2];
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) w_op[q] = expand(w.c[q][i >> 2][i & 3]);
+                        for (int q = 0; q < 2; ++q) w_op[q] = expand(w[q].c[i >> 2][i & 3]);
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
                             const bf8 xo = __builtin_bit_cast(bf8, *reinterpret_cast<const u32x4 *>(at + row[m] + 64 * i));
@@ -163,7 +168,7 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) stream_kernel(const W4Ge
                     }
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        const float f = scale_value<HALF>(w.s[q][gr / 2], gr & 1);
+                        const float f = scale_value<HALF>(w[q].s[gr / 2], gr & 1);
 #pragma unroll
                         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -226,8 +231,6 @@ constexpr int kWideWaves = 8, kWidePieces = 4;  // of 16 rows in a turn
 template <int GROUP, bool HALF, bool ZEROS>
 __global__ void __launch_bounds__(64 * kWideWaves, 2) wide_stream_kernel(const W4GemmArgs p) {
     constexpr int kGroups = kW4Step / GROUP;      // per step
-    constexpr int kWords = (kGroups + 1) / 2;     // of scales
-    constexpr int kZeroWords = (kGroups + 3) / 4;
     __shared__ __attribute__((aligned(16))) float part[kWideWaves][16 * kWidePieces][36];
     const Expander expand;
     const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
@@ -247,39 +250,12 @@ __global__ void __launch_bounds__(64 * kWideWaves, 2) wide_stream_kernel(const W
     }
     const int s0 = wave * p.steps / kWideWaves, s1 = (wave + 1) * p.steps / kWideWaves;
 
-    struct Weights {
-        u32x4 c[2][2];
-        uint32_t s[2][kWords], z[2][kZeroWords];
-    };
+    typedef Step<GROUP, ZEROS> Weights[2];
     auto load = [&](int s, Weights &w) __attribute__((always_inline)) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                w.c[q][h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(codes[q] + (int64_t)s * 2048 + h * 1024));
-            const uint8_t *sp = scales[q] + (int64_t)s * (32 * kGroups);
-            if constexpr (kWords == 1) {
-                w.s[q][0] = *reinterpret_cast<const uint32_t *>(sp);
-            } else if constexpr (kWords == 2) {
-                const u32x2 v = *reinterpret_cast<const u32x2 *>(sp);
-                w.s[q][0] = v.x, w.s[q][1] = v.y;
-            } else {
-                const u32x4 v = *reinterpret_cast<const u32x4 *>(sp);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w.s[q][i] = v[i];
-            }
-            if constexpr (ZEROS) {
-                const uint8_t *zp = zeros[q] + (int64_t)s * (16 * kGroups);
-                if constexpr (kGroups == 2) {
-                    w.z[q][0] = *reinterpret_cast<const uint16_t *>(zp);
-                } else if constexpr (kGroups == 4) {
-                    w.z[q][0] = *reinterpret_cast<const uint32_t *>(zp);
-                } else {
-                    const u32x2 v = *reinterpret_cast<const u32x2 *>(zp);
-                    w.z[q][0] = v.x, w.z[q][1] = v.y;
-                }
-            }
-        }
+        for (int q = 0; q < 2; ++q)
+            w[q].load(codes[q] + (int64_t)s * 2048, 0, scales[q] + (int64_t)s * (32 * kGroups),
+                      ZEROS ? zeros[q] + (int64_t)s * (16 * kGroups) : nullptr, 0);
     };
 
     Weights first;
@@ -293,10 +269,10 @@ __global__ void __launch_bounds__(64 * kWideWaves, 2) wide_stream_kernel(const W
 #pragma unroll
         for (int m = 0; m < MT; ++m) x[m] = p.x + (int64_t)min(m0 + 16 * m + i16, rows - 1) * K + 8 * g;
         f4 acc[MT][2] = {};
-        Weights next = first;
+        Weights next = {first[0], first[1]};
         if (m0 > 0 && s0 < s1) load(s0, next);
         for (int s = s0; s < s1; ++s) {
-            const Weights w = next;
+            const Step<GROUP, ZEROS> w[2] = {next[0], next[1]};
 #pragma unroll
             for (int b = 0; b < 8 / kRuns; ++b) {
                 u32x4 xv[kRuns][MT];
@@ -316,7 +292,7 @@ __global__ void __launch_bounds__(64 * kWideWaves, 2) wide_stream_kernel(const W
                     for (int i = gr * (GROUP / 32); i < (gr + 1) * (GROUP / 32); ++i) {
                         bf8 wv[2];
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) wv[q] = expand(w.c[q][i >> 2][i & 3]);
+                        for (int q = 0; q < 2; ++q) wv[q] = expand(w[q].c[i >> 2][i & 3]);
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
                             const bf8 xo = __builtin_bit_cast(bf8, xv[i % kRuns][m]);
@@ -327,8 +303,8 @@ __global__ void __launch_bounds__(64 * kWideWaves, 2) wide_stream_kernel(const W
                     }
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        const float f = scale_value<HALF>(w.s[q][gr / 2], gr & 1);
-                        const float off = ZEROS ? 0.125f * (float)((w.z[q][gr / 4] >> (8 * (gr & 3))) & 255u) : 24.0f;
+                        const float f = scale_value<HALF>(w[q].s[gr / 2], gr & 1);
+                        const float off = ZEROS ? 0.125f * (float)((w[q].z[gr / 4] >> (8 * (gr & 3))) & 255u) : 24.0f;
 #pragma unroll
                         for (int m = 0; m < MT; ++m)
 #pragma unroll
