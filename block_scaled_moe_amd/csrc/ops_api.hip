@@ -3,7 +3,7 @@
 // stream.
 #include "ops_internal.h"
 
-#include <initializer_list>
+#include "api_common.h"
 
 using namespace moe;
 
@@ -41,9 +41,7 @@ GroupsPlan groups_plan(int32_t T, int32_t top_k, int32_t n) {
 
 namespace {
 
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 constexpr int32_t kMaxRows = INT32_MAX / 2;  // slots, or rows of one group: rounded up to runs they stay in 32 bits
-int32_t to_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 // The size fields of g.
 int32_t check_sizes(const moe_groups *g) {
@@ -59,7 +57,7 @@ int32_t check_groups(const moe_groups *g) {
     if (rc != MOE_OK) return rc;
     if (!g->offsets || (g->T > 0 && (!g->sorted_slot || !g->slot_pos))) return MOE_ERR_INVALID_ARG;
     if (!g->plan || g->plan_bytes < groups_plan(g->T, g->top_k, g->e_end - g->e_begin).total) return MOE_ERR_WORKSPACE;
-    if (!aligned16(g->offsets) || !aligned16(g->sorted_slot) || !aligned16(g->slot_pos) || ((uintptr_t)g->plan & 255u))
+    if (!aligned(g->offsets, 16) || !aligned(g->sorted_slot, 16) || !aligned(g->slot_pos, 16) || ((uintptr_t)g->plan & 255u))
         return MOE_ERR_ALIGNMENT;
     return MOE_OK;
 }
@@ -71,26 +69,14 @@ int32_t check_rows(const moe_groups *g, int32_t D) {
     return g->T < (1 << 24) && D <= (1 << 30) ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
-// A buffer of a call: n items of `item` bytes at p.
-struct Buffer {
-    const void *p;
-    int64_t n, item;
-};
-bool overlap(const Buffer &a, const Buffer &b) {
-    typedef unsigned __int128 wide;  // sizes that no memory holds are compared too
-    const wide a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
-    return a.n && b.n && a0 < b0 + (wide)b.n * (wide)b.item && b0 < a0 + (wide)a.n * (wide)a.item;
-}
 // The output meets one of the buffers; a call refuses that (buffers not given are NULL).
-bool overlaps_any(const Buffer &out, std::initializer_list<Buffer> others) {
-    for (const Buffer &b : others)
-        if (out.p && b.p && overlap(out, b)) return true;
+bool overlaps_any(const Extent &out, std::initializer_list<Extent> others) {
+    for (const Extent &b : others)
+        if (meet(out, b)) return true;
     return false;
 }
 
-int64_t row_bytes(int32_t dtype, int32_t D) { return (int64_t)D * (dtype == MOE_DT_BF16 ? 2 : 4); }
-
-bool dtype_ok(int32_t d) { return d == MOE_DT_BF16 || d == MOE_DT_FP32; }
+int64_t row_bytes(int32_t dtype, int32_t D) { return D * type_bytes(dtype); }
 
 // Blocks of a column form that a call touches at most: of g's slots, or of the one group of `rows` rows.
 int64_t column_blocks(const moe_groups *g, int32_t rows) {
@@ -144,7 +130,7 @@ int32_t moe_sort(const moe_groups *g, const int32_t *topk_idx, void *stream) {
     const int32_t rc = check_groups(g);
     if (rc != MOE_OK) return rc;
     if (g->T > 0 && !topk_idx) return MOE_ERR_INVALID_ARG;
-    if (!aligned16(topk_idx)) return MOE_ERR_ALIGNMENT;
+    if (!aligned(topk_idx, 16)) return MOE_ERR_ALIGNMENT;
     const int32_t n = g->e_end - g->e_begin;
     const GroupsPlan p = groups_plan(g->T, g->top_k, n);
     uint8_t *at = static_cast<uint8_t *>(g->plan);
@@ -168,70 +154,70 @@ int32_t moe_sort(const moe_groups *g, const int32_t *topk_idx, void *stream) {
     a.ctrl = reinterpret_cast<Ctrl *>(at + p.ctrl);
     a.fill_tail = 1;
     hipStream_t s = (hipStream_t)stream;
-    return to_status(n <= kSortMaxLocal ? launch_sort(a, g->T * g->top_k, s) : launch_permute(a, s));
+    return status_of(n <= kSortMaxLocal ? launch_sort(a, g->T * g->top_k, s) : launch_permute(a, s));
 }
 
 int32_t moe_gather(const moe_groups *g, int32_t dtype, int32_t D, const void *x, void *rows, void *stream) {
     const int32_t rc = check_groups(g);
     if (rc != MOE_OK) return rc;
-    if (!dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
+    if (!type_ok(dtype)) return MOE_ERR_INVALID_ARG;
     const int32_t rr = check_rows(g, D);
     if (rr != MOE_OK) return rr;
     if (g->T == 0) return MOE_OK;
     if (!x || !rows) return MOE_ERR_INVALID_ARG;
-    if (!aligned16(x) || !aligned16(rows)) return MOE_ERR_ALIGNMENT;
+    if (!aligned(x, 16) || !aligned(rows, 16)) return MOE_ERR_ALIGNMENT;
     const int64_t bytes = row_bytes(dtype, D);
     if (overlaps_any({rows, (int64_t)g->T * g->top_k, bytes}, {{x, g->T, bytes}})) return MOE_ERR_INVALID_ARG;
-    return to_status(launch_gather(*g, dtype, D, x, rows, (hipStream_t)stream));
+    return status_of(launch_gather(*g, dtype, D, x, rows, (hipStream_t)stream));
 }
 
 int32_t moe_gather_backward(const moe_groups *g, int32_t dtype, int32_t D, const void *d_rows, void *dx, void *stream) {
     const int32_t rc = check_groups(g);
     if (rc != MOE_OK) return rc;
-    if (!dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
+    if (!type_ok(dtype)) return MOE_ERR_INVALID_ARG;
     const int32_t rr = check_rows(g, D);
     if (rr != MOE_OK) return rr;
     if (g->T == 0) return MOE_OK;
     if (!d_rows || !dx) return MOE_ERR_INVALID_ARG;
-    if (!aligned16(d_rows) || !aligned16(dx)) return MOE_ERR_ALIGNMENT;
+    if (!aligned(d_rows, 16) || !aligned(dx, 16)) return MOE_ERR_ALIGNMENT;
     const int64_t bytes = row_bytes(dtype, D);
     if (overlaps_any({dx, g->T, bytes}, {{d_rows, (int64_t)g->T * g->top_k, bytes}})) return MOE_ERR_INVALID_ARG;
-    return to_status(launch_combine_rows(*g, dtype, dtype, D, d_rows, nullptr, dx, (hipStream_t)stream));
+    return status_of(launch_combine_rows(*g, dtype, dtype, D, d_rows, nullptr, dx, (hipStream_t)stream));
 }
 
 int32_t moe_combine(const moe_groups *g, int32_t y_dtype, int32_t out_dtype, int32_t D, const void *y, const float *w,
                     void *out, void *stream) {
     const int32_t rc = check_groups(g);
     if (rc != MOE_OK) return rc;
-    if (!dtype_ok(y_dtype) || !dtype_ok(out_dtype)) return MOE_ERR_INVALID_ARG;
+    if (!type_ok(y_dtype) || !type_ok(out_dtype)) return MOE_ERR_INVALID_ARG;
     const int32_t rr = check_rows(g, D);
     if (rr != MOE_OK) return rr;
     if (g->T == 0) return MOE_OK;
     if (!y || !w || !out) return MOE_ERR_INVALID_ARG;
-    if (!aligned16(y) || !aligned16(w) || !aligned16(out)) return MOE_ERR_ALIGNMENT;
+    if (!aligned(y, 16) || !aligned(w, 16) || !aligned(out, 16)) return MOE_ERR_ALIGNMENT;
     const int64_t slots = (int64_t)g->T * g->top_k;
     if (overlaps_any({out, g->T, row_bytes(out_dtype, D)}, {{y, slots, row_bytes(y_dtype, D)}, {w, slots, 4}}))
         return MOE_ERR_INVALID_ARG;
-    return to_status(launch_combine_rows(*g, y_dtype, out_dtype, D, y, w, out, (hipStream_t)stream));
+    return status_of(launch_combine_rows(*g, y_dtype, out_dtype, D, y, w, out, (hipStream_t)stream));
 }
 
 int32_t moe_combine_backward(const moe_groups *g, int32_t y_dtype, int32_t out_dtype, int32_t D, const void *d_out,
                              const void *y, const float *w, void *d_y, float *d_w, void *stream) {
     const int32_t rc = check_groups(g);
     if (rc != MOE_OK) return rc;
-    if (!dtype_ok(y_dtype) || !dtype_ok(out_dtype)) return MOE_ERR_INVALID_ARG;
+    if (!type_ok(y_dtype) || !type_ok(out_dtype)) return MOE_ERR_INVALID_ARG;
     const int32_t rr = check_rows(g, D);
     if (rr != MOE_OK) return rr;
     if (g->T == 0) return MOE_OK;
     if (!d_out || !y || !w || !d_y || !d_w) return MOE_ERR_INVALID_ARG;
-    if (!aligned16(d_out) || !aligned16(y) || !aligned16(w) || !aligned16(d_y) || !aligned16(d_w))
+    if (!aligned(d_out, 16) || !aligned(y, 16) || !aligned(w, 16) || !aligned(d_y, 16) || !aligned(d_w, 16))
         return MOE_ERR_ALIGNMENT;
     const int64_t slots = (int64_t)g->T * g->top_k;
-    const Buffer bo = {d_out, g->T, row_bytes(out_dtype, D)}, by = {y, slots, row_bytes(y_dtype, D)}, bw = {w, slots, 4};
-    const Buffer bdy = {d_y, slots, by.item}, bdw = {d_w, slots, 4};
-    if (overlaps_any(bdy, {bo, by, bw, bdw}) || overlaps_any(bdw, {bo, by}) || (d_w != w && overlap(bdw, bw)))
+    const Extent bo = {d_out, g->T, row_bytes(out_dtype, D)}, by = {y, slots, row_bytes(y_dtype, D)}, bw = {w, slots, 4};
+    const Extent bdy = {d_y, slots, by.item}, bdw = {d_w, slots, 4};
+    if (overlaps_any(bdy, {bo, by, bw, bdw}) || overlaps_any(bdw, {bo, by}) || (d_w != w && meet(bdw, bw)))
         return MOE_ERR_INVALID_ARG;
-    return to_status(launch_combine_backward(*g, y_dtype, out_dtype, D, d_out, y, w, d_y, d_w, (hipStream_t)stream));
+    return status_of(launch_combine_backward(*g, y_dtype, out_dtype, D, d_out, y, w, d_y, d_w, (hipStream_t)stream));
 }
 
 int64_t moe_block_column_blocks(int32_t rows, int32_t n) {
@@ -255,13 +241,13 @@ int32_t moe_block_quantize(const moe_block_quantize_args *q, void *stream) {
     if ((by_rows && !rows_form_fits(q->rows, q->C)) || q->rows > kMaxRows) return MOE_ERR_UNSUPPORTED;
     if (q->rows == 0) return MOE_OK;
     if (!q->x) return MOE_ERR_INVALID_ARG;
-    if (!aligned16(q->x) || !aligned16(q->codes) || !aligned16(q->scales) || !aligned16(q->col_codes) ||
-        !aligned16(q->col_scales))
+    if (!aligned(q->x, 16) || !aligned(q->codes, 16) || !aligned(q->scales, 16) || !aligned(q->col_codes, 16) ||
+        !aligned(q->col_scales, 16))
         return MOE_ERR_ALIGNMENT;
-    const Buffer x = {q->x, q->rows, (int64_t)q->C * 2};
-    const Buffer c = {q->codes, q->rows, q->C}, s = {q->scales, q->rows, (int64_t)scale_stride(q->C) * 4};
+    const Extent x = {q->x, q->rows, (int64_t)q->C * 2};
+    const Extent c = {q->codes, q->rows, q->C}, s = {q->scales, q->rows, (int64_t)scale_stride(q->C) * 4};
     const int64_t blocks = column_blocks(q->g, q->rows);
-    const Buffer cc = {q->col_codes, blocks, (int64_t)q->C * 128}, cs = {q->col_scales, blocks, (int64_t)q->C * 4};
+    const Extent cc = {q->col_codes, blocks, (int64_t)q->C * 128}, cs = {q->col_scales, blocks, (int64_t)q->C * 4};
     if (overlaps_any(x, {c, s, cc, cs}) || overlaps_any(c, {s, cc, cs}) || overlaps_any(s, {cc, cs}) || overlaps_any(cc, {cs}))
         return MOE_ERR_INVALID_ARG;
     BlockQuantArgs a{};
@@ -277,12 +263,12 @@ int32_t moe_block_quantize(const moe_block_quantize_args *q, void *stream) {
     a.col_codes = q->col_codes;
     a.col_scales = q->col_scales;
     hipStream_t hs = (hipStream_t)stream;
-    return to_status(by_columns ? launch_block_quant_columns(a, hs) : launch_block_quant_rows(a, hs));
+    return status_of(by_columns ? launch_block_quant_columns(a, hs) : launch_block_quant_rows(a, hs));
 }
 
 // Codes and scales of weights [E][N][K].
-static Buffer weight_codes(const void *p, int32_t E, int32_t N, int32_t K) { return {p, E, (int64_t)N * K}; }
-static Buffer weight_scales(const void *p, int32_t E, int32_t N, int32_t K) { return {p, E, (int64_t)(N / 128) * (K / 128) * 4}; }
+static Extent weight_codes(const void *p, int32_t E, int32_t N, int32_t K) { return {p, E, (int64_t)N * K}; }
+static Extent weight_scales(const void *p, int32_t E, int32_t N, int32_t K) { return {p, E, (int64_t)(N / 128) * (K / 128) * 4}; }
 
 // Sizes and buffers of weights [E][N][K].
 static int32_t check_weights(int32_t E, int32_t N, int32_t K, const void *codes, const void *scales) {
@@ -290,7 +276,7 @@ static int32_t check_weights(int32_t E, int32_t N, int32_t K, const void *codes,
     if (N % 128 || K % 128 || N > kMaxBlockDim || K > kMaxBlockDim) return MOE_ERR_UNSUPPORTED;
     if (!codes || !scales) return MOE_ERR_INVALID_ARG;
     // the scales are read one at a time: those of an expert in the middle are as good as the first's
-    if (!aligned16(codes) || ((uintptr_t)scales & 3u)) return MOE_ERR_ALIGNMENT;
+    if (!aligned(codes, 16) || ((uintptr_t)scales & 3u)) return MOE_ERR_ALIGNMENT;
     return MOE_OK;
 }
 
@@ -299,19 +285,19 @@ int32_t moe_block_quantize_weights(const uint16_t *w, int32_t E, int32_t N, int3
     const int32_t rc = check_weights(E, N, K, codes, scales);
     if (rc != MOE_OK) return rc;
     if (!w) return MOE_ERR_INVALID_ARG;
-    if (!aligned16(w)) return MOE_ERR_ALIGNMENT;
-    const Buffer c = weight_codes(codes, E, N, K), s = weight_scales(scales, E, N, K), x = {w, E, (int64_t)N * K * 2};
+    if (!aligned(w, 16)) return MOE_ERR_ALIGNMENT;
+    const Extent c = weight_codes(codes, E, N, K), s = weight_scales(scales, E, N, K), x = {w, E, (int64_t)N * K * 2};
     if (overlaps_any(x, {c, s}) || overlaps_any(c, {s})) return MOE_ERR_INVALID_ARG;
-    return to_status(launch_block_quant_weights(w, E, N, K, codes, scales, (hipStream_t)stream));
+    return status_of(launch_block_quant_weights(w, E, N, K, codes, scales, (hipStream_t)stream));
 }
 
 int32_t moe_block_pack_weights(const uint8_t *rowmajor, int32_t E, int32_t N, int32_t K, uint8_t *codes, void *stream) {
     const int32_t rc = check_weights(E, N, K, codes, codes);
     if (rc != MOE_OK) return rc;
     if (!rowmajor) return MOE_ERR_INVALID_ARG;
-    if (!aligned16(rowmajor)) return MOE_ERR_ALIGNMENT;
+    if (!aligned(rowmajor, 16)) return MOE_ERR_ALIGNMENT;
     if (overlaps_any(weight_codes(codes, E, N, K), {weight_codes(rowmajor, E, N, K)})) return MOE_ERR_INVALID_ARG;
-    return to_status(launch_pack_rowmajor(MOE_FMT_FP8, rowmajor, nullptr, E, N, K, codes, nullptr, (hipStream_t)stream));
+    return status_of(launch_pack_rowmajor(MOE_FMT_FP8, rowmajor, nullptr, E, N, K, codes, nullptr, (hipStream_t)stream));
 }
 
 int32_t moe_block_gemm(const moe_block_gemm_args *a, void *stream) {
@@ -330,7 +316,7 @@ int32_t moe_block_gemm(const moe_block_gemm_args *a, void *stream) {
     if (!rows_form_fits(a->rows, a->transposed ? a->w.N : a->w.K)) return MOE_ERR_UNSUPPORTED;
     if (a->rows == 0) return MOE_OK;
     if (!a->x_codes || !a->x_scales || !a->out) return MOE_ERR_INVALID_ARG;
-    if (!aligned16(a->x_codes) || !aligned16(a->x_scales) || !aligned16(a->out)) return MOE_ERR_ALIGNMENT;
+    if (!aligned(a->x_codes, 16) || !aligned(a->x_scales, 16) || !aligned(a->out, 16)) return MOE_ERR_ALIGNMENT;
     BlockGemmArgs p{};
     p.v = group_view(a->g, a->rows);
     p.by_token = a->by_token ? 1 : 0;
@@ -350,7 +336,7 @@ int32_t moe_block_gemm(const moe_block_gemm_args *a, void *stream) {
                      {{a->x_codes, a->rows, p.R}, {a->x_scales, a->rows, (int64_t)scale_stride(p.R) * 4},
                       weight_codes(a->w.codes, a->w.E, a->w.N, a->w.K), weight_scales(a->w.scales, a->w.E, a->w.N, a->w.K)}))
         return MOE_ERR_INVALID_ARG;
-    return to_status(launch_block_gemm(p, a->transposed != 0, (hipStream_t)stream));
+    return status_of(launch_block_gemm(p, a->transposed != 0, (hipStream_t)stream));
 }
 
 int32_t moe_block_wgrad(const moe_block_wgrad_args *a, void *stream) {
@@ -364,8 +350,8 @@ int32_t moe_block_wgrad(const moe_block_wgrad_args *a, void *stream) {
     }
     if (!a->dw || (a->rows > 0 && (!a->g_codes || !a->g_scales || !a->x_codes || !a->x_scales)))
         return MOE_ERR_INVALID_ARG;
-    if (!aligned16(a->dw) || !aligned16(a->g_codes) || !aligned16(a->g_scales) || !aligned16(a->x_codes) ||
-        !aligned16(a->x_scales))
+    if (!aligned(a->dw, 16) || !aligned(a->g_codes, 16) || !aligned(a->g_scales, 16) || !aligned(a->x_codes, 16) ||
+        !aligned(a->x_scales, 16))
         return MOE_ERR_ALIGNMENT;
     const int64_t blocks = column_blocks(a->g, a->rows);
     if (overlaps_any({a->dw, a->g ? a->g->e_end - a->g->e_begin : 1, (int64_t)a->N * a->K * 2},
@@ -383,7 +369,7 @@ int32_t moe_block_wgrad(const moe_block_wgrad_args *a, void *stream) {
     p.g_scales = a->g_scales;
     p.x_scales = a->x_scales;
     p.dw = a->dw;
-    return to_status(launch_block_wgrad(p, (hipStream_t)stream));
+    return status_of(launch_block_wgrad(p, (hipStream_t)stream));
 }
 
 }  // extern "C"
