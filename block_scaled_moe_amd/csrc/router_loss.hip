@@ -262,19 +262,19 @@ __global__ void __launch_bounds__(kThreads) loss_kernel(const LossArgs a) {
     }
 }
 
-// The sums of EXPERTS experts of one sequence over its runs, 1024 / EXPERTS runs at a time. Where that is not all of them, the
-// workgroup that comes last for a sequence adds the parts of its balance loss, in the order of the experts.
-constexpr int kJoinThreads = 1024, kJoinWaves = kJoinThreads / 64;
-template <int EXPERTS>
+// The sums of 64 experts of one sequence over its runs, a run a wave. Where that is not all of them, the workgroup that comes last
+// for a sequence adds the parts of its balance loss, in the order of the experts. (16 experts a workgroup, four runs a wave, read the
+// runs in fewer turns, but more of them meet: 16384 x 384 in eight sequences 17.9 us for the losses, so 15.5; 5003 x 61 in 17 11.0
+// and 8.8; 131072 x 384 in one 40.9 and 41.4; 2000 x 16 in one 7.9 and 8.2.)
+constexpr int kJoinThreads = 1024, kJoinWaves = kJoinThreads / 64, kJoinExperts = 64;
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LossArgs a) {
-    constexpr int kRunsAtATime = kJoinThreads / EXPERTS;
-    __shared__ double sum[kJoinWaves][EXPERTS];
-    __shared__ int32_t count[kJoinWaves][EXPERTS];
+    __shared__ double sum[kJoinWaves][kJoinExperts];
+    __shared__ int32_t count[kJoinWaves][kJoinExperts];
     __shared__ double squares[kJoinWaves];
     __shared__ int32_t tokens[kJoinWaves];
-    const int E = a.l.E, ne = (E + EXPERTS - 1) / EXPERTS;
+    const int E = a.l.E, ne = (E + kJoinExperts - 1) / kJoinExperts;
     const int s = blockIdx.x / ne, eb = blockIdx.x % ne, t = threadIdx.x;
-    const int e = eb * EXPERTS + t % EXPERTS;
+    const int e = eb * kJoinExperts + t % 64;
     int32_t lo = 0, hi = a.l.T;
     int64_t first = 0;
     if (a.l.seq) {
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LossArgs a) {
     int32_t c = 0, m = 0;
     if (e < E) {
 #pragma unroll 8
-        for (int i = t / EXPERTS; i < n; i += kRunsAtATime) {
+        for (int i = t / 64; i < n; i += kJoinWaves) {
             p += a.sums[(first + i) * E + e];
             c += a.counts[(first + i) * E + e];
         }
@@ -298,17 +298,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LossArgs a) {
     }
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) {
-        if (off >= EXPERTS) {
-            p += __shfl_xor(p, off);
-            c += __shfl_xor(c, off);
-        }
         z += __shfl_xor(z, off);
         m += __shfl_xor(m, off);
     }
-    if (t % 64 < EXPERTS) {
-        sum[t / 64][t % 64] = p;
-        count[t / 64][t % 64] = c;
-    }
+    sum[t / 64][t % 64] = p;
+    count[t / 64][t % 64] = c;
     if (t % 64 == 0) {
         squares[t / 64] = z;
         tokens[t / 64] = m;
@@ -316,7 +310,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const LossArgs a) {
     __syncthreads();
     if (t >= 64) return;
     double part = 0.0;
-    if (t < EXPERTS && e < E) {
+    if (e < E) {
         p = sum[0][t];
         c = count[0][t];
 #pragma unroll
@@ -485,7 +479,8 @@ __global__ void __launch_bounds__(kGradThreads) logits_grad_kernel(const GradArg
 }
 
 // f is called with the lanes a token and pieces a lane for rows of E values: the fewest lanes that hold a row in at most
-// four pieces each, more pieces only where a wave is not enough.
+// four pieces each, more pieces only where a wave is not enough. Three pieces, so that no quarter of the places is empty, stand only
+// at 257 to 384 values.
 template <typename F>
 void by_row(int32_t E, F &&f) {
     using std::integral_constant;
@@ -525,7 +520,7 @@ LossPlan loss_plan(int32_t T, int32_t E, int32_t B, bool seq) {
     p.counts = take(4 * (size_t)p.runs.n * E);
     p.squares = take(8 * (size_t)p.runs.n);
     p.tokens = take(4 * (size_t)p.runs.n);
-    p.parts = take(8 * (size_t)B * ((E + 15) / 16));
+    p.parts = take(8 * (size_t)B * ((E + kJoinExperts - 1) / kJoinExperts));
     p.arrived = take(4 * (size_t)B);
     p.total = off > 0 ? off : 256;
     return p;
@@ -562,10 +557,8 @@ hipError_t launch_router_losses(const moe_losses &l, int32_t dtype, const void *
         }
     });
     if (!one) {
-        // 16 experts a workgroup read the runs in fewer turns, 64 are done without the exchange between workgroups
-        const int experts = l.E <= 64 && p.runs.n <= 128ll * l.B ? 64 : 16;
-        const unsigned groups = (unsigned)(l.B * ((l.E + experts - 1) / experts));
-        hipLaunchKernelGGL(experts == 64 ? join_kernel<64> : join_kernel<16>, dim3(groups), dim3(kJoinThreads), 0, s, a);
+        const unsigned groups = (unsigned)(l.B * ((l.E + kJoinExperts - 1) / kJoinExperts));
+        hipLaunchKernelGGL(join_kernel, dim3(groups), dim3(kJoinThreads), 0, s, a);
     }
     return hipGetLastError();
 }
