@@ -374,6 +374,11 @@ __global__ void __launch_bounds__(64 * kWideWaves, 2) wide_stream_kernel(const W
 // 304, 342; 42 rows 474, 352 and 373, 378; unevenly (the largest group of five to thirty times the mean) 10 rows 220, 273 and 167,
 // 270; 21 rows 322, 348 and 187, 294; 42 rows 444, 424 and 311, 360.
 constexpr int kStreamMean = 24, kStreamRows = 16, kWideRows = 160;
+// Waves that share a block of two column tiles, by the blocks of a call: eight up to kBlocksOfEight, four up to kBlocksOfFour, then each
+// its own. us of eight, four and one: one row, K 4096, 256 blocks 8.2, 8.8, 18.3; 384 blocks 10.8, 9.5, 18.8; 2048 blocks 42, 32, 34. One token of
+// eight experts, K 2560, 256 blocks 7.1, 7.8, 13.4; 384 blocks 9.0, 8.4, 13.6; 1024 blocks 16.9, 12.9, 16.1; 1536 blocks 24.1, 20.7, 17.5.
+// 48 tokens on 48 experts, K 2048, 392 blocks 9.0, 8.7, 13.3; 784 blocks 14.9, 12.1, 13.4; 1176 blocks 19.8, 17.6, 14.6; 6272 blocks 83, 64, 50.
+constexpr int kBlocksOfEight = 320, kBlocksOfFour = 1024;
 
 hipError_t launch_w4_gemm(const W4GemmArgs &args, hipStream_t s) {
     W4GemmArgs a = args;
@@ -391,8 +396,8 @@ hipError_t launch_w4_gemm(const W4GemmArgs &args, hipStream_t s) {
             hipLaunchKernelGGL(kernel, dim3((unsigned)(a.v.max_tiles * a.shares * ((nb + per_group - 1) / per_group))), dim3(512), 0, s, a);
         };
         if (!a.v.offsets && rows > kStreamRows) go(wide_stream_kernel<kGroup, kHalf, kZeros>, 1);
-        else if (blocks >= 4096) go(stream_kernel<kGroup, kHalf, kZeros, 1>, 8);
-        else if (blocks >= 1024) go(stream_kernel<kGroup, kHalf, kZeros, 4>, 2);
+        else if (blocks > kBlocksOfFour) go(stream_kernel<kGroup, kHalf, kZeros, 1>, 8);
+        else if (blocks > kBlocksOfEight) go(stream_kernel<kGroup, kHalf, kZeros, 4>, 2);
         else go(stream_kernel<kGroup, kHalf, kZeros, 8>, 1);
     });
     return hipGetLastError();
