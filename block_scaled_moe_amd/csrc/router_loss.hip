@@ -1,7 +1,7 @@
 // router_loss.hip - losses of the router and the gradient of its logits (include/moe_router.h,
 // moe_router_losses, moe_logits_grad).
 //
-//   p[t][e] = exp(l[t][e] - m[t]) / sum over e of the same,  m[t] = max over e
+//   p[t][e] = exp(l[t][e] - m[t]) / sum over e of the same,  m[t] = max over e (in both: none goes by the rounded lse)
 //   P[e] = sum over t of p, N[e] = slots of e;  balance = E / (k n^2) sum of N P,  z = mean of (m + log sum)^2
 //   d_l = p (a - <a, p>) + b lse p + gate,  a[e] = d_balance E / (k n^2) N[e],  b = 2 d_z / n
 //
@@ -12,9 +12,9 @@
 // workgroups take: the losses' leave one line of partial sums each, which a second launch adds in the order of
 // the runs; there are no atomics on values.
 //
-// 131072 x 384 fp32 logits, one sequence: losses 45 to 59 us (201 MB, as far as they lie in the last-level cache or not) and
-// 6.5 us to join the runs, gradient 70 us (403 MB, 5.8 TB/s of reads and writes). 16384 x 384, eight sequences: 11.6, 7.9 and
-// 15.0 us. Small batches: 4 us a kernel, of which a launch is most.
+// Medians: 131072 x 384 fp32 logits, one sequence, losses 59 us (201 MB; 45 where they lie in the last-level cache) and 7.4 us to join
+// the runs, gradient 75 us (403 MB, 5.4 TB/s of reads and writes). 16384 x 384, eight sequences: 11.8, 6.3 and 16.4 us. Small
+// batches: 4 us a kernel, of which a launch is most.
 #include "router_internal.h"
 
 namespace moe {
@@ -516,10 +516,11 @@ LossPlan loss_plan(int32_t T, int32_t E, int32_t B, bool seq) {
         off += (bytes + 255) & ~(size_t)255;
         return at;
     };
-    p.sums = take(4 * (size_t)p.runs.n * E);
-    p.counts = take(4 * (size_t)p.runs.n * E);
-    p.squares = take(8 * (size_t)p.runs.n);
-    p.tokens = take(4 * (size_t)p.runs.n);
+    const size_t lines = (size_t)run_split(T, B, true, 1 << p.runs.log_rows, INT32_MAX).n;  // the same with and without seq
+    p.sums = take(4 * lines * E);
+    p.counts = take(4 * lines * E);
+    p.squares = take(8 * lines);
+    p.tokens = take(4 * lines);
     p.parts = take(8 * (size_t)B * ((E + kJoinExperts - 1) / kJoinExperts));
     p.arrived = take(4 * (size_t)B);
     p.total = off > 0 ? off : 256;
