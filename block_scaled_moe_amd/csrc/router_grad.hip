@@ -5,17 +5,18 @@
 // Both are products of a fp32 matrix with a bf16 one whose rows run along the reduction, so one kernel does both. The
 // fp32 one, which is the smaller, goes through the bf16 MFMA in pieces: its value is the sum of its upper 8 bits, the next 8
 // and the last 8, each a bf16 exactly. All three are needed for bf16 results too: a row of g sums to nearly nothing, so what
-// the experts' weights have in common cancels, and the leading bits with it. Where many column tiles share it, split_kernel cuts it once into the order in which
-// the MFMA takes it, for either product: tiles of 128 rows, steps of 32 of the reduction, pieces, 16 rows, lanes; a tile's
-// step is one contiguous copy. Where few do, a launch costs more than cutting it in every workgroup.
+// the experts' weights have in common cancels, and the leading bits with it. Where many column tiles share it, split_kernel cuts
+// it once into the order in which the MFMA takes it, for either product: tiles of 128 rows, steps of 32 of the reduction,
+// pieces, 16 rows, lanes; a tile's step is one contiguous copy. Where few do, a launch costs more than cutting it in every workgroup.
 //
 // product_kernel: BM rows x 256 columns a workgroup of 4 waves, two workgroups a CU, a step of 32 of the reduction in one LDS
 // buffer while the next one arrives in the other. The bf16 matrix comes as it is and is turned over by the transposing
 // LDS read (4 rows x 16 columns per 16 lanes), the same operand for all pieces.
 //
-// Bound by the MFMAs where they are many: 16384 x 384, 4096 columns, bf16 results: 272 us a call (309 GFLOP of pieces; 212 with
-// two pieces, whose results were up to 2^-15 of each value of g off). 5003 x 61, 1088 columns, fp32 results with the bias's: 18.8
-// and 4.1 us. 300 x 64, 256 columns: 11.8 us, two steps' latency and the launch.
+// Bound by the MFMAs where they are many: 16384 x 384, 4096 columns, bf16 results: split 23 us, both products 268 (309 GFLOP of
+// pieces, 1.15 PFLOP/s; 231 and 1.34 at best, the matrix cores then busy 62% of the cycles), joining dwr's parts 7.8; two pieces took 190
+// for results up to 2^-15 of each value of g off. 5003 x 61, 1088 columns, fp32 results with the bias's: 19.1 and 4.0 us. 300 x 64,
+// 256 columns: 13.3 us, ten steps' latency one behind the other and the launch.
 #include "block_mma.h"
 #include "router_internal.h"
 

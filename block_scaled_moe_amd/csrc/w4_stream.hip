@@ -3,9 +3,9 @@
 //
 // Bound by the weights' bytes. A wave takes two column tiles of 16 (with swiglu one of the first half's columns and the same of
 // the second half's) of one tile of rows; its load of codes is 1 KiB in a row, and those of the next step are in flight
-// while the current one is multiplied. 64 tokens on 96 of 384 experts, 5120 x 4096, groups of 32 with zero points: 148 us, 6.0
-// TB/s. One token, eight experts 4096 x 2560, groups of 128: 11.1 to 12.8 us for 41 MB; one row, 5120 x 4096: 7.8 us for 11.5 MB:
-// a load's latency, the rows' way into LDS and the launch.
+// while the current one is multiplied. 64 tokens on 96 of 384 experts, 5120 x 4096, groups of 32 with zero points: 147 us, 6.0
+// TB/s. One token, eight experts 4096 x 2560, groups of 128: 13.2 us for 41 MB; one row, 5120 x 4096: 8.1 us for 11.5 MB: a load's
+// latency, the rows' way into LDS and the launch.
 #include "w4_mma.h"
 
 namespace moe {

@@ -10,15 +10,16 @@
 //    three ahead at once, and the next stage's operands are read and expanded behind those products.
 //  - The sums of x per row and group are the same for all columns: each wave forms those of one piece of 16 rows, two stages
 //    ahead, and leaves them in LDS, from where they are the products' first addends.
-//  - MFMAs (16 clocks) and vector instructions (4 clocks) are about as much work, so each MFMA stands beside the
+//  - MFMAs (16 clocks) and other vector instructions (4 clocks) are about as much work, so each MFMA stands beside the
 //    instructions that expand a later operand or add an earlier group's sum.
 //  - A workgroup a CU (157 KiB of LDS) walks its items, parts with many rows first. Where the next part's rows are is found out
 //    while this one's first stages arrive: three loads in a row, each of which needs the one before, no longer begin a part.
-// Bound by what a CU issues: of a stage's 3600 clocks at 85 rows about 2000 are MFMAs and vector instructions, the rest are waits
-// for LDS and barriers that two waves a SIMD do not hide; about 8 us of an item are its beginning and end. 8192 rows of 96
-// experts, 5120 x 4096, groups of 128: 510 us (0.67 PFLOP/s; 1920 items, of which a workgroup takes seven or eight). 3003 rows of
-// 60 experts (1 to 553 each), 1002 x 2592, groups of 32: 98 us; 126 with the parts in the list's order, 116 once they
-// are spread over the XCDs. Evenly routed the order costs 2%.
+// Bound by waits: on 8192 rows of 96 experts, 5120 x 4096, groups of 128, the matrix cores are busy 33% of the cycles and other vector
+// instructions take 36%; a wave issues in 36% of its time, waits for its turn in 24%, and in 40% for LDS and for the other waves at a
+// stage's barrier, which two waves a SIMD do not hide. About 8 us of an item are its beginning and end. That product: 538 us in the
+// median, 514 at best (0.64 to 0.67 PFLOP/s; 1920 items, of which a workgroup takes seven or eight). 3003 rows of 60 experts (1 to 553
+// each), 1002 x 2592, groups of 32: 104 us; a fourth more with the parts in the list's order, a tenth once they are spread over
+// the XCDs. Evenly routed the order costs 2%.
 #include "w4_mma.h"
 #include "w4_parts.h"
 
