@@ -311,9 +311,10 @@ __global__ void __launch_bounds__(256) parts_kernel(const float *__restrict__ pa
     }
 }
 
-// Values of g times column tiles from which on g is cut beforehand, which takes a launch and a pass over g, instead of anew for every
-// column tile. us cut in the workgroups and beforehand (bf16 dh, fp32 dwr): 2^19 (2000 x 64, 1024 columns) 19, 25; 2^21.6 (1024 x 384, 2048) 29, 33;
-// 2^23 (4096 x 256, 2048) 39, 41; 2^23.6 (4096 x 384, 2048) 52, 50; 2^25 (8192 x 256, 4096) 120, 97; 2^26.6 (16384 x 384, 4096) 349, 263.
+// Values of g times column tiles from which on g is cut beforehand, which takes a launch and a pass over g, instead of anew
+// for every column tile. us cut in the workgroups and beforehand (bf16 dh, fp32 dwr): 2^19 (2000 x 64, 1024 columns) 19, 25;
+// 2^21.6 (1024 x 384, 2048) 29, 33; 2^23 (4096 x 256, 2048) 39, 41; 2^23.6 (4096 x 384, 2048) 52, 50; 2^25 (8192 x 256, 4096)
+// 120, 97; 2^26.6 (16384 x 384, 4096) 349, 263.
 constexpr int64_t kCutFrom = 1 << 23;
 
 }  // namespace

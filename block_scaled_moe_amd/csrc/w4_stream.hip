@@ -20,7 +20,8 @@ struct Step {
     u32x4 c[2];
     uint32_t s[kWords], z[kZeroWords];
     // from the step's places in the packed arrays, and this lane's in them
-    __device__ __forceinline__ void load(const uint8_t *codes, uint32_t code_at, const uint8_t *scales, const uint8_t *zeros, uint32_t scale_at) {
+    __device__ __forceinline__ void load(const uint8_t *codes, uint32_t code_at, const uint8_t *scales, const uint8_t *zeros,
+                                         uint32_t scale_at) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             c[h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(codes + (code_at + h * 1024)));
@@ -225,8 +226,9 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) stream_kernel(const W4Ge
     }
 }
 
-// 17 to kWideRows rows of the one weight there is (no groups, so x's rows are in order): a workgroup takes two column tiles, its waves a
-// part of the steps each, and their partial sums meet in LDS in the waves' order. Turns of up to 64 rows, each of which reads the weights.
+// 17 to kWideRows rows of the one weight there is (no groups, so x's rows are in order): a workgroup takes two column tiles, its
+// waves a part of the steps each, and their partial sums meet in LDS in the waves' order. Turns of up to 64 rows, each of which
+// reads the weights.
 constexpr int kWideWaves = 8, kWidePieces = 4;  // of 16 rows in a turn
 template <int GROUP, bool HALF, bool ZEROS>
 __global__ void __launch_bounds__(64 * kWideWaves, 2) wide_stream_kernel(const W4GemmArgs p) {
@@ -374,10 +376,11 @@ __global__ void __launch_bounds__(64 * kWideWaves, 2) wide_stream_kernel(const W
 // 304, 342; 42 rows 474, 352 and 373, 378; unevenly (the largest group of five to thirty times the mean) 10 rows 220, 273 and 167,
 // 270; 21 rows 322, 348 and 187, 294; 42 rows 444, 424 and 311, 360.
 constexpr int kStreamMean = 24, kStreamRows = 16, kWideRows = 160;
-// Waves that share a block of two column tiles, by the blocks of a call: eight up to kBlocksOfEight, four up to kBlocksOfFour, then each
-// its own. us of eight, four and one: one row, K 4096, 256 blocks 8.2, 8.8, 18.3; 384 blocks 10.8, 9.5, 18.8; 2048 blocks 42, 32, 34. One token of
-// eight experts, K 2560, 256 blocks 7.1, 7.8, 13.4; 384 blocks 9.0, 8.4, 13.6; 1024 blocks 16.9, 12.9, 16.1; 1536 blocks 24.1, 20.7, 17.5.
-// 48 tokens on 48 experts, K 2048, 392 blocks 9.0, 8.7, 13.3; 784 blocks 14.9, 12.1, 13.4; 1176 blocks 19.8, 17.6, 14.6; 6272 blocks 83, 64, 50.
+// Waves that share a block of two column tiles, by the blocks of a call: eight up to kBlocksOfEight, four up to kBlocksOfFour,
+// then each its own. us of eight, four and one: one row, K 4096, 256 blocks 8.2, 8.8, 18.3; 384 blocks 10.8, 9.5, 18.8; 2048
+// blocks 42, 32, 34. One token of eight experts, K 2560, 256 blocks 7.1, 7.8, 13.4; 384 blocks 9.0, 8.4, 13.6; 1024 blocks 16.9,
+// 12.9, 16.1; 1536 blocks 24.1, 20.7, 17.5. 48 tokens on 48 experts, K 2048, 392 blocks 9.0, 8.7, 13.3; 784 blocks 14.9, 12.1,
+// 13.4; 1176 blocks 19.8, 17.6, 14.6; 6272 blocks 83, 64, 50.
 constexpr int kBlocksOfEight = 320, kBlocksOfFour = 1024;
 
 hipError_t launch_w4_gemm(const W4GemmArgs &args, hipStream_t s) {

@@ -465,9 +465,10 @@ hipError_t launch_w4_tile(const W4GemmArgs &a, hipStream_t s) {
     const int64_t tiles = a.v.offsets ? a.v.max_tiles : (a.v.rows + kBM - 1) / kBM;
     auto items = [&](int columns) { return tiles * ((a.C + columns - 1) / columns); };
     // A second half that starts inside a packed tile needs one more of them, for which only the narrow tile has room, as for the
-    // sums of groups of 32. Else by the items of a call, us of the narrow tiles and the wide: 50 rows each of 64 experts, K 2560, 156 items
-    // 30.6, 44.1; 390 items 66.6, 71.3; 624 items 86, 77; 1248 items 171, 144. One weight, K 2560, 96 items 35, 51; 320 items 92, 99; 576
-    // items 152, 145 (between them, where the narrow ones begin one round of the CUs more, the wide are up to a sixth faster: 256 items 66, 57).
+    // sums of groups of 32. Else by the items of a call, us of the narrow tiles and the wide: 50 rows each of 64 experts, K 2560,
+    // 156 items 30.6, 44.1; 390 items 66.6, 71.3; 624 items 86, 77; 1248 items 171, 144. One weight, K 2560, 96 items 35, 51; 320
+    // items 92, 99; 576 items 152, 145 (between them, where the narrow ones begin one round of the CUs more, the wide are up to a
+    // sixth faster: 256 items 66, 57).
     const bool narrow = a.w.group == 32 || (a.swiglu && a.C % 16) || items(a.swiglu ? 128 : 256) < 512;
     const int64_t n = ((a.v.offsets ? 2 : 1) * items(narrow ? (a.swiglu ? 64 : 128) : (a.swiglu ? 128 : 256)) + 7) / 8 * 8;
     if (n > INT32_MAX) return hipErrorInvalidValue;

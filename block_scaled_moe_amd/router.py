@@ -168,7 +168,8 @@ def router_losses(logits: torch.Tensor, topk_idx: torch.Tensor, valid: torch.Ten
                   seq: torch.Tensor | None = None, out: RouterLosses | None = None) -> RouterLosses:
     """logits [T, E] (fp32 or bf16) and topk_idx int32 [T, k] -> RouterLosses (moe_router_losses). valid: bool or uint8 [T],
     the tokens that count (default: all). seq: int32 [B + 1] starts of packed sequences, each with losses of its own
-    (default: one sequence); tokens before the first one or from the last start on count nowhere. `out`: losses of the same sizes to fill again, which hold their own seq."""
+    (default: one sequence); tokens before the first one or from the last start on count nowhere. `out`: losses of the same
+    sizes to fill again, which hold their own seq."""
     T, E = _matrix("logits", logits)
     k = _matrix("topk_idx", topk_idx)[1]
     dev = logits.device
